@@ -77,6 +77,7 @@ typedef enum {
 #define REPLAY_SEQERR_ROLLBACK_RANGE 2  /* rollback(r) with r < 0 or r > count */
 #define REPLAY_SEQERR_TOO_FEW        4  /* decode / verify(W) with count < W; y of that sequence is NaN */
 #define REPLAY_SEQERR_POS_OVERFLOW   8  /* append would take pos past 2^31 - 1 */
+#define REPLAY_SEQERR_BAD_RANGE     16  /* prompts: a sequence's range decreases, leaves 0..T or is too long */
 
 typedef enum {
     REPLAY_NONE = -1,
@@ -378,6 +379,68 @@ replay_status replay_eager_select(const replay_config *cfg, const float *snaps, 
    multiple of 16. */
 replay_status replay_stream_probe(int32_t mode, const void *src, void *dst, size_t bytes,
                                   void *stream);
+
+/* ---- from projected rows to the inputs of the recurrence ------------------
+   What an SSM layer of this kind does between its projection and the
+   recurrence (background to the pages, which start from q, k, v, dt, a): a
+   short causal convolution of every channel, an activation, and the step
+   size and decay from the projection's last columns.  A projected row holds
+   C = H P + 2 G N channels in the order [v | k | q]; rows may lie any
+   stride apart (a view into wider rows), in the io dtype. */
+typedef struct {
+    int32_t width;         /* K, the taps: 2..4 */
+    int32_t slots;         /* R, rows a sequence's convolution state keeps */
+    int32_t silu;          /* 1: o = z / (1 + exp(-z)) of the sum z; 0: o = z */
+    const float *weight;   /* [C][K], the last tap meets the token itself */
+    const float *bias;     /* [C], or NULL for none */
+    const float *dt_bias;  /* [H], or NULL for none */
+    const float *a_log;    /* [H]: the head's decay rate is -exp(a_log); needed with dt_raw */
+    float dt_min, dt_max;  /* dt = softplus(dt_raw + dt_bias) clamped to these; dt_max 0: no upper bound */
+} replay_conv_params;
+
+/* Inputs of packed prompts: cfg->batch sequences, sequence b in rows
+   cu_seqlens[b] .. cu_seqlens[b + 1] - 1 of T (device int32 [B + 1]; lengths
+   of 0 are allowed, rows outside every range are left as they are).
+   x: C channels per row, rows x_stride elements apart; dt_raw: H values per
+   row, dt_stride apart, or NULL (then dt and a are not written; Gated
+   DeltaNet layers, whose two scalars are made otherwise, need NULL:
+   UNSUPPORTED).  Outputs as the recurrence takes them: q, k [T][G][N], v
+   [T][H][P] (io dtype), dt, a [T][H] f32.
+   state_in: [B][R][C] (io dtype) the rows before each sequence, NULL for
+   zeros; state_out: [B][R][C], receives the last K - 1 rows (for a
+   sequence shorter than that, earlier ones of state_in among them); it may
+   equal state_in, and must not overlap it otherwise.  The row i before the
+   next token sits in slot (pos[b] - i) mod R, where replay_conv_step looks
+   for it; pos: the layer's pos, or NULL for 0.  R >= K - 1.
+   err: device int32 [B + 1], the layer's err or one like it.  A sequence
+   whose range decreases or leaves 0..T gets BAD_RANGE, and its rows and its
+   state are left as they are; where some range decreases, rows of other
+   sequences may be left or taken for a neighbour's.  T >= 1. */
+replay_status replay_conv_prompt(const replay_config *cfg, const replay_conv_params *conv, int32_t T,
+                                 const int32_t *cu_seqlens, const void *x, int64_t x_stride,
+                                 const void *dt_raw, int64_t dt_stride, const int32_t *pos,
+                                 const void *state_in, void *state_out, void *q, void *k, void *v,
+                                 float *dt, float *a, int32_t *err, void *stream);
+
+/* Inputs of the next W tokens of every sequence, to be called before the
+   replay_append, replay_step or replay_verify_step that takes them (it reads
+   the pointer that call moves).  x: [B W] rows (row b W + w), x_stride
+   apart; dt_raw likewise, or NULL.  Outputs: q, k [B][W][G][N], v
+   [B][W][H][P], dt, a [B][W][H].  conv_state: [B][R][C], row n of a sequence
+   in slot n mod R: its K - 1 newest rows are read, the W new ones written.
+   A rollback of r tokens takes the convolution back too while
+   R >= K - 1 + r; R = K - 1 + W serves every round of W drafts, and keeps
+   the state whole where the append is refused.  R >= max(K - 1, W).
+   n_reject (device int32 [B], or NULL): the rollback that the coming
+   replay_rollback_verify_step will apply; the tokens then follow
+   pos[b] - n_reject[b] (an out-of-range one leaves the pointer where it is,
+   as that call does; its bit is set there).  base: the layer's base, needed
+   with n_reject.  1 <= W <= 16. */
+replay_status replay_conv_step(const replay_config *cfg, const replay_conv_params *conv, int32_t W,
+                               const void *x, int64_t x_stride, const void *dt_raw, int64_t dt_stride,
+                               const int32_t *pos, const int32_t *base, const int32_t *n_reject,
+                               void *conv_state, void *q, void *k, void *v, float *dt, float *a,
+                               void *stream);
 
 #ifdef __cplusplus
 }

@@ -23,12 +23,14 @@ __all__ = [
     "replay_verify", "replay_rollback", "replay_flush", "replay_step", "replay_step_layers", "replay_step_static",
     "replay_verify_step", "replay_rollback_verify_step", "replay_set_flush_skipping", "replay_get_error",
     "replay_eager_step", "replay_eager_select", "replay_stream_probe",
+    "ReplayConvParams", "ReplayConv", "SEQERR_BAD_RANGE", "replay_conv_prompt", "replay_conv_step",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libreplayssm.so")
 
 NONE, F32, BF16, FP8_E4M3, FP4_E2M1 = -1, 0, 1, 2, 3
 SEQERR_RING_OVERFLOW, SEQERR_ROLLBACK_RANGE, SEQERR_TOO_FEW, SEQERR_POS_OVERFLOW = 1, 2, 4, 8
+SEQERR_BAD_RANGE = 16
 
 # every symbol include/replayssm.h declares
 EXPORTS = (
@@ -37,10 +39,12 @@ EXPORTS = (
     "replay_verify", "replay_rollback", "replay_flush", "replay_step", "replay_step_layers", "replay_step_static",
     "replay_verify_step", "replay_rollback_verify_step", "replay_set_flush_skipping", "replay_get_error",
     "replay_eager_step", "replay_eager_select", "replay_stream_probe",
+    "replay_conv_prompt", "replay_conv_step",
 )
 
 _VP = ctypes.c_void_p
 _I32 = ctypes.c_int32
+_I64 = ctypes.c_int64
 
 
 class ReplayConfig(ctypes.Structure):
@@ -55,6 +59,11 @@ BUFFER_FIELDS = ("s_master", "s_copy", "s_scale", "ring_q", "ring_k", "ring_v", 
 
 class ReplayBuffers(ctypes.Structure):
     _fields_ = [(name, _VP) for name in BUFFER_FIELDS]
+
+
+class ReplayConvParams(ctypes.Structure):
+    _fields_ = [("width", _I32), ("slots", _I32), ("silu", _I32), ("weight", _VP), ("bias", _VP),
+                ("dt_bias", _VP), ("a_log", _VP), ("dt_min", ctypes.c_float), ("dt_max", ctypes.c_float)]
 
 
 class ReplayError(RuntimeError):
@@ -89,6 +98,10 @@ def _load():
     L.replay_eager_step.argtypes = [ctypes.POINTER(ReplayConfig)] + [_VP] * 9
     L.replay_eager_select.argtypes = [ctypes.POINTER(ReplayConfig), _VP, _I32, _VP, _VP, _VP]
     L.replay_stream_probe.argtypes = [_I32, _VP, _VP, ctypes.c_size_t, _VP]
+    L.replay_conv_prompt.argtypes = ([ctypes.POINTER(ReplayConfig), ctypes.POINTER(ReplayConvParams), _I32, _VP, _VP,
+                                      _I64, _VP, _I64] + [_VP] * 10)
+    L.replay_conv_step.argtypes = ([ctypes.POINTER(ReplayConfig), ctypes.POINTER(ReplayConvParams), _I32, _VP, _I64,
+                                    _VP, _I64] + [_VP] * 10)
     for name in EXPORTS:
         if name not in ("replay_status_string", "replay_abi_version"):
             getattr(L, name).restype = ctypes.c_int
@@ -228,6 +241,102 @@ def replay_stream_probe(mode, src, dst, nbytes, stream=None):
            "replay_stream_probe")
 
 
+# ---- prompts and the inputs of the recurrence -------------------------------
+# These calls take torch tensors and check what their pointers cannot say:
+# the kernels go by the shapes of cfg.
+
+def _want(what, t, shape, dtype):
+    """A contiguous tensor of this shape and type on the current GPU (None passes)."""
+    if t is None:
+        return None
+    if tuple(t.shape) != shape or t.dtype != dtype or not t.is_contiguous():
+        raise ReplayError(f"{what}: want a contiguous {dtype} tensor of shape {shape}, got {t.dtype} of "
+                          f"{tuple(t.shape)} with strides {t.stride()}")
+    return _here(what, t)
+
+
+def _here(what, t):
+    import torch
+    if t.device.type != "cuda" or t.device.index != torch.cuda.current_device():
+        raise ReplayError(f"{what}: the tensor is on {t.device}, not on the current GPU")
+    return t.data_ptr()
+
+
+def _rows(what, t, n, width, dtype):
+    """(pointer, row stride) of a [n, width] tensor whose rows may lie any stride apart (None: (None, 0))."""
+    if t is None:
+        return None, 0
+    if t.dim() != 2 or t.shape[0] != n or t.shape[1] != width or t.dtype != dtype or (width > 1 and t.stride(1) != 1):
+        raise ReplayError(f"{what}: want a {dtype} tensor of shape {(n, width)} with unit stride along its rows, got "
+                          f"{t.dtype} of {tuple(t.shape)} with strides {t.stride()}")
+    return _here(what, t), (t.stride(0) if n > 1 else max(t.stride(0), width))
+
+
+def _io_type(cfg):
+    import torch
+    return torch.bfloat16 if cfg.io_dtype == BF16 else torch.float32
+
+
+class ReplayConv:
+    """The convolution and discretisation of one layer (replay_conv_params):
+    weight [C, K] and bias [C] f32, dt_bias and a_log [H] f32 (None where the
+    layer has none), `slots` rows of state a sequence (K - 1 + W serves
+    rounds of W drafts).  Holds its tensors."""
+
+    def __init__(self, weight, bias=None, dt_bias=None, a_log=None, slots=None, silu=True, dt_min=0.0,
+                 dt_max=float("inf")):
+        import torch
+        channels, self.width = weight.shape
+        self.channels, self.slots = channels, self.width - 1 if slots is None else int(slots)
+        heads = next((t.shape for t in (a_log, dt_bias) if t is not None), None)
+        self.heads = None if heads is None else heads[0]
+        self.tensors = (weight, bias, dt_bias, a_log)
+        f32 = torch.float32
+        self.params = ReplayConvParams(
+            self.width, self.slots, int(bool(silu)), _want("weight", weight, (channels, self.width), f32),
+            _want("bias", bias, (channels,), f32), _want("dt_bias", dt_bias, (self.heads,), f32),
+            _want("a_log", a_log, (self.heads,), f32), dt_min, 0.0 if dt_max == float("inf") else dt_max)
+
+
+def _conv_call(what, cfg, conv, n, lead, x, dt_raw, q, k, v, dt, a):
+    """The pointers that the two convolution calls share: x, its stride, dt_raw, its stride, q, k, v, dt, a."""
+    import torch
+    io, f32 = _io_type(cfg), torch.float32
+    H, G, P, N = cfg.heads, cfg.groups, cfg.head_dim, cfg.state_dim
+    if conv.channels != H * P + 2 * G * N or (dt_raw is not None and conv.heads != H):
+        raise ReplayError(f"{what}: a convolution of {conv.channels} channels and {conv.heads} heads for a layer of "
+                          f"{H * P + 2 * G * N} channels and {H} heads")
+    rows = _rows("x", x, n, conv.channels, io) + _rows("dt_raw", dt_raw, n, H, io)
+    outs = (_want("q", q, (*lead, G, N), io), _want("k", k, (*lead, G, N), io), _want("v", v, (*lead, H, P), io))
+    return rows, outs + ((None, None) if dt_raw is None else
+                         (_want("dt", dt, (*lead, H), f32), _want("a", a, (*lead, H), f32)))
+
+
+def replay_conv_prompt(cfg, conv, T, cu_seqlens, x, dt_raw, pos, state_in, state_out, q, k, v, dt, a, err, stream=None):
+    """x [T, C] and dt_raw [T, H] may be views into wider rows; conv: ReplayConv; pos, state_in, dt_raw may be None."""
+    import torch
+    i32, B = torch.int32, cfg.batch
+    rows, outs = _conv_call("replay_conv_prompt", cfg, conv, T, (T,), x, dt_raw, q, k, v, dt, a)
+    state = (B, conv.slots, conv.channels)
+    io = _io_type(cfg)
+    _check(lib.replay_conv_prompt(
+        ctypes.byref(cfg), ctypes.byref(conv.params), T, _want("cu_seqlens", cu_seqlens, (B + 1,), i32), *rows,
+        _want("pos", pos, (B,), i32), _want("state_in", state_in, state, io), _want("state_out", state_out, state, io),
+        *outs, _want("err", err, (B + 1,), i32), _stream(stream)), "replay_conv_prompt")
+
+
+def replay_conv_step(cfg, conv, W, x, dt_raw, pos, conv_state, q, k, v, dt, a, base=None, n_reject=None, stream=None):
+    """x [B W, C] and dt_raw [B W, H] may be views into wider rows; conv: ReplayConv; dt_raw may be None."""
+    import torch
+    i32, B = torch.int32, cfg.batch
+    rows, outs = _conv_call("replay_conv_step", cfg, conv, B * W, (B, W), x, dt_raw, q, k, v, dt, a)
+    _check(lib.replay_conv_step(
+        ctypes.byref(cfg), ctypes.byref(conv.params), W, *rows, _want("pos", pos, (B,), i32),
+        _want("base", base, (B,), i32), _want("n_reject", n_reject, (B,), i32),
+        _want("conv_state", conv_state, (B, conv.slots, conv.channels), _io_type(cfg)), *outs, _stream(stream)),
+        "replay_conv_step")
+
+
 # ---- one layer's state, allocated with torch -------------------------------
 
 _DTYPE_CODE = {"f32": F32, "bf16": BF16, "fp8": FP8_E4M3, "fp4": FP4_E2M1, None: NONE, "none": NONE}
@@ -322,6 +431,16 @@ class ReplayLayer:
         """rollback(n_reject), then verify_step(W, ...), fused where the round is one launch."""
         fa = self.cfg.ring_len - W + 1 if flush_at is None else flush_at
         replay_rollback_verify_step(self.h, n_reject, W, q, k, v, dt, a, y, fa, stream)
+
+    def conv_prompt(self, conv, T, cu_seqlens, x, dt_raw, state_in, state_out, q, k, v, dt, a, stream=None):
+        """The inputs of packed prompts (replay_conv_prompt), their last rows kept for this layer's next tokens."""
+        replay_conv_prompt(self.cfg, conv, T, cu_seqlens, x, dt_raw, self.t["pos"], state_in, state_out, q, k, v, dt, a,
+                           self.t["err"], stream)
+
+    def conv_step(self, conv, W, x, dt_raw, conv_state, q, k, v, dt, a, n_reject=None, stream=None):
+        """The inputs of the next W tokens; n_reject: the rollback that the coming rollback_verify_step applies."""
+        replay_conv_step(self.cfg, conv, W, x, dt_raw, self.t["pos"], conv_state, q, k, v, dt, a, self.t["base"],
+                         n_reject, stream)
 
     def load_checkpoint(self, s_src, stream=None):
         replay_load_checkpoint(self.h, s_src, stream)

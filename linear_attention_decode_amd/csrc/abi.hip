@@ -5,7 +5,8 @@
 // fused decode step, one layer or stacked layers), verify_step.hip (the
 // fused speculative round), flush.hip and flush_shared.hip (the folds of a
 // float32 master and of a shared low-precision checkpoint), gdn.hip (Gated
-// DeltaNet layers), ring.hip (append, rollback, fills), eager.hip and
+// DeltaNet layers), ring.hip (append, rollback, fills), conv.hip (the
+// convolution and discretisation ahead of the recurrence), eager.hip and
 // probe.hip.
 #include <hip/hip_runtime.h>
 
@@ -682,6 +683,106 @@ replay_status replay_stream_probe(int32_t mode, const void *src, void *dst, size
     if ((mode != 0 && mode != 1) || !src || !dst || !aligned16(src) || !aligned16(dst) || bytes % 16 != 0)
         return REPLAY_ERR_INVALID_ARG;
     return from_hip(launch_probe(mode, src, dst, bytes, as_stream(stream)));
+}
+
+}  // extern "C"
+
+namespace {
+
+// What the two convolution calls check and fill alike.
+replay_status conv_args(const replay_config *cfg, const replay_conv_params *cv, const void *x, int64_t x_stride,
+                        const void *dt_raw, int64_t dt_stride, void *q, void *k, void *v, float *dt, float *a,
+                        ConvArgs *out) {
+    replay_status st = check_shape(cfg);
+    if (st != REPLAY_OK) return st;
+    if (!cv || cv->width < 2 || cv->slots < 1 || (cv->silu != 0 && cv->silu != 1)) return REPLAY_ERR_INVALID_ARG;
+    if (cv->width > 4) return REPLAY_ERR_UNSUPPORTED;
+    if (cv->slots < cv->width - 1) return REPLAY_ERR_INVALID_ARG;
+    const int64_t C = (int64_t)cfg->heads * cfg->head_dim + 2 * (int64_t)cfg->groups * cfg->state_dim;
+    if (C > (int64_t(1) << 24)) return REPLAY_ERR_UNSUPPORTED;
+    const size_t io_mask = io_bytes(*cfg) - 1;
+    if (!x || (reinterpret_cast<uintptr_t>(x) & io_mask) || x_stride < C) return REPLAY_ERR_INVALID_ARG;
+    if (!cv->weight || !aligned4(cv->weight) || !aligned4(cv->bias)) return REPLAY_ERR_INVALID_ARG;
+    for (const void *p : {q, k, v})
+        if (!p || !aligned16(p)) return REPLAY_ERR_INVALID_ARG;
+    if (dt_raw) {
+        if (cfg->rule == REPLAY_RULE_GATED_DELTA) return REPLAY_ERR_UNSUPPORTED;
+        if ((reinterpret_cast<uintptr_t>(dt_raw) & io_mask) || dt_stride < cfg->heads) return REPLAY_ERR_INVALID_ARG;
+        if (!dt || !a || !aligned4(dt) || !aligned4(a) || !cv->a_log || !aligned4(cv->a_log) ||
+            !aligned4(cv->dt_bias))
+            return REPLAY_ERR_INVALID_ARG;
+        if (!(cv->dt_min >= 0.f) || !(cv->dt_max == 0.f || cv->dt_max >= cv->dt_min)) return REPLAY_ERR_INVALID_ARG;
+    }
+    *out = ConvArgs{};
+    out->B = cfg->batch;
+    out->H = cfg->heads;
+    out->G = cfg->groups;
+    out->P = cfg->head_dim;
+    out->N = cfg->state_dim;
+    out->C = (int32_t)C;
+    out->K = cv->width;
+    out->R = cv->slots;
+    out->silu = cv->silu;
+    out->io_bf16 = cfg->io_dtype == REPLAY_BF16;
+    out->x = x;
+    out->x_stride = x_stride;
+    out->dt_raw = dt_raw;
+    out->dt_stride = dt_stride;
+    out->weight = cv->weight;
+    out->bias = cv->bias;
+    out->dt_bias = cv->dt_bias;
+    out->a_log = cv->a_log;
+    out->dt_min = cv->dt_min;
+    out->dt_max = cv->dt_max == 0.f ? __builtin_inff() : cv->dt_max;
+    out->q = q;
+    out->k = k;
+    out->v = v;
+    out->dt = dt;
+    out->a = a;
+    return REPLAY_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+replay_status replay_conv_prompt(const replay_config *cfg, const replay_conv_params *conv, int32_t T,
+                                 const int32_t *cu_seqlens, const void *x, int64_t x_stride, const void *dt_raw,
+                                 int64_t dt_stride, const int32_t *pos, const void *state_in, void *state_out,
+                                 void *q, void *k, void *v, float *dt, float *a, int32_t *err, void *stream) {
+    ConvArgs c;
+    replay_status st = conv_args(cfg, conv, x, x_stride, dt_raw, dt_stride, q, k, v, dt, a, &c);
+    if (st != REPLAY_OK) return st;
+    if (T < 1 || !cu_seqlens || !aligned4(cu_seqlens) || !aligned4(pos) || !err || !aligned4(err) || !state_out ||
+        !aligned16(state_out) || !aligned16(state_in))
+        return REPLAY_ERR_INVALID_ARG;
+    c.T = T;
+    c.cu = cu_seqlens;
+    c.pos = pos;
+    c.state_in = state_in;
+    c.state_out = state_out;
+    c.err = err;
+    return from_hip(launch_conv_prompt(c, as_stream(stream)));
+}
+
+replay_status replay_conv_step(const replay_config *cfg, const replay_conv_params *conv, int32_t W, const void *x,
+                               int64_t x_stride, const void *dt_raw, int64_t dt_stride, const int32_t *pos,
+                               const int32_t *base, const int32_t *n_reject, void *conv_state, void *q, void *k,
+                               void *v, float *dt, float *a, void *stream) {
+    ConvArgs c;
+    replay_status st = conv_args(cfg, conv, x, x_stride, dt_raw, dt_stride, q, k, v, dt, a, &c);
+    if (st != REPLAY_OK) return st;
+    if (W < 1 || W > kMaxWideWindow || W > conv->slots || !pos || !aligned4(pos) || !conv_state ||
+        !aligned16(conv_state) || !aligned4(n_reject) || (n_reject && (!base || !aligned4(base))))
+        return REPLAY_ERR_INVALID_ARG;
+    if ((int64_t)cfg->batch * W > INT32_MAX) return REPLAY_ERR_UNSUPPORTED;
+    c.T = cfg->batch * W;
+    c.W = W;
+    c.pos = pos;
+    c.base = base;
+    c.n_reject = n_reject;
+    c.state_out = conv_state;
+    return from_hip(launch_conv_step(c, as_stream(stream)));
 }
 
 }  // extern "C"

@@ -105,7 +105,28 @@ struct EagerArgs {
     int32_t io_bf16;
 };
 
+// The inputs of the recurrence from projected rows (conv.hip): T packed rows
+// of a prompt batch, or T = B W rows of a step or round.
+struct ConvArgs {
+    int32_t B, H, G, P, N, C;      // C = H P + 2 G N channels, [v | k | q]
+    int32_t K, R, silu, io_bf16;
+    int32_t T, W;
+    const int32_t *cu;             // prompts: [B + 1]
+    const void *x, *dt_raw;        // rows x_stride, dt_stride elements apart; dt_raw null: no dt, a
+    int64_t x_stride, dt_stride;
+    const int32_t *pos, *base, *n_reject;
+    const void *state_in;          // prompts: [B][R][C] or null (zeros)
+    void *state_out;               // [B][R][C]; a step reads its history here too
+    const float *weight, *bias, *dt_bias, *a_log;   // [C][K], [C], [H], [H]
+    float dt_min, dt_max;
+    void *q, *k, *v;
+    float *dt, *a;
+    int32_t *err;
+};
+
 // Launchers (return hipSuccess or the launch error).
+hipError_t launch_conv_prompt(const ConvArgs &a, hipStream_t s);
+hipError_t launch_conv_step(const ConvArgs &a, hipStream_t s);
 hipError_t launch_decode(int P, int N, int st, const DecodeArgs &a, hipStream_t s);
 hipError_t launch_verify_wide(int P, int N, int st, const DecodeArgs &a, hipStream_t s);   // 1 <= W <= 16
 bool verify_wide_supported(int st, const DecodeArgs &a);

@@ -1,0 +1,93 @@
+"""What the prompt, token-input and sampling calls refuse on the host.  No
+call here reaches the device: every one is rejected before any launch."""
+import ctypes
+
+import pytest
+
+P16 = 0x1000
+
+
+@pytest.fixture(scope="module")
+def lad():
+    import linear_attention_decode_amd as m
+    return m
+
+
+def _cfg(lad, **kw):
+    c = lad.ReplayConfig(2, 4, 2, 64, 128, 16, lad.BF16, lad.NONE, 0)
+    for k, v in kw.items():
+        setattr(c, k, v)
+    return c
+
+
+def _conv(lad, **kw):
+    c = lad.ReplayConvParams(4, 8, 1, P16, P16, P16, P16, 0.0, 0.0)
+    for k, v in kw.items():
+        setattr(c, k, v)
+    return c
+
+
+C = 4 * 64 + 2 * 2 * 128
+
+
+def _prompt(lad, cfg=None, conv=None, T=8, **kw):
+    a = dict(cu=P16, x=P16, x_stride=C, raw=P16, raw_stride=4, pos=P16, state_in=P16, state_out=P16, q=P16, k=P16, v=P16,
+             dt=P16, a=P16, err=P16) | kw
+    cfg, conv = cfg or _cfg(lad), conv or _conv(lad)
+    return lad.lib.replay_conv_prompt(ctypes.byref(cfg), ctypes.byref(conv), T, a["cu"], a["x"], a["x_stride"], a["raw"],
+                                      a["raw_stride"], a["pos"], a["state_in"], a["state_out"], a["q"], a["k"], a["v"],
+                                      a["dt"], a["a"], a["err"], None)
+
+
+def _step(lad, cfg=None, conv=None, W=2, **kw):
+    a = dict(x=P16, x_stride=C, raw=P16, raw_stride=4, pos=P16, base=P16, rej=P16, state=P16, q=P16, k=P16, v=P16, dt=P16,
+             a=P16) | kw
+    cfg, conv = cfg or _cfg(lad), conv or _conv(lad)
+    return lad.lib.replay_conv_step(ctypes.byref(cfg), ctypes.byref(conv), W, a["x"], a["x_stride"], a["raw"],
+                                    a["raw_stride"], a["pos"], a["base"], a["rej"], a["state"], a["q"], a["k"], a["v"],
+                                    a["dt"], a["a"], None)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(cu=None), 1), (dict(x=None), 1), (dict(x=0x1001), 1), (dict(x_stride=C - 1), 1), (dict(raw=0x1001), 1),
+    (dict(raw_stride=3), 1), (dict(pos=0x1002), 1), (dict(state_in=0x1008), 1), (dict(state_out=None), 1),
+    (dict(state_out=0x1004), 1), (dict(q=None), 1), (dict(k=0x1008), 1), (dict(v=None), 1), (dict(dt=None), 1),
+    (dict(a=None), 1), (dict(err=None), 1), (dict(T=0), 1), (dict(T=-5), 1),
+])
+def test_prompt_convolution_refusals(lad, kw, status):
+    assert _prompt(lad, **kw) == status
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(x=None), 1), (dict(x_stride=C - 1), 1), (dict(pos=None), 1), (dict(base=None), 1), (dict(rej=0x1001), 1),
+    (dict(state=None), 1), (dict(state=0x1008), 1), (dict(W=0), 1), (dict(W=17), 1), (dict(W=9), 1), (dict(q=0x1002), 1),
+])
+def test_token_convolution_refusals(lad, kw, status):
+    assert _step(lad, **kw) == status
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(width=1), 1), (dict(width=5), 2), (dict(slots=2), 1), (dict(silu=2), 1), (dict(weight=None), 1),
+    (dict(weight=0x1002), 1), (dict(bias=0x1001), 1), (dict(a_log=None), 1), (dict(dt_min=-1.0), 1),
+    (dict(dt_min=0.5, dt_max=0.1), 1), (dict(dt_min=float("nan")), 1),
+])
+def test_convolution_parameters(lad, kw, status):
+    assert _prompt(lad, conv=_conv(lad, **kw)) == status
+    assert _step(lad, conv=_conv(lad, **kw)) == status
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(batch=0), 1), (dict(heads=3), 1), (dict(head_dim=32), 2), (dict(io_dtype=2), 2), (dict(rule=2), 1),
+    (dict(rule=1), 2),                               # Gated DeltaNet: no dt_raw
+    (dict(heads=1 << 20, groups=1 << 18), 2),       # channels past 2^24
+])
+def test_convolution_shapes(lad, kw, status):
+    wide = dict(x_stride=1 << 30, raw_stride=1 << 30)
+    assert _prompt(lad, cfg=_cfg(lad, **kw), **wide) == status
+    assert _step(lad, cfg=_cfg(lad, **kw), **wide) == status
+
+
+def test_null_structs(lad):
+    assert lad.lib.replay_conv_prompt(None, None, 8, *([P16, P16, C, P16, 4] + [P16] * 10)) == 1
+    cfg = _cfg(lad)
+    assert lad.lib.replay_conv_step(ctypes.byref(cfg), None, 1, P16, C, P16, 4, *([P16] * 9), None) == 1
