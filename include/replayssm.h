@@ -442,6 +442,31 @@ replay_status replay_conv_step(const replay_config *cfg, const replay_conv_param
                                void *conv_state, void *q, void *k, void *v, float *dt, float *a,
                                void *stream);
 
+/* ---- prompts -------------------------------------------------------------
+   The recurrence over packed prompts (page "ReplaySSM: Cachear Inputs, No
+   Estado", section "La solucion", eqs. "Forma resumen" and "Forma
+   historia"), from each sequence's state s_in ([B][H][P][N] f32, NULL for
+   zeros) to the state it leaves in s_out, which replay_load_checkpoint
+   takes.  Sequence b holds rows cu_seqlens[b] .. cu_seqlens[b + 1] - 1 of T
+   (device int32 [B + 1]), at most max_len of them; a sequence of none leaves
+   its state.  q, k: [T][G][N], v: [T][H][P] (io dtype); dt, a: [T][H] f32,
+   a any finite number (0 resets the state).  y: [T][H][P] in the io dtype, as a
+   model's next product takes it; rows outside every range are left as they
+   are.  With bf16 io the products run on bf16 operands: inputs are taken as
+   they are, sums and states are float32.  s_out must not overlap s_in.
+   A sequence whose range decreases, leaves 0..T or is longer than max_len
+   gets BAD_RANGE in err (device int32 [B + 1]); its rows and its s_out are
+   left as they are.
+   workspace: device memory of the size that replay_scan_workspace gives for
+   the same cfg, T and max_len (0 while the sequences alone fill the GPU; NULL
+   then); it holds nothing between calls, and calls that can overlap need one
+   each.  Mamba-2 layers only (Gated DeltaNet: UNSUPPORTED). */
+replay_status replay_scan_workspace(const replay_config *cfg, int32_t T, int32_t max_len, size_t *bytes);
+replay_status replay_scan(const replay_config *cfg, int32_t T, int32_t max_len, const int32_t *cu_seqlens,
+                          const void *q, const void *k, const void *v, const float *dt, const float *a,
+                          const float *s_in, float *s_out, void *y, int32_t *err, void *workspace,
+                          size_t workspace_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -24,6 +24,7 @@ __all__ = [
     "replay_verify_step", "replay_rollback_verify_step", "replay_set_flush_skipping", "replay_get_error",
     "replay_eager_step", "replay_eager_select", "replay_stream_probe",
     "ReplayConvParams", "ReplayConv", "SEQERR_BAD_RANGE", "replay_conv_prompt", "replay_conv_step",
+    "replay_scan_workspace", "replay_scan",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libreplayssm.so")
@@ -39,7 +40,7 @@ EXPORTS = (
     "replay_verify", "replay_rollback", "replay_flush", "replay_step", "replay_step_layers", "replay_step_static",
     "replay_verify_step", "replay_rollback_verify_step", "replay_set_flush_skipping", "replay_get_error",
     "replay_eager_step", "replay_eager_select", "replay_stream_probe",
-    "replay_conv_prompt", "replay_conv_step",
+    "replay_conv_prompt", "replay_conv_step", "replay_scan_workspace", "replay_scan",
 )
 
 _VP = ctypes.c_void_p
@@ -102,6 +103,8 @@ def _load():
                                       _I64, _VP, _I64] + [_VP] * 10)
     L.replay_conv_step.argtypes = ([ctypes.POINTER(ReplayConfig), ctypes.POINTER(ReplayConvParams), _I32, _VP, _I64,
                                     _VP, _I64] + [_VP] * 10)
+    L.replay_scan_workspace.argtypes = [ctypes.POINTER(ReplayConfig), _I32, _I32, ctypes.POINTER(ctypes.c_size_t)]
+    L.replay_scan.argtypes = ([ctypes.POINTER(ReplayConfig), _I32, _I32] + [_VP] * 11 + [ctypes.c_size_t, _VP])
     for name in EXPORTS:
         if name not in ("replay_status_string", "replay_abi_version"):
             getattr(L, name).restype = ctypes.c_int
@@ -245,31 +248,37 @@ def replay_stream_probe(mode, src, dst, nbytes, stream=None):
 # These calls take torch tensors and check what their pointers cannot say:
 # the kernels go by the shapes of cfg.
 
-def _want(what, t, shape, dtype):
-    """A contiguous tensor of this shape and type on the current GPU (None passes)."""
+def _gpu():
+    import torch
+    return torch.cuda.current_device()
+
+
+def _on(stream, gpu):
+    """_stream, without building a Stream object for the current one (2.5 of a token call's 12 us on the host)."""
+    if stream is None:
+        import torch
+        return torch._C._cuda_getCurrentRawStream(gpu)
+    return _stream(stream)
+
+
+def _want(what, t, shape, dtype, gpu):
+    """The address of a contiguous tensor of this shape and type on that GPU (None passes)."""
     if t is None:
         return None
-    if tuple(t.shape) != shape or t.dtype != dtype or not t.is_contiguous():
-        raise ReplayError(f"{what}: want a contiguous {dtype} tensor of shape {shape}, got {t.dtype} of "
-                          f"{tuple(t.shape)} with strides {t.stride()}")
-    return _here(what, t)
-
-
-def _here(what, t):
-    import torch
-    if t.device.type != "cuda" or t.device.index != torch.cuda.current_device():
-        raise ReplayError(f"{what}: the tensor is on {t.device}, not on the current GPU")
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != gpu or not t.is_contiguous():
+        raise ReplayError(f"{what}: want a contiguous {dtype} tensor of shape {shape} on the current GPU ({gpu}), got "
+                          f"{t.dtype} of {tuple(t.shape)} with strides {t.stride()} on {t.device}")
     return t.data_ptr()
 
 
-def _rows(what, t, n, width, dtype):
-    """(pointer, row stride) of a [n, width] tensor whose rows may lie any stride apart (None: (None, 0))."""
+def _rows(what, t, n, width, dtype, gpu):
+    """(address, row stride) of a [n, width] tensor whose rows may lie any stride apart (None: (None, 0))."""
     if t is None:
         return None, 0
-    if t.dim() != 2 or t.shape[0] != n or t.shape[1] != width or t.dtype != dtype or (width > 1 and t.stride(1) != 1):
-        raise ReplayError(f"{what}: want a {dtype} tensor of shape {(n, width)} with unit stride along its rows, got "
-                          f"{t.dtype} of {tuple(t.shape)} with strides {t.stride()}")
-    return _here(what, t), (t.stride(0) if n > 1 else max(t.stride(0), width))
+    if t.shape != (n, width) or t.dtype is not dtype or t.get_device() != gpu or (width > 1 and t.stride(1) != 1):
+        raise ReplayError(f"{what}: want a {dtype} tensor of shape {(n, width)} with unit stride along its rows on the "
+                          f"current GPU ({gpu}), got {t.dtype} of {tuple(t.shape)} with strides {t.stride()} on {t.device}")
+    return t.data_ptr(), (t.stride(0) if n > 1 else max(t.stride(0), width))
 
 
 def _io_type(cfg):
@@ -291,50 +300,81 @@ class ReplayConv:
         heads = next((t.shape for t in (a_log, dt_bias) if t is not None), None)
         self.heads = None if heads is None else heads[0]
         self.tensors = (weight, bias, dt_bias, a_log)
-        f32 = torch.float32
+        f32, gpu = torch.float32, _gpu()
         self.params = ReplayConvParams(
-            self.width, self.slots, int(bool(silu)), _want("weight", weight, (channels, self.width), f32),
-            _want("bias", bias, (channels,), f32), _want("dt_bias", dt_bias, (self.heads,), f32),
-            _want("a_log", a_log, (self.heads,), f32), dt_min, 0.0 if dt_max == float("inf") else dt_max)
+            self.width, self.slots, int(bool(silu)), _want("weight", weight, (channels, self.width), f32, gpu),
+            _want("bias", bias, (channels,), f32, gpu), _want("dt_bias", dt_bias, (self.heads,), f32, gpu),
+            _want("a_log", a_log, (self.heads,), f32, gpu), dt_min, 0.0 if dt_max == float("inf") else dt_max)
 
 
-def _conv_call(what, cfg, conv, n, lead, x, dt_raw, q, k, v, dt, a):
-    """The pointers that the two convolution calls share: x, its stride, dt_raw, its stride, q, k, v, dt, a."""
-    import torch
-    io, f32 = _io_type(cfg), torch.float32
+def _conv_call(what, cfg, conv, n, lead, x, dt_raw, q, k, v, dt, a, io, f32, gpu):
+    """What the two convolution calls share: x, its stride, dt_raw, its stride; and q, k, v, dt, a."""
     H, G, P, N = cfg.heads, cfg.groups, cfg.head_dim, cfg.state_dim
-    if conv.channels != H * P + 2 * G * N or (dt_raw is not None and conv.heads != H):
+    C = H * P + 2 * G * N
+    if conv.channels != C or (dt_raw is not None and conv.heads != H):
         raise ReplayError(f"{what}: a convolution of {conv.channels} channels and {conv.heads} heads for a layer of "
-                          f"{H * P + 2 * G * N} channels and {H} heads")
-    rows = _rows("x", x, n, conv.channels, io) + _rows("dt_raw", dt_raw, n, H, io)
-    outs = (_want("q", q, (*lead, G, N), io), _want("k", k, (*lead, G, N), io), _want("v", v, (*lead, H, P), io))
-    return rows, outs + ((None, None) if dt_raw is None else
-                         (_want("dt", dt, (*lead, H), f32), _want("a", a, (*lead, H), f32)))
+                          f"{C} channels and {H} heads")
+    rows = _rows("x", x, n, C, io, gpu) + _rows("dt_raw", dt_raw, n, H, io, gpu)
+    outs = (_want("q", q, (*lead, G, N), io, gpu), _want("k", k, (*lead, G, N), io, gpu),
+            _want("v", v, (*lead, H, P), io, gpu))
+    if dt_raw is None:
+        return rows, (*outs, None, None)
+    return rows, (*outs, _want("dt", dt, (*lead, H), f32, gpu), _want("a", a, (*lead, H), f32, gpu))
 
 
 def replay_conv_prompt(cfg, conv, T, cu_seqlens, x, dt_raw, pos, state_in, state_out, q, k, v, dt, a, err, stream=None):
     """x [T, C] and dt_raw [T, H] may be views into wider rows; conv: ReplayConv; pos, state_in, dt_raw may be None."""
     import torch
-    i32, B = torch.int32, cfg.batch
-    rows, outs = _conv_call("replay_conv_prompt", cfg, conv, T, (T,), x, dt_raw, q, k, v, dt, a)
+    i32, io, gpu, B = torch.int32, _io_type(cfg), _gpu(), cfg.batch
+    rows, outs = _conv_call("replay_conv_prompt", cfg, conv, T, (T,), x, dt_raw, q, k, v, dt, a, io, torch.float32, gpu)
     state = (B, conv.slots, conv.channels)
-    io = _io_type(cfg)
     _check(lib.replay_conv_prompt(
-        ctypes.byref(cfg), ctypes.byref(conv.params), T, _want("cu_seqlens", cu_seqlens, (B + 1,), i32), *rows,
-        _want("pos", pos, (B,), i32), _want("state_in", state_in, state, io), _want("state_out", state_out, state, io),
-        *outs, _want("err", err, (B + 1,), i32), _stream(stream)), "replay_conv_prompt")
+        ctypes.byref(cfg), ctypes.byref(conv.params), T, _want("cu_seqlens", cu_seqlens, (B + 1,), i32, gpu), *rows,
+        _want("pos", pos, (B,), i32, gpu), _want("state_in", state_in, state, io, gpu),
+        _want("state_out", state_out, state, io, gpu), *outs, _want("err", err, (B + 1,), i32, gpu), _on(stream, gpu)),
+        "replay_conv_prompt")
 
 
 def replay_conv_step(cfg, conv, W, x, dt_raw, pos, conv_state, q, k, v, dt, a, base=None, n_reject=None, stream=None):
     """x [B W, C] and dt_raw [B W, H] may be views into wider rows; conv: ReplayConv; dt_raw may be None."""
     import torch
-    i32, B = torch.int32, cfg.batch
-    rows, outs = _conv_call("replay_conv_step", cfg, conv, B * W, (B, W), x, dt_raw, q, k, v, dt, a)
+    i32, io, gpu, B = torch.int32, _io_type(cfg), _gpu(), cfg.batch
+    rows, outs = _conv_call("replay_conv_step", cfg, conv, B * W, (B, W), x, dt_raw, q, k, v, dt, a, io, torch.float32,
+                            gpu)
     _check(lib.replay_conv_step(
-        ctypes.byref(cfg), ctypes.byref(conv.params), W, *rows, _want("pos", pos, (B,), i32),
-        _want("base", base, (B,), i32), _want("n_reject", n_reject, (B,), i32),
-        _want("conv_state", conv_state, (B, conv.slots, conv.channels), _io_type(cfg)), *outs, _stream(stream)),
+        ctypes.byref(cfg), ctypes.byref(conv.params), W, *rows, _want("pos", pos, (B,), i32, gpu),
+        _want("base", base, (B,), i32, gpu), _want("n_reject", n_reject, (B,), i32, gpu),
+        _want("conv_state", conv_state, (B, conv.slots, conv.channels), io, gpu), *outs, _on(stream, gpu)),
         "replay_conv_step")
+
+
+def replay_scan_workspace(cfg, T, max_len) -> int:
+    """Bytes of workspace that replay_scan needs for T rows, up to max_len of them a sequence."""
+    n = ctypes.c_size_t()
+    _check(lib.replay_scan_workspace(ctypes.byref(cfg), T, max_len, ctypes.byref(n)), "replay_scan_workspace")
+    return n.value
+
+
+def _workspace(t, gpu):
+    """(address, bytes) of a contiguous tensor of any type (None: (None, 0))."""
+    if t is None:
+        return None, 0
+    if t.get_device() != gpu or not t.is_contiguous():
+        raise ReplayError(f"workspace: want a contiguous tensor on the current GPU ({gpu}), got one on {t.device}")
+    return t.data_ptr(), t.numel() * t.element_size()
+
+
+def replay_scan(cfg, T, max_len, cu_seqlens, q, k, v, dt, a, s_in, s_out, y, err, workspace=None, stream=None):
+    """Packed prompts: q, k [T, G, N], v and y [T, H, P], dt, a [T, H]; s_in may be None (zeros)."""
+    import torch
+    f32, i32, io, gpu = torch.float32, torch.int32, _io_type(cfg), _gpu()
+    B, H, G, P, N = cfg.batch, cfg.heads, cfg.groups, cfg.head_dim, cfg.state_dim
+    _check(lib.replay_scan(
+        ctypes.byref(cfg), T, max_len, _want("cu_seqlens", cu_seqlens, (B + 1,), i32, gpu),
+        _want("q", q, (T, G, N), io, gpu), _want("k", k, (T, G, N), io, gpu), _want("v", v, (T, H, P), io, gpu),
+        _want("dt", dt, (T, H), f32, gpu), _want("a", a, (T, H), f32, gpu), _want("s_in", s_in, (B, H, P, N), f32, gpu),
+        _want("s_out", s_out, (B, H, P, N), f32, gpu), _want("y", y, (T, H, P), io, gpu),
+        _want("err", err, (B + 1,), i32, gpu), *_workspace(workspace, gpu), _on(stream, gpu)), "replay_scan")
 
 
 # ---- one layer's state, allocated with torch -------------------------------
@@ -441,6 +481,10 @@ class ReplayLayer:
         """The inputs of the next W tokens; n_reject: the rollback that the coming rollback_verify_step applies."""
         replay_conv_step(self.cfg, conv, W, x, dt_raw, self.t["pos"], conv_state, q, k, v, dt, a, self.t["base"],
                          n_reject, stream)
+
+    def scan(self, T, max_len, cu_seqlens, q, k, v, dt, a, s_in, s_out, y, workspace=None, stream=None):
+        """The recurrence over packed prompts (replay_scan); load_checkpoint(s_out) makes its states this layer's."""
+        replay_scan(self.cfg, T, max_len, cu_seqlens, q, k, v, dt, a, s_in, s_out, y, self.t["err"], workspace, stream)
 
     def load_checkpoint(self, s_src, stream=None):
         replay_load_checkpoint(self.h, s_src, stream)

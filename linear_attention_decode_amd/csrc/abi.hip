@@ -6,8 +6,8 @@
 // fused speculative round), flush.hip and flush_shared.hip (the folds of a
 // float32 master and of a shared low-precision checkpoint), gdn.hip (Gated
 // DeltaNet layers), ring.hip (append, rollback, fills), conv.hip (the
-// convolution and discretisation ahead of the recurrence), eager.hip and
-// probe.hip.
+// convolution and discretisation ahead of the recurrence), scan.hip (the
+// recurrence over prompts), eager.hip and probe.hip.
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
@@ -783,6 +783,73 @@ replay_status replay_conv_step(const replay_config *cfg, const replay_conv_param
     c.n_reject = n_reject;
     c.state_out = conv_state;
     return from_hip(launch_conv_step(c, as_stream(stream)));
+}
+
+}  // extern "C"
+
+namespace {
+
+// The segments of a scan; false where its launches cannot be numbered.
+bool scan_plan(const replay_config &c, int32_t T, int32_t max_len, int *nseg, int *seg_len, size_t *bytes) {
+    *nseg = scan_segments(c.head_dim, c.state_dim, c.batch, c.heads, T, max_len, seg_len);
+    const int64_t bh = (int64_t)c.batch * c.heads;
+    const size_t slots = (size_t)bh * (*nseg - 1);
+    *bytes = slots * ((size_t)c.head_dim * c.state_dim + 1) * sizeof(float);
+    return bh * (*nseg > 16 ? *nseg : 16) <= INT32_MAX;
+}
+
+}  // namespace
+
+extern "C" {
+
+replay_status replay_scan_workspace(const replay_config *cfg, int32_t T, int32_t max_len, size_t *bytes) {
+    replay_status st = check_shape(cfg);
+    if (st != REPLAY_OK) return st;
+    if (!bytes || T < 1 || max_len < 1) return REPLAY_ERR_INVALID_ARG;
+    if (cfg->rule == REPLAY_RULE_GATED_DELTA) return REPLAY_ERR_UNSUPPORTED;
+    int nseg, seg_len;
+    return scan_plan(*cfg, T, max_len, &nseg, &seg_len, bytes) ? REPLAY_OK : REPLAY_ERR_UNSUPPORTED;
+}
+
+replay_status replay_scan(const replay_config *cfg, int32_t T, int32_t max_len, const int32_t *cu_seqlens,
+                          const void *q, const void *k, const void *v, const float *dt, const float *a,
+                          const float *s_in, float *s_out, void *y, int32_t *err, void *workspace,
+                          size_t workspace_bytes, void *stream) {
+    replay_status st = check_shape(cfg);
+    if (st != REPLAY_OK) return st;
+    if (cfg->rule == REPLAY_RULE_GATED_DELTA) return REPLAY_ERR_UNSUPPORTED;
+    if (T < 1 || max_len < 1 || !cu_seqlens || !aligned4(cu_seqlens) || !err || !aligned4(err) || !aligned16(s_in))
+        return REPLAY_ERR_INVALID_ARG;
+    for (const void *p : {q, k, v, static_cast<const void *>(s_out), static_cast<const void *>(y)})
+        if (!p || !aligned16(p)) return REPLAY_ERR_INVALID_ARG;
+    for (const void *p : {dt, a})
+        if (!p || !aligned4(p)) return REPLAY_ERR_INVALID_ARG;
+    const size_t state = (size_t)cfg->batch * cfg->heads * cfg->head_dim * cfg->state_dim;
+    const uintptr_t in = reinterpret_cast<uintptr_t>(s_in), out = reinterpret_cast<uintptr_t>(s_out);
+    if (s_in && in < out + state * sizeof(float) && out < in + state * sizeof(float)) return REPLAY_ERR_INVALID_ARG;
+    ScanArgs r{};
+    size_t need;
+    if (!scan_plan(*cfg, T, max_len, &r.nseg, &r.seg_len, &need)) return REPLAY_ERR_UNSUPPORTED;
+    if (need && (!workspace || !aligned16(workspace) || workspace_bytes < need)) return REPLAY_ERR_INVALID_ARG;
+    r.B = cfg->batch;
+    r.H = cfg->heads;
+    r.G = cfg->groups;
+    r.T = T;
+    r.max_len = max_len;
+    r.io_bf16 = cfg->io_dtype == REPLAY_BF16;
+    r.cu = cu_seqlens;
+    r.q = q;
+    r.k = k;
+    r.v = v;
+    r.dt = dt;
+    r.a = a;
+    r.s_in = s_in;
+    r.s_out = s_out;
+    r.y = y;
+    r.err = err;
+    r.ws = static_cast<float *>(workspace);
+    r.ws_decay = need ? r.ws + need / sizeof(float) - (size_t)r.B * r.H * (r.nseg - 1) : nullptr;
+    return from_hip(launch_scan(cfg->head_dim, cfg->state_dim, r, as_stream(stream)));
 }
 
 }  // extern "C"

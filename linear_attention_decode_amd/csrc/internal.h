@@ -124,7 +124,24 @@ struct ConvArgs {
     int32_t *err;
 };
 
+// The recurrence over packed prompts (scan.hip).
+struct ScanArgs {
+    int32_t B, H, G, T, max_len, io_bf16;
+    const int32_t *cu;             // [B + 1]
+    const void *q, *k, *v;         // [T][G][N] x2, [T][H][P]
+    const float *dt, *a;           // [T][H]
+    const float *s_in;             // [B][H][P][N] or null (zeros)
+    float *s_out;
+    void *y;                       // [T][H][P], io dtype
+    int32_t *err;
+    int32_t nseg, seg_len;         // segments of a sequence, tokens of a segment
+    float *ws;                     // nseg > 1: states [B][H][nseg - 1][P][N], then
+    float *ws_decay;               // decays [B][H][nseg - 1]
+};
+
 // Launchers (return hipSuccess or the launch error).
+hipError_t launch_scan(int P, int N, const ScanArgs &a, hipStream_t s);
+int scan_segments(int P, int N, int B, int H, int T, int max_len, int *seg_len);   // the number of segments, and their length
 hipError_t launch_conv_prompt(const ConvArgs &a, hipStream_t s);
 hipError_t launch_conv_step(const ConvArgs &a, hipStream_t s);
 hipError_t launch_decode(int P, int N, int st, const DecodeArgs &a, hipStream_t s);

@@ -33,3 +33,16 @@ def discretise(raw, dt_bias, a_log, dt_min=0.0, dt_max=np.inf):
     x = raw.astype(np.float64) + (0.0 if dt_bias is None else dt_bias.astype(np.float64))
     dt = np.clip(np.logaddexp(x, 0.0), dt_min, dt_max)
     return dt, np.exp(-np.exp(a_log.astype(np.float64)) * dt)
+
+
+def scan(q, k, v, dt, a, S):
+    """One sequence, token after token: q, k [n, G, N], v [n, H, P], dt, a [n, H], S [H, P, N].
+    Returns (y [n, H, P], the last state)."""
+    H, G = v.shape[1], q.shape[1]
+    y = np.zeros(v.shape)
+    S = S.copy()
+    for t in range(len(v)):
+        kk, qq = np.repeat(k[t], H // G, 0), np.repeat(q[t], H // G, 0)
+        S = a[t][:, None, None] * S + (dt[t][:, None] * v[t])[:, :, None] * kk[:, None, :]
+        y[t] = np.einsum("hpn,hn->hp", S, qq)
+    return y, S

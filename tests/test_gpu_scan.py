@@ -1,0 +1,296 @@
+"""The recurrence over packed prompts (replay_scan) against float64.
+
+Bounds, before any run, in units of the sums of magnitudes: Y, the outputs,
+and Z, the states, of the recurrence on |q|, |k|, |v|, |a| (every partial sum
+lies below them).  A decay over n tokens is a product of n factors, off by
+n 2^-24; the state takes a product and a sum per token and one more product
+per chunk, a dot product N sums, a weight four products.  So a float32 result
+is off by at most (3 n + N + 64) 2^-24 of Y or Z.  With bf16 io the state and
+the weights of earlier tokens enter their products as bf16, 2^-8 of Y at
+most, and y is rounded to bf16, 2^-8 of itself; states keep the float32
+bound (their products take v, scaled, in parts that hold 24 bits)."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import prompt as op
+from tests import gpu_util as gu
+
+pytestmark = pytest.mark.gpu
+E24 = 2.0 ** -24
+
+
+def _lad():
+    import linear_attention_decode_amd as lad
+    return lad
+
+
+def _cfg(B, H, G, P, N, io):
+    lad = _lad()
+    return lad.ReplayConfig(B, H, G, P, N, 16, lad.BF16 if io == "bf16" else lad.F32, lad.NONE, 0)
+
+
+def _workspace(cfg, T, most):
+    """The workspace, filled with NaN: it holds nothing that a call may read before it wrote it."""
+    n = _lad().replay_scan_workspace(cfg, T, most)
+    return torch.full((n // 4,), float("nan"), device=gu.DEV) if n else None
+
+
+class Prompts:
+    def __init__(self, lens, H, G, P, N, io, first=0, extra=5, resume=True, seed=0, decay=None):
+        r = np.random.default_rng(seed)
+        self.B, self.lens, self.io = len(lens), lens, torch.bfloat16 if io == "bf16" else torch.float32
+        self.shape = (H, G, P, N)
+        self.T = T = max(1, first + sum(lens) + extra)
+        self.cfg = _cfg(self.B, H, G, P, N, io)
+        self.ends = first + np.cumsum(lens)
+        self.cu = torch.tensor([first, *self.ends], dtype=torch.int32, device=gu.DEV)
+        dev = lambda a, t=None: torch.from_numpy(a.astype(np.float32)).to(t or torch.float32).to(gu.DEV)  # noqa: E731
+        act = lambda x: x / (1 + np.exp(-x))  # noqa: E731
+        self.q, self.k = (dev(act(r.standard_normal((T, G, N))), self.io) for _ in range(2))
+        self.v = dev(act(r.standard_normal((T, H, P))), self.io)
+        dt = np.logaddexp(r.standard_normal((T, H)) - 3, 0)
+        self.dt = dev(dt)
+        self.a = dev(np.exp(-dt * r.uniform(1, 16, H)) if decay is None else decay(r, (T, H)))
+        self.s_in = dev(0.5 * r.standard_normal((self.B, H, P, N))) if resume else None
+        for t in (self.q, self.k, self.v, self.dt, self.a):   # rows of no sequence are read by none
+            t[:first] = float("nan")
+            t[self.ends[-1]:] = float("nan")
+        self.first = first
+        self.err = torch.zeros(self.B + 1, dtype=torch.int32, device=gu.DEV)
+        self.y = torch.full((T, H, P), 7.0, dtype=self.io, device=gu.DEV)
+        self.s_out = torch.full((self.B, H, P, N), 7.0, device=gu.DEV)
+
+    def run(self, most=None, ws="make", stream=None):
+        most = max(1, max(self.lens)) if most is None else most
+        ws = _workspace(self.cfg, self.T, most) if isinstance(ws, str) else ws
+        _lad().replay_scan(self.cfg, self.T, most, self.cu, self.q, self.k, self.v, self.dt, self.a, self.s_in, self.s_out,
+                           self.y, self.err, ws, stream)
+        return ws
+
+    def reference(self, b, mag=False):
+        rows = slice(int(self.ends[b]) - self.lens[b], int(self.ends[b]))
+        f = (lambda t: np.abs(t.double().cpu().numpy())) if mag else (lambda t: t.double().cpu().numpy())
+        H, G, P, N = self.shape
+        S = np.zeros((H, P, N)) if self.s_in is None else f(self.s_in[b])
+        return op.scan(*(f(t[rows]) for t in (self.q, self.k, self.v, self.dt, self.a)), S)
+
+    def check(self, seqs=None):
+        N = self.shape[3]
+        assert self.err.cpu().eq(0).all()
+        assert bool((self.y[:self.first] == 7.0).all()) and bool((self.y[int(self.ends[-1]):] == 7.0).all())
+        for b in range(self.B) if seqs is None else seqs:
+            n = self.lens[b]
+            rows = slice(int(self.ends[b]) - n, int(self.ends[b]))
+            (y, S), (Y, Z) = self.reference(b), self.reference(b, True)
+            c = (3 * n + N + 64) * E24
+            tol = c * Y if self.io == torch.float32 else (c + 2.0 ** -8) * Y + 2.0 ** -8 * np.abs(y)
+            got, gs = self.y[rows].double().cpu().numpy(), self.s_out[b].double().cpu().numpy()
+            assert np.all(np.abs(got - y) <= tol + 1e-37), (b, float(np.max(np.abs(got - y) / (tol + 1e-37))))
+            assert np.all(np.abs(gs - S) <= c * Z + 1e-37), (b, float(np.max(np.abs(gs - S) / (c * Z + 1e-37))))
+
+
+SHAPES = [(16, 16), (64, 64), (64, 128), (128, 128)]
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("P,N", SHAPES)
+@pytest.mark.parametrize("lens,first,resume", [
+    ([1], 0, False), ([0, 1, 2, 0], 0, True), ([15, 16, 17], 3, True), ([31, 32, 33], 0, False),
+    ([63, 1, 64, 65, 0, 100], 2, True), ([200], 1, True)])
+def test_ragged(io, P, N, lens, first, resume):
+    gu.note(f"scan {lens} P={P} N={N} {io}")
+    p = Prompts(lens, 4, 2, P, N, io, first=first, resume=resume, seed=P + N + sum(lens))
+    p.run()
+    torch.cuda.synchronize()
+    p.check()
+    for b, n in enumerate(lens):     # a sequence of no tokens leaves its state
+        if n == 0:
+            assert torch.equal(p.s_out[b], p.s_in[b] if resume else torch.zeros_like(p.s_out[b]))
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("lens,H,G,P,N", [
+    ([700, 1, 300], 2, 1, 64, 128), ([1111], 1, 1, 16, 16), ([513, 0, 900], 3, 3, 128, 128), ([1024, 512], 2, 2, 64, 64)])
+def test_long_sequences_in_segments(io, lens, H, G, P, N):
+    gu.note(f"scan segments {lens} H={H} P={P} N={N} {io}")
+    p = Prompts(lens, H, G, P, N, io, seed=sum(lens))
+    assert p.run() is not None       # the workspace form
+    torch.cuda.synchronize()
+    p.check()
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+def test_slow_decay(io):
+    """Decays near one: what the first tokens left is still whole at the end of every segment."""
+    gu.note(f"scan slow decay {io}")
+    p = Prompts([800, 77], 2, 1, 64, 128, io, seed=4, decay=lambda r, s: np.exp(-r.uniform(0, 1e-3, s)))
+    p.run()
+    torch.cuda.synchronize()
+    p.check()
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+def test_decays_of_zero_below_zero_and_underflow(io):
+    """a = 0 forgets all before it, exactly; negative, above one and tiny ones follow the recurrence."""
+    gu.note(f"scan odd decays {io}")
+
+    def decay(r, s):
+        x = r.uniform(-1, 1.01, s)
+        pick = r.uniform(0, 1, s)
+        x[pick < 0.1] = 0.0
+        x[pick > 0.9] = 1e-30
+        return x
+
+    p = Prompts([130, 40], 4, 2, 64, 64, io, seed=8, decay=decay)
+    p.run()
+    torch.cuda.synchronize()
+    p.check()
+    # a reset at the last token: the state is that token's own product
+    p.a[int(p.ends[0]) - 1] = 0.0
+    p.run()
+    torch.cuda.synchronize()
+    t = int(p.ends[0]) - 1
+    u = (p.v[t].float() * p.dt[t].unsqueeze(-1)).double()
+    want = u.unsqueeze(-1) * p.k[t].double().repeat_interleave(2, 0).unsqueeze(1)
+    assert bool(((p.s_out[0].double() - want).abs() <= 4 * E24 * want.abs()).all())
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("P,N", SHAPES)
+def test_whole_numbers_are_exact(io, P, N):
+    """Whole numbers small enough that every sum is exact, resets and steps among them: states to the bit, and y."""
+    gu.note(f"scan whole numbers P={P} N={N} {io}")
+    p = Prompts([97, 64, 3], 4, 2, P, N, io, seed=2)
+    r = np.random.default_rng(7)
+    dev = lambda a, t: torch.from_numpy(a.astype(np.float32)).to(t).to(gu.DEV)  # noqa: E731
+    T, (H, G) = p.T, p.shape[:2]
+    few = lambda s: (r.integers(-1, 2, s) * (r.uniform(0, 1, s) < 0.2))  # noqa: E731
+    p.q, p.k, p.v = dev(few((T, G, N)), p.io), dev(few((T, G, N)), p.io), dev(few((T, H, P)), p.io)
+    p.dt = dev(2.0 ** r.integers(0, 2, (T, H)), torch.float32)
+    p.a = dev(r.choice([1.0, 1.0, -1.0, 0.0], (T, H), p=[0.5, 0.3, 0.17, 0.03]), torch.float32)
+    p.s_in = dev(r.integers(-3, 4, p.s_in.shape), torch.float32)
+    p.run()
+    torch.cuda.synchronize()
+    for b in range(p.B):
+        y, S = p.reference(b)
+        assert np.array_equal(p.s_out[b].double().cpu().numpy(), S), b
+        rows = slice(int(p.ends[b]) - p.lens[b], int(p.ends[b]))
+        # whole numbers below 256: as bf16 they are themselves, whatever order they were summed in
+        assert np.abs(S).max() < 256 and np.abs(y).max() < 2 ** 24
+        want = torch.from_numpy(y).to(p.io)
+        assert torch.equal(p.y[rows].cpu(), want), b
+
+
+def test_ranges():
+    """Ranges that decrease, leave 0..T or are longer than max_len: flagged, their rows and states left as they were."""
+    lad = _lad()
+    gu.note("scan bad ranges")
+    for cu, most, bad in (([0, 10, 5, 20], 20, [1]), ([0, 10, 20, 50], 40, [2]), ([-1, 8, 8, 20], 20, [0]),
+                          ([0, 10, 30, 40], 15, [1]), ([0, 50, 3, 20], 50, [0, 1])):
+        p = Prompts([10, 10, 15], 2, 1, 16, 16, "bf16", seed=1)
+        assert p.T == 40
+        p.cu = torch.tensor(cu, dtype=torch.int32, device=gu.DEV)
+        for t in (p.q, p.k, p.v, p.dt, p.a):
+            t[35:] = 0.5
+        p.run(most=most)
+        torch.cuda.synchronize()
+        err = p.err.cpu().tolist()
+        assert err[0] == lad.SEQERR_BAD_RANGE and [b for b in range(3) if err[1 + b]] == bad, cu
+        assert all(bool((p.s_out[b] == 7.0).all()) for b in bad)
+        taken = torch.zeros(40, dtype=torch.bool)
+        for b in range(3):
+            if b not in bad:
+                taken[cu[b]:cu[b + 1]] = True
+                assert bool(p.s_out[b].isfinite().all()) and not bool((p.s_out[b] == 7.0).all())
+        assert bool((p.y[~taken.to(gu.DEV)] == 7.0).all()), cu
+
+
+def test_nan_stays_in_its_sequence_and_head():
+    gu.note("scan NaN")
+    p = Prompts([50, 40], 2, 2, 64, 64, "bf16", seed=3)
+    p.v[20, 0, 5] = float("nan")
+    p.run()
+    torch.cuda.synchronize()
+    y, S = p.y, p.s_out
+    assert y[20:50, 0, 5].isnan().all() and S[0, 0, 5].isnan().any()
+    y2 = y.clone()
+    y2[20:50, 0, 5] = 0.0
+    assert y2[:90].isfinite().all() and S[1].isfinite().all() and S[0, 1].isfinite().all()
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+def test_in_pieces(io):
+    """A prompt in pieces that hand their states on is the prompt at once, within the bound of one of them each."""
+    gu.note(f"scan in pieces {io}")
+    p = Prompts([300], 4, 2, 64, 128, io, seed=6)
+    p.run()
+    whole = p.y.clone(), p.s_out.clone()
+    lad, S = _lad(), p.s_in
+    y = torch.full_like(p.y, 7.0)
+    for lo, hi in ((0, 1), (1, 34), (34, 290), (290, 300)):
+        nxt = torch.empty_like(p.s_out)
+        cu = torch.tensor([0, hi - lo], dtype=torch.int32, device=gu.DEV)
+        lad.replay_scan(p.cfg, hi - lo, hi - lo, cu, p.q[lo:hi], p.k[lo:hi], p.v[lo:hi], p.dt[lo:hi], p.a[lo:hi], S, nxt,
+                        y[lo:hi], p.err, _workspace(p.cfg, hi - lo, hi - lo))
+        S = nxt
+    torch.cuda.synchronize()
+    p.y, p.s_out = y, S
+    p.check()
+    p.y, p.s_out = whole
+    p.check()
+
+
+def test_replays_and_streams():
+    """A captured scan (segments, workspace) replayed on new inputs equals the eager call, bit for bit, on its own
+    stream; two calls at once on two streams, a workspace each, do too."""
+    gu.note("scan in a graph")
+    p = Prompts([700, 40], 2, 1, 64, 128, "bf16", seed=12)
+    ws = _workspace(p.cfg, p.T, 700)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=side):
+        p.run(ws=ws)
+    for i in range(3):
+        fresh = Prompts([700, 40], 2, 1, 64, 128, "bf16", seed=20 + i)
+        for n in ("q", "k", "v", "dt", "a", "s_in"):
+            getattr(p, n).copy_(getattr(fresh, n))
+        fresh.run()
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(p.s_out, fresh.s_out) and torch.equal(p.y[:740], fresh.y[:740]), i
+    two = [Prompts([700, 40], 2, 1, 64, 128, "bf16", seed=20 + i) for i in range(2)]
+    streams = [torch.cuda.Stream() for _ in two]
+    torch.cuda.synchronize()
+    spaces = [_workspace(t.cfg, t.T, 700) for t in two]
+    torch.cuda.synchronize()
+    for t, s, w in zip(two, streams, spaces):
+        t.run(ws=w, stream=s)
+    torch.cuda.synchronize()
+    for i, t in enumerate(two):
+        alone = Prompts([700, 40], 2, 1, 64, 128, "bf16", seed=20 + i)
+        alone.run()
+        torch.cuda.synchronize()
+        assert torch.equal(t.s_out, alone.s_out) and torch.equal(t.y[:740], alone.y[:740])
+
+
+def test_refusals():
+    lad = _lad()
+    gu.note("scan refusals")
+    p = Prompts([700], 1, 1, 16, 16, "bf16")
+    need = lad.replay_scan_workspace(p.cfg, p.T, 700)
+    assert need > 0
+    for ws in (None, torch.empty(need - 4, dtype=torch.uint8, device=gu.DEV)):
+        with pytest.raises(lad.ReplayError, match="status 1"):
+            p.run(ws=ws)
+    with pytest.raises(lad.ReplayError):
+        p.run(ws=torch.empty(need, dtype=torch.uint8))
+    p.s_out = p.s_in                                  # in place
+    with pytest.raises(lad.ReplayError, match="status 1"):
+        p.run()
+    p.s_out = torch.empty_like(p.s_in)
+    p.y = p.y.float()
+    with pytest.raises(lad.ReplayError):
+        p.run()

@@ -91,3 +91,43 @@ def test_null_structs(lad):
     assert lad.lib.replay_conv_prompt(None, None, 8, *([P16, P16, C, P16, 4] + [P16] * 10)) == 1
     cfg = _cfg(lad)
     assert lad.lib.replay_conv_step(ctypes.byref(cfg), None, 1, P16, C, P16, 4, *([P16] * 9), None) == 1
+
+
+def _scan(lad, cfg=None, T=64, most=64, **kw):
+    a = dict(cu=P16, q=P16, k=P16, v=P16, dt=P16, a=P16, s_in=P16, s_out=0x10000000, y=P16, err=P16, ws=None, ws_bytes=0) | kw
+    cfg = cfg or _cfg(lad)
+    return lad.lib.replay_scan(ctypes.byref(cfg), T, most, a["cu"], a["q"], a["k"], a["v"], a["dt"], a["a"], a["s_in"],
+                               a["s_out"], a["y"], a["err"], a["ws"], a["ws_bytes"], None)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(T=0), 1), (dict(most=0), 1), (dict(cu=None), 1), (dict(cu=0x1002), 1), (dict(q=None), 1), (dict(k=0x1008), 1),
+    (dict(v=None), 1), (dict(dt=None), 1), (dict(a=0x1001), 1), (dict(s_in=0x1004), 1), (dict(s_out=None), 1),
+    (dict(s_out=P16), 1),                            # in place
+    (dict(s_out=P16 + 2 * 4 * 64 * 128 * 4 - 16), 1),   # the last bytes of s_in
+    (dict(y=None), 1), (dict(err=None), 1),
+    (dict(T=4096, most=4096), 1),                    # segments without their workspace
+    (dict(T=4096, most=4096, ws=0x1008, ws_bytes=1 << 40), 1),
+])
+def test_scan_refusals(lad, kw, status):
+    assert _scan(lad, **kw) == status
+
+
+@pytest.mark.parametrize("kw,status", [(dict(batch=0), 1), (dict(head_dim=32), 2), (dict(rule=1), 2), (dict(io_dtype=3), 2),
+                                       (dict(batch=1 << 20, heads=512), 2)])
+def test_scan_shapes(lad, kw, status):
+    assert _scan(lad, cfg=_cfg(lad, **kw), s_in=None) == status
+    n = ctypes.c_size_t()
+    assert lad.lib.replay_scan_workspace(ctypes.byref(_cfg(lad, **kw)), 64, 64, ctypes.byref(n)) == status
+
+
+def test_scan_workspace(lad):
+    """None where the (sequence, head) pairs fill the GPU or the prompts are short; whole states and decays otherwise."""
+    assert lad.replay_scan_workspace(_cfg(lad, batch=64, heads=128), 64 * 4096, 4096) == 0
+    assert lad.replay_scan_workspace(_cfg(lad, batch=1, heads=4), 200, 200) == 0
+    n = lad.replay_scan_workspace(_cfg(lad, batch=1, heads=8), 8192, 8192)
+    assert n > 0 and n % (8 * (64 * 128 + 1) * 4) == 0
+    assert lad.replay_scan_workspace(_cfg(lad, batch=1, heads=8), 8192, 1 << 30) == n    # no sequence is longer than T
+    for args in ((0, 8), (8, 0)):
+        with pytest.raises(lad.ReplayError, match="status 1"):
+            lad.replay_scan_workspace(_cfg(lad), *args)
