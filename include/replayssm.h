@@ -467,6 +467,45 @@ replay_status replay_scan(const replay_config *cfg, int32_t T, int32_t max_len, 
                           const float *s_in, float *s_out, void *y, int32_t *err, void *workspace,
                           size_t workspace_bytes, void *stream);
 
+/* ---- sampling --------------------------------------------------------------
+   A token for each of W positions of B sequences from V logits, and the
+   drafts that it rejects (pages as for replay_rollback: the caller's sampler
+   decides what the pointer moves back over).  Per sequence, device arrays of
+   B entries or NULL where the setting is off for all: */
+typedef struct {
+    const float *temperature;   /* T; 0: the largest logit.  NULL: 1 */
+    const int32_t *top_k;       /* the k first of the order; k <= 0 or k >= V: off */
+    const float *top_p;         /* the fewest first of the order (of the top-k's) that hold this share of their
+                                   weight, one at least; >= 1: off */
+    const float *min_p;         /* those of at least this share of the largest weight; <= 0: off, > 1: as 1 */
+} replay_sampling;
+
+/* Weights are whole numbers, w_i = rint(2^45 exp((x_i - max) / T)) of logit
+   x_i, so that sums are exact; the order is by logit, largest first, equal
+   ones by index; the filters keep what all of them keep.  The token is the
+   lowest index whose kept weight, with that of the kept ones before it,
+   exceeds floor(u Z), Z being all kept weight.  u: [B][W] f32, the caller's
+   random numbers from [0, 1) (others count as the nearest of these).
+   Logits of -infinity are never drawn.  A row that holds a NaN or +infinity
+   or nothing but -infinity, a T that is negative, infinite or NaN, a u that
+   is NaN: token -1.
+   logits: B W rows of V, row_stride elements apart, in float32 or bf16
+   (logits_dtype); V <= 2^18.  tokens: int32 [B][W]; probs: f32 [B][W], the
+   token's share of Z (1 where T = 0, 0 beside a token of -1), or NULL.
+   fed: int32 [B][W], the tokens that this round was given, or NULL:
+   position w > 0 of a window stays while the token drawn at w - 1 is
+   fed[w], and n_reject (int32 [B]) receives W minus the number that stays,
+   as replay_rollback takes it; the sequence goes on with the last kept
+   position's token, tokens[b][W - 1 - n_reject[b]].  fed and n_reject: both
+   or neither.  workspace: device memory of replay_sample_workspace bytes
+   (NULL where that is 0), holding nothing between calls; calls that can
+   overlap need one each. */
+replay_status replay_sample_workspace(int32_t B, int32_t W, int32_t V, size_t *bytes);
+replay_status replay_sample(int32_t B, int32_t W, int32_t V, const void *logits, int32_t logits_dtype,
+                            int64_t row_stride, const replay_sampling *opt, const float *u, int32_t *tokens,
+                            float *probs, const int32_t *fed, int32_t *n_reject, void *workspace,
+                            size_t workspace_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

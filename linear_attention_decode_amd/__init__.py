@@ -24,7 +24,7 @@ __all__ = [
     "replay_verify_step", "replay_rollback_verify_step", "replay_set_flush_skipping", "replay_get_error",
     "replay_eager_step", "replay_eager_select", "replay_stream_probe",
     "ReplayConvParams", "ReplayConv", "SEQERR_BAD_RANGE", "replay_conv_prompt", "replay_conv_step",
-    "replay_scan_workspace", "replay_scan",
+    "replay_scan_workspace", "replay_scan", "ReplaySampling", "replay_sample_workspace", "replay_sample",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libreplayssm.so")
@@ -41,6 +41,7 @@ EXPORTS = (
     "replay_verify_step", "replay_rollback_verify_step", "replay_set_flush_skipping", "replay_get_error",
     "replay_eager_step", "replay_eager_select", "replay_stream_probe",
     "replay_conv_prompt", "replay_conv_step", "replay_scan_workspace", "replay_scan",
+    "replay_sample_workspace", "replay_sample",
 )
 
 _VP = ctypes.c_void_p
@@ -65,6 +66,10 @@ class ReplayBuffers(ctypes.Structure):
 class ReplayConvParams(ctypes.Structure):
     _fields_ = [("width", _I32), ("slots", _I32), ("silu", _I32), ("weight", _VP), ("bias", _VP),
                 ("dt_bias", _VP), ("a_log", _VP), ("dt_min", ctypes.c_float), ("dt_max", ctypes.c_float)]
+
+
+class ReplaySampling(ctypes.Structure):
+    _fields_ = [("temperature", _VP), ("top_k", _VP), ("top_p", _VP), ("min_p", _VP)]
 
 
 class ReplayError(RuntimeError):
@@ -105,6 +110,9 @@ def _load():
                                     _VP, _I64] + [_VP] * 10)
     L.replay_scan_workspace.argtypes = [ctypes.POINTER(ReplayConfig), _I32, _I32, ctypes.POINTER(ctypes.c_size_t)]
     L.replay_scan.argtypes = ([ctypes.POINTER(ReplayConfig), _I32, _I32] + [_VP] * 11 + [ctypes.c_size_t, _VP])
+    L.replay_sample_workspace.argtypes = [_I32, _I32, _I32, ctypes.POINTER(ctypes.c_size_t)]
+    L.replay_sample.argtypes = ([_I32, _I32, _I32, _VP, _I32, _I64, ctypes.POINTER(ReplaySampling)] + [_VP] * 6
+                                + [ctypes.c_size_t, _VP])
     for name in EXPORTS:
         if name not in ("replay_status_string", "replay_abi_version"):
             getattr(L, name).restype = ctypes.c_int
@@ -375,6 +383,36 @@ def replay_scan(cfg, T, max_len, cu_seqlens, q, k, v, dt, a, s_in, s_out, y, err
         _want("dt", dt, (T, H), f32, gpu), _want("a", a, (T, H), f32, gpu), _want("s_in", s_in, (B, H, P, N), f32, gpu),
         _want("s_out", s_out, (B, H, P, N), f32, gpu), _want("y", y, (T, H, P), io, gpu),
         _want("err", err, (B + 1,), i32, gpu), *_workspace(workspace, gpu), _on(stream, gpu)), "replay_scan")
+
+
+def replay_sample_workspace(B, W, V) -> int:
+    """Bytes of workspace that replay_sample needs for B sequences of W positions and V logits."""
+    n = ctypes.c_size_t()
+    _check(lib.replay_sample_workspace(B, W, V, ctypes.byref(n)), "replay_sample_workspace")
+    return n.value
+
+
+def replay_sample(logits, u, tokens, temperature=None, top_k=None, top_p=None, min_p=None, probs=None, fed=None,
+                  n_reject=None, workspace=None, stream=None):
+    """logits [B, W, V] (float32 or bf16; positions may lie any stride apart), u [B, W] f32, tokens [B, W] int32;
+    temperature, top_p, min_p [B] f32 and top_k [B] int32 (None: off); probs [B, W] f32; fed [B, W] and n_reject [B]
+    int32 for the rounds of drafts."""
+    import torch
+    f32, i32, gpu = torch.float32, torch.int32, _gpu()
+    B, W, V = logits.shape
+    row = logits.stride(1) if W > 1 else logits.stride(0) if B > 1 else V
+    if (logits.dtype not in (f32, torch.bfloat16) or logits.get_device() != gpu or (V > 1 and logits.stride(2) != 1)
+            or (B > 1 and logits.stride(0) != W * row)):
+        raise ReplayError("logits: want a float32 or bf16 tensor [B, W, V] of evenly spaced rows with unit stride along "
+                          f"them on the current GPU ({gpu}), got {logits.dtype} with strides {logits.stride()} on "
+                          f"{logits.device}")
+    opt = ReplaySampling(_want("temperature", temperature, (B,), f32, gpu), _want("top_k", top_k, (B,), i32, gpu),
+                         _want("top_p", top_p, (B,), f32, gpu), _want("min_p", min_p, (B,), f32, gpu))
+    _check(lib.replay_sample(
+        B, W, V, logits.data_ptr(), F32 if logits.dtype is f32 else BF16, row, ctypes.byref(opt),
+        _want("u", u, (B, W), f32, gpu), _want("tokens", tokens, (B, W), i32, gpu), _want("probs", probs, (B, W), f32, gpu),
+        _want("fed", fed, (B, W), i32, gpu), _want("n_reject", n_reject, (B,), i32, gpu), *_workspace(workspace, gpu),
+        _on(stream, gpu)), "replay_sample")
 
 
 # ---- one layer's state, allocated with torch -------------------------------

@@ -7,7 +7,8 @@
 // float32 master and of a shared low-precision checkpoint), gdn.hip (Gated
 // DeltaNet layers), ring.hip (append, rollback, fills), conv.hip (the
 // convolution and discretisation ahead of the recurrence), scan.hip (the
-// recurrence over prompts), eager.hip and probe.hip.
+// recurrence over prompts), sample.hip (tokens from logits), eager.hip and
+// probe.hip.
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
@@ -850,6 +851,67 @@ replay_status replay_scan(const replay_config *cfg, int32_t T, int32_t max_len, 
     r.ws = static_cast<float *>(workspace);
     r.ws_decay = need ? r.ws + need / sizeof(float) - (size_t)r.B * r.H * (r.nseg - 1) : nullptr;
     return from_hip(launch_scan(cfg->head_dim, cfg->state_dim, r, as_stream(stream)));
+}
+
+}  // extern "C"
+
+namespace {
+
+replay_status check_sample(int32_t B, int32_t W, int32_t V) {
+    if (B < 1 || W < 1 || V < 1) return REPLAY_ERR_INVALID_ARG;
+    if (V > kMaxVocab || (int64_t)B * W > INT32_MAX) return REPLAY_ERR_UNSUPPORTED;
+    return REPLAY_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+replay_status replay_sample_workspace(int32_t B, int32_t W, int32_t V, size_t *bytes) {
+    replay_status st = check_sample(B, W, V);
+    if (st != REPLAY_OK) return st;
+    if (!bytes) return REPLAY_ERR_INVALID_ARG;
+    *bytes = sample_workspace(B, W, V);
+    return REPLAY_OK;
+}
+
+replay_status replay_sample(int32_t B, int32_t W, int32_t V, const void *logits, int32_t logits_dtype,
+                            int64_t row_stride, const replay_sampling *opt, const float *u, int32_t *tokens,
+                            float *probs, const int32_t *fed, int32_t *n_reject, void *workspace,
+                            size_t workspace_bytes, void *stream) {
+    replay_status st = check_sample(B, W, V);
+    if (st != REPLAY_OK) return st;
+    if (logits_dtype != REPLAY_F32 && logits_dtype != REPLAY_BF16) return REPLAY_ERR_UNSUPPORTED;
+    const size_t mask = logits_dtype == REPLAY_BF16 ? 1 : 3;
+    if (!logits || (reinterpret_cast<uintptr_t>(logits) & mask) || row_stride < V) return REPLAY_ERR_INVALID_ARG;
+    if (!u || !aligned4(u) || !tokens || !aligned4(tokens) || !aligned4(probs) || !aligned4(fed) || !aligned4(n_reject) ||
+        !fed != !n_reject)
+        return REPLAY_ERR_INVALID_ARG;
+    SampleArgs a{};
+    if (opt) {
+        for (const void *p : {static_cast<const void *>(opt->temperature), static_cast<const void *>(opt->top_k),
+                              static_cast<const void *>(opt->top_p), static_cast<const void *>(opt->min_p)})
+            if (!aligned4(p)) return REPLAY_ERR_INVALID_ARG;
+        a.temperature = opt->temperature;
+        a.top_k = opt->top_k;
+        a.top_p = opt->top_p;
+        a.min_p = opt->min_p;
+    }
+    const size_t need = sample_workspace(B, W, V);
+    if (need && (!workspace || !aligned16(workspace) || workspace_bytes < need)) return REPLAY_ERR_INVALID_ARG;
+    a.B = B;
+    a.W = W;
+    a.V = V;
+    a.bf16 = logits_dtype == REPLAY_BF16;
+    a.logits = logits;
+    a.stride = row_stride;
+    a.u = u;
+    a.tokens = tokens;
+    a.probs = probs;
+    a.fed = fed;
+    a.n_reject = n_reject;
+    a.ws = workspace;
+    return from_hip(launch_sample(a, as_stream(stream)));
 }
 
 }  // extern "C"

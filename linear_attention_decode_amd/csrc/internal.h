@@ -139,7 +139,25 @@ struct ScanArgs {
     float *ws_decay;               // decays [B][H][nseg - 1]
 };
 
+// Sampling (sample.hip).
+struct SampleArgs {
+    int32_t B, W, V, bf16;
+    const void *logits;            // B W rows of V, stride elements apart
+    int64_t stride;
+    const float *temperature, *top_p, *min_p;   // [B] each, or null
+    const int32_t *top_k;
+    const float *u;                // [B][W]
+    int32_t *tokens;               // [B][W]
+    float *probs;                  // [B][W] or null
+    const int32_t *fed;            // [B][W], with
+    int32_t *n_reject;             // [B]; both or neither
+    void *ws;
+};
+constexpr int kMaxVocab = 1 << 18;
+
 // Launchers (return hipSuccess or the launch error).
+hipError_t launch_sample(const SampleArgs &a, hipStream_t s);
+size_t sample_workspace(int B, int W, int V);
 hipError_t launch_scan(int P, int N, const ScanArgs &a, hipStream_t s);
 int scan_segments(int P, int N, int B, int H, int T, int max_len, int *seg_len);   // the number of segments, and their length
 hipError_t launch_conv_prompt(const ConvArgs &a, hipStream_t s);

@@ -46,3 +46,45 @@ def scan(q, k, v, dt, a, S):
         S = a[t][:, None, None] * S + (dt[t][:, None] * v[t])[:, :, None] * kk[:, None, :]
         y[t] = np.einsum("hpn,hn->hp", S, qq)
     return y, S
+
+
+ONE = 1 << 45   # the weight of the largest logit
+
+
+def weights(x, T):
+    """rint(2^45 exp((x - max) / T)) of one row, as Python whole numbers."""
+    with np.errstate(under="ignore"):
+        return [int(w) for w in np.rint(np.exp((x - x.max()) / T) * ONE)]
+
+
+def sample(x, u, T=1.0, top_k=0, top_p=1.0, min_p=0.0):
+    """One row of float64 logits: (token, its share of the kept weight), whole-number sums throughout.
+    T, top_p, min_p, u: float32 values."""
+    x = np.asarray(x, np.float64)
+    if np.isnan(x).any() or np.isposinf(x).any() or np.isneginf(x).all() or not (0 <= T < np.inf) or u != u:
+        return -1, 0.0
+    if T == 0:
+        return int(np.argmax(x)), 1.0
+    w = weights(x, float(T))
+    order = sorted(range(len(x)), key=lambda i: (-x[i], i))
+    if 0 < top_k < len(x):
+        order = order[:top_k]
+    if top_p < 1:
+        want = max(1, int(np.ceil(np.float64(top_p) * np.float64(sum(w[i] for i in order)))))
+        kept, ahead = [], 0
+        for i in order:
+            if ahead >= want:
+                break
+            kept.append(i)
+            ahead += w[i]
+        order = kept
+    least = int(np.ceil(min(float(min_p), 1.0) * ONE)) if min_p > 0 else 0
+    order = sorted(i for i in order if w[i] >= least)
+    total = sum(w[i] for i in order)
+    target = min(max(int(np.floor(np.float64(u) * np.float64(total))), 0), total - 1)
+    upto = 0
+    for i in order:
+        upto += w[i]
+        if upto > target:
+            return i, w[i] / total
+    raise AssertionError("no token")

@@ -131,3 +131,31 @@ def test_scan_workspace(lad):
     for args in ((0, 8), (8, 0)):
         with pytest.raises(lad.ReplayError, match="status 1"):
             lad.replay_scan_workspace(_cfg(lad), *args)
+
+
+def _sample(lad, B=2, W=3, V=100, **kw):
+    a = dict(logits=P16, dtype=lad.BF16, stride=V, opt=lad.ReplaySampling(P16, P16, P16, P16), u=P16, tokens=P16, probs=P16,
+             fed=P16, rej=P16, ws=None, ws_bytes=0) | kw
+    opt = None if a["opt"] is None else ctypes.byref(a["opt"])
+    return lad.lib.replay_sample(B, W, V, a["logits"], a["dtype"], a["stride"], opt, a["u"], a["tokens"], a["probs"], a["fed"],
+                                 a["rej"], a["ws"], a["ws_bytes"], None)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(B=0), 1), (dict(W=0), 1), (dict(V=0), 1), (dict(V=(1 << 18) + 1), 2), (dict(B=1 << 20, W=1 << 12), 2),
+    (dict(dtype=2), 2), (dict(dtype=-1), 2), (dict(logits=None), 1), (dict(logits=0x1001), 1), (dict(stride=99), 1),
+    (dict(u=None), 1), (dict(u=0x1002), 1), (dict(tokens=None), 1), (dict(probs=0x1001), 1), (dict(fed=None), 1),
+    (dict(rej=None), 1),
+])
+def test_sample_refusals(lad, kw, status):
+    assert _sample(lad, **kw) == status
+
+
+@pytest.mark.parametrize("name", ["temperature", "top_k", "top_p", "min_p"])
+def test_sample_settings_refusals(lad, name):
+    opt = lad.ReplaySampling(P16, P16, P16, P16)
+    setattr(opt, name, 0x1001)
+    assert _sample(lad, opt=opt) == 1
+    n = ctypes.c_size_t()
+    assert lad.lib.replay_sample_workspace(0, 1, 1, ctypes.byref(n)) == 1
+    assert lad.lib.replay_sample_workspace(1, 1, 1, None) == 1
