@@ -792,7 +792,8 @@ namespace {
 
 // The segments of a scan; false where its launches cannot be numbered.
 bool scan_plan(const replay_config &c, int32_t T, int32_t max_len, int *nseg, int *seg_len, size_t *bytes) {
-    *nseg = scan_segments(c.head_dim, c.state_dim, c.batch, c.heads, T, max_len, seg_len);
+    *nseg = scan_segments(c.head_dim, c.state_dim, c.batch, c.heads, c.groups, c.io_dtype == REPLAY_BF16, T, max_len,
+                          seg_len);
     const int64_t bh = (int64_t)c.batch * c.heads;
     const size_t slots = (size_t)bh * (*nseg - 1);
     *bytes = slots * ((size_t)c.head_dim * c.state_dim + 1) * sizeof(float);

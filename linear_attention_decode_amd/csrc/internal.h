@@ -159,7 +159,7 @@ constexpr int kMaxVocab = 1 << 18;
 hipError_t launch_sample(const SampleArgs &a, hipStream_t s);
 size_t sample_workspace(int B, int W, int V);
 hipError_t launch_scan(int P, int N, const ScanArgs &a, hipStream_t s);
-int scan_segments(int P, int N, int B, int H, int T, int max_len, int *seg_len);   // the number of segments, and their length
+int scan_segments(int P, int N, int B, int H, int G, bool bf16, int T, int max_len, int *seg_len);   // the number of segments, and their length
 hipError_t launch_conv_prompt(const ConvArgs &a, hipStream_t s);
 hipError_t launch_conv_step(const ConvArgs &a, hipStream_t s);
 hipError_t launch_decode(int P, int N, int st, const DecodeArgs &a, hipStream_t s);

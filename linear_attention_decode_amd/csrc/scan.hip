@@ -18,7 +18,7 @@
 // whole segment: a 16 x 16 accumulator tile (lane: column l % 16, rows
 // 4 (l / 16) + r) is laid out as the operand of the product S q, whose
 // contraction runs over its rows, so the state never passes through LDS.
-#include "device_common.h"
+#include "scan_common.h"
 
 namespace replay {
 
@@ -31,23 +31,6 @@ typedef float acc4 __attribute__((ext_vector_type(4)));
 
 __device__ __forceinline__ acc4 mma(float a, float b, acc4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x4f32(a, b, c, 0, 0, 0);
-}
-
-__device__ __forceinline__ bool finite(float x) { return (__float_as_uint(x) & 0x7f800000u) != 0x7f800000u; }
-
-// Where a workgroup's tokens are.
-struct Span {
-    int t0, n;         // first row and number of tokens of the segment
-    bool run, last;    // there is such a segment; it ends its sequence
-};
-
-__device__ __forceinline__ Span find_span(const ScanArgs &a, int b, int seg) {
-    const int s0 = a.cu[b], s1 = a.cu[b + 1];
-    if (s0 < 0 || s1 < s0 || s1 > a.T || s1 - s0 > a.max_len) return {0, 0, false, false};
-    const int n = s1 - s0, at = seg * a.seg_len;
-    if (at > 0 && at >= n) return {0, 0, false, false};
-    const int left = n - at;
-    return {s0 + at, left < a.seg_len ? left : a.seg_len, true, left <= a.seg_len};
 }
 
 template <int P, int N>
@@ -227,22 +210,27 @@ __global__ __launch_bounds__((Shape<P, N>::NT)) void scan_kernel(ScanArgs s) {
                     for (int r = 0; r < 4; ++r) y = mma(S[t][r], qq[r], y);
                 }
                 y *= m.d0[i];
-                const acc4 inter = y;
+                // A weight of 0 does not hide a later token's NaN or infinity
+                // in v: the product goes without them, and they are added for
+                // the tokens from theirs on.
+                bool odd = false;
 #pragma unroll
                 for (int tj = 0; tj <= ti; ++tj) {
                     const f32x4 gg = *reinterpret_cast<const f32x4 *>(&m.g[i][16 * tj + 4 * lg]);
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) y = mma(m.v[16 * tj + 4 * lg + r][16 * w + c], gg[r], y);
+                    for (int r = 0; r < 4; ++r) {
+                        const float v = m.v[16 * tj + 4 * lg + r][16 * w + c];
+                        odd |= !finite(v);
+                        y = mma(finite(v) ? v : 0.f, gg[r], y);
+                    }
                 }
-                // A weight of 0 does not hide a later token's NaN or infinity
-                // in v: where a result is not finite, the sum goes over j <= i.
-                if (__any(!(finite(y[0]) && finite(y[1]) && finite(y[2]) && finite(y[3])))) {
-                    y = inter;
+                if (__any(odd))
                     for (int j = 0; j < 16 * (ti + 1); ++j)
-                        if (j <= i)
 #pragma unroll
-                            for (int r = 0; r < 4; ++r) y[r] = fmaf(m.g[i][j], m.v[j][16 * w + 4 * lg + r], y[r]);
-                }
+                        for (int r = 0; r < 4; ++r) {
+                            const float v = m.v[j][16 * w + 4 * lg + r];
+                            if (j <= i && !finite(v)) y[r] = fmaf(m.g[i][j], v, y[r]);
+                        }
                 if (i < n) {
                     const size_t o = ((size_t)(sp.t0 + at + i) * s.H + h) * P + 16 * w + 4 * lg;
                     if constexpr (IOB)
@@ -299,46 +287,52 @@ __global__ __launch_bounds__(256) void scan_join_kernel(ScanArgs s, int tile4) {
 }
 
 template <int P, int N, bool IOB>
-hipError_t launch_one(const ScanArgs &a, hipStream_t s) {
-    constexpr int NT = Shape<P, N>::NT;
+hipError_t launch_one(const ScanArgs &a, bool state_only, hipStream_t s) {
     const unsigned blocks = (unsigned)((size_t)a.B * a.H * a.nseg);
-    if (a.nseg > 1) {
-        scan_kernel<P, N, IOB, true><<<blocks, NT, 0, s>>>(a);
-        const unsigned per = (P * N / 4 + 255) / 256;
-        scan_join_kernel<<<(unsigned)a.B * a.H * per, 256, 0, s>>>(a, P * N / 4);
-    }
-    scan_kernel<P, N, IOB, false><<<blocks, NT, 0, s>>>(a);
+    if (state_only)
+        scan_kernel<P, N, IOB, true><<<blocks, Shape<P, N>::NT, 0, s>>>(a);
+    else
+        scan_kernel<P, N, IOB, false><<<blocks, Shape<P, N>::NT, 0, s>>>(a);
     return hipGetLastError();
 }
 
-template <bool IOB>
-hipError_t launch_shape(int P, int N, const ScanArgs &a, hipStream_t s) {
-    if (P == 16 && N == 16) return launch_one<16, 16, IOB>(a, s);
-    if (P == 64 && N == 64) return launch_one<64, 64, IOB>(a, s);
-    if (P == 64 && N == 128) return launch_one<64, 128, IOB>(a, s);
-    if (P == 128 && N == 128) return launch_one<128, 128, IOB>(a, s);
+hipError_t launch_kernel(int P, int N, const ScanArgs &a, bool state_only, hipStream_t s) {
+    if (scan_mx_supported(P, N, a)) return launch_scan_mx(P, N, a, state_only, s);
+    if (P == 16 && N == 16) return a.io_bf16 ? launch_one<16, 16, true>(a, state_only, s) : launch_one<16, 16, false>(a, state_only, s);
+    if (P == 64 && N == 64) return launch_one<64, 64, false>(a, state_only, s);
+    if (P == 64 && N == 128) return launch_one<64, 128, false>(a, state_only, s);
+    if (P == 128 && N == 128) return launch_one<128, 128, false>(a, state_only, s);
     return hipErrorInvalidValue;
 }
 
 }  // namespace
 
-// Segments of a sequence, where the (sequence, head) pairs alone leave CUs
-// without work: as many as give every CU a few workgroups, none shorter than
+// Segments of a sequence, where the workgroups of whole sequences leave CUs
+// without work: as many as give every CU a few, none shorter than
 // kMinSegment tokens.
-int scan_segments(int P, int N, int B, int H, int T, int max_len, int *seg_len) {
+int scan_segments(int P, int N, int B, int H, int G, bool bf16, int T, int max_len, int *seg_len) {
     constexpr int kEnough = 512, kMinSegment = 256;
     const int longest = max_len < T ? max_len : T;
-    const int64_t pairs = (int64_t)B * H;
-    int64_t n = pairs >= kEnough ? 1 : (kEnough + pairs - 1) / pairs;
+    const int64_t groups = (int64_t)B * H / (bf16 ? scan_mx_heads(P, H, G) : 1);
+    int64_t n = groups >= kEnough ? 1 : (kEnough + groups - 1) / groups;
     if (n > longest / kMinSegment) n = longest / kMinSegment;
     if (n < 1) n = 1;
     const int64_t len = (longest + n - 1) / n;
-    *seg_len = (int)((len + kQ - 1) / kQ * kQ);
+    *seg_len = (int)((len + kScanChunk - 1) / kScanChunk * kScanChunk);
     return (int)((longest + *seg_len - 1) / *seg_len);
 }
 
 hipError_t launch_scan(int P, int N, const ScanArgs &a, hipStream_t s) {
-    return a.io_bf16 ? launch_shape<true>(P, N, a, s) : launch_shape<false>(P, N, a, s);
+    hipError_t e = hipSuccess;
+    if (a.nseg > 1) {
+        e = launch_kernel(P, N, a, true, s);
+        if (e != hipSuccess) return e;
+        const unsigned per = (P * N / 4 + 255) / 256;
+        scan_join_kernel<<<(unsigned)a.B * a.H * per, 256, 0, s>>>(a, P * N / 4);
+        e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    return launch_kernel(P, N, a, false, s);
 }
 
 }  // namespace replay

@@ -206,17 +206,26 @@ def test_ranges():
         assert bool((p.y[~taken.to(gu.DEV)] == 7.0).all()), cu
 
 
-def test_nan_stays_in_its_sequence_and_head():
-    gu.note("scan NaN")
-    p = Prompts([50, 40], 2, 2, 64, 64, "bf16", seed=3)
-    p.v[20, 0, 5] = float("nan")
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), -float("inf")])
+def test_nan_stays_in_its_sequence_and_head(io, value):
+    """What is not finite reaches the outputs from its own token on, in its head and column only."""
+    gu.note(f"scan {value} {io}")
+    p = Prompts([50, 40], 2, 2, 64, 64, io, seed=3)
+    p.v[20, 0, 5] = value
     p.run()
     torch.cuda.synchronize()
     y, S = p.y, p.s_out
-    assert y[20:50, 0, 5].isnan().all() and S[0, 0, 5].isnan().any()
+    assert not y[20:50, 0, 5].isfinite().any() and not S[0, 0, 5].isfinite().all()
+    assert y[20, 0, 5].isnan() if value != value else True
     y2 = y.clone()
     y2[20:50, 0, 5] = 0.0
     assert y2[:90].isfinite().all() and S[1].isfinite().all() and S[0, 1].isfinite().all()
+    clean = Prompts([50, 40], 2, 2, 64, 64, io, seed=3)
+    clean.run()
+    torch.cuda.synchronize()
+    y2[20:50, 0, 5] = clean.y[20:50, 0, 5]
+    assert torch.equal(y2[:90], clean.y[:90]) and torch.equal(S[0, 1], clean.s_out[0, 1])
 
 
 @pytest.mark.parametrize("io", ["f32", "bf16"])
