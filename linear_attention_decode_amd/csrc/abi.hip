@@ -797,7 +797,7 @@ bool scan_plan(const replay_config &c, int32_t T, int32_t max_len, int *nseg, in
     const int64_t bh = (int64_t)c.batch * c.heads;
     const size_t slots = (size_t)bh * (*nseg - 1);
     *bytes = slots * ((size_t)c.head_dim * c.state_dim + 1) * sizeof(float);
-    return bh * (*nseg > 16 ? *nseg : 16) <= INT32_MAX;
+    return (bh + 8 * (int64_t)c.heads) * (*nseg > 16 ? *nseg : 16) <= INT32_MAX;
 }
 
 }  // namespace

@@ -135,9 +135,9 @@ __global__ __launch_bounds__((Shape<P, N>::NT)) void scan_kernel(ScanArgs s) {
     constexpr int NW = Sh::NW, TN = N / 16;
     __shared__ Tile<P, N> m;
 
-    const int lid = xcd_remap(blockIdx.x, gridDim.x);
-    const int h = lid % s.H, seg = (lid / s.H) % s.nseg, b = lid / s.H / s.nseg;
-    const int g = h / (s.H / s.G);
+    Place place;
+    if (!find_place(s, 1, &place)) return;
+    const int h = place.h, seg = place.seg, b = place.b, g = place.g;
     const Span sp = find_span(s, b, seg);
     const int tid = threadIdx.x, w = tid >> 6, lane = tid & 63, c = lane & 15, lg = lane >> 4;
     if (!STATE_ONLY && seg == 0 && h == 0 && !sp.run && tid == 0) raise_seq_error(s.err, b, REPLAY_SEQERR_BAD_RANGE);
@@ -288,7 +288,7 @@ __global__ __launch_bounds__(256) void scan_join_kernel(ScanArgs s, int tile4) {
 
 template <int P, int N, bool IOB>
 hipError_t launch_one(const ScanArgs &a, bool state_only, hipStream_t s) {
-    const unsigned blocks = (unsigned)((size_t)a.B * a.H * a.nseg);
+    const unsigned blocks = scan_blocks(a, 1);
     if (state_only)
         scan_kernel<P, N, IOB, true><<<blocks, Shape<P, N>::NT, 0, s>>>(a);
     else

@@ -8,6 +8,41 @@ namespace replay {
 
 constexpr int kScanChunk = 64;   // segments are whole chunks of either kernel
 
+// Workgroup -> (sequence, segment, first head): the workgroups of one group's
+// heads (`per` of them, HB heads each) read the same q and k, so they go to
+// one XCD (workgroup i runs on XCD i mod 8) one after the other; neighbouring
+// groups go to neighbouring XCDs, so that each gets a share of every sequence
+// where lengths differ.  Of up to 64 sequences the longest go first (a lane
+// each, ranked by 64 comparisons): the last workgroups to start are then the
+// shortest.  False for the places that fill up the last round.
+struct Place {
+    int b, seg, h, g;
+};
+__device__ __forceinline__ bool find_place(const ScanArgs &a, int HB, Place *p) {
+    const int per = a.H / a.G / HB, x = blockIdx.x & 7, j = blockIdx.x >> 3;
+    const int64_t unit = (int64_t)(j / per) * 8 + x;
+    if (unit >= (int64_t)a.B * a.nseg * a.G) return false;
+    p->g = (int)(unit % a.G);
+    p->seg = (int)(unit / a.G % a.nseg);
+    p->b = (int)(unit / a.G / a.nseg);
+    if (a.B > 1 && a.B <= 64) {
+        const int lane = threadIdx.x & 63;
+        const int len = lane < a.B ? a.cu[lane + 1] - a.cu[lane] : 0;
+        int rank = 0;
+        for (int o = 0; o < a.B; ++o) {
+            const int other = __builtin_amdgcn_readlane(len, o);
+            rank += other > len || (other == len && o < lane);
+        }
+        p->b = __builtin_ctzll(__ballot(lane < a.B && rank == p->b));
+    }
+    p->h = p->g * (a.H / a.G) + j % per * HB;
+    return true;
+}
+inline unsigned scan_blocks(const ScanArgs &a, int HB) {
+    const int64_t units = (int64_t)a.B * a.nseg * a.G;
+    return (unsigned)((units + 7) / 8 * 8 * (a.H / a.G / HB));
+}
+
 // Where a workgroup's tokens are.
 struct Span {
     int t0, n;         // first row and number of tokens of the segment

@@ -54,20 +54,33 @@ __device__ __forceinline__ int at(int row, int b) {
     return row * RB + (b ^ (f << 4));
 }
 
-__device__ __forceinline__ bf8 row8(const uint8_t *m, int off) {
+__device__ __forceinline__ bf8 row8(const uint8_t *m, uint32_t off) {
     return __builtin_bit_cast(bf8, *reinterpret_cast<const u32x4 *>(m + off));
 }
 
-// Operand over tokens j0 .. j0 + 15 (lane half hh: j0 + 8 hh ..): lane c of
-// 32 gets column c0 + pi(c).
+// Offsets into a swizzled array: a lane's own part, with the parts that
+// step through rows (multiples of 16 rows: added) and through a row's bytes
+// (whole 32s or 64s: exclusive-or'd, they meet no bit of the lane's but the
+// swizzle's) applied at the read.  A base made opaque once a chunk keeps
+// the compiler from holding each step's offset in a register of its own.
+__device__ __forceinline__ uint32_t opaque(uint32_t x) {
+    asm volatile("" : "+v"(x));
+    return x;
+}
+
+// Operand over tokens j0 .. j0 + 15 (lane half hh: j0 + 8 hh ..), from
+// col_base's offset for tokens from 0 and columns from a multiple of 32: lane
+// c of 32 gets column pi(c) of them.
 template <int RB>
-__device__ __forceinline__ bf8 col8(const uint8_t *m, int j0, int c0) {
-    typedef __attribute__((address_space(3))) s16x4 lds4;
+__device__ __forceinline__ uint32_t col_base() {
     const int l = threadIdx.x & 63, c = l & 15, x = c & 3;
-    const int row = j0 + 8 * (l >> 5) + (c >> 2);
-    const int col = c0 + (l & 16) + 4 * (x == 1 ? 2 : (x == 2 ? 1 : x));
-    const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4 *)(m + at<RB>(row, 2 * col)));
-    const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4 *)(m + at<RB>(row + 4, 2 * col)));
+    return at<RB>(8 * (l >> 5) + (c >> 2), 2 * ((l & 16) + 4 * (x == 1 ? 2 : (x == 2 ? 1 : x))));
+}
+template <int RB>
+__device__ __forceinline__ bf8 col8(const uint8_t *m, uint32_t off, int j0) {
+    typedef __attribute__((address_space(3))) s16x4 lds4;
+    const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4 *)(m + off + j0 * RB));
+    const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4 *)(m + (off ^ 16) + (j0 + 4) * RB));
     return __builtin_bit_cast(bf8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
 }
 
@@ -125,43 +138,45 @@ struct Tile {
     Decays d[Sh::HB];
 };
 
-// The next chunk's rows on their way to LDS.
+// The next chunk's rows on their way to LDS.  Loads go through buffer
+// resources over the chunk's own rows: those past its n tokens read zero.
 template <int P, int N, int VW, bool STATE_ONLY>
 struct Ahead {
     using Sh = Shape<P, N, VW>;
     u32x4 q[STATE_ONLY ? 1 : Sh::IQ], k[Sh::IQ], v[Sh::IV];
     float a, dt;
+    uint32_t oqk, ov, oa;   // this thread's byte offsets in a chunk's rows
+    uint32_t sqk, sv;       // bytes from one piece's row to the next piece's
+    __device__ __forceinline__ void init(const ScanArgs &s) {
+        const uint32_t tid = threadIdx.x, rqk = (uint32_t)s.G * Sh::QB, rv = (uint32_t)s.H * P * 2;
+        oqk = tid / (Sh::QB / 16) * rqk + tid % (Sh::QB / 16) * 16;
+        ov = tid / (Sh::VB / 16) * rv + tid % (Sh::VB / 16) * 16;
+        oa = (tid & 63) * (uint32_t)s.H * 4 + (tid >> 6) % Sh::HB * 4;
+        sqk = Sh::NT / (Sh::QB / 16) * rqk;
+        sv = Sh::NT / (Sh::VB / 16) * rv;
+    }
+    // n <= 0: nothing is read
     __device__ __forceinline__ void load(const ScanArgs &s, int t0, int n, int h, int g) {
-        const int tid = threadIdx.x;
-        const uint16_t *sq = static_cast<const uint16_t *>(s.q), *sk = static_cast<const uint16_t *>(s.k);
-        const uint16_t *sv = static_cast<const uint16_t *>(s.v);
-        // rows past the n tokens are zero
+        const uint32_t rqk = (uint32_t)s.G * Sh::QB, rv = (uint32_t)s.H * P * 2, ra = (uint32_t)s.H * 4;
+        const uint32_t more = n < kQ ? n - 1 : kQ - 1;   // rows behind the first
+        const size_t bqk = (size_t)t0 * rqk + (size_t)g * Sh::QB, bv = (size_t)t0 * rv + (size_t)h * P * 2;
+        const size_t ba = (size_t)t0 * ra + (size_t)h * 4;
+        const auto rk = make_rsrc(static_cast<const char *>(s.k) + bqk, n > 0 ? more * rqk + Sh::QB : 0);
+        const auto rq = make_rsrc(static_cast<const char *>(s.q) + bqk, n > 0 ? more * rqk + Sh::QB : 0);
+        const auto rv_ = make_rsrc(static_cast<const char *>(s.v) + bv, n > 0 ? more * rv + Sh::VB : 0);
+        const auto rda = make_rsrc(reinterpret_cast<const char *>(s.a) + ba, n > 0 ? more * ra + Sh::HB * 4 : 0);
+        const auto rdt = make_rsrc(reinterpret_cast<const char *>(s.dt) + ba, n > 0 ? more * ra + Sh::HB * 4 : 0);
 #pragma unroll
         for (int i = 0; i < Sh::IQ; ++i) {
-            const int e = (i * Sh::NT + tid) * 8, t = e / N;
-            k[i] = u32x4{0, 0, 0, 0};
-            if constexpr (!STATE_ONLY) q[i] = u32x4{0, 0, 0, 0};
-            if (t < n) {
-                const size_t o = ((size_t)(t0 + t) * s.G + g) * N + e % N;
-                k[i] = *reinterpret_cast<const u32x4 *>(sk + o);
-                if constexpr (!STATE_ONLY) q[i] = *reinterpret_cast<const u32x4 *>(sq + o);
-            }
+            k[i] = __builtin_amdgcn_raw_buffer_load_b128(rk, oqk, i * sqk, 0);
+            if constexpr (!STATE_ONLY) q[i] = __builtin_amdgcn_raw_buffer_load_b128(rq, oqk, i * sqk, 0);
         }
 #pragma unroll
-        for (int i = 0; i < Sh::IV; ++i) {
-            const int e = (i * Sh::NT + tid) * 8, t = e / VW;
-            v[i] = u32x4{0, 0, 0, 0};
-            if (t < n) v[i] = *reinterpret_cast<const u32x4 *>(sv + ((size_t)(t0 + t) * s.H + h) * P + e % VW);
-        }
-        a = 1.f;
-        dt = 0.f;
-        const int hb = tid >> 6, t = tid & 63;
-        if (hb < Sh::HB && t < n) {
-            a = s.a[(size_t)(t0 + t) * s.H + h + hb];
-            dt = s.dt[(size_t)(t0 + t) * s.H + h + hb];
-        }
+        for (int i = 0; i < Sh::IV; ++i) v[i] = __builtin_amdgcn_raw_buffer_load_b128(rv_, ov, i * sv, 0);
+        a = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rda, oa, 0, 0));
+        dt = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rdt, oa, 0, 0));
     }
-    __device__ __forceinline__ void store(Tile<P, N, VW> &m) const {
+    __device__ __forceinline__ void store(Tile<P, N, VW> &m, int n) {
         const int tid = threadIdx.x;
 #pragma unroll
         for (int i = 0; i < Sh::IQ; ++i) {
@@ -176,6 +191,7 @@ struct Ahead {
         }
         const int hb = tid >> 6, t = tid & 63;
         if (hb < Sh::HB) {   // whole wavefronts, a token a lane
+            a = t < n ? a : 1.f;
             const float pre = row_upto(a), suf = row_move<0x101>(row_from(a));
             const float t0 = lane_value(pre, 15), t1 = lane_value(pre, 31), t2 = lane_value(pre, 47), t3 = lane_value(pre, 63);
             const int tile = t >> 4;
@@ -203,6 +219,72 @@ __device__ __forceinline__ uint32_t upper_pair(float x, float y) {
     return __builtin_amdgcn_perm(__float_as_uint(y), __float_as_uint(x), 0x07060302u);
 }
 
+// G = the weighted scores, in 16 x 16 tiles (ti, tj) of K Q^T, lane (column i
+// = l % 16, rows j = 4 (l / 16) + r).  A fourth of the work is the diagonal
+// tile x, two below it and, for x = 0 and 2, the one beside it, zero (y's
+// products run over 32 tokens); wavefront w takes x = w (of two: w, w + 2).
+template <int P, int N, int VW>
+__device__ __forceinline__ void weigh(Tile<P, N, VW> &m, int w, int lane) {
+    using Sh = Shape<P, N, VW>;
+    const int ci = lane & 15, lg = lane >> 4;
+    const uint32_t in = opaque(at<Sh::QB>(ci, 16 * lg)), out = opaque(at<Sh::GB>(ci, 8 * lg)), lg4 = opaque(4 * lg);
+#pragma unroll
+    for (int step = 0; step < 4 / Sh::NW; ++step) {
+        const int x = w + step * Sh::NW;
+        const int ti[3] = {x, x == 0 ? 1 : (x == 1 ? 2 : 3), x == 0 ? 0 : (x == 1 ? 2 : (x == 2 ? 2 : 3))};
+        const int tj[3] = {x, x == 3 ? 1 : 0, x == 0 ? 1 : (x == 1 ? 1 : (x == 2 ? 3 : 2))};
+        acc4 d[3];
+#pragma unroll
+        for (int z = 0; z < 3; ++z) {
+            const uint32_t ko = in + 16 * Sh::QB * tj[z], qo = in + 16 * Sh::QB * ti[z];
+            bf8 k[N / 32], q[N / 32];
+#pragma unroll
+            for (int st = 0; st < N / 32; ++st) {
+                k[st] = row8(m.k, ko ^ (64 * st));
+                q[st] = row8(m.q, qo ^ (64 * st));
+            }
+            d[z] = acc4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int st = 0; st < N / 32; ++st) d[z] = mma16(k[st], q[st], d[z]);
+        }
+#pragma unroll
+        for (int y = 0; y < Sh::HB; ++y) {
+            const Decays &dc = m.d[y];
+#pragma unroll
+            for (int z = 0; z < 3; ++z) {
+                const int i = 16 * ti[z] + ci, j0 = 16 * tj[z] + lg4;
+                f32x4 o;
+                if (z == 0) {
+                    // blocks of 4: a over those between j's and i, times what is behind j in its block
+                    const f32x4 aa = *reinterpret_cast<const f32x4 *>(&dc.a[j0]);
+                    const f32x4 dt = *reinterpret_cast<const f32x4 *>(&dc.dt[j0]);
+                    const float own = dc.a[i];
+                    const float R = row_upto(ci >= 4 * (lg + 1) ? own : 1.f);
+                    f32x4 D = {R, R, R, R};
+                    float f = 1.f;
+#pragma unroll
+                    for (int r = 2; r >= 0; --r) {
+                        f = j0 + r + 1 <= i ? f * aa[r + 1] : 1.f;
+                        D[r] *= f;
+                    }
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) o[r] = j0 + r <= i ? d[z][r] * (D[r] * dt[r]) : 0.f;
+                } else {
+                    // a over the tiles between and i's own up to i, times what is behind j in its tile
+                    const float t1 = dc.tot[(tj[z] + 1) & 3], t2 = dc.tot[(tj[z] + 2) & 3];
+                    const float R = dc.pre[i] * (ti[z] - tj[z] > 1 ? t1 : 1.f) * (ti[z] - tj[z] > 2 ? t2 : 1.f);
+                    const f32x4 sd = *reinterpret_cast<const f32x4 *>(&dc.sd[j0]);
+                    const bool below = z == 1 || (x & 1);
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) o[r] = below ? d[z][r] * (R * sd[r]) : 0.f;
+                }
+                *reinterpret_cast<u32x2 *>(m.g[y] + ((out + 16 * Sh::GB * ti[z]) ^ (32 * tj[z]))) =
+                    u32x2{f32x2_to_bf16_pair(o[0], o[1]), f32x2_to_bf16_pair(o[2], o[3])};
+            }
+        }
+    }
+}
+
 // Steps 16 x + 8 hh .. of S^T's tile as an operand, x = 0, 1
 __device__ __forceinline__ bf8 state_operand(const acc16 &S, int x) {
     u32x4 f;
@@ -217,9 +299,9 @@ __global__ __launch_bounds__((Shape<P, N, VW>::NT), (VW == 128 ? 2 : 1)) void sc
     constexpr int NW = Sh::NW, HB = Sh::HB, TN = N / 32, KN = N / 16;
     __shared__ Tile<P, N, VW> m;
 
-    const int lid = xcd_remap(blockIdx.x, gridDim.x), HP = s.H / HB;
-    const int h = (lid % HP) * HB, seg = (lid / HP) % s.nseg, b = lid / HP / s.nseg;
-    const int g = h / (s.H / s.G);
+    Place place;
+    if (!find_place(s, HB, &place)) return;
+    const int h = place.h, seg = place.seg, b = place.b, g = place.g;
     const Span sp = find_span(s, b, seg);
     const int tid = threadIdx.x, w = tid >> 6, lane = tid & 63, c = lane & 31, hh = lane >> 5;
     if (!STATE_ONLY && seg == 0 && h == 0 && !sp.run && tid == 0) raise_seq_error(s.err, b, REPLAY_SEQERR_BAD_RANGE);
@@ -243,82 +325,56 @@ __global__ __launch_bounds__((Shape<P, N, VW>::NT), (VW == 128 ? 2 : 1)) void sc
             for (int r = 0; r < 4; ++r) S[t][4 * x + r] = f[r];
         }
     }
-    if constexpr (!STATE_ONLY) {   // the tiles of G above the diagonal's are never written again
-        for (int i = tid; i < HB * kQ * Sh::GB / 16; i += Sh::NT)
-            *reinterpret_cast<u32x4 *>(&m.g[0][0] + 16 * i) = u32x4{0, 0, 0, 0};
-    }
-
     Ahead<P, N, VW, STATE_ONLY> ahead;
     float decay = 1.f;
+    ahead.init(s);
     ahead.load(s, sp.t0, sp.n, h, g);
+    const uint32_t ry = (uint32_t)s.H * P * 2;
+    const uint32_t yo = (c & 15) * ry + 64 * w + 16 * hh + 2 * (c & 16);   // this lane's place in a chunk's y
+    if constexpr (!STATE_ONLY) {
+        // Stores over no bytes: every turn of the loop then finds its loads
+        // behind as many stores, and waits for the loads alone.
+        const auto none = make_rsrc(s.y, 0);
+#pragma unroll
+        for (int x = 0; x < 4; ++x) __builtin_amdgcn_raw_buffer_store_b128(u32x4{0, 0, 0, 0}, none, yo, 16 * x * ry, 0);
+    }
     for (int done = 0; done < sp.n; done += kQ) {
         const int n = sp.n - done < kQ ? sp.n - done : kQ;
         __syncthreads();   // the last chunk is read to its end
-        ahead.store(m);
-        if (done + kQ < sp.n) ahead.load(s, sp.t0 + done + kQ, sp.n - done - kQ, h, g);
+        ahead.store(m, n);
         __syncthreads();
 
         bf8 V[kQ / 16];
+        ahead.load(s, sp.t0 + done + kQ, sp.n - done - kQ, h, g);
+        const uint32_t vo = opaque(col_base<Sh::VB>() ^ (64 * w));
         if constexpr (!STATE_ONLY) {
-            // 16 x 16 tiles (ti, tj) of K Q^T: lane (column i = l % 16, rows j = 4 (l / 16) + r)
-            const int ci = lane & 15, lg = lane >> 4;
-            for (int x = w; x < 10; x += NW) {
-                const int ti = x < 1 ? 0 : (x < 3 ? 1 : (x < 6 ? 2 : 3)), tj = x - ti * (ti + 1) / 2;
-                acc4 d = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int st = 0; st < N / 32; ++st) {
-                    const int byte = 64 * st + 16 * lg;
-                    d = mma16(row8(m.k, at<Sh::QB>(16 * tj + ci, byte)), row8(m.q, at<Sh::QB>(16 * ti + ci, byte)), d);
-                }
-                const int i = 16 * ti + ci, j0 = 16 * tj + 4 * lg;
-#pragma unroll
-                for (int y = 0; y < HB; ++y) {
-                    const Decays &dc = m.d[y];
-                    f32x4 o;
-                    if (ti != tj) {
-                        float R = dc.pre[i];   // a over the tiles between and this one's, up to i
-                        if (ti - tj > 1) R *= dc.tot[tj + 1];
-                        if (ti - tj > 2) R *= dc.tot[tj + 2];
-                        const f32x4 sd = *reinterpret_cast<const f32x4 *>(&dc.sd[j0]);
-#pragma unroll
-                        for (int r = 0; r < 4; ++r) o[r] = d[r] * (R * sd[r]);
-                    } else {
-                        // blocks of 4: a over those between j's and i, times what is behind j in its block
-                        const f32x4 aa = *reinterpret_cast<const f32x4 *>(&dc.a[j0]);
-                        const f32x4 dt = *reinterpret_cast<const f32x4 *>(&dc.dt[j0]);
-                        const float own = dc.a[i];
-                        const float R = row_upto(ci >= 4 * (lg + 1) ? own : 1.f);
-                        f32x4 D = {R, R, R, R};
-                        float z = 1.f;
-#pragma unroll
-                        for (int r = 2; r >= 0; --r) {
-                            z = j0 + r + 1 <= i ? z * aa[r + 1] : 1.f;
-                            D[r] *= z;
-                        }
-#pragma unroll
-                        for (int r = 0; r < 4; ++r) o[r] = j0 + r <= i ? d[r] * (D[r] * dt[r]) : 0.f;
-                    }
-                    *reinterpret_cast<u32x2 *>(m.g[y] + at<Sh::GB>(i, 2 * j0)) =
-                        u32x2{f32x2_to_bf16_pair(o[0], o[1]), f32x2_to_bf16_pair(o[2], o[3])};
-                }
-            }
+            weigh<P, N, VW>(m, w, lane);
             // y^T = S Q^T, lane (token c of the 32, rows p)
             acc16 y[2];
 #pragma unroll
             for (int I = 0; I < 2; ++I)
 #pragma unroll
                 for (int r = 0; r < 16; ++r) y[I][r] = 0.f;
+            const uint32_t qo = opaque(at<Sh::QB>(c, 16 * hh));
+            constexpr int U = 4;   // steps whose operands are loaded together
 #pragma unroll
-            for (int st = 0; st < KN; ++st) {
-                const bf8 sf = state_operand(S[st / 2], st & 1);
+            for (int st0 = 0; st0 < KN; st0 += U) {
+                bf8 q[2][U];
 #pragma unroll
-                for (int I = 0; I < 2; ++I) y[I] = mma32(sf, row8(m.q, at<Sh::QB>(32 * I + c, 32 * st + 16 * hh)), y[I]);
+                for (int x = 0; x < U; ++x)
+#pragma unroll
+                    for (int I = 0; I < 2; ++I) q[I][x] = row8(m.q, (qo ^ (32 * (st0 + x))) + 32 * Sh::QB * I);
+#pragma unroll
+                for (int x = 0; x < U; ++x) {
+                    const bf8 sf = state_operand(S[(st0 + x) / 2], x & 1);
+#pragma unroll
+                    for (int I = 0; I < 2; ++I) y[I] = mma32(sf, q[I][x], y[I]);
+                }
             }
 #pragma unroll
             for (int I = 0; I < 2; ++I) y[I] *= m.d[hb].d0[32 * I + c];
-            __syncthreads();
 #pragma unroll
-            for (int st = 0; st < kQ / 16; ++st) V[st] = col8<Sh::VB>(m.v, 16 * st, 32 * w);
+            for (int st = 0; st < kQ / 16; ++st) V[st] = col8<Sh::VB>(m.v, vo, 16 * st);
             // A weight of 0 does not hide a later token's NaN or infinity in
             // v: where there is one (0 x = NaN), the product goes without
             // them, and they are added for the tokens from theirs on.
@@ -340,43 +396,66 @@ __global__ __launch_bounds__((Shape<P, N, VW>::NT), (VW == 128 ? 2 : 1)) void sc
                     V[st] = __builtin_bit_cast(bf8, x);
                 }
             }
+            __syncthreads();
+            const uint32_t go = opaque(at<Sh::GB>(c, 16 * hh));
+            bf8 G[6];   // 2 steps for the first 32 tokens, 4 for the others
 #pragma unroll
-            for (int I = 0; I < 2; ++I) {
-                const int i = 32 * I + c;
+            for (int x = 0; x < 6; ++x) G[x] = row8(m.g[hb], (go ^ (32 * (x < 2 ? x : x - 2))) + (x < 2 ? 0 : 32 * Sh::GB));
 #pragma unroll
-                for (int st = 0; st < 2 * (I + 1); ++st) y[I] = mma32(V[st], row8(m.g[hb], at<Sh::GB>(i, 32 * st + 16 * hh)), y[I]);
-                if (odd)
-                    for (int j = 0; j <= 32 * I + 31; ++j) {
-                        const float gg = load_io1<true>(m.g[hb] + at<Sh::GB>(i, 2 * j), 0);
+            for (int x = 0; x < 6; ++x) y[x < 2 ? 0 : 1] = mma32(V[x < 2 ? x : x - 2], G[x], y[x < 2 ? 0 : 1]);
+            // y: after the exchange of odd and even rows of 16 lanes a store
+            // writes 64 bytes of each of 16 tokens.  Through a buffer resource
+            // over the chunk's tokens, so that it is not conditional: a wait
+            // for the next chunk's loads then need not wait for these stores.
+            {
+                const auto ys = make_rsrc(static_cast<char *>(s.y) + (size_t)(sp.t0 + done) * ry + (size_t)h * P * 2,
+                                          (uint32_t)(n - 1) * ry + Sh::VB);
 #pragma unroll
-                        for (int r = 0; r < 16; ++r) {
-                            const float x = load_io1<true>(m.v + at<Sh::VB>(j, 2 * (32 * w + pi(8 * (r / 4) + 4 * hh + r % 4))), 0);
-                            if (j <= i && !finite(x)) y[I][r] = fmaf(gg, x, y[I][r]);
-                        }
+                for (int I = 0; I < 2; ++I) {
+                    u32x4 f[2];
+#pragma unroll
+                    for (int x = 0; x < 2; ++x)
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) f[x][r] = f32x2_to_bf16_pair(y[I][8 * x + 2 * r], y[I][8 * x + 2 * r + 1]);
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const auto z = __builtin_amdgcn_permlane16_swap(f[0][r], f[1][r], false, false);
+                        f[0][r] = z[0];
+                        f[1][r] = z[1];
                     }
-                if (i < n) {
-                    uint16_t *o = static_cast<uint16_t *>(s.y) + ((size_t)(sp.t0 + done + i) * s.H + h) * P + 32 * w + 8 * hh;
 #pragma unroll
-                    for (int x = 0; x < 2; ++x) {
-                        u32x4 f;
-#pragma unroll
-                        for (int r = 0; r < 4; ++r) f[r] = f32x2_to_bf16_pair(y[I][8 * x + 2 * r], y[I][8 * x + 2 * r + 1]);
-                        *reinterpret_cast<u32x4 *>(o + 16 * x) = f;
-                    }
+                    for (int x = 0; x < 2; ++x) __builtin_amdgcn_raw_buffer_store_b128(f[x], ys, yo, (32 * I + 16 * x) * ry, 0);
                 }
             }
-            if (odd)
+            if (odd) {
+                // in the stored outputs, by the lanes that stored them, when the stores are done
+                __builtin_amdgcn_s_waitcnt(0);
+                const uint32_t token = opaque(c & 15), first = opaque(8 * hh + (c & 16));
+#pragma unroll 1
+                for (uint32_t x = 0; x < 32; ++x) {
+                    const int i = 16 * (x >> 3) + token, p = first + (x & 7);
+                    uint16_t *o = static_cast<uint16_t *>(s.y) + ((size_t)(sp.t0 + done + i) * s.H + h) * P + 32 * w + p;
+#pragma unroll 1
+                    for (int j = 0; j <= i && i < n; ++j) {
+                        const float v = load_io1<true>(m.v + at<Sh::VB>(j, 2 * (32 * w + p)), 0);
+                        const float gg = load_io1<true>(m.g[hb] + at<Sh::GB>(i, 2 * j), 0);
+                        if (!finite(v)) *o = (uint16_t)f32_to_bf16_bits(fmaf(gg, v, bf16_bits_to_f32(*o)));
+                    }
+                }
 #pragma unroll
-                for (int st = 0; st < kQ / 16; ++st) V[st] = col8<Sh::VB>(m.v, 16 * st, 32 * w);
-        } else {
+                for (int st = 0; st < kQ / 16; ++st) V[st] = col8<Sh::VB>(m.v, vo, 16 * st);
+            }
+        }
+        if constexpr (STATE_ONLY) {
 #pragma unroll
-            for (int st = 0; st < kQ / 16; ++st) V[st] = col8<Sh::VB>(m.v, 16 * st, 32 * w);
+            for (int st = 0; st < kQ / 16; ++st) V[st] = col8<Sh::VB>(m.v, vo, 16 * st);
         }
         // S^T <- (whole decay) S^T + K^T (e V), e V in three parts of 8 bits
         const float all = m.d[hb].d0[kQ - 1];
         decay *= all;
 #pragma unroll
         for (int t = 0; t < TN; ++t) S[t] *= all;
+        const uint32_t ko = opaque(col_base<Sh::QB>());
 #pragma unroll
         for (int st = 0; st < kQ / 16; ++st) {
             const u32x4 vv = __builtin_bit_cast(u32x4, V[st]);
@@ -397,7 +476,7 @@ __global__ __launch_bounds__((Shape<P, N, VW>::NT), (VW == 128 ? 2 : 1)) void sc
             }
             bf8 K[TN];
 #pragma unroll
-            for (int t = 0; t < TN; ++t) K[t] = col8<Sh::QB>(m.k, 16 * st, 32 * t);
+            for (int t = 0; t < TN; ++t) K[t] = col8<Sh::QB>(m.k, ko ^ (64 * t), 16 * st);
 #pragma unroll
             for (int z = 2; z >= 0; --z)
 #pragma unroll
@@ -425,7 +504,7 @@ __global__ __launch_bounds__((Shape<P, N, VW>::NT), (VW == 128 ? 2 : 1)) void sc
 template <int P, int N, int VW>
 hipError_t launch_one(const ScanArgs &a, bool state_only, hipStream_t s) {
     using Sh = Shape<P, N, VW>;
-    const unsigned blocks = (unsigned)((size_t)a.B * (a.H / Sh::HB) * a.nseg);
+    const unsigned blocks = scan_blocks(a, Sh::HB);
     if (state_only)
         scan_mx_kernel<P, N, VW, true><<<blocks, Sh::NT, 0, s>>>(a);
     else
