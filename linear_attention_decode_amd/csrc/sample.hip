@@ -11,35 +11,52 @@
 // Tokens are ordered by logit, largest first, ties by index: the order of
 // the composite number (~key << 32 | index), key being the logit's bits made
 // monotone.  Top-k and top-p keep a prefix of that order, hence all tokens
-// whose composite is at most some bound.  The bound is found without
-// sorting the row: a histogram over kBins steps of the distance to the
-// maximum finds the step where the prefix ends, and the tokens of that step
-// (with top-k: of all steps up to it) are gathered into LDS and sorted
-// there; rows where more than kList would have to be (thousands of equal
-// logits, or a large k) take a radix selection over the composite's digits.
+// whose composite is at most some bound.
 //
-// One workgroup a row; the row comes from HBM once, later passes from the
-// caches.
+// One workgroup a row.  Where filters leave few tokens, these are gathered
+// into LDS: a second pass that loads again the blocks alone whose maximum,
+// kept from the first, says that they hold one.  Whom to gather is found from the
+// threads' own maxima, four each: of 2048 of them, the k-th largest is no
+// larger than the k-th largest logit, so that all of the top k lie within the
+// step (of 1/16 of a temperature) where it does; for k = 50 that gathers some
+// 60 tokens, for k = 1000 some 1400.  Rows that this does not settle (top-p
+// alone, thousands of equal logits, k past 2048) take a histogram of the
+// steps over all tokens, and where its last step is too full to sort, a radix
+// selection over the composite's digits.
 #include "device_common.h"
 
 namespace replay {
 
 namespace {
 
-constexpr int kNT = 1024, kWaves = kNT / 64;
-constexpr int kBins = 1024;      // steps of the distance to the maximum, 1/32 of a temperature each; the last takes the rest
+constexpr int kNT = 512, kWaves = kNT / 64;   // 1024 threads would have 128 registers each, 50 too few
+constexpr int kBins = kNT;       // steps of the distance to the maximum, 1/16 of a temperature each; the last takes the rest
+constexpr float kSteps = kBins / 32;   // steps of a temperature
 constexpr int kList = 4096;      // tokens sorted in LDS
 constexpr int kIndexBits = 18;   // V <= 2^18
 constexpr int kOneBits = 45;     // the largest logit's weight is 2^45
 
+constexpr int kFine = 64;        // entries of the exponential's table
+
 struct Lds {
-    uint64_t list[kList];
+    uint64_t list[kList], part[kList];
+    double fine[kFine];          // 2^(j / 64)
     uint64_t mass[kBins];
     uint32_t count[kBins];
     uint64_t wave[kWaves];
     uint64_t pick[4];
-    uint32_t n, flag;
+    u32x4 edge[2];               // the row's first and last block, where they are not whole
+    uint32_t n, listed, flag;
 };
+
+// The thread's number, hidden from the compiler's view of what a loop leaves
+// unchanged: it would keep every address of every pass in a register from
+// the kernel's start on, 70 more than there are.
+__device__ __forceinline__ int thread() {
+    int t = threadIdx.x;
+    asm volatile("" : "+v"(t));
+    return t;
+}
 
 __device__ __forceinline__ uint32_t key_of(float x) {
     const uint32_t u = __float_as_uint(x + 0.f);   // -0 is 0
@@ -51,27 +68,32 @@ __device__ __forceinline__ float value_of(uint32_t key) {
 __device__ __forceinline__ uint64_t composite(float x, int i) { return ((uint64_t)~key_of(x) << 32) | (uint32_t)i; }
 __device__ __forceinline__ float value_at(uint64_t comp) { return value_of(~(uint32_t)(comp >> 32)); }
 
-// rint(2^45 2^t), t <= 0: 2^f by its Taylor series in f ln 2, |f| <= 1/2
-// (13 terms: 2e-16 of the value), rounded to a whole number by adding 2^52.
-__device__ __forceinline__ uint64_t weight_of(float x, double top, double scale) {
-    const double t = ((double)x - top) * scale;
-    if (!(t > -(kOneBits + 2.0))) return 0;
-    const double n = rint(t), f = (t - n) * 0.69314718055994530942;
-    double p = 1.0 / 479001600.0;
-    p = fma(p, f, 1.0 / 39916800.0);
-    p = fma(p, f, 1.0 / 3628800.0);
-    p = fma(p, f, 1.0 / 362880.0);
-    p = fma(p, f, 1.0 / 40320.0);
-    p = fma(p, f, 1.0 / 5040.0);
-    p = fma(p, f, 1.0 / 720.0);
-    p = fma(p, f, 1.0 / 120.0);
-    p = fma(p, f, 1.0 / 24.0);
-    p = fma(p, f, 1.0 / 6.0);
-    p = fma(p, f, 0.5);
-    p = fma(p, f, 1.0);
-    p = fma(p, f, 1.0);
-    const double w = ldexp(p, (int)n + kOneBits) + 0x1p52;
-    return __double_as_longlong(w) & ((1ull << 52) - 1);
+// the bits of the least bf16 that is not below x (x no NaN)
+__device__ __forceinline__ uint32_t bf16_above(float x) {
+    const uint32_t u = __float_as_uint(x);
+    return (u >> 31 ? u : u + 0xffffu) >> 16;
+}
+
+// rint(2^45 exp((x - top) / T)), scale = 64 log2(e) / T.  2^(n / 64) from
+// l.fine and a shift, the rest, y = f ln 2 / 64 with |f| <= 1/2, by its
+// Taylor series (y^6 / 720 < 4e-17).  The rounding to a whole number is the
+// addition of 2^52, that of n the addition of 1.5 2^52, whose low word is n.
+// Distances past 48 powers of two, infinite ones among them, round to nothing there.
+__device__ __forceinline__ uint64_t weight_of(const double *fine, float x, double top, double scale) {
+    const double t = fmax(((double)x - top) * scale, -64.0 * (kOneBits + 3));
+    const double shifted = t + 0x1.8p52;
+    const int n = (int)(uint32_t)__double_as_longlong(shifted);
+    const double f = t - (shifted - 0x1.8p52);
+    constexpr double c = 0.69314718055994530942 / 64;
+    double p = c * c * c * c * c / 120;
+    p = fma(p, f, c * c * c * c / 24);
+    p = fma(p, f, c * c * c / 6);
+    p = fma(p, f, c * c / 2);
+    p = fma(p, f, c);
+    const double b = fine[n & (kFine - 1)];
+    p = fma(b * f, p, b);
+    const uint64_t e = (uint64_t)(uint32_t)((n >> 6) + kOneBits) << 52;
+    return (uint64_t)__double_as_longlong(__longlong_as_double(__double_as_longlong(p) + e) + 0x1p52) & ((1ull << 52) - 1);
 }
 
 // A row in 16-byte blocks on 16-byte boundaries: block i holds elements
@@ -90,8 +112,6 @@ struct Logits {
         blocks = (off + V + E - 1) / E;
     }
     __device__ __forceinline__ int first(int i) const { return E * i - off; }
-    __device__ __forceinline__ bool inside(int i) const { return first(i) >= 0 && first(i) + E <= V; }
-    __device__ __forceinline__ u32x4 raw(int i) const { return *reinterpret_cast<const u32x4 *>(base + (size_t)16 * i); }
     __device__ __forceinline__ void widen(u32x4 r, float *x) const {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -103,26 +123,84 @@ struct Logits {
             }
         }
     }
-    __device__ __forceinline__ void load(int i, float *x) const {
-        if (inside(i)) {
-            widen(raw(i), x);
-        } else {
+    // block i, whichever of its elements lie in the row
+    __device__ __forceinline__ u32x4 load_edge(int i) const {
+        u32x4 r = none();
 #pragma unroll
-            for (int e = 0; e < E; ++e) {
-                const int j = first(i) + e;
-                x[e] = -__builtin_inff();
-                if (j >= 0 && j < V) x[e] = load_io1<BF16>(base, (size_t)(j + off));
+        for (int e = 0; e < E; ++e) {
+            const int j = first(i) + e;
+            if (j < 0 || j >= V) continue;
+            if constexpr (BF16) {
+                const uint32_t x = reinterpret_cast<const uint16_t *>(base)[(size_t)(j + off)];
+                r[e / 2] = e & 1 ? (r[e / 2] & 0xffffu) | (x << 16) : (r[e / 2] & 0xffff0000u) | x;
+            } else {
+                r[e] = reinterpret_cast<const uint32_t *>(base)[(size_t)(j + off)];
             }
         }
+        return r;
     }
-    // f(x, index) for every element, in no order
+    static __device__ __forceinline__ u32x4 none() {
+        constexpr uint32_t x = BF16 ? 0xff80ff80u : 0xff800000u;
+        return u32x4{x, x, x, x};
+    }
+};
+
+// The row as the threads go over it: block t kNT + tid in turn t.  Whole
+// blocks come through a buffer resource over them alone; the first and the
+// last, where they are not whole, from LDS.
+constexpr int kTurns = 64;   // turns whose block maxima a thread keeps: 256 K bf16, 128 K float32 logits
+template <bool BF16>
+struct Row : Logits<BF16> {
+    using L = Logits<BF16>;
+    int turns, lo, hi;   // blocks lo .. hi - 1 are whole
+    const u32x4 *edge;
+    __amdgpu_buffer_rsrc_t whole;
+    // every thread calls; the edges are there behind the next barrier
+    __device__ __forceinline__ Row(Lds &l, const void *logits, int64_t row, int64_t stride, int V)
+        : L(logits, row, stride, V), turns((L::blocks + kNT - 1) / kNT), lo(L::off ? 1 : 0), hi((L::off + V) / L::E),
+          edge(l.edge) {
+        whole = make_rsrc(L::base + 16 * lo, hi > lo ? (uint32_t)(hi - lo) * 16u : 0u);
+        if (threadIdx.x < 2) l.edge[threadIdx.x] = L::load_edge(threadIdx.x ? L::blocks - 1 : 0);
+    }
+    // block i as far as it is whole, and what it is
+    __device__ __forceinline__ u32x4 load_block(int i) const {
+        return __builtin_amdgcn_raw_buffer_load_b128(whole, (uint32_t)(i - lo) * 16u, 0, 0);
+    }
+    __device__ __forceinline__ u32x4 mend(int i, u32x4 r) const {
+        if (i < lo || i >= hi) r = i < L::blocks ? edge[i < lo ? 0 : 1] : L::none();
+        return r;
+    }
+    // U turns from t on, all loads in flight together
+    template <int U>
+    __device__ __forceinline__ void load_turns(int t, u32x4 *r) const {
+        const int i0 = t * kNT + thread();
+#pragma unroll
+        for (int v = 0; v < U; ++v) r[v] = load_block(i0 + v * kNT);
+        if ((t + U) * kNT > hi || (t == 0 && lo)) {
+#pragma unroll
+            for (int v = 0; v < U; ++v) r[v] = mend(i0 + v * kNT, r[v]);
+        }
+    }
+    // f(turn, the elements of a block, the first one's index) for every turn,
+    // four turns' loads ahead; elements outside the row are -infinity
     template <class F>
     __device__ __forceinline__ void each(F f) const {
-        for (int i = threadIdx.x; i < blocks; i += kNT) {
-            float x[E];
-            load(i, x);
+        constexpr int U = 4;
+        const int tid = thread();
+        u32x4 r[U], ahead[U];
+        load_turns<U>(0, ahead);
+#pragma unroll 1
+        for (int t = 0; t < turns; t += U) {
 #pragma unroll
-            for (int e = 0; e < E; ++e) f(x[e], first(i) + e);
+            for (int v = 0; v < U; ++v) r[v] = ahead[v];
+            load_turns<U>(t + U, ahead);   // past the row: nothing is read
+#pragma unroll 1
+            for (int v = 0; v < U; ++v) {
+                if (t + v >= turns) break;
+                float x[L::E];
+                L::widen(v < 2 ? (v ? r[1] : r[0]) : (v == 2 ? r[2] : r[3]), x);
+                f(t + v, x, L::first((t + v) * kNT + tid));
+            }
         }
     }
 };
@@ -144,9 +222,9 @@ __device__ __forceinline__ uint64_t wave_upto(uint64_t v) {   // inclusive, by l
 // The sum of v over the threads before this one (and over all, in *total).
 // Every thread calls; l.wave is free afterwards.
 __device__ __forceinline__ uint64_t before(Lds &l, uint64_t v, uint64_t *total) {
-    const int w = threadIdx.x >> 6;
+    const int tid = thread(), w = tid >> 6;
     const uint64_t upto = wave_upto(v);
-    if ((threadIdx.x & 63) == 63) l.wave[w] = upto;
+    if ((tid & 63) == 63) l.wave[w] = upto;
     __syncthreads();
     uint64_t ahead = 0, all = 0;
     for (int i = 0; i < kWaves; ++i) {
@@ -159,24 +237,34 @@ __device__ __forceinline__ uint64_t before(Lds &l, uint64_t v, uint64_t *total) 
     return ahead + upto - v;
 }
 
-// list[0, n) in ascending order; entries n .. the next power of two are overwritten.
-__device__ void sort_list(Lds &l, int n) {
-    int m = 1;
+// list[0, n), of kList places, in ascending order; entries n .. the next power of two are
+// overwritten.  Exchanges over up to 64 entries stay within the 128 that a
+// wavefront's own threads hold, and need no barrier of the workgroup.
+__device__ void sort_list(uint64_t *list, int n) {
+    const int tid = thread();
+    int m = 2;
     while (m < n) m <<= 1;
-    for (int i = n + threadIdx.x; i < m; i += kNT) l.list[i] = ~0ull;
+    for (int i = n + tid; i < m; i += kNT) list[i] = ~0ull;
     __syncthreads();
     for (int k = 2; k <= m; k <<= 1)
         for (int j = k >> 1; j; j >>= 1) {
-            for (int t = threadIdx.x; t < m / 2; t += kNT) {
+            for (int t = tid; t < m / 2; t += kNT) {
                 const int lo = 2 * t - (t & (j - 1)), hi = lo + j;
-                const uint64_t a = l.list[lo], b = l.list[hi];
+                const uint64_t a = list[lo], b = list[hi];
                 if ((a > b) == ((lo & k) == 0)) {
-                    l.list[lo] = b;
-                    l.list[hi] = a;
+                    list[lo] = b;
+                    list[hi] = a;
                 }
             }
-            __syncthreads();
+            const int next = j > 1 ? j >> 1 : k;
+            if (j > 64 || next > 64) {
+                __syncthreads();
+            } else {
+                __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+                __builtin_amdgcn_wave_barrier();
+            }
         }
+    __syncthreads();
 }
 
 // Where a prefix of the order ends.
@@ -185,14 +273,14 @@ struct Cut {
     uint64_t mass;   // its weight
 };
 
-// The prefix of the first `want` tokens (BY_MASS: of the fewest tokens that
+// The prefix of the first `want` tokens (by_mass: of the fewest tokens that
 // weigh at least `want`), by the composite's digits, high to low.  `want` is
 // between 1 and the row's number of tokens (weight).
-template <bool BF16, bool BY_MASS>
-__device__ Cut radix_cut(Lds &l, const Logits<BF16> &row, double top, double scale, uint64_t want) {
+template <class R>
+__device__ Cut radix_cut(Lds &l, const R &row, bool by_mass, double top, double scale, uint64_t want) {
     uint64_t prefix = 0, mass = 0;
-    // 32 bits of key, then the index
-    constexpr int kDigits = 7;
+    constexpr int kDigits = 7;   // 32 bits of key, then the index
+#pragma unroll 1
     for (int d = 0; d < kDigits; ++d) {
         const int shift = d < 4 ? 56 - 8 * d : 16 - 8 * (d - 4);
         const uint64_t above = d == 0 ? 0 : ~0ull << (d < 4 ? shift + 8 : (d == 4 ? 32 : shift + 8));
@@ -201,14 +289,16 @@ __device__ Cut radix_cut(Lds &l, const Logits<BF16> &row, double top, double sca
             l.count[threadIdx.x] = 0;
         }
         __syncthreads();
-        row.each([&](float x, int i) {
-            if (i < 0 || i >= row.V) return;
-            const uint64_t c = composite(x, i);
-            if ((c & above) != prefix) return;
-            const int digit = (int)(c >> shift) & 255;
-            atomicAdd(&l.count[digit], 1u);
-            const uint64_t w = weight_of(x, top, scale);
-            if (w) atomicAdd((unsigned long long *)&l.mass[digit], (unsigned long long)w);
+        row.each([&](int, const float *x, int i) {
+#pragma unroll 1
+            for (int e = 0; e < R::E; ++e, ++i) {
+                const uint64_t c = composite(x[e], i);
+                if (i < 0 || i >= row.V || (c & above) != prefix) continue;
+                const int digit = (int)(c >> shift) & 255;
+                atomicAdd(&l.count[digit], 1u);
+                const uint64_t w = weight_of(l.fine, x[e], top, scale);
+                if (w) atomicAdd((unsigned long long *)&l.mass[digit], (unsigned long long)w);
+            }
         });
         __syncthreads();
         uint64_t w = 0, c = 0, all;
@@ -216,7 +306,7 @@ __device__ Cut radix_cut(Lds &l, const Logits<BF16> &row, double top, double sca
             w = l.mass[threadIdx.x];
             c = l.count[threadIdx.x];
         }
-        const uint64_t v = BY_MASS ? w : c;
+        const uint64_t v = by_mass ? w : c;
         const uint64_t ahead = before(l, v, &all), massed = before(l, w, &all);
         if (threadIdx.x < 256 && ahead < want && want <= ahead + v) {
             l.pick[0] = threadIdx.x;
@@ -230,48 +320,103 @@ __device__ Cut radix_cut(Lds &l, const Logits<BF16> &row, double top, double sca
         __syncthreads();
     }
     // the last digit's token is one
-    return {prefix, mass + weight_of(value_at(prefix), top, scale)};
+    return {prefix, mass + weight_of(l.fine, value_at(prefix), top, scale)};
 }
 
 // Step of the distance to the maximum: monotone in x.
 __device__ __forceinline__ int step_of(float x, float top, float rate) {
-    return (int)fminf((top - x) * rate, (float)(kBins - 1));
+    return (int)fminf(fmaxf((top - x) * rate, 0.f), (float)(kBins - 1));
 }
 
-// Histogram of the row over the steps.
-template <bool BF16, bool MASS>
-__device__ void histogram(Lds &l, const Logits<BF16> &row, float top, float rate, double scale) {
+// Histogram of the row over the steps: of its tokens, or of their weight.
+template <class R>
+__device__ void histogram(Lds &l, const R &row, bool mass, float top, float rate, double scale) {
     l.count[threadIdx.x] = 0;
     l.mass[threadIdx.x] = 0;
     __syncthreads();
-    row.each([&](float x, int i) {
-        if (i < 0 || i >= row.V) return;
-        const int s = step_of(x, top, rate);
-        atomicAdd(&l.count[s], 1u);
-        if constexpr (MASS) {
-            const uint64_t w = weight_of(x, (double)top, scale);
-            if (w) atomicAdd((unsigned long long *)&l.mass[s], (unsigned long long)w);
-        }
-    });
+    if (mass) {
+        row.each([&](int, const float *x, int) {
+            uint64_t w[R::E];
+#pragma unroll
+            for (int e = 0; e < R::E; ++e) w[e] = weight_of(l.fine, x[e], (double)top, scale);
+#pragma unroll
+            for (int e = 0; e < R::E; ++e)
+                atomicAdd((unsigned long long *)&l.mass[step_of(x[e], top, rate)], (unsigned long long)w[e]);
+        });
+    } else {
+        row.each([&](int, const float *x, int i) {
+#pragma unroll
+            for (int e = 0; e < R::E; ++e)
+                if (i + e >= 0 && i + e < row.V) atomicAdd(&l.count[step_of(x[e], top, rate)], 1u);
+        });
+    }
     __syncthreads();
 }
 
-// The composites of the row's tokens in steps lo..hi, sorted.
-template <bool BF16>
-__device__ int gather(Lds &l, const Logits<BF16> &row, float top, float rate, int lo, int hi) {
-    if (threadIdx.x == 0) l.n = 0;
+// The composites of the row's tokens of x >= low (and, where step >= 0, of
+// that step alone) into the list, unsorted; their number, or more than the
+// list holds (where a float32 block's rounded maximum says so, it may be less:
+// the caller then goes the way of too many).  low is above -infinity; `blocks` has a bit for each of the
+// first kTurns turns whose block of this thread may hold one.  These blocks
+// are listed first, so that the threads share them out evenly, and loaded again.
+template <class R>
+__device__ int gather(Lds &l, const R &row, uint64_t blocks, float low, int step, float top, float rate) {
+    const int tid = thread();
+    if (tid < 2) (tid ? l.listed : l.n) = 0;
     __syncthreads();
-    row.each([&](float x, int i) {
-        const int s = step_of(x, top, rate);
-        if (s >= lo && s <= hi && i >= 0 && i < row.V) {
-            const uint32_t at = atomicAdd(&l.n, 1u);
-            if (at < (uint32_t)kList) l.list[at] = composite(x, i);
+    uint32_t *list = reinterpret_cast<uint32_t *>(l.part);
+    constexpr uint32_t kRoom = 2 * kList;
+    uint32_t at = blocks ? atomicAdd(&l.listed, (uint32_t)__popcll(blocks)) : 0u;
+    for (; blocks && at < kRoom; blocks &= blocks - 1, ++at) list[at] = __builtin_ctzll(blocks) * kNT + tid;
+    __syncthreads();
+    // the listed blocks and all behind those turns; all of the row where they are too many to list
+    if (step < 0 && l.listed > (uint32_t)kList) return kList + 1;   // a token of each
+    const uint32_t listed = l.listed > kRoom ? 0u : l.listed, from = l.listed > kRoom ? 0u : kTurns * kNT;
+    const uint32_t more = (uint32_t)row.blocks > from ? (uint32_t)row.blocks - from : 0u;
+    constexpr int U = 4;
+#pragma unroll 1
+    for (uint32_t j0 = 0; j0 < listed + more; j0 += U * kNT) {
+        if (*(volatile uint32_t *)&l.n > (uint32_t)kList) break;   // too many already: how many is not asked
+        int block[U];
+        u32x4 r[U];
+#pragma unroll
+        for (int v = 0; v < U; ++v) {
+            const uint32_t j = j0 + v * kNT + tid;
+            block[v] = j < listed ? (int)list[j] : (j < listed + more ? (int)(j - listed + from) : row.blocks);
         }
-    });
+#pragma unroll
+        for (int v = 0; v < U; ++v) r[v] = row.load_block(block[v]);
+#pragma unroll
+        for (int v = 0; v < U; ++v) {
+            float x[R::E];
+            row.widen(row.mend(block[v], r[v]), x);
+            uint32_t hits = 0;
+#pragma unroll
+            for (int e = 0; e < R::E; ++e)
+                hits |= x[e] >= low && (step < 0 || step_of(x[e], top, rate) == step) ? 1u << e : 0u;
+            if (hits) {
+                uint32_t to = atomicAdd(&l.n, (uint32_t)__popc(hits));
+#pragma unroll
+                for (int e = 0; e < R::E; ++e) {
+                    if ((hits >> e & 1u) && to < (uint32_t)kList) l.list[to] = composite(x[e], row.first(block[v]) + e);
+                    to += hits >> e & 1u;
+                }
+            }
+        }
+    }
     __syncthreads();
-    const int n = l.n < (uint32_t)kList ? (int)l.n : kList;
-    sort_list(l, n);
-    return n;
+    return (int)l.n;
+}
+
+// the weight that top-p asks for of this much
+__device__ __forceinline__ uint64_t share_of(float p, uint64_t mass) {
+    const double x = ceil((double)p * (double)mass);
+    return x >= 1.0 ? (uint64_t)x : 1ull;
+}
+
+// top - distance, and a little less
+__device__ __forceinline__ float below(float top, float distance) {
+    return top - distance - (fabsf(top) + distance) * 0x1p-20f;
 }
 
 // floor(u mass), within 0 .. mass - 1
@@ -281,213 +426,360 @@ __device__ __forceinline__ uint64_t target_of(float u, uint64_t mass) {
     return t < mass ? t : mass - 1;
 }
 
-constexpr int kEach = kList / kNT;   // list entries a thread holds, in order
+constexpr int kEach = kList / kNT;   // list entries a thread holds
+
+// The end of the prefix of the list's order that has `want` tokens (by_mass:
+// that weighs `want`, with the fewest), and its weight, from the histogram
+// (l.count, l.mass) of the list's steps: the step that it ends in is sorted.
+__device__ Cut list_cut(Lds &l, int n, bool by_mass, float top, float peak, float rate, double scale, uint64_t want) {
+    const int tid = thread();
+    const uint64_t m = l.mass[tid], c = l.count[tid], v = by_mass ? m : c;
+    uint64_t all;
+    const uint64_t passed = before(l, m, &all), ahead = by_mass ? passed : before(l, c, &all);
+    if (tid == 0) l.n = 0;
+    if (ahead < want && want <= ahead + v) {
+        l.pick[0] = tid;
+        l.pick[1] = want - ahead;
+        l.pick[2] = passed;
+    }
+    __syncthreads();
+    const int step = (int)l.pick[0];
+    want = l.pick[1];
+    const uint64_t base = l.pick[2];
+    for (int i = tid; i < n; i += kNT)
+        if (step_of(value_at(l.list[i]), peak, rate) == step) l.part[atomicAdd(&l.n, 1u)] = l.list[i];
+    __syncthreads();
+    const int members = (int)l.n;
+    sort_list(l.part, members);
+    uint64_t w[kEach], sum = 0;
+#pragma unroll
+    for (int e = 0; e < kEach; ++e) {
+        const int i = tid * kEach + e;
+        w[e] = i < members ? weight_of(l.fine, value_at(l.part[i]), (double)top, scale) : 0;
+        sum += w[e];
+    }
+    uint64_t at = before(l, sum, &all);
+#pragma unroll
+    for (int e = 0; e < kEach; ++e) {
+        const uint64_t i = tid * kEach + e;
+        if (by_mass ? at < want && want <= at + w[e] : i + 1 == want) {
+            l.pick[0] = l.part[i];
+            l.pick[1] = base + at + w[e];
+        }
+        at += w[e];
+    }
+    __syncthreads();
+    const Cut cut = {l.pick[0], l.pick[1]};
+    __syncthreads();
+    return cut;
+}
 
 template <bool BF16>
 __global__ __launch_bounds__(kNT) void sample_kernel(SampleArgs a) {
     __shared__ Lds l;
-    const int r = blockIdx.x, b = r / a.W, tid = threadIdx.x;
-    const Logits<BF16> row(a.logits, r, a.stride, a.V);
+    using R = Row<BF16>;
+    const int r = blockIdx.x, b = r / a.W, tid = threadIdx.x, w = tid >> 6, lane = tid & 63;
+    const R row(l, a.logits, r, a.stride, a.V);
+    __syncthreads();
     const float T = a.temperature ? a.temperature[b] : 1.f, u = a.u[r];
 
-    // the maximum and the first token that has it
-    uint64_t best = ~0ull;
-    bool bad = false;
-    row.each([&](float x, int i) {
-        bad |= !(x < __builtin_inff());   // NaN or +infinity
-        const uint64_t c = composite(x, i);
-        best = (i >= 0 && i < row.V && c < best) ? c : best;
-    });
+    // the thread's maximum and the row's; NaN or +infinity
+    // a block's maximum as the least bf16 not below it
+    float own[4];   // of every fourth turn
 #pragma unroll
-    for (int d = 32; d; d >>= 1) {
-        const uint64_t o = __shfl_xor((unsigned long long)best, d);
-        best = o < best ? o : best;
+    for (int t = 0; t < 4; ++t) own[t] = -__builtin_inff();
+    uint32_t block_max[kTurns / 2];
+    uint32_t odd = 0;
+    auto look = [&](u32x4 raw, int t) {
+        float x[R::E], m = -__builtin_inff();
+        row.widen(raw, x);
+#pragma unroll
+        for (int e = 0; e < R::E; ++e) m = fmaxf(m, x[e]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            if constexpr (BF16) {   // the larger magnitude of each half
+                typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+                odd = __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2, odd),
+                                                                             __builtin_bit_cast(u16x2, raw[e] & 0x7fff7fffu)));
+            } else {
+                odd = odd > (raw[e] & 0x7fffffffu) ? odd : raw[e] & 0x7fffffffu;
+            }
+        }
+        own[t] = fmaxf(own[t], m);
+        return m;
+    };
+#pragma unroll
+    for (int t0 = 0; t0 < kTurns; t0 += 16) {
+        if (t0 >= row.turns) {
+#pragma unroll
+            for (int t = 0; t < 16; t += 2) block_max[(t0 + t) / 2] = 0xff80ff80u;
+            continue;
+        }
+        u32x4 raw[16];
+        row.template load_turns<16>(t0, raw);
+#pragma unroll
+        for (int t = 0; t < 16; t += 2)
+            block_max[(t0 + t) / 2] = bf16_above(look(raw[t], t & 2)) | bf16_above(look(raw[t + 1], (t & 2) + 1)) << 16;
     }
+#pragma unroll 1
+    for (int t = kTurns; t < row.turns; t += 4) {
+        u32x4 raw[4];
+        row.template load_turns<4>(t, raw);
+#pragma unroll
+        for (int v = 0; v < 4; ++v) (void)look(raw[v], v);
+    }
+    const bool nan = BF16 ? (odd & 0xffffu) > 0x7f80u || (odd >> 16) > 0x7f80u : odd > 0x7f800000u;
+    float top = fmaxf(fmaxf(own[0], own[1]), fmaxf(own[2], own[3]));
+#pragma unroll
+    for (int d = 32; d; d >>= 1) top = fmaxf(top, __shfl_xor(top, d));
     if (tid == 0) l.flag = 0;
     __syncthreads();
-    if (bad) l.flag = 1;
-    if ((tid & 63) == 0) l.wave[tid >> 6] = best;
+    if (nan) l.flag = 1;
+    if (lane == 0) l.wave[w] = __float_as_uint(top);
     __syncthreads();
-    bad = l.flag != 0;
-    for (int i = 0; i < kWaves; ++i) best = l.wave[i] < best ? l.wave[i] : best;
+    const bool bad = l.flag != 0;
+    for (int i = 0; i < kWaves; ++i) top = fmaxf(top, __uint_as_float((uint32_t)l.wave[i]));
     __syncthreads();
-    const float top = value_at(best);
-    if (bad || !(top > -__builtin_inff()) || !(T >= 0.f && T < __builtin_inff()) || u != u || T == 0.f) {
-        const bool greedy = !bad && top > -__builtin_inff() && T == 0.f;
+    const bool finite_top = top > -__builtin_inff() && top < __builtin_inff();
+    if (bad || !finite_top || !(T > 0.f && T < __builtin_inff()) || u != u) {
+        const bool greedy = !bad && finite_top && u == u && T == 0.f;
+        uint32_t i = ~0u;
+        if (greedy) {   // the first of the largest
+            row.each([&](int, const float *x, int j) {
+#pragma unroll
+                for (int e = 0; e < R::E; ++e) i = x[e] == top && (uint32_t)(j + e) < i ? (uint32_t)(j + e) : i;
+            });
+            if (tid == 0) l.n = ~0u;
+            __syncthreads();
+            atomicMin(&l.n, i);
+            __syncthreads();
+            i = l.n;
+        }
         if (tid == 0) {
-            a.tokens[r] = greedy ? (int32_t)(uint32_t)best : -1;
+            a.tokens[r] = greedy ? (int32_t)i : -1;
             if (a.probs) a.probs[r] = greedy ? 1.f : 0.f;
         }
         return;
     }
 
-    const double dtop = (double)top, scale = 1.4426950408889634074 / (double)T;
-    const float rate = fminf(32.f / T, 3e38f);
+    const double dtop = (double)top, scale = kFine * 1.4426950408889634074 / (double)T;
+    const float rate = fminf(kSteps / T, 3e38f);
     const int k = a.top_k ? a.top_k[b] : 0;
     const float p = a.top_p ? a.top_p[b] : 1.f, mp = a.min_p ? a.min_p[b] : 0.f;
     const bool by_k = k > 0 && k < a.V, by_p = p < 1.f;
     const uint64_t least = mp > 0.f ? (uint64_t)ceil(fmin((double)mp, 1.0) * (double)(1ull << kOneBits)) : 0;
-    uint64_t last = ~0ull;   // composites up to this one are kept
-    // the weight that top-p asks for of one that is kept so far
-    auto share = [&](uint64_t mass) {
-        const double x = ceil((double)p * (double)mass);
-        return x >= 1.0 ? (uint64_t)x : 1ull;
-    };
-    if (by_k) {
-        histogram<BF16, false>(l, row, top, rate, scale);
-        uint64_t all;
-        const uint64_t ahead = before(l, l.count[tid], &all);
-        if (ahead < (uint64_t)k && (uint64_t)k <= ahead + l.count[tid]) {
-            l.pick[0] = tid;
-            l.pick[1] = ahead + l.count[tid];
-        }
+    if (tid < kFine) l.fine[tid] = exp2((double)tid / kFine);
+    __syncthreads();
+
+    // how low the list goes: by the threads' maxima, or, where nothing asks
+    // for the weight of more, by min-p (with a step of slack for its logarithm);
+    // bounds are lowered by a part in 2^20 of top and distance, so that none
+    // of the tokens they stand for is lost to a rounding
+    float low = -__builtin_inff();
+    if (by_k && k <= 4 * kNT) {
+        l.count[tid] = 0;
         __syncthreads();
-        if (l.pick[1] <= (uint64_t)kList) {
-            // everything that can be kept is in LDS
-            gather<BF16>(l, row, top, rate, 0, (int)l.pick[0]);
-            uint64_t w[kEach], sum = 0, mass;
 #pragma unroll
-            for (int e = 0; e < kEach; ++e) {
-                const int i = tid * kEach + e;
-                w[e] = i < k ? weight_of(value_at(l.list[i]), dtop, scale) : 0;
-                sum += w[e];
-            }
-            uint64_t at = before(l, sum, &mass);
-            const uint64_t want = by_p ? share(mass) : ~0ull;
-            // those that are kept, by their index: (index, weight) pairs
-            uint64_t kept = 0, total;
-#pragma unroll
-            for (int e = 0; e < kEach; ++e) {
-                const bool in = w[e] > 0 && at < want && w[e] >= least;
-                at += w[e];
-                w[e] = in ? ((l.list[tid * kEach + e] & ((1ull << kIndexBits) - 1)) << (kOneBits + 1)) | w[e] : 0;
-                kept += in;
-            }
-            const uint64_t slot = before(l, kept, &total);
-            uint64_t s = slot;
-#pragma unroll
-            for (int e = 0; e < kEach; ++e)
-                if (w[e]) l.list[s++] = w[e];
-            __syncthreads();
-            sort_list(l, (int)total);
-            sum = 0;
-            constexpr uint64_t kWeight = (1ull << (kOneBits + 1)) - 1;
-#pragma unroll
-            for (int e = 0; e < kEach; ++e) {
-                const int i = tid * kEach + e;
-                w[e] = i < (int)total ? l.list[i] & kWeight : 0;
-                sum += w[e];
-            }
-            at = before(l, sum, &mass);
-            const uint64_t target = target_of(u, mass);
-#pragma unroll
-            for (int e = 0; e < kEach; ++e) {
-                if (at <= target && target < at + w[e]) {
-                    a.tokens[r] = (int32_t)(l.list[tid * kEach + e] >> (kOneBits + 1));
-                    if (a.probs) a.probs[r] = (float)((double)w[e] / (double)mass);
-                }
-                at += w[e];
-            }
-            return;
-        }
-        const Cut cut = radix_cut<BF16, false>(l, row, dtop, scale, (uint64_t)k);
-        last = cut.last;
-        if (by_p) {
-            const Cut c2 = radix_cut<BF16, true>(l, row, dtop, scale, share(cut.mass));
-            last = c2.last < last ? c2.last : last;
-        }
-    } else if (by_p) {
-        histogram<BF16, true>(l, row, top, rate, scale);
-        uint64_t all;
-        const uint64_t m = l.mass[tid], ahead = before(l, m, &all), want = share(all);
-        if (ahead < want && want <= ahead + m) {
-            l.pick[0] = tid;
-            l.pick[1] = ahead;
-        }
+        for (int t = 0; t < 4; ++t) atomicAdd(&l.count[step_of(own[t], top, rate)], 1u);
+        __syncthreads();
+        const uint64_t c = l.count[tid];
+        uint64_t sum;
+        const uint64_t ahead = before(l, c, &sum);
+        if (ahead < (uint64_t)k && (uint64_t)k <= ahead + c) l.pick[0] = tid;
         __syncthreads();
         const int s = (int)l.pick[0];
-        const uint64_t passed = l.pick[1];
-        if (l.count[s] <= (uint32_t)kList) {
-            const int n = gather<BF16>(l, row, top, rate, s, s);
-            uint64_t w[kEach], sum = 0;
-#pragma unroll
-            for (int e = 0; e < kEach; ++e) {
-                const int i = tid * kEach + e;
-                w[e] = i < n ? weight_of(value_at(l.list[i]), dtop, scale) : 0;
-                sum += w[e];
-            }
-            uint64_t at = passed + before(l, sum, &all);
-#pragma unroll
-            for (int e = 0; e < kEach; ++e) {
-                if (at < want && want <= at + w[e]) l.pick[2] = l.list[tid * kEach + e];
-                at += w[e];
+        if (s < kBins - 1) low = below(top, (float)(s + 1) / rate);
+    }
+    if (mp > 0.f && !by_p) low = fmaxf(low, below(top, T * (1.f / kSteps - logf(fminf(mp, 1.f)))));
+    if (a.V <= kList && (by_k || by_p)) low = fmaxf(low, -3.402823466e+38f);   // all but -infinity: those weigh nothing
+
+    uint64_t last = ~0ull;     // composites up to this one are kept
+    uint64_t want = 0;         // what the prefix of step `step` weighs in it
+    int step = -1;
+    bool cut_k = by_k, cut_p = by_p;   // what the list is still to be cut by
+    // 0: the list as found above; 1: as a histogram of the row says; 2: the prefix is known
+    for (int stage = 0; stage < 3; ++stage) {
+        const int tid = thread();
+        if (stage == 1) {
+            if (!by_k && !by_p) break;
+            histogram(l, row, !by_k, top, rate, scale);
+            const uint64_t v = by_k ? l.count[tid] : l.mass[tid];
+            uint64_t all;
+            const uint64_t ahead = before(l, v, &all);
+            want = by_k ? (uint64_t)k : share_of(p, all);
+            if (ahead < want && want <= ahead + v) {
+                l.pick[0] = tid;
+                l.pick[1] = ahead;
             }
             __syncthreads();
-            last = l.pick[2];
-        } else {
-            last = radix_cut<BF16, true>(l, row, dtop, scale, want).last;
-        }
-    }
-
-    // the draw, in the order of the indexes: each wavefront sums a run of
-    // blocks, the run that holds the target is split again, down to a block a lane
-    const int w = tid >> 6, lane = tid & 63;
-    auto kept = [&](float x, int i) -> uint64_t {
-        if (composite(x, i) > last) return 0;
-        const uint64_t v = weight_of(x, dtop, scale);
-        return v >= least ? v : 0;
-    };
-    int lo = 0, hi = row.blocks;
-    uint64_t target = 0, mass = 0;
-    while (true) {
-        const int run = hi - lo > 64 ? ((hi - lo + kWaves - 1) / kWaves + 63) / 64 * 64 : 64;
-        const int from = lo + w * run, to = from + run < hi ? from + run : hi;
-        uint64_t sum = 0;
-        for (int i = from + lane; i < to; i += 64) {
-            float x[Logits<BF16>::E];
-            row.load(i, x);
-#pragma unroll
-            for (int e = 0; e < Logits<BF16>::E; ++e) sum += kept(x[e], row.first(i) + e);
-        }
-        const bool narrow = hi - lo <= 64;   // one block a lane of wavefront 0
-        if (narrow) {
-            if (w == 0) {
-                if (mass == 0) {   // a row of 64 blocks or fewer
-                    mass = wave_sum(sum);
-                    target = target_of(u, mass);
+            const int s = (int)l.pick[0];
+            if (!by_k) {
+                step = s;
+                want -= l.pick[1];
+            }
+            low = s < kBins - 1 ? below(top, (float)(s + 1) / rate) : -3.402823466e+38f;
+            __syncthreads();
+        } else if (stage == 2) {
+            if (last == ~0ull) {   // too full to sort: by digits
+                if (by_k) {
+                    const Cut cut = radix_cut(l, row, false, dtop, scale, (uint64_t)k);
+                    last = cut.last;
+                    want = share_of(p, cut.mass);
                 }
-                uint64_t at = wave_upto(sum) - sum;
-                if (at <= target && target < at + sum) {
-                    float x[Logits<BF16>::E];
-                    row.load(lo + lane, x);
+                if (by_p) {
+                    if (!by_k) {   // of the whole row's weight again, without the steps before
+                        uint64_t sum = 0;
+                        row.each([&](int, const float *x, int) {
 #pragma unroll
-                    for (int e = 0; e < Logits<BF16>::E; ++e) {
-                        const uint64_t v = kept(x[e], row.first(lo + lane) + e);
-                        if (at <= target && target < at + v) {
-                            a.tokens[r] = row.first(lo + lane) + e;
-                            if (a.probs) a.probs[r] = (float)((double)v / (double)mass);
-                        }
-                        at += v;
+                            for (int e = 0; e < R::E; ++e) sum += weight_of(l.fine, x[e], dtop, scale);
+                        });
+                        (void)before(l, sum, &want);
+                        want = share_of(p, want);
                     }
+                    const uint64_t end = radix_cut(l, row, true, dtop, scale, want).last;
+                    last = end < last ? end : last;
                 }
             }
-            return;
+            low = value_at(last);
+            step = -1;
+            cut_k = cut_p = false;
         }
+        if (!(low > -__builtin_inff())) continue;
+        uint64_t blocks = 0;
+#pragma unroll
+        for (int t = 0; t < kTurns; t += 2) {
+            uint32_t two = block_max[t / 2];
+            asm volatile("" : "+v"(two));   // unpacked here, not for good
+            blocks |= bf16_bits_to_f32(two & 0xffffu) < low ? 0ull : 1ull << t;
+            blocks |= bf16_bits_to_f32(two >> 16) < low ? 0ull : 2ull << t;
+        }
+        const int n = gather(l, row, blocks, low, step, top, rate);
+        if (n > kList) continue;
+
+        // steps that share out the list's range, as far as it weighs anything
+        const float peak = step < 0 ? top : top - (float)step / rate;
+        const float fine = fminf(fmaxf((float)(kBins - 1) / (peak - low), rate), 3e38f);
+        uint64_t c[kEach], v[kEach], sum = 0, mass;
+        const bool cut = (cut_k && k < n) || cut_p;
+        if (cut) {
+            l.count[tid] = 0;
+            l.mass[tid] = 0;
+            __syncthreads();
+        }
+#pragma unroll
+        for (int e = 0; e < kEach; ++e) {
+            const int i = e * kNT + tid;
+            c[e] = i < n ? l.list[i] : ~0ull;
+            v[e] = i < n ? weight_of(l.fine, value_at(c[e]), dtop, scale) : 0;
+            sum += v[e];
+            if (i < n && cut) {
+                const int s = step_of(value_at(c[e]), peak, fine);
+                atomicAdd(&l.count[s], 1u);
+                atomicAdd((unsigned long long *)&l.mass[s], (unsigned long long)v[e]);
+            }
+        }
+        if (cut) {
+            (void)before(l, sum, &mass);
+#pragma unroll 1
+            for (int by = 0; by < 2; ++by) {
+                if (by == 0 ? !(cut_k && k < n) : !cut_p) continue;
+                const Cut end = list_cut(l, n, by == 1, top, peak, fine, scale,
+                                         by == 0 ? (uint64_t)k : (step >= 0 ? want : share_of(p, mass)));
+                last = end.last < last ? end.last : last;
+                mass = end.mass;
+            }
+            if (step >= 0) continue;   // that was the prefix's end; the list is not the whole prefix
+        }
+        sum = 0;
+#pragma unroll
+        for (int e = 0; e < kEach; ++e) {
+            v[e] = c[e] <= last && v[e] >= least ? v[e] : 0;
+            sum += v[e];
+        }
+        (void)before(l, sum, &mass);
+        uint64_t target = target_of(u, mass);
+        // in the order of the indexes, by three digits of 6 bits: the weight of each digit's value, and where the target falls
+        uint32_t prefix = 0;
+#pragma unroll 1
+        for (int shift = kIndexBits - 6; shift >= 0; shift -= 6) {
+            if (tid < 64) l.mass[tid] = 0;
+            __syncthreads();
+#pragma unroll
+            for (int e = 0; e < kEach; ++e) {
+                const uint32_t i = (uint32_t)c[e];
+                if (v[e] && (i >> (shift + 6)) == prefix)
+                    atomicAdd((unsigned long long *)&l.mass[(i >> shift) & 63], (unsigned long long)v[e]);
+            }
+            __syncthreads();
+            const uint64_t m = l.mass[lane], upto = wave_upto(m);
+            const int digit = __builtin_ctzll(__ballot(target < upto));
+            target -= __shfl((unsigned long long)(upto - m), digit);
+            prefix = prefix << 6 | digit;
+            sum = __shfl((unsigned long long)m, digit);
+            __syncthreads();
+        }
+        if (tid == 0) {
+            a.tokens[r] = (int32_t)prefix;
+            if (a.probs) a.probs[r] = (float)((double)sum / (double)mass);
+        }
+        return;
+    }
+    const float x_last = value_at(last);   // NaN where all is kept
+
+    // the draw over the row, in the order of the indexes: a wavefront's weight
+    // in each turn, then the wavefront that holds the target, lane by lane
+    auto kept = [&](float x, int i) -> uint64_t {
+        const uint64_t v = weight_of(l.fine, x, dtop, scale);
+        const bool past = x < x_last || (x == x_last && (uint32_t)i > (uint32_t)last);   // composite(x, i) > last
+        return !past && v >= least ? v : 0;
+    };
+    uint64_t *part = l.list;   // [turn][wavefront]
+    row.each([&](int t, const float *x, int i) {
+        uint64_t sum = 0;
+#pragma unroll
+        for (int e = 0; e < R::E; ++e) sum += kept(x[e], i + e);
         sum = wave_sum(sum);
-        if (lane == 0) l.wave[w] = sum;
-        __syncthreads();
-        if (mass == 0) {
-            for (int i = 0; i < kWaves; ++i) mass += l.wave[i];
-            target = target_of(u, mass);
+        if (lane == 0) part[t * kWaves + w] = sum;
+    });
+    __syncthreads();
+    // parts in order, kEach a thread (turns of up to 2^18 float32 logits: 65)
+    const int parts = (row.blocks + kNT - 1) / kNT * kWaves;
+    uint64_t v[kEach], sum = 0, mass;
+#pragma unroll
+    for (int e = 0; e < kEach; ++e) {
+        v[e] = tid * kEach + e < parts ? part[tid * kEach + e] : 0;
+        sum += v[e];
+    }
+    uint64_t at = before(l, sum, &mass);
+    const uint64_t target = target_of(u, mass);
+#pragma unroll
+    for (int e = 0; e < kEach; ++e) {
+        if (at <= target && target < at + v[e]) {
+            l.pick[0] = tid * kEach + e;
+            l.pick[1] = at;
         }
-        int next = 0;
-        for (; next < kWaves - 1; ++next) {
-            if (target < l.wave[next]) break;
-            target -= l.wave[next];
+        at += v[e];
+    }
+    __syncthreads();
+    const int t = (int)l.pick[0] / kWaves, i = t * kNT + ((int)l.pick[0] % kWaves) * 64 + lane;
+    if (w == 0) {
+        float x[R::E];
+        uint64_t v8[R::E], s8 = 0;
+        row.widen(row.load_edge(i < row.blocks ? i : 0), x);
+#pragma unroll
+        for (int e = 0; e < R::E; ++e) {
+            v8[e] = i < row.blocks ? kept(x[e], row.first(i) + e) : 0;
+            s8 += v8[e];
         }
-        __syncthreads();
-        lo += next * run;
-        hi = lo + run < hi ? lo + run : hi;
+        uint64_t from = l.pick[1] + wave_upto(s8) - s8;
+#pragma unroll
+        for (int e = 0; e < R::E; ++e) {
+            if (from <= target && target < from + v8[e]) {
+                a.tokens[r] = row.first(i) + e;
+                if (a.probs) a.probs[r] = (float)((double)v8[e] / (double)mass);
+            }
+            from += v8[e];
+        }
     }
 }
 
