@@ -264,27 +264,65 @@ __global__ __launch_bounds__(kNT) void conv_prompt_kernel(ConvArgs a, int CB, in
         if ((mask >> (i / a.H)) & 1) discretise<BF16>(a, (size_t)t0 + i / a.H, i % a.H);
 }
 
-// The tokens of a step or round: workgroups [0, B CB) take one sequence's
-// channels, the rest (token, head) pairs.  The thread that reads a channel's
-// history is the one that writes its new rows.
-template <bool BF16, bool AL, int K>
-__global__ __launch_bounds__(kStepNT) void conv_step_kernel(ConvArgs a, int CB) {
-    constexpr int E = BF16 ? 8 : 4, U = 4;
-    int id = blockIdx.x;
-    if (id >= a.B * CB) {
-        const size_t i = (size_t)(id - a.B * CB) * kStepNT + threadIdx.x;
-        if (i < (size_t)a.T * a.H) discretise<BF16>(a, i / a.H, (int)(i % a.H));
-        return;
-    }
-    const int b = id / CB, c0 = ((id % CB) * kStepNT + (int)threadIdx.x) * E;
-    if (c0 >= a.C) return;
+// Where the history of a sequence's next token is: the slot of that token.
+__device__ __forceinline__ int step_slot(const ConvArgs &a, int b) {
     int p = a.pos[b];
     if (a.n_reject) {   // as the rollback itself: out of range, the pointer stays
         const int r = a.n_reject[b];
         if (r >= 0 && r <= p - a.base[b]) p -= r;
     }
-    const int pm = (int)((uint32_t)p % (uint32_t)a.R);
-    const size_t st = (size_t)b * a.R * a.C + c0;
+    return (int)((uint32_t)p % (uint32_t)a.R);
+}
+
+// The tokens of a step or round: workgroups [0, ceil(B / S) CB) take S
+// sequences' channels, the rest (token, head) pairs.  The thread that reads a
+// channel's history is the one that writes its new rows.  S > 1, for single
+// tokens: the taps, 9 times a token's bytes (bf16), are loaded once for S of them.
+template <bool BF16, bool AL, int K, int S>
+__global__ __launch_bounds__(kStepNT) void conv_step_kernel(ConvArgs a, int CB) {
+    constexpr int E = BF16 ? 8 : 4, U = 4;
+    int id = blockIdx.x;
+    const int groups = (a.B + S - 1) / S;
+    if (id >= groups * CB) {
+        const size_t i = (size_t)(id - groups * CB) * kStepNT + threadIdx.x;
+        if (i < (size_t)a.T * a.H) discretise<BF16>(a, i / a.H, (int)(i % a.H));
+        return;
+    }
+    const int b0 = id / CB * S, c0 = ((id % CB) * kStepNT + (int)threadIdx.x) * E;
+    if (c0 >= a.C) return;
+    Channels<BF16, K> ch;
+    float hist[K - 1][E];
+    if constexpr (S > 1) {
+        Row<BF16, true> old[S][K - 1];
+        Row<BF16, AL> cur[S];
+        int slot[S];
+#pragma unroll
+        for (int s = 0; s < S; ++s) {
+            const int b = b0 + s < a.B ? b0 + s : a.B - 1;
+            slot[s] = step_slot(a, b);
+            cur[s].load(a.x, (size_t)b * a.x_stride + c0);
+#pragma unroll
+            for (int j = 0; j < K - 1; ++j) {
+                int from = slot[s] - (K - 1 - j);
+                from += from < 0 ? a.R : 0;
+                old[s][j].load(a.state_out, ((size_t)b * a.R + from) * a.C + c0);
+            }
+        }
+        ch.init(a, c0);
+#pragma unroll
+        for (int s = 0; s < S; ++s) {
+            if (b0 + s >= a.B) break;
+            float x[E];
+#pragma unroll
+            for (int j = 0; j < K - 1; ++j) old[s][j].widen(hist[j]);
+            cur[s].widen(x);
+            ch.apply(hist, x, b0 + s);
+            store_row<BF16, E>(a.state_out, ((size_t)(b0 + s) * a.R + slot[s]) * a.C + c0, x);
+        }
+        return;
+    }
+    const int pm = step_slot(a, b0);
+    const size_t st = (size_t)b0 * a.R * a.C + c0;
     Row<BF16, true> old[K - 1];
 #pragma unroll
     for (int j = 0; j < K - 1; ++j) {
@@ -292,14 +330,12 @@ __global__ __launch_bounds__(kStepNT) void conv_step_kernel(ConvArgs a, int CB) 
         slot += slot < 0 ? a.R : 0;
         old[j].load(a.state_out, st + (size_t)slot * a.C);
     }
-    Channels<BF16, K> ch;
-    const size_t t0 = (size_t)b * a.W;
+    const size_t t0 = (size_t)b0 * a.W;
     Row<BF16, AL> cur[U];
 #pragma unroll
     for (int i = 0; i < U; ++i)
         if (i < a.W) cur[i].load(a.x, (t0 + i) * a.x_stride + c0);
     ch.init(a, c0);
-    float hist[K - 1][E];
 #pragma unroll
     for (int j = 0; j < K - 1; ++j) old[j].widen(hist[j]);
     int slot = pm;
@@ -329,6 +365,10 @@ bool rows_aligned(const ConvArgs &a) {
     return (reinterpret_cast<uintptr_t>(a.x) & 15u) == 0 && (a.x_stride * esz) % 16 == 0;
 }
 
+// Sequences a thread of the step takes: several where one each makes more
+// workgroups of single tokens than the card holds at a time (32 a CU).
+constexpr int kShare = 4, kManyGroups = 2048;
+
 template <bool BF16, bool AL, int K>
 hipError_t launch_one(const ConvArgs &a, bool step, hipStream_t s) {
     constexpr int E = BF16 ? 8 : 4;
@@ -336,12 +376,15 @@ hipError_t launch_one(const ConvArgs &a, bool step, hipStream_t s) {
     const int64_t cb = (a.C / E + nt - 1) / nt;
     const int64_t tiles = step ? 0 : ((int64_t)a.T + kTile - 1) / kTile;
     const int64_t gates = !a.dt_raw ? 0 : step ? ((int64_t)a.T * a.H + nt - 1) / nt : ((int64_t)a.T + 63) / 64;
-    const int64_t blocks = a.B * cb + tiles * cb + gates;
+    const bool share = step && a.W == 1 && a.B * cb >= kManyGroups;
+    const int64_t blocks = (share ? (a.B + kShare - 1) / kShare : a.B) * cb + tiles * cb + gates;
     if (blocks > INT32_MAX) return hipErrorInvalidValue;
-    if (step)
-        conv_step_kernel<BF16, AL, K><<<(unsigned)blocks, kStepNT, 0, s>>>(a, (int)cb);
-    else
+    if (!step)
         conv_prompt_kernel<BF16, AL, K><<<(unsigned)blocks, kNT, 0, s>>>(a, (int)cb, (int)tiles);
+    else if (share)
+        conv_step_kernel<BF16, AL, K, kShare><<<(unsigned)blocks, kStepNT, 0, s>>>(a, (int)cb);
+    else
+        conv_step_kernel<BF16, AL, K, 1><<<(unsigned)blocks, kStepNT, 0, s>>>(a, (int)cb);
     return hipGetLastError();
 }
 

@@ -309,9 +309,13 @@ hipError_t launch_kernel(int P, int N, const ScanArgs &a, bool state_only, hipSt
 
 // Segments of a sequence, where the workgroups of whole sequences leave CUs
 // without work: as many as give every CU a few, none shorter than
-// kMinSegment tokens.
+// kMinSegment tokens, since a segment costs a second reading of its k and v
+// and a state.  The float32 kernel, whose matrix instructions take most of
+// its time, gains from evener shares: 1999 ragged tokens of 32 heads of 128 x
+// 128 take 120 us at (1024, 192) and 150 us at (512, 256); 8192 tokens of 128
+// heads in bf16 take 226 us and 208 us.
 int scan_segments(int P, int N, int B, int H, int G, bool bf16, int T, int max_len, int *seg_len) {
-    constexpr int kEnough = 512, kMinSegment = 256;
+    const int kEnough = bf16 ? 512 : 1024, kMinSegment = bf16 ? 256 : 192;
     const int longest = max_len < T ? max_len : T;
     const int64_t groups = (int64_t)B * H / (bf16 ? scan_mx_heads(P, H, G) : 1);
     int64_t n = groups >= kEnough ? 1 : (kEnough + groups - 1) / groups;

@@ -172,6 +172,30 @@ def test_step(io, pad, K, W, slots):
         assert torch.equal(c.state[b, rest], before[b, rest])
 
 
+@pytest.mark.parametrize("io,pad,K,H", [("bf16", 0, 4, 8), ("bf16", 1, 3, 8), ("f32", 0, 2, 8), ("f32", 3, 4, 8)])
+def test_step_of_many_sequences(io, pad, K, H):
+    """Enough sequences that a thread takes several, their number no multiple of that; pending rollbacks."""
+    lad = _lad()
+    B, R = 1030, 5
+    gu.note(f"conv_step B={B} {io} pad={pad} K={K}")
+    c = Case(B, B, H, 2, 64, 64, io, K, R, True, pad, seed=K)
+    r = np.random.default_rng(K)
+    pos, base = r.integers(0, 2 ** 31 - 20, B), None
+    base, rej = np.maximum(pos - r.integers(0, 4, B), 0), r.integers(-1, 4, B)
+    t = lambda a: torch.tensor(a, dtype=torch.int32, device=gu.DEV)  # noqa: E731
+    outs, before = c.outs(B, 1), c.state.clone()
+    lad.replay_conv_step(c.cfg, c.conv, 1, c.x, c.raw, t(pos), c.state, *outs, base=t(base), n_reject=t(rej))
+    torch.cuda.synchronize()
+    flat = [o.reshape(B, *o.shape[2:]) for o in outs]
+    at = np.where((rej >= 0) & (rej <= pos - base), pos - rej, pos)
+    for b in [*range(0, B, 97), B - 3, B - 2, B - 1]:
+        hist = before[b, [(int(at[b]) - i) % R for i in range(K - 1, 0, -1)]].double().cpu().numpy()
+        c.check(flat, slice(b, b + 1), c.x[b:b + 1].double().cpu().numpy(), hist)
+    want = before.clone()
+    want[torch.arange(B, device=gu.DEV), t(at % R).long()] = c.x
+    assert torch.equal(c.state, want)
+
+
 def test_step_rollback():
     """The tokens follow pos - n_reject where the rollback is in range, pos where it is not."""
     lad = _lad()
