@@ -36,11 +36,11 @@ constexpr int kList = 4096;      // tokens sorted in LDS
 constexpr int kIndexBits = 18;   // V <= 2^18
 constexpr int kOneBits = 45;     // the largest logit's weight is 2^45
 
-constexpr int kFine = 64;        // entries of the exponential's table
+constexpr int kFine = 16;        // entries of the exponential's table: one for each pair of banks, so that no two lanes wait
 
 struct Lds {
     uint64_t list[kList], part[kList];
-    double fine[kFine];          // 2^(j / 64)
+    double fine[kFine];          // 2^(j / 16)
     uint64_t mass[kBins];
     uint32_t count[kBins];
     uint64_t wave[kWaves];
@@ -74,25 +74,26 @@ __device__ __forceinline__ uint32_t bf16_above(float x) {
     return (u >> 31 ? u : u + 0xffffu) >> 16;
 }
 
-// rint(2^45 exp((x - top) / T)), scale = 64 log2(e) / T.  2^(n / 64) from
-// l.fine and a shift, the rest, y = f ln 2 / 64 with |f| <= 1/2, by its
-// Taylor series (y^6 / 720 < 4e-17).  The rounding to a whole number is the
+// rint(2^45 exp((x - top) / T)), scale = 16 log2(e) / T.  2^(n / 16) from
+// l.fine and a shift, the rest, y = f ln 2 / 16 with |f| <= 1/2, by its
+// Taylor series (y^7 / 5040 < 5e-16).  The rounding to a whole number is the
 // addition of 2^52, that of n the addition of 1.5 2^52, whose low word is n.
 // Distances past 48 powers of two, infinite ones among them, round to nothing there.
 __device__ __forceinline__ uint64_t weight_of(const double *fine, float x, double top, double scale) {
-    const double t = fmax(((double)x - top) * scale, -64.0 * (kOneBits + 3));
+    const double t = fmax(((double)x - top) * scale, -(double)kFine * (kOneBits + 3));
     const double shifted = t + 0x1.8p52;
     const int n = (int)(uint32_t)__double_as_longlong(shifted);
     const double f = t - (shifted - 0x1.8p52);
-    constexpr double c = 0.69314718055994530942 / 64;
-    double p = c * c * c * c * c / 120;
+    constexpr double c = 0.69314718055994530942 / kFine;
+    double p = c * c * c * c * c * c / 720;
+    p = fma(p, f, c * c * c * c * c / 120);
     p = fma(p, f, c * c * c * c / 24);
     p = fma(p, f, c * c * c / 6);
     p = fma(p, f, c * c / 2);
     p = fma(p, f, c);
     const double b = fine[n & (kFine - 1)];
     p = fma(b * f, p, b);
-    const uint64_t e = (uint64_t)(uint32_t)((n >> 6) + kOneBits) << 52;
+    const uint64_t e = (uint64_t)(uint32_t)((n >> 4) + kOneBits) << 52;
     return (uint64_t)__double_as_longlong(__longlong_as_double(__double_as_longlong(p) + e) + 0x1p52) & ((1ull << 52) - 1);
 }
 
@@ -205,18 +206,27 @@ struct Row : Logits<BF16> {
     }
 };
 
-__device__ __forceinline__ uint64_t wave_sum(uint64_t v) {
-#pragma unroll
-    for (int d = 32; d; d >>= 1) v += __shfl_xor((unsigned long long)v, d);
+// Sums over the lanes up to this one, by moves between lanes that pass no
+// memory (within rows of 16, then from row to row).  64 summands of 22 bits
+// stay within 32, so a 64-bit sum goes in three parts.
+__device__ __forceinline__ uint32_t lanes_upto(uint32_t v) {
+    v += __builtin_amdgcn_update_dpp(0, (int)v, 0x111, 0xf, 0xf, false);
+    v += __builtin_amdgcn_update_dpp(0, (int)v, 0x112, 0xf, 0xf, false);
+    v += __builtin_amdgcn_update_dpp(0, (int)v, 0x114, 0xf, 0xf, false);
+    v += __builtin_amdgcn_update_dpp(0, (int)v, 0x118, 0xf, 0xf, false);
+    v += __builtin_amdgcn_update_dpp(0, (int)v, 0x142, 0xa, 0xf, false);
+    v += __builtin_amdgcn_update_dpp(0, (int)v, 0x143, 0xc, 0xf, false);
     return v;
 }
-__device__ __forceinline__ uint64_t wave_upto(uint64_t v) {   // inclusive, by lane
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-        const uint64_t o = __shfl_up((unsigned long long)v, d);
-        if ((int)(threadIdx.x & 63) >= d) v += o;
-    }
-    return v;
+__device__ __forceinline__ uint64_t wave_upto(uint64_t v) {
+    constexpr uint32_t m = (1u << 22) - 1;
+    const uint64_t a = lanes_upto((uint32_t)v & m), b = lanes_upto((uint32_t)(v >> 22) & m), c = lanes_upto((uint32_t)(v >> 44));
+    return a + (b << 22) + (c << 44);
+}
+__device__ __forceinline__ uint64_t wave_sum(uint64_t v) {   // the same in every lane
+    const uint64_t all = wave_upto(v);
+    return (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(all >> 32), 63) << 32 |
+           (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)all, 63);
 }
 
 // The sum of v over the threads before this one (and over all, in *total).
@@ -452,16 +462,20 @@ __device__ Cut list_cut(Lds &l, int n, bool by_mass, float top, float peak, floa
     const int members = (int)l.n;
     sort_list(l.part, members);
     uint64_t w[kEach], sum = 0;
+    const int per = (members + kNT - 1) / kNT;   // entries a thread takes
 #pragma unroll
     for (int e = 0; e < kEach; ++e) {
-        const int i = tid * kEach + e;
+        w[e] = 0;
+        if (e >= per) break;
+        const int i = tid * per + e;
         w[e] = i < members ? weight_of(l.fine, value_at(l.part[i]), (double)top, scale) : 0;
         sum += w[e];
     }
     uint64_t at = before(l, sum, &all);
 #pragma unroll
     for (int e = 0; e < kEach; ++e) {
-        const uint64_t i = tid * kEach + e;
+        if (e >= per) break;
+        const uint64_t i = tid * per + e;
         if (by_mass ? at < want && want <= at + w[e] : i + 1 == want) {
             l.pick[0] = l.part[i];
             l.pick[1] = base + at + w[e];
@@ -669,6 +683,9 @@ __global__ __launch_bounds__(kNT) void sample_kernel(SampleArgs a) {
 #pragma unroll
         for (int e = 0; e < kEach; ++e) {
             const int i = e * kNT + tid;
+            c[e] = ~0ull;
+            v[e] = 0;
+            if (e * kNT >= n) continue;
             c[e] = i < n ? l.list[i] : ~0ull;
             v[e] = i < n ? weight_of(l.fine, value_at(c[e]), dtop, scale) : 0;
             sum += v[e];
@@ -706,6 +723,7 @@ __global__ __launch_bounds__(kNT) void sample_kernel(SampleArgs a) {
             __syncthreads();
 #pragma unroll
             for (int e = 0; e < kEach; ++e) {
+                if (e * kNT >= n) break;
                 const uint32_t i = (uint32_t)c[e];
                 if (v[e] && (i >> (shift + 6)) == prefix)
                     atomicAdd((unsigned long long *)&l.mass[(i >> shift) & 63], (unsigned long long)v[e]);
