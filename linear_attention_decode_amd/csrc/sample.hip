@@ -363,6 +363,15 @@ __device__ void histogram(Lds &l, const R &row, bool mass, float top, float rate
     __syncthreads();
 }
 
+// Room for `mine` more entries of a counted list: where this lane's start.
+// One addition a wavefront; every lane of it calls.
+__device__ __forceinline__ uint32_t reserve(uint32_t *count, uint32_t mine) {
+    const uint32_t upto = lanes_upto(mine), all = (uint32_t)__builtin_amdgcn_readlane((int)upto, 63);
+    uint32_t at = 0;
+    if (all && (threadIdx.x & 63) == 0) at = atomicAdd(count, all);
+    return (uint32_t)__builtin_amdgcn_readfirstlane((int)at) + upto - mine;
+}
+
 // The composites of the row's tokens of x >= low (and, where step >= 0, of
 // that step alone) into the list, unsorted; their number, or more than the
 // list holds (where a float32 block's rounded maximum says so, it may be less:
@@ -376,7 +385,7 @@ __device__ int gather(Lds &l, const R &row, uint64_t blocks, float low, int step
     __syncthreads();
     uint32_t *list = reinterpret_cast<uint32_t *>(l.part);
     constexpr uint32_t kRoom = 2 * kList;
-    uint32_t at = blocks ? atomicAdd(&l.listed, (uint32_t)__popcll(blocks)) : 0u;
+    uint32_t at = reserve(&l.listed, (uint32_t)__popcll(blocks));
     for (; blocks && at < kRoom; blocks &= blocks - 1, ++at) list[at] = __builtin_ctzll(blocks) * kNT + tid;
     __syncthreads();
     // the listed blocks and all behind those turns; all of the row where they are too many to list
@@ -404,8 +413,8 @@ __device__ int gather(Lds &l, const R &row, uint64_t blocks, float low, int step
 #pragma unroll
             for (int e = 0; e < R::E; ++e)
                 hits |= x[e] >= low && (step < 0 || step_of(x[e], top, rate) == step) ? 1u << e : 0u;
-            if (hits) {
-                uint32_t to = atomicAdd(&l.n, (uint32_t)__popc(hits));
+            if (__ballot(hits != 0)) {
+                uint32_t to = reserve(&l.n, (uint32_t)__popc(hits));
 #pragma unroll
                 for (int e = 0; e < R::E; ++e) {
                     if ((hits >> e & 1u) && to < (uint32_t)kList) l.list[to] = composite(x[e], row.first(block[v]) + e);
@@ -493,9 +502,12 @@ __global__ __launch_bounds__(kNT) void sample_kernel(SampleArgs a) {
     __shared__ Lds l;
     using R = Row<BF16>;
     const int r = blockIdx.x, b = r / a.W, tid = threadIdx.x, w = tid >> 6, lane = tid & 63;
-    const R row(l, a.logits, r, a.stride, a.V);
-    __syncthreads();
     const float T = a.temperature ? a.temperature[b] : 1.f, u = a.u[r];
+    const int k = a.top_k ? a.top_k[b] : 0;
+    const float p = a.top_p ? a.top_p[b] : 1.f, mp = a.min_p ? a.min_p[b] : 0.f;
+    const R row(l, a.logits, r, a.stride, a.V);
+    if (tid < kFine) l.fine[tid] = exp2((double)tid / kFine);
+    __syncthreads();
 
     // the thread's maximum and the row's; NaN or +infinity
     // a block's maximum as the least bf16 not below it
@@ -578,13 +590,8 @@ __global__ __launch_bounds__(kNT) void sample_kernel(SampleArgs a) {
 
     const double dtop = (double)top, scale = kFine * 1.4426950408889634074 / (double)T;
     const float rate = fminf(kSteps / T, 3e38f);
-    const int k = a.top_k ? a.top_k[b] : 0;
-    const float p = a.top_p ? a.top_p[b] : 1.f, mp = a.min_p ? a.min_p[b] : 0.f;
     const bool by_k = k > 0 && k < a.V, by_p = p < 1.f;
     const uint64_t least = mp > 0.f ? (uint64_t)ceil(fmin((double)mp, 1.0) * (double)(1ull << kOneBits)) : 0;
-    if (tid < kFine) l.fine[tid] = exp2((double)tid / kFine);
-    __syncthreads();
-
     // how low the list goes: by the threads' maxima, or, where nothing asks
     // for the weight of more, by min-p (with a step of slack for its logarithm);
     // bounds are lowered by a part in 2^20 of top and distance, so that none
@@ -661,11 +668,17 @@ __global__ __launch_bounds__(kNT) void sample_kernel(SampleArgs a) {
         if (!(low > -__builtin_inff())) continue;
         uint64_t blocks = 0;
 #pragma unroll
-        for (int t = 0; t < kTurns; t += 2) {
-            uint32_t two = block_max[t / 2];
-            asm volatile("" : "+v"(two));   // unpacked here, not for good
-            blocks |= bf16_bits_to_f32(two & 0xffffu) < low ? 0ull : 1ull << t;
-            blocks |= bf16_bits_to_f32(two >> 16) < low ? 0ull : 2ull << t;
+        for (int t0 = 0; t0 < kTurns; t0 += 16) {
+            if (t0 >= row.turns) break;
+            uint32_t some = 0;
+#pragma unroll
+            for (int t = 0; t < 16; t += 2) {
+                uint32_t two = block_max[(t0 + t) / 2];
+                asm volatile("" : "+v"(two));   // unpacked here, not for good
+                some |= bf16_bits_to_f32(two & 0xffffu) < low ? 0u : 1u << t;
+                some |= bf16_bits_to_f32(two >> 16) < low ? 0u : 2u << t;
+            }
+            blocks |= (uint64_t)some << t0;
         }
         const int n = gather(l, row, blocks, low, step, top, rate);
         if (n > kList) continue;
