@@ -18,6 +18,7 @@
 
 #include "count_bound.h"
 #include "internal.h"
+#include "prompt.h"
 
 using namespace replay;
 

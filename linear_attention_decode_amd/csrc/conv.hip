@@ -15,6 +15,7 @@
 // channels and keeps their taps and the last K - 1 rows in registers, so
 // every row is read once (plus K - 1 rows of halo per kTile).
 #include "device_common.h"
+#include "prompt.h"
 
 namespace replay {
 

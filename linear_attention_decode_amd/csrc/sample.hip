@@ -24,6 +24,7 @@
 // steps over all tokens, and where its last step is too full to sort, a radix
 // selection over the composite's digits.
 #include "device_common.h"
+#include "prompt.h"
 
 namespace replay {
 
@@ -506,6 +507,7 @@ __global__ __launch_bounds__(kNT) void sample_kernel(SampleArgs a) {
     const int k = a.top_k ? a.top_k[b] : 0;
     const float p = a.top_p ? a.top_p[b] : 1.f, mp = a.min_p ? a.min_p[b] : 0.f;
     const R row(l, a.logits, r, a.stride, a.V);
+    if (a.W == 1 && a.n_reject && tid == 0) a.n_reject[b] = 0;   // the one position stays
     if (tid < kFine) l.fine[tid] = exp2((double)tid / kFine);
     __syncthreads();
 
@@ -835,7 +837,7 @@ hipError_t launch_sample(const SampleArgs &a, hipStream_t s) {
         sample_kernel<true><<<rows, kNT, 0, s>>>(a);
     else
         sample_kernel<false><<<rows, kNT, 0, s>>>(a);
-    if (a.n_reject) reject_kernel<<<(a.B + 255) / 256, 256, 0, s>>>(a.tokens, a.fed, a.n_reject, a.B, a.W);
+    if (a.n_reject && a.W > 1) reject_kernel<<<(a.B + 255) / 256, 256, 0, s>>>(a.tokens, a.fed, a.n_reject, a.B, a.W);
     return hipGetLastError();
 }
 

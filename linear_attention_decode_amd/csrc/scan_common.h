@@ -3,6 +3,7 @@
 #pragma once
 
 #include "device_common.h"
+#include "prompt.h"
 
 namespace replay {
 
