@@ -412,7 +412,8 @@ typedef struct {
    equal state_in, and must not overlap it otherwise.  The row i before the
    next token sits in slot (pos[b] - i) mod R, where replay_conv_step looks
    for it; pos: the layer's pos, or NULL for 0.  R >= K - 1.
-   err: device int32 [B + 1], the layer's err or one like it.  A sequence
+   Outputs overlap nothing else that the call reads or writes.  err: device
+   int32 [B + 1], the layer's err or one like it.  A sequence
    whose range decreases or leaves 0..T gets BAD_RANGE, and its rows and its
    state are left as they are; where some range decreases, rows of other
    sequences may be left or taken for a neighbour's.  T >= 1. */
@@ -435,7 +436,8 @@ replay_status replay_conv_prompt(const replay_config *cfg, const replay_conv_par
    replay_rollback_verify_step will apply; the tokens then follow
    pos[b] - n_reject[b] (an out-of-range one leaves the pointer where it is,
    as that call does; its bit is set there).  base: the layer's base, needed
-   with n_reject.  1 <= W <= 16. */
+   with n_reject.  1 <= W <= 16.  Outputs overlap nothing else that the call
+   reads or writes. */
 replay_status replay_conv_step(const replay_config *cfg, const replay_conv_params *conv, int32_t W,
                                const void *x, int64_t x_stride, const void *dt_raw, int64_t dt_stride,
                                const int32_t *pos, const int32_t *base, const int32_t *n_reject,
@@ -453,7 +455,9 @@ replay_status replay_conv_step(const replay_config *cfg, const replay_conv_param
    a any finite number (0 resets the state).  y: [T][H][P] in the io dtype, as a
    model's next product takes it; rows outside every range are left as they
    are.  With bf16 io the products run on bf16 operands: inputs are taken as
-   they are, sums and states are float32.  s_out must not overlap s_in.
+   they are, sums and states are float32.  y and s_out overlap nothing else
+   that the call reads or writes (s_out over s_in: INVALID_ARG).  T <= 2^30,
+   H P and G N <= 2^24.
    A sequence whose range decreases, leaves 0..T or is longer than max_len
    gets BAD_RANGE in err (device int32 [B + 1]); its rows and its s_out are
    left as they are.
@@ -497,7 +501,8 @@ typedef struct {
    fed[w], and n_reject (int32 [B]) receives W minus the number that stays,
    as replay_rollback takes it; the sequence goes on with the last kept
    position's token, tokens[b][W - 1 - n_reject[b]].  fed and n_reject: both
-   or neither.  workspace: device memory of replay_sample_workspace bytes
+   or neither.  Outputs overlap nothing else that the call reads or writes.
+   B W < 2^23.  workspace: device memory of replay_sample_workspace bytes
    (NULL where that is 0), holding nothing between calls; calls that can
    overlap need one each. */
 replay_status replay_sample_workspace(int32_t B, int32_t W, int32_t V, size_t *bytes);

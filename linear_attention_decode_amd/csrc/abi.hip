@@ -691,6 +691,10 @@ replay_status replay_stream_probe(int32_t mode, const void *src, void *dst, size
 
 namespace {
 
+replay_status from_conv(hipError_t e) {
+    return e == hipErrorInvalidConfiguration ? REPLAY_ERR_UNSUPPORTED : from_hip(e);
+}
+
 // What the two convolution calls check and fill alike.
 replay_status conv_args(const replay_config *cfg, const replay_conv_params *cv, const void *x, int64_t x_stride,
                         const void *dt_raw, int64_t dt_stride, void *q, void *k, void *v, float *dt, float *a,
@@ -701,7 +705,7 @@ replay_status conv_args(const replay_config *cfg, const replay_conv_params *cv, 
     if (cv->width > 4) return REPLAY_ERR_UNSUPPORTED;
     if (cv->slots < cv->width - 1) return REPLAY_ERR_INVALID_ARG;
     const int64_t C = (int64_t)cfg->heads * cfg->head_dim + 2 * (int64_t)cfg->groups * cfg->state_dim;
-    if (C > (int64_t(1) << 24)) return REPLAY_ERR_UNSUPPORTED;
+    if (C > kMaxRow) return REPLAY_ERR_UNSUPPORTED;
     const size_t io_mask = io_bytes(*cfg) - 1;
     if (!x || (reinterpret_cast<uintptr_t>(x) & io_mask) || x_stride < C) return REPLAY_ERR_INVALID_ARG;
     if (!cv->weight || !aligned4(cv->weight) || !aligned4(cv->bias)) return REPLAY_ERR_INVALID_ARG;
@@ -764,7 +768,7 @@ replay_status replay_conv_prompt(const replay_config *cfg, const replay_conv_par
     c.state_in = state_in;
     c.state_out = state_out;
     c.err = err;
-    return from_hip(launch_conv_prompt(c, as_stream(stream)));
+    return from_conv(launch_conv_prompt(c, as_stream(stream)));
 }
 
 replay_status replay_conv_step(const replay_config *cfg, const replay_conv_params *conv, int32_t W, const void *x,
@@ -784,21 +788,23 @@ replay_status replay_conv_step(const replay_config *cfg, const replay_conv_param
     c.base = base;
     c.n_reject = n_reject;
     c.state_out = conv_state;
-    return from_hip(launch_conv_step(c, as_stream(stream)));
+    return from_conv(launch_conv_step(c, as_stream(stream)));
 }
 
 }  // extern "C"
 
 namespace {
 
-// The segments of a scan; false where its launches cannot be numbered.
+// The segments of a scan; false where its launches cannot be numbered, or its
+// rows or tokens not within a chunk's 32-bit offsets or an int.
 bool scan_plan(const replay_config &c, int32_t T, int32_t max_len, int *nseg, int *seg_len, size_t *bytes) {
+    if ((int64_t)c.heads * c.head_dim > kMaxRow || (int64_t)c.groups * c.state_dim > kMaxRow || T > 1 << 30) return false;
     *nseg = scan_segments(c.head_dim, c.state_dim, c.batch, c.heads, c.groups, c.io_dtype == REPLAY_BF16, T, max_len,
                           seg_len);
     const int64_t bh = (int64_t)c.batch * c.heads;
     const size_t slots = (size_t)bh * (*nseg - 1);
     *bytes = slots * ((size_t)c.head_dim * c.state_dim + 1) * sizeof(float);
-    return (bh + 8 * (int64_t)c.heads) * (*nseg > 16 ? *nseg : 16) <= INT32_MAX;
+    return launch_fits((bh + 8 * (int64_t)c.heads) * *nseg, 4 * c.head_dim);   // a wavefront 16 columns of a head, or more
 }
 
 }  // namespace
@@ -861,7 +867,7 @@ namespace {
 
 replay_status check_sample(int32_t B, int32_t W, int32_t V) {
     if (B < 1 || W < 1 || V < 1) return REPLAY_ERR_INVALID_ARG;
-    if (V > kMaxVocab || (int64_t)B * W > INT32_MAX) return REPLAY_ERR_UNSUPPORTED;
+    if (V > kMaxVocab || !launch_fits((int64_t)B * W, kSampleNT)) return REPLAY_ERR_UNSUPPORTED;
     return REPLAY_OK;
 }
 

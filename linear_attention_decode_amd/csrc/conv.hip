@@ -14,6 +14,11 @@
 // element against a read and a write of it.  A thread owns 16 bytes of
 // channels and keeps their taps and the last K - 1 rows in registers, so
 // every row is read once (plus K - 1 rows of halo per kTile).
+//
+// Measured (bf16, K = 4, 10240 channels, 128 heads, with dt and a): a
+// prompt batch of 15013 tokens 167 us, 3.8 TB/s of its 635 MB (a large copy
+// reaches 4.85); single tokens of 256 sequences 9.6 us, 3.3 TB/s of 32 MB,
+// and of one 3.6 us, a launch and one chain of loads.
 #include "device_common.h"
 #include "prompt.h"
 
@@ -379,7 +384,7 @@ hipError_t launch_one(const ConvArgs &a, bool step, hipStream_t s) {
     const int64_t gates = !a.dt_raw ? 0 : step ? ((int64_t)a.T * a.H + nt - 1) / nt : ((int64_t)a.T + 63) / 64;
     const bool share = step && a.W == 1 && a.B * cb >= kManyGroups;
     const int64_t blocks = (share ? (a.B + kShare - 1) / kShare : a.B) * cb + tiles * cb + gates;
-    if (blocks > INT32_MAX) return hipErrorInvalidValue;
+    if (!launch_fits(blocks, nt)) return hipErrorInvalidConfiguration;
     if (!step)
         conv_prompt_kernel<BF16, AL, K><<<(unsigned)blocks, kNT, 0, s>>>(a, (int)cb, (int)tiles);
     else if (share)

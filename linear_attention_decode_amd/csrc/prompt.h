@@ -7,6 +7,13 @@
 
 namespace replay {
 
+// A launch numbers its threads, over all workgroups, in 32 bits.
+inline bool launch_fits(int64_t blocks, int64_t threads) { return blocks <= (int64_t)UINT32_MAX / threads; }
+
+// Most values in a row of x, q, k, v or y: 64 rows, a chunk of the scan, then
+// stay within 32-bit byte offsets.
+constexpr int64_t kMaxRow = 1 << 24;
+
 // The inputs of the recurrence from projected rows (conv.hip): T packed rows
 // of a prompt batch, or T = B W rows of a step or round.
 struct ConvArgs {
@@ -56,12 +63,14 @@ struct SampleArgs {
     void *ws;
 };
 constexpr int kMaxVocab = 1 << 18;
+constexpr int kSampleNT = 512;   // threads of a row, a workgroup each
 
 // Launchers (return hipSuccess or the launch error).
 hipError_t launch_sample(const SampleArgs &a, hipStream_t s);
 size_t sample_workspace(int B, int W, int V);
 hipError_t launch_scan(int P, int N, const ScanArgs &a, hipStream_t s);
 int scan_segments(int P, int N, int B, int H, int G, bool bf16, int T, int max_len, int *seg_len);   // the number of segments, and their length
+// hipErrorInvalidConfiguration: more workgroups than a launch numbers
 hipError_t launch_conv_prompt(const ConvArgs &a, hipStream_t s);
 hipError_t launch_conv_step(const ConvArgs &a, hipStream_t s);
 

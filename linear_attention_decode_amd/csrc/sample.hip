@@ -23,6 +23,14 @@
 // alone, thousands of equal logits, k past 2048) take a histogram of the
 // steps over all tokens, and where its last step is too full to sort, a radix
 // selection over the composite's digits.
+//
+// Bound by the chain of steps of a row (two passes, a dozen barriers, sorts of
+// few tokens) and by the float64 exponentials, more than by reading the
+// logits.  Rows of 131072 in bf16, 256 of them, all filters on: 38 us, 1.8
+// TB/s of 67 MB (the copy rate would take 14 us); top-k of 50 alone 29 us, of
+// 1000 37 us; top-p of .98 alone 164 us and no filter 78 us, where every
+// token's weight is computed and every token counts.  One row 22 us.  512
+// threads a row: 1024 leave half the registers, and spill.
 #include "device_common.h"
 #include "prompt.h"
 
@@ -30,7 +38,7 @@ namespace replay {
 
 namespace {
 
-constexpr int kNT = 512, kWaves = kNT / 64;   // 1024 threads would have 128 registers each, 50 too few
+constexpr int kNT = kSampleNT, kWaves = kNT / 64;   // 1024 threads would have 128 registers each, 50 too few
 constexpr int kBins = kNT;       // steps of the distance to the maximum, 1/16 of a temperature each; the last takes the rest
 constexpr float kSteps = kBins / 32;   // steps of a temperature
 constexpr int kList = 4096;      // tokens sorted in LDS

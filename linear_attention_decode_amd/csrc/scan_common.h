@@ -28,7 +28,7 @@ __device__ __forceinline__ bool find_place(const ScanArgs &a, int HB, Place *p) 
     p->b = (int)(unit / a.G / a.nseg);
     if (a.B > 1 && a.B <= 64) {
         const int lane = threadIdx.x & 63;
-        const int len = lane < a.B ? a.cu[lane + 1] - a.cu[lane] : 0;
+        const int len = lane < a.B ? (int)((uint32_t)a.cu[lane + 1] - (uint32_t)a.cu[lane]) : 0;
         int rank = 0;
         for (int o = 0; o < a.B; ++o) {
             const int other = __builtin_amdgcn_readlane(len, o);

@@ -235,3 +235,16 @@ def test_refusals():
             lad.replay_sample(x, u, tok, **kw)
     with pytest.raises(lad.ReplayError, match="status 2"):
         lad.replay_sample(torch.zeros((1, 1, (1 << 18) + 1), device=gu.DEV), u[:1, :1].contiguous(), tok[:1, :1].contiguous())
+
+
+def test_one_position_rejects_nothing():
+    lad = _lad()
+    gu.note("sample one position with drafts")
+    x = torch.randn(37, 1, 100, device=gu.DEV)
+    x[3] = float("nan")
+    u = torch.rand(37, 1, device=gu.DEV)
+    tokens = torch.empty(37, 1, dtype=torch.int32, device=gu.DEV)
+    reject = torch.full((37,), 9, dtype=torch.int32, device=gu.DEV)
+    lad.replay_sample(x, u, tokens, fed=torch.zeros_like(tokens), n_reject=reject)
+    torch.cuda.synchronize()
+    assert bool((reject == 0).all()) and int(tokens[3, 0]) == -1

@@ -303,3 +303,42 @@ def test_refusals():
     p.y = p.y.float()
     with pytest.raises(lad.ReplayError):
         p.run()
+
+
+@pytest.mark.parametrize("N", [64, 128])
+@pytest.mark.parametrize("H,G", [(3, 1), (3, 3), (5, 1)])
+@pytest.mark.parametrize("lens", [[63, 1, 64, 65, 0, 100], [700, 3]])
+def test_odd_heads_per_group(lens, H, G, N):
+    """64-wide heads in bf16 go two to a workgroup; groups of an odd number of heads, one."""
+    gu.note(f"scan odd heads {lens} H={H} G={G} N={N}")
+    p = Prompts(lens, H, G, 64, N, "bf16", first=2, seed=H + N + sum(lens))
+    p.run()
+    torch.cuda.synchronize()
+    p.check()
+
+
+@pytest.mark.parametrize("H,G,P,N", [(3, 1, 64, 64), (3, 3, 64, 128), (2, 1, 128, 128)])
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+def test_nan_stays_in_its_column(value, H, G, P, N):
+    gu.note(f"scan {value} H={H} G={G} P={P} N={N}")
+    p, clean = (Prompts([90, 20], H, G, P, N, "bf16", seed=5) for _ in range(2))
+    p.v[37, H - 1, 40] = value
+    p.run()
+    clean.run()
+    torch.cuda.synchronize()
+    assert not p.y[37:90, H - 1, 40].isfinite().any() and not p.s_out[0, H - 1, 40].isfinite().all()
+    p.y[37:90, H - 1, 40] = clean.y[37:90, H - 1, 40]
+    p.s_out[0, H - 1, 40] = clean.s_out[0, H - 1, 40]
+    assert torch.equal(p.y[:110], clean.y[:110]) and torch.equal(p.s_out, clean.s_out)
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("B", [63, 64, 65, 130])
+def test_many_sequences(io, B):
+    """Around the number of sequences that are put in order of their lengths; equal lengths, and none, among them."""
+    gu.note(f"scan of {B} sequences {io}")
+    lens = [(7 * b * b) % 41 for b in range(B)]
+    p = Prompts(lens, 2, 1, 64, 64, io, seed=B)
+    p.run()
+    torch.cuda.synchronize()
+    p.check()

@@ -159,3 +159,28 @@ def test_sample_settings_refusals(lad, name):
     n = ctypes.c_size_t()
     assert lad.lib.replay_sample_workspace(0, 1, 1, ctypes.byref(n)) == 1
     assert lad.lib.replay_sample_workspace(1, 1, 1, None) == 1
+
+
+@pytest.mark.parametrize("io", [0, 1])
+def test_scan_limits(lad, io):
+    """Rows that a chunk's 32-bit offsets do not reach, tokens an int does not count, workgroups a launch does not number."""
+    for kw, T in ((dict(heads=1 << 18, groups=2), 64), (dict(heads=1 << 18, groups=1 << 18), 64),
+                  (dict(batch=1, heads=2), (1 << 30) + 1), (dict(batch=1 << 20, heads=64), 64)):
+        cfg, n = _cfg(lad, io_dtype=io, **kw), ctypes.c_size_t()
+        if T == 64 and "batch" not in kw:
+            cfg.heads = cfg.heads * 2          # H P = 2^25
+        assert _scan(lad, cfg=cfg, T=T, most=T, s_in=None) == 2, kw
+        assert lad.lib.replay_scan_workspace(ctypes.byref(cfg), T, T, ctypes.byref(n)) == 2, kw
+    n = ctypes.c_size_t()
+    assert lad.lib.replay_scan_workspace(ctypes.byref(_cfg(lad, io_dtype=io, batch=1, heads=2)), 1 << 30, 1 << 30,
+                                         ctypes.byref(n)) == 0
+
+
+def test_launch_limits(lad):
+    """More workgroups than a launch numbers (its threads in 32 bits)."""
+    assert _prompt(lad, T=(1 << 31) - 1) == 2
+    assert _step(lad, cfg=_cfg(lad, batch=1 << 27), W=8) == 2
+    assert _sample(lad, B=1 << 23, W=1) == 2
+    n = ctypes.c_size_t()
+    assert lad.lib.replay_sample_workspace(1 << 22, 2, 8, ctypes.byref(n)) == 2
+    assert lad.lib.replay_sample_workspace((1 << 23) - 1, 1, 8, ctypes.byref(n)) == 0
