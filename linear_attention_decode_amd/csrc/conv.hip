@@ -13,11 +13,11 @@
 // Both kernels are bound by HBM: a handful of FMAs and one exponential per
 // element against a read and a write of it.  A thread owns 16 bytes of
 // channels and keeps their taps and the last K - 1 rows in registers, so
-// every row is read once (plus K - 1 rows of halo per kTile).
+// every row is read once (plus K - 1 rows of halo per tile).
 //
 // Measured (bf16, K = 4, 10240 channels, 128 heads, with dt and a): a
-// prompt batch of 15013 tokens 167 us, 3.8 TB/s of its 635 MB (a large copy
-// reaches 4.85); single tokens of 256 sequences 9.6 us, 3.3 TB/s of 32 MB,
+// prompt batch of 15013 tokens 134 us, 4.75 TB/s of its 635 MB (a large copy
+// reaches 4.85), 154 us out of projection rows of 18560; single tokens of 256 sequences 9.6 us, 3.3 TB/s of 32 MB,
 // and of one 3.6 us, a launch and one chain of loads.
 #include "device_common.h"
 #include "prompt.h"
@@ -26,10 +26,18 @@ namespace replay {
 
 namespace {
 
-constexpr int kTile = 32;     // prompt tokens per workgroup: 9 % of halo, read again from the L2
+// Prompt tokens per workgroup; their K - 1 rows of halo come from the L2.
+// 15013 tokens x 10240 channels in bf16: tiles of 8, 16 and 32 take 144, 134
+// and 141 us (204, 154 and 148 us out of wider projection rows).  Tiles of 8 where those of 16 would not give every CU one: 203
+// tokens then take 6.0 us, not 7.9; at 1024, past that, both take 14.8.
+constexpr int kTile = 16, kShortTile = 8, kCUs = 256;
 constexpr int kNT = 256;      // threads of a prompt workgroup
 constexpr int kStepNT = 64;   // threads of a step workgroup: one sequence's channels spread over many CUs
 constexpr int kAhead = 8;     // rows a thread loads before it uses the first
+// (token, head) pairs of a prompt workgroup that makes dt and a, 4 a thread:
+// its exponentials and logarithms are a chain, and 32 of them (64 tokens of
+// 128 heads) took 25 us, the whole time of a short prompt.
+constexpr int kGates = 1024;
 
 // 16 bytes of io elements as floats, by one load where the row is 16-byte
 // aligned and element by element otherwise.
@@ -160,11 +168,11 @@ __device__ __forceinline__ uint64_t token_mask(const int32_t *cu, int B, int T, 
 
 // Workgroups: [0, B CB) one sequence's first K - 1 tokens and its state (the
 // only ones that read or write it, each thread its own channels: state_in
-// and state_out may be the same buffer), then one tile of kTile packed
+// and state_out may be the same buffer), then one tile of `tile` packed
 // tokens each (tokens from the K - 1st of their sequence on, whose history
-// is in x), then 64 tokens' dt and a each.
+// is in x), then `gate` tokens' dt and a each.
 template <bool BF16, bool AL, int K>
-__global__ __launch_bounds__(kNT) void conv_prompt_kernel(ConvArgs a, int CB, int tiles) {
+__global__ __launch_bounds__(kNT) void conv_prompt_kernel(ConvArgs a, int CB, int tiles, int tile, int gate) {
     constexpr int E = BF16 ? 8 : 4;
     int id = blockIdx.x;
     if (id < a.B * CB) {
@@ -223,9 +231,9 @@ __global__ __launch_bounds__(kNT) void conv_prompt_kernel(ConvArgs a, int CB, in
     }
     id -= a.B * CB;
     if (id < tiles * CB) {
-        const int t0 = (id / CB) * kTile, c0 = ((id % CB) * kNT + (int)threadIdx.x) * E;
+        const int t0 = (id / CB) * tile, c0 = ((id % CB) * kNT + (int)threadIdx.x) * E;
         const uint64_t mask = token_mask(a.cu, a.B, a.T, t0, K - 1);
-        if (c0 >= a.C || !(mask & ((1ull << kTile) - 1))) return;
+        if (c0 >= a.C || !(mask & ((1ull << tile) - 1))) return;
         Channels<BF16, K> ch;
         ch.init(a, c0);
         Row<BF16, AL> halo[K - 1], ahead[kAhead];
@@ -242,11 +250,11 @@ __global__ __launch_bounds__(kNT) void conv_prompt_kernel(ConvArgs a, int CB, in
         }
 #pragma unroll
         for (int j = 0; j < K - 1; ++j) halo[j].widen(hist[j]);
-        for (int i0 = 0; i0 < kTile; i0 += kAhead) {
+        for (int i0 = 0; i0 < tile; i0 += kAhead) {
             Row<BF16, AL> cur[kAhead];
 #pragma unroll
             for (int i = 0; i < kAhead; ++i) cur[i] = ahead[i];
-            if (i0 + kAhead < kTile) {
+            if (i0 + kAhead < tile) {
 #pragma unroll
                 for (int i = 0; i < kAhead; ++i) {
                     const int t = t0 + i0 + kAhead + i;
@@ -264,9 +272,9 @@ __global__ __launch_bounds__(kNT) void conv_prompt_kernel(ConvArgs a, int CB, in
         return;
     }
     id -= tiles * CB;
-    const int t0 = id * 64;
+    const int t0 = id * gate;
     const uint64_t mask = token_mask(a.cu, a.B, a.T, t0, 0);
-    for (int i = threadIdx.x; i < 64 * a.H; i += kNT)
+    for (int i = threadIdx.x; i < gate * a.H; i += kNT)
         if ((mask >> (i / a.H)) & 1) discretise<BF16>(a, (size_t)t0 + i / a.H, i % a.H);
 }
 
@@ -380,13 +388,15 @@ hipError_t launch_one(const ConvArgs &a, bool step, hipStream_t s) {
     constexpr int E = BF16 ? 8 : 4;
     const int64_t nt = step ? kStepNT : kNT;
     const int64_t cb = (a.C / E + nt - 1) / nt;
-    const int64_t tiles = step ? 0 : ((int64_t)a.T + kTile - 1) / kTile;
-    const int64_t gates = !a.dt_raw ? 0 : step ? ((int64_t)a.T * a.H + nt - 1) / nt : ((int64_t)a.T + 63) / 64;
+    const int tile = ((int64_t)a.T + kTile - 1) / kTile * cb < kCUs ? kShortTile : kTile;
+    const int64_t tiles = step ? 0 : ((int64_t)a.T + tile - 1) / tile;
+    const int gate = kGates / a.H < 1 ? 1 : (kGates / a.H > 64 ? 64 : kGates / a.H);
+    const int64_t gates = !a.dt_raw ? 0 : step ? ((int64_t)a.T * a.H + nt - 1) / nt : ((int64_t)a.T + gate - 1) / gate;
     const bool share = step && a.W == 1 && a.B * cb >= kManyGroups;
     const int64_t blocks = (share ? (a.B + kShare - 1) / kShare : a.B) * cb + tiles * cb + gates;
     if (!launch_fits(blocks, nt)) return hipErrorInvalidConfiguration;
     if (!step)
-        conv_prompt_kernel<BF16, AL, K><<<(unsigned)blocks, kNT, 0, s>>>(a, (int)cb, (int)tiles);
+        conv_prompt_kernel<BF16, AL, K><<<(unsigned)blocks, kNT, 0, s>>>(a, (int)cb, (int)tiles, tile, gate);
     else if (share)
         conv_step_kernel<BF16, AL, K, kShare><<<(unsigned)blocks, kStepNT, 0, s>>>(a, (int)cb);
     else
