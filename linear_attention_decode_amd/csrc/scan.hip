@@ -27,6 +27,8 @@
 // chunk's steps behind the other.
 #include "scan_common.h"
 
+#include <algorithm>
+
 namespace replay {
 
 namespace {
@@ -285,11 +287,25 @@ __global__ __launch_bounds__(256) void scan_join_kernel(ScanArgs s, int tile4) {
     f32x4 *ws = reinterpret_cast<f32x4 *>(s.ws) + (size_t)bh * (s.nseg - 1) * tile4 + e;
     f32x4 x = {0.f, 0.f, 0.f, 0.f};
     if (s.s_in) x = reinterpret_cast<const f32x4 *>(s.s_in)[(size_t)bh * tile4 + e];
-    for (int seg = 0; seg + 1 < s.nseg; ++seg) {
-        const Span sp = find_span(s, b, seg);
-        if (!sp.run || sp.last) return;
-        x = s.ws_decay[(size_t)bh * (s.nseg - 1) + seg] * x + ws[(size_t)seg * tile4];
-        ws[(size_t)seg * tile4] = x;
+    if (!find_span(s, b, 0).run) return;
+    const int ends = (s.cu[b + 1] - s.cu[b] - 1) / s.seg_len;   // segments that are followed by another
+    const float *decay = s.ws_decay + (size_t)bh * (s.nseg - 1);
+    constexpr int U = 8;   // segments whose states are loaded together
+    for (int seg0 = 0; seg0 < ends; seg0 += U) {
+        f32x4 own[U];
+        float d[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int seg = seg0 + u < ends ? seg0 + u : ends - 1;
+            own[u] = ws[(size_t)seg * tile4];
+            d[u] = decay[seg];
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (seg0 + u >= ends) break;
+            x = d[u] * x + own[u];
+            ws[(size_t)(seg0 + u) * tile4] = x;
+        }
     }
 }
 
@@ -315,19 +331,24 @@ hipError_t launch_kernel(int P, int N, const ScanArgs &a, bool state_only, hipSt
 }  // namespace
 
 // Segments of a sequence, where the workgroups of whole sequences leave CUs
-// without work: as many as give every CU a few, none shorter than
-// kMinSegment tokens, since a segment costs a second reading of its k and v
-// and a state.  The float32 kernel, whose matrix instructions take most of
-// its time, gains from evener shares: 1999 ragged tokens of 32 heads of 128 x
-// 128 take 120 us at (1024, 192) and 150 us at (512, 256); 8192 tokens of 128
-// heads in bf16 take 226 us and 208 us.
+// without work.  A segment costs a second reading of its k and v and a state
+// that is written, joined and read; what it saves is the chain of chunks, 4
+// to 5 us each.  Two are never worth it: both passes over a half are as long
+// as one over the whole.  So: as many as give a CU one workgroup, of a chunk
+// or more, and up to two (float32, whose matrix instructions take most of its
+// time and gain from evener shares: four) while segments stay long.  Measured
+// against segments of 256 (192) tokens or more alone: one prompt of 512 tokens,
+// 24 heads of 64 x 128, bf16 41 -> 26 us, float32 82 -> 35; 2048 tokens of 8
+// heads of 64 x 64, bf16 30 -> 22; four of 512 tokens, 128 heads, unsplit 45
+// us, in two 75.  Below the shortest lengths here whole sequences are as fast
+// (320 tokens of 128 heads, bf16: 29 us, in three segments 36).
 int scan_segments(int P, int N, int B, int H, int G, bool bf16, int T, int max_len, int *seg_len) {
-    const int kEnough = bf16 ? 512 : 1024, kMinSegment = bf16 ? 256 : 192;
     const int longest = max_len < T ? max_len : T;
     const int64_t groups = (int64_t)B * H / (bf16 ? scan_mx_heads(P, H, G) : 1);
-    int64_t n = groups >= kEnough ? 1 : (kEnough + groups - 1) / groups;
-    if (n > longest / kMinSegment) n = longest / kMinSegment;
-    if (n < 1) n = 1;
+    const int64_t even = std::min<int64_t>((bf16 ? 512 : 1024) / groups, longest / (bf16 ? 256 : 192));
+    const int64_t chain = std::min<int64_t>(256 / groups, longest / kScanChunk);
+    int64_t n = std::max(even, chain);
+    if (n < 3 || longest < (bf16 ? 384 : 192)) n = 1;
     const int64_t len = (longest + n - 1) / n;
     *seg_len = (int)((len + kScanChunk - 1) / kScanChunk * kScanChunk);
     return (int)((longest + *seg_len - 1) / *seg_len);

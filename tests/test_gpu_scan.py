@@ -342,3 +342,17 @@ def test_many_sequences(io, B):
     p.run()
     torch.cuda.synchronize()
     p.check()
+
+
+@pytest.mark.parametrize("io,lens,H,G,P,N", [
+    ("bf16", [384], 2, 1, 64, 64), ("bf16", [383, 2], 2, 1, 64, 64), ("f32", [192, 191], 1, 1, 64, 64),
+    ("f32", [193], 1, 1, 16, 16), ("bf16", [2049, 64, 65, 0], 8, 1, 64, 64), ("bf16", [1537], 1, 1, 128, 128),
+    ("f32", [1300, 1299], 2, 2, 16, 16)])
+def test_segments_of_a_chunk(io, lens, H, G, P, N):
+    """Around the lengths from which few heads are split, into segments as short as a chunk; more than eight of them."""
+    gu.note(f"scan short segments {lens} H={H} P={P} N={N} {io}")
+    p = Prompts(lens, H, G, P, N, io, seed=sum(lens) + H)
+    ws = p.run()
+    torch.cuda.synchronize()
+    assert (ws is None) == (max(lens) == 383)
+    p.check()
