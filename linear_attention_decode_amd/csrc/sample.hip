@@ -21,15 +21,16 @@
 // step (of 1/16 of a temperature) where it does; for k = 50 that gathers some
 // 60 tokens, for k = 1000 some 1400.  Rows that this does not settle (top-p
 // alone, thousands of equal logits, k past 2048) take a histogram of the
-// steps over all tokens, and where its last step is too full to sort, a radix
-// selection over the composite's digits.
+// steps over all tokens and gather the step that the prefix ends in, and
+// where that is too full to sort, a radix selection over the composite's
+// digits.
 //
 // Bound by the chain of steps of a row (two passes, a dozen barriers, sorts of
 // few tokens) and by the float64 exponentials, more than by reading the
 // logits.  Rows of 131072 in bf16, 256 of them, all filters on: 38 us, 1.8
-// TB/s of 67 MB (the copy rate would take 14 us); top-k of 50 alone 29 us, of
-// 1000 37 us; top-p of .98 alone 164 us and no filter 78 us, where every
-// token's weight is computed and every token counts.  One row 22 us.  512
+// TB/s of 67 MB (the copy rate would take 14 us); top-k of 50 alone 27 us, of
+// 1000 34 us, of 5000 113 us; top-p of .98 alone 175 us and no filter 71 us,
+// where every token's weight is computed and every token counts.  One row 22 us.  512
 // threads a row: 1024 leave half the registers, and spill.
 #include "device_common.h"
 #include "prompt.h"
@@ -54,6 +55,8 @@ struct Lds {
     uint32_t count[kBins];
     uint64_t wave[kWaves];
     uint64_t pick[4];
+    uint64_t k_step, k_mass;     // the step that a k past the list ends in, and what its prefix weighs in it
+    uint64_t p_want;             // what top-p asks for behind such a k
     u32x4 edge[2];               // the row's first and last block, where they are not whole
     uint32_t n, listed, flag;
 };
@@ -628,31 +631,42 @@ __global__ __launch_bounds__(kNT) void sample_kernel(SampleArgs a) {
     uint64_t want = 0;         // what the prefix of step `step` weighs in it
     int step = -1;
     bool cut_k = by_k, cut_p = by_p;   // what the list is still to be cut by
-    // 0: the list as found above; 1: as a histogram of the row says; 2: the prefix is known
-    for (int stage = 0; stage < 3; ++stage) {
+    bool k_known = false, p_known = false;   // the end of a k past the list, of top-p: found in its step
+    // 0: the list as found above; 1: as a histogram of the row says; 2: top-p behind such a k; 3: the prefix is known
+    for (int stage = 0; stage < 4; ++stage) {
         const int tid = thread();
-        if (stage == 1) {
-            if (!by_k && !by_p) break;
-            histogram(l, row, !by_k, top, rate, scale);
-            const uint64_t v = by_k ? l.count[tid] : l.mass[tid];
+        if (stage == 1 || stage == 2) {
+            if (stage == 1 && !by_k && !by_p) break;
+            if (stage == 2 && !(by_p && k_known)) continue;
+            const bool count = stage == 1 && by_k;
+            histogram(l, row, !count, top, rate, scale);
+            const uint64_t v = count ? l.count[tid] : l.mass[tid];
             uint64_t all;
             const uint64_t ahead = before(l, v, &all);
-            want = by_k ? (uint64_t)k : share_of(p, all);
+            if (stage == 2) {   // the k's whole weight
+                if (tid == (int)l.k_step) l.pick[2] = ahead + l.k_mass;
+                __syncthreads();
+                all = l.pick[2];
+            }
+            want = count ? (uint64_t)k : share_of(p, all);
+            if (tid == 0) l.p_want = want;
             if (ahead < want && want <= ahead + v) {
                 l.pick[0] = tid;
                 l.pick[1] = ahead;
             }
             __syncthreads();
             const int s = (int)l.pick[0];
-            if (!by_k) {
+            step = -1;
+            if (!count || k > kList) {
                 step = s;
                 want -= l.pick[1];
             }
             low = s < kBins - 1 ? below(top, (float)(s + 1) / rate) : -3.402823466e+38f;
             __syncthreads();
-        } else if (stage == 2) {
-            if (last == ~0ull) {   // too full to sort: by digits
-                if (by_k) {
+        } else if (stage == 3) {
+            if (last == ~0ull || (by_p && k_known && !p_known)) {   // too full to sort: by digits
+                want = l.p_want;
+                if (last == ~0ull && by_k) {
                     const Cut cut = radix_cut(l, row, false, dtop, scale, (uint64_t)k);
                     last = cut.last;
                     want = share_of(p, cut.mass);
@@ -697,7 +711,9 @@ __global__ __launch_bounds__(kNT) void sample_kernel(SampleArgs a) {
         const float peak = step < 0 ? top : top - (float)step / rate;
         const float fine = fminf(fmaxf((float)(kBins - 1) / (peak - low), rate), 3e38f);
         uint64_t c[kEach], v[kEach], sum = 0, mass;
-        const bool cut = (cut_k && k < n) || cut_p;
+        const bool do_k = step < 0 ? cut_k && k < n : stage == 1 && by_k, do_p = step < 0 ? cut_p : !do_k;
+        if (step >= 0 && do_k && want > (uint64_t)n) continue;   // it ends among -infinities, which are not gathered
+        const bool cut = do_k || do_p;
         if (cut) {
             l.count[tid] = 0;
             l.mass[tid] = 0;
@@ -722,13 +738,21 @@ __global__ __launch_bounds__(kNT) void sample_kernel(SampleArgs a) {
             (void)before(l, sum, &mass);
 #pragma unroll 1
             for (int by = 0; by < 2; ++by) {
-                if (by == 0 ? !(cut_k && k < n) : !cut_p) continue;
+                if (by == 0 ? !do_k : !do_p) continue;
                 const Cut end = list_cut(l, n, by == 1, top, peak, fine, scale,
-                                         by == 0 ? (uint64_t)k : (step >= 0 ? want : share_of(p, mass)));
+                                         step >= 0 ? want : (by == 0 ? (uint64_t)k : share_of(p, mass)));
                 last = end.last < last ? end.last : last;
                 mass = end.mass;
             }
-            if (step >= 0) continue;   // that was the prefix's end; the list is not the whole prefix
+            if (step >= 0) {   // that was the prefix's end; the list is not the whole prefix
+                if (do_k && tid == 0) {
+                    l.k_step = (uint64_t)step;
+                    l.k_mass = mass;
+                }
+                k_known = by_k;
+                p_known = do_p;
+                continue;
+            }
         }
         sum = 0;
 #pragma unroll

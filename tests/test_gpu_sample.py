@@ -248,3 +248,20 @@ def test_one_position_rejects_nothing():
     lad.replay_sample(x, u, tokens, fed=torch.zeros_like(tokens), n_reject=reject)
     torch.cuda.synchronize()
     assert bool((reject == 0).all()) and int(tokens[3, 0]) == -1
+
+
+@pytest.mark.parametrize("io,V", [("bf16", 131072), ("f32", 50021), ("f32", 2049), ("bf16", 20011)])
+def test_top_k_past_the_list(io, V):
+    """A k of thousands, with and without the other filters; a k that ends among masked tokens, or in a step of many."""
+    r = np.random.default_rng(V + 1)
+    gu.note(f"sample large k V={V} {io}")
+    x = _logits(r, 9, V)
+    x[5, r.permutation(V)[:V - V // 8]] = -np.inf      # an eighth is left
+    x[6] = np.where(r.uniform(0, 1, V) < 0.3, x[6], -np.inf)
+    x[7] = np.round(x[7] * 2) / 2                      # steps of thousands
+    x[8, :V // 2] = -1e30                              # half of it beyond the last step
+    rows = Rows(x, io)
+    n = 9
+    for k in (2048, 2049, 2500, V // 3, V // 2 + 7, V - 1):
+        for T, p, mp in ((1, 1, 0), (0.7, 0.95, 0), (2.5, 0.999, 0), (1.3, 1, 1e-4), (4, 0.5, 1e-3)):
+            rows.run(r.uniform(0, 1, n), T, np.full(n, k), p, mp).check((k, T, p, mp))
