@@ -309,6 +309,7 @@ class ReplayConv:
         self.heads = None if heads is None else heads[0]
         self.tensors = (weight, bias, dt_bias, a_log)
         f32, gpu = torch.float32, _gpu()
+        self.gpu = gpu
         self.params = ReplayConvParams(
             self.width, self.slots, int(bool(silu)), _want("weight", weight, (channels, self.width), f32, gpu),
             _want("bias", bias, (channels,), f32, gpu), _want("dt_bias", dt_bias, (self.heads,), f32, gpu),
@@ -322,6 +323,8 @@ def _conv_call(what, cfg, conv, n, lead, x, dt_raw, q, k, v, dt, a, io, f32, gpu
     if conv.channels != C or (dt_raw is not None and conv.heads != H):
         raise ReplayError(f"{what}: a convolution of {conv.channels} channels and {conv.heads} heads for a layer of "
                           f"{C} channels and {H} heads")
+    if conv.gpu != gpu:
+        raise ReplayError(f"{what}: the convolution's tensors are on GPU {conv.gpu}, the current one is {gpu}")
     rows = _rows("x", x, n, C, io, gpu) + _rows("dt_raw", dt_raw, n, H, io, gpu)
     outs = (_want("q", q, (*lead, G, N), io, gpu), _want("k", k, (*lead, G, N), io, gpu),
             _want("v", v, (*lead, H, P), io, gpu))

@@ -337,3 +337,16 @@ def test_refusals_of_the_binding():
                              narrow.state, *narrow.outs(2, 5))
     call()
     torch.cuda.synchronize()
+
+
+def test_parameters_of_another_gpu():
+    """Taps that lie on another GPU than the current one are refused: the kernels would read them there."""
+    import copy
+    lad = _lad()
+    gu.note("conv parameters of another GPU")
+    c = Case(6, 2, 4, 2, 16, 16, "bf16", 4, 3, seed=1)
+    pos = torch.zeros(2, dtype=torch.int32, device=gu.DEV)
+    other = copy.copy(c.conv)
+    other.gpu = c.conv.gpu + 1
+    with pytest.raises(lad.ReplayError, match="the current one"):
+        lad.replay_conv_step(c.cfg, other, 3, c.x, c.raw, pos, c.state, *c.outs(2, 3))
