@@ -30,8 +30,8 @@
 // logits.  Rows of 131072 in bf16, 256 of them, all filters on: 38 us, 1.8
 // TB/s of 67 MB (the copy rate would take 14 us); top-k of 50 alone 27 us, of
 // 1000 34 us, of 5000 113 us; top-p of .98 alone 175 us and no filter 71 us,
-// where every token's weight is computed and every token counts.  One row 22 us.  512
-// threads a row: 1024 leave half the registers, and spill.
+// where every token's weight is computed and every token counts.  One row 24
+// us.  512 threads a row: 1024 leave half the registers, and spill.
 #include "device_common.h"
 #include "prompt.h"
 
