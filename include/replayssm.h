@@ -455,7 +455,9 @@ replay_status replay_conv_step(const replay_config *cfg, const replay_conv_param
    a any finite number (0 resets the state).  y: [T][H][P] in the io dtype, as a
    model's next product takes it; rows outside every range are left as they
    are.  With bf16 io the products run on bf16 operands: inputs are taken as
-   they are, sums and states are float32.  y and s_out overlap nothing else
+   they are, the state and the tokens' weights go into y's products as two bf16
+   parts that hold them to 2^-15 of each term, s_out is what float32 products
+   give; sums are float32.  y and s_out overlap nothing else
    that the call reads or writes (s_out over s_in: INVALID_ARG).  T <= 2^30,
    H P and G N <= 2^24.
    A sequence whose range decreases, leaves 0..T or is longer than max_len

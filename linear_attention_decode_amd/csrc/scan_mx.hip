@@ -7,24 +7,24 @@
 // accumulators as S^T, N x 32, float32, for the whole segment.  Per chunk of
 // kQ tokens:
 //   G   the weighted scores, 16 x 16 tiles of K Q^T over the wavefronts, one
-//       product for both heads, weighted for each and kept in LDS as bf16;
+//       product for both heads, weighted for each and kept in LDS;
 //   y   S Q^T decayed, plus V^T G^T, both into the y^T accumulators;
 //   S   decayed, plus K^T (e V).
-// What is rounded to bf16: the state and G, as operands of y, itself rounded
-// to bf16 (together 1.3 times the error of that last rounding on SiLU-like
-// inputs).  The state is not: e V is cut into three bf16 parts that hold its
-// 24 bits exactly (8 each, by truncation), so S is what float32 products give.
+// What bf16 operands leave out: the state and G enter y's products as two
+// bf16 parts, the upper 8 bits by truncation and the rest rounded, so that a
+// term lacks at most 2^-15 of itself and y is a float32 sum rounded once; the
+// second parts cost 28 us of the 278 below, and without them y had 1.3 times
+// the error of its own rounding.  e V is cut into three parts that hold its
+// 24 bits exactly (8 each), so the state is what float32 products give.
 //
 // What bounds it.  One sequence of 8192 tokens (128 heads, 8 groups, 64 x
-// 128): 74 us for the segments' states, 12 us to join them, 115 us for the
-// outputs, 315 MB in all, 1.6 TB/s.  Sixteen ragged sequences of 15013 tokens
-// from states (703 MB): 250 us, 2.8 TB/s.  With the products left out that
-// launch takes 190 us, with the loads left out 185 us: two workgroups a CU
-// overlap the two in part.  Of its arithmetic a wavefront's chunk is 82 matrix
-// instructions and 774 others, most of them roundings, cuts and decays; the
-// three parts of e V cost 48 us against one bf16 rounding, which would lose
-// the state's float32.  Chunks of 32 tokens with three workgroups a CU take
-// the same 250 us, one workgroup a CU 332 us; the float32 kernel 1677 us.
+// 128): 209 us, of which 65 for the segments' states and 11 to join them, 315
+// MB in all, 1.5 TB/s.  Sixteen ragged sequences of 15013 tokens from states
+// (703 MB): 278 us, 2.5 TB/s.  A wavefront's chunk is 104 matrix instructions
+// and 893 others, most of them cuts, roundings and decays, and two workgroups
+// a CU overlap these with the loads in part.  The second and third part of e V
+// cost 48 us, and would lose the state's float32; the float32 kernel takes
+// 1677 us.
 //
 // Layouts.  A 32 x 32 accumulator tile holds in lane (column c, half hh)
 // rows 8 (r / 4) + 4 hh + r % 4; an operand of 16 steps holds in the same
@@ -142,10 +142,15 @@ struct Decays {
     float tot[4];    // a 16-tile's whole product
 };
 
-template <int P, int N, int VW>
+// STATE_ONLY needs neither q nor G.
+template <int P, int N, int VW, bool STATE_ONLY>
 struct Tile {
     using Sh = Shape<P, N, VW>;
-    __align__(16) uint8_t q[kQ * Sh::QB], k[kQ * Sh::QB], v[kQ * Sh::VB], g[Sh::HB][kQ * Sh::GB];
+    __align__(16) uint8_t k[kQ * Sh::QB], v[kQ * Sh::VB], q[STATE_ONLY ? 16 : kQ * Sh::QB];
+    // G's upper parts in rows 0..63, a token each; the lower parts of tokens
+    // 0..31, which weigh no more than 32, behind their upper ones, those of
+    // tokens 32..63 in rows 64..95
+    uint8_t g[Sh::HB][STATE_ONLY ? 16 : (kQ + 32) * Sh::GB];
     Decays d[Sh::HB];
 };
 
@@ -187,7 +192,7 @@ struct Ahead {
         a = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rda, oa, 0, 0));
         dt = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rdt, oa, 0, 0));
     }
-    __device__ __forceinline__ void store(Tile<P, N, VW> &m, int n) {
+    __device__ __forceinline__ void store(Tile<P, N, VW, STATE_ONLY> &m, int n) {
         const int tid = threadIdx.x;
 #pragma unroll
         for (int i = 0; i < Sh::IQ; ++i) {
@@ -229,13 +234,17 @@ struct Ahead {
 __device__ __forceinline__ uint32_t upper_pair(float x, float y) {
     return __builtin_amdgcn_perm(__float_as_uint(y), __float_as_uint(x), 0x07060302u);
 }
+// what these leave of x
+__device__ __forceinline__ float below_upper(float x) { return x - __uint_as_float(__float_as_uint(x) & 0xffff0000u); }
+// ... of both, as a bf16 pair
+__device__ __forceinline__ uint32_t lower_pair(float x, float y) { return f32x2_to_bf16_pair(below_upper(x), below_upper(y)); }
 
 // G = the weighted scores, in 16 x 16 tiles (ti, tj) of K Q^T, lane (column i
 // = l % 16, rows j = 4 (l / 16) + r).  A fourth of the work is the diagonal
 // tile x, two below it and, for x = 0 and 2, the one beside it, zero (y's
 // products run over 32 tokens); wavefront w takes x = w (of two: w, w + 2).
 template <int P, int N, int VW>
-__device__ __forceinline__ void weigh(Tile<P, N, VW> &m, int w, int lane) {
+__device__ __forceinline__ void weigh(Tile<P, N, VW, false> &m, int w, int lane) {
     using Sh = Shape<P, N, VW>;
     const int ci = lane & 15, lg = lane >> 4;
     const uint32_t in = opaque(at<Sh::QB>(ci, 16 * lg)), out = opaque(at<Sh::GB>(ci, 8 * lg)), lg4 = opaque(4 * lg);
@@ -289,26 +298,32 @@ __device__ __forceinline__ void weigh(Tile<P, N, VW> &m, int w, int lane) {
 #pragma unroll
                     for (int r = 0; r < 4; ++r) o[r] = below ? d[z][r] * (R * sd[r]) : 0.f;
                 }
-                *reinterpret_cast<u32x2 *>(m.g[y] + ((out + 16 * Sh::GB * ti[z]) ^ (32 * tj[z]))) =
-                    u32x2{f32x2_to_bf16_pair(o[0], o[1]), f32x2_to_bf16_pair(o[2], o[3])};
+                const uint32_t upper = (out + 16 * Sh::GB * ti[z]) ^ (32 * tj[z]);
+                const uint32_t lower = ti[z] < 2 ? upper ^ 64 : upper + 32 * Sh::GB;
+                *reinterpret_cast<u32x2 *>(m.g[y] + upper) = u32x2{upper_pair(o[0], o[1]), upper_pair(o[2], o[3])};
+                *reinterpret_cast<u32x2 *>(m.g[y] + lower) = u32x2{lower_pair(o[0], o[1]), lower_pair(o[2], o[3])};
             }
         }
     }
 }
 
-// Steps 16 x + 8 hh .. of S^T's tile as an operand, x = 0, 1
-__device__ __forceinline__ bf8 state_operand(const acc16 &S, int x) {
-    u32x4 f;
+// Steps 16 x + 8 hh .. of S^T's tile as an operand, x = 0, 1, in two parts
+__device__ __forceinline__ void state_operand(const acc16 &S, int x, bf8 *upper, bf8 *lower) {
+    u32x4 u, l;
 #pragma unroll
-    for (int r = 0; r < 4; ++r) f[r] = f32x2_to_bf16_pair(S[8 * x + 2 * r], S[8 * x + 2 * r + 1]);
-    return __builtin_bit_cast(bf8, f);
+    for (int r = 0; r < 4; ++r) {
+        u[r] = upper_pair(S[8 * x + 2 * r], S[8 * x + 2 * r + 1]);
+        l[r] = lower_pair(S[8 * x + 2 * r], S[8 * x + 2 * r + 1]);
+    }
+    *upper = __builtin_bit_cast(bf8, u);
+    *lower = __builtin_bit_cast(bf8, l);
 }
 
 template <int P, int N, int VW, bool STATE_ONLY>
 __global__ __launch_bounds__((Shape<P, N, VW>::NT), (VW == 128 ? 2 : 1)) void scan_mx_kernel(ScanArgs s) {
     using Sh = Shape<P, N, VW>;
     constexpr int NW = Sh::NW, HB = Sh::HB, TN = N / 32, KN = N / 16;
-    __shared__ Tile<P, N, VW> m;
+    __shared__ Tile<P, N, VW, STATE_ONLY> m;
 
     Place place;
     if (!find_place(s, HB, &place)) return;
@@ -377,9 +392,12 @@ __global__ __launch_bounds__((Shape<P, N, VW>::NT), (VW == 128 ? 2 : 1)) void sc
                     for (int I = 0; I < 2; ++I) q[I][x] = row8(m.q, (qo ^ (32 * (st0 + x))) + 32 * Sh::QB * I);
 #pragma unroll
                 for (int x = 0; x < U; ++x) {
-                    const bf8 sf = state_operand(S[(st0 + x) / 2], x & 1);
+                    bf8 upper, lower;
+                    state_operand(S[(st0 + x) / 2], x & 1, &upper, &lower);
 #pragma unroll
-                    for (int I = 0; I < 2; ++I) y[I] = mma32(sf, q[I][x], y[I]);
+                    for (int I = 0; I < 2; ++I) y[I] = mma32(lower, q[I][x], y[I]);
+#pragma unroll
+                    for (int I = 0; I < 2; ++I) y[I] = mma32(upper, q[I][x], y[I]);
                 }
             }
 #pragma unroll
@@ -409,11 +427,20 @@ __global__ __launch_bounds__((Shape<P, N, VW>::NT), (VW == 128 ? 2 : 1)) void sc
             }
             __syncthreads();
             const uint32_t go = opaque(at<Sh::GB>(c, 16 * hh));
-            bf8 G[6];   // 2 steps for the first 32 tokens, 4 for the others
+            // the first 32 tokens take 2 steps of either part, the others 4
 #pragma unroll
-            for (int x = 0; x < 6; ++x) G[x] = row8(m.g[hb], (go ^ (32 * (x < 2 ? x : x - 2))) + (x < 2 ? 0 : 32 * Sh::GB));
+            for (int rows = 0; rows < 3; ++rows) {
+                bf8 G[4];
 #pragma unroll
-            for (int x = 0; x < 6; ++x) y[x < 2 ? 0 : 1] = mma32(V[x < 2 ? x : x - 2], G[x], y[x < 2 ? 0 : 1]);
+                for (int x = 0; x < 4; ++x) G[x] = row8(m.g[hb], (go ^ (32 * x)) + 32 * Sh::GB * rows);
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    if (rows == 0)
+                        y[0] = mma32(V[x & 1], G[x], y[0]);
+                    else
+                        y[1] = mma32(V[x], G[x], y[1]);
+                }
+            }
             // y: after the exchange of odd and even rows of 16 lanes a store
             // writes 64 bytes of each of 16 tokens.  Through a buffer resource
             // over the chunk's tokens, so that it is not conditional: a wait
@@ -482,7 +509,7 @@ __global__ __launch_bounds__((Shape<P, N, VW>::NT), (VW == 128 ? 2 : 1)) void sc
                 for (int z = 0; z < 3; ++z) {
                     part[z][r] = upper_pair(x[0], x[1]);
 #pragma unroll
-                    for (int u = 0; u < 2; ++u) x[u] -= __uint_as_float(__float_as_uint(x[u]) & 0xffff0000u);
+                    for (int u = 0; u < 2; ++u) x[u] = below_upper(x[u]);
                 }
             }
             bf8 K[TN];

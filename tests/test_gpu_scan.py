@@ -356,3 +356,26 @@ def test_segments_of_a_chunk(io, lens, H, G, P, N):
     torch.cuda.synchronize()
     assert (ws is None) == (max(lens) == 383)
     p.check()
+
+
+@pytest.mark.parametrize("H,G,P,N", [(4, 2, 64, 64), (4, 2, 64, 128), (3, 1, 64, 128), (2, 1, 128, 128)])
+@pytest.mark.parametrize("lens", [[150, 33, 1], [1100]])
+def test_sums_of_either_sign(lens, H, G, P, N):
+    """bf16 io, terms that cancel (q, k, v of either sign, slow decay): y is a float32 sum rounded once.
+
+    The state and the weights enter y's products as two bf16 parts each, the first cut, the second rounded: what they
+    leave out of x is at most 2^-7 |x| of a cut to 8 bits, and of that the 2^-8 of a rounding; 2^-15 of Y with the float32
+    sums' (3 n + N + 64) 2^-24, then the rounding of y itself."""
+    gu.note(f"scan of either sign {lens} H={H} G={G} P={P} N={N}")
+    p = Prompts(lens, H, G, P, N, "bf16", seed=sum(lens) + N + H, decay=lambda r, s: np.exp(-r.uniform(0, 0.02, s)))
+    r = np.random.default_rng(1)
+    for t in (p.q, p.k, p.v):
+        t.copy_(torch.from_numpy(r.standard_normal(tuple(t.shape)).astype(np.float32)).to(p.io))
+    p.run()
+    torch.cuda.synchronize()
+    for b, n in enumerate(lens):
+        rows = slice(int(p.ends[b]) - n, int(p.ends[b]))
+        (y, _), (Y, _) = p.reference(b), p.reference(b, True)
+        e = ((3 * n + N + 64) * E24 + 2.0 ** -15) * Y
+        off = np.abs(p.y[rows].double().cpu().numpy() - y) / (e + 2.0 ** -8 * (np.abs(y) + e) + 1e-37)
+        assert np.all(off <= 1), (b, float(off.max()), float((off > 1).mean()))
