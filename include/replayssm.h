@@ -451,8 +451,11 @@ replay_status replay_conv_step(const replay_config *cfg, const replay_conv_param
    zeros) to the state it leaves in s_out, which replay_load_checkpoint
    takes.  Sequence b holds rows cu_seqlens[b] .. cu_seqlens[b + 1] - 1 of T
    (device int32 [B + 1]), at most max_len of them; a sequence of none leaves
-   its state.  q, k: [T][G][N], v: [T][H][P] (io dtype); dt, a: [T][H] f32,
-   a any finite number (0 resets the state).  y: [T][H][P] in the io dtype, as a
+   its state.  q, k: [T][G][N], v: [T][H][P] (io dtype); dt, a: [T][H] f32.
+   a of 0 resets the state.  Decays of several tokens are multiplied before they
+   meet the state: |a| <= 1 is always right; beyond it the product of a over any
+   consecutive tokens of a sequence, times the dt and the q . k of two of them,
+   has to be finite in float32.  y: [T][H][P] in the io dtype, as a
    model's next product takes it; rows outside every range are left as they
    are.  With bf16 io the products run on bf16 operands: inputs are taken as
    they are, the state and the tokens' weights go into y's products as two bf16

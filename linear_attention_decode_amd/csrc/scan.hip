@@ -12,6 +12,9 @@
 // logarithms: a = 0 (a reset), values that underflow and long chunks are as
 // exact as the recurrence.  D over two tiles of 16 tokens is the product of
 // the later tile's prefix, the earlier one's suffix and the tiles between.
+// Only a's of consecutive tokens are multiplied, and these products have to be
+// finite, as they always are for |a| <= 1: one that overflows has met no state
+// yet, and a state of zero or a reset behind it would make it NaN.
 //
 // A workgroup takes one (sequence, head, segment), wavefront w columns
 // 16 w .. 16 w + 15 of S^T [N][P], which stay in its accumulators for the

@@ -290,9 +290,10 @@ __device__ __forceinline__ void weigh(Tile<P, N, VW, false> &m, int w, int lane)
 #pragma unroll
                     for (int r = 0; r < 4; ++r) o[r] = j0 + r <= i ? d[z][r] * (D[r] * dt[r]) : 0.f;
                 } else {
-                    // a over the tiles between and i's own up to i, times what is behind j in its tile
+                    // a over i's own tile up to i and the tiles between, the nearest first (every product is one
+                    // of consecutive tokens), times what is behind j in its tile
                     const float t1 = dc.tot[(tj[z] + 1) & 3], t2 = dc.tot[(tj[z] + 2) & 3];
-                    const float R = dc.pre[i] * (ti[z] - tj[z] > 1 ? t1 : 1.f) * (ti[z] - tj[z] > 2 ? t2 : 1.f);
+                    const float R = dc.pre[i] * (ti[z] - tj[z] > 2 ? t2 : 1.f) * (ti[z] - tj[z] > 1 ? t1 : 1.f);
                     const f32x4 sd = *reinterpret_cast<const f32x4 *>(&dc.sd[j0]);
                     const bool below = z == 1 || (x & 1);
 #pragma unroll

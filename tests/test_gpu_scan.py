@@ -379,3 +379,34 @@ def test_sums_of_either_sign(lens, H, G, P, N):
         e = ((3 * n + N + 64) * E24 + 2.0 ** -15) * Y
         off = np.abs(p.y[rows].double().cpu().numpy() - y) / (e + 2.0 ** -8 * (np.abs(y) + e) + 1e-37)
         assert np.all(off <= 1), (b, float(off.max()), float((off > 1).mean()))
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("P,N", SHAPES)
+def test_growth_and_decay_in_turns(io, P, N):
+    """Decays far above and below one, whose products over consecutive tokens stay finite (2^96 at most) while those of
+    stretches that lie apart would not; every second chunk starts with a reset."""
+    gu.note(f"scan growth and decay P={P} N={N} {io}")
+    p = Prompts([128, 60], 4, 2, P, N, io, seed=P + N, decay=lambda r, s: r.uniform(0.5, 1.0, s))
+    for s0 in (0, 64, 128):
+        p.a[s0 + 16:s0 + 32], p.a[s0 + 32:s0 + 48], p.a[s0 + 48:s0 + 60] = 64.0, 1 / 64, 64.0
+        p.a[s0 + 60:s0 + 64] = 0.75
+    p.a[64] = 0.0
+    p.a[188:] = float("nan")
+    p.run()
+    torch.cuda.synchronize()
+    p.check()
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("start", [0.0, 1e-10])
+def test_growth_then_a_reset(io, start):
+    """A product of 1e28 over a prompt in segments, from no state and from a small one; then a reset, and growth again."""
+    gu.note(f"scan growth then reset from {start} {io}")
+    p = Prompts([700, 90], 2, 1, 64, 128, io, seed=14, decay=lambda r, s: np.full(s, 1.1))
+    p.s_in.mul_(start)
+    p.v[:500] = 0.0
+    p.a[650] = 0.0
+    assert p.run() is not None
+    torch.cuda.synchronize()
+    p.check()
