@@ -336,10 +336,13 @@ hipError_t launch_kernel(int P, int N, const ScanArgs &a, bool state_only, hipSt
 // Segments of a sequence, where the workgroups of whole sequences leave CUs
 // without work.  A segment costs a second reading of its k and v and a state
 // that is written, joined and read; what it saves is the chain of chunks, 4
-// to 5 us each.  Two are never worth it: both passes over a half are as long
-// as one over the whole.  So: as many as give a CU one workgroup, of a chunk
+// to 5 us each.  Two are never the best: both passes over a half are about as
+// long as one over the whole.  So: as many as give a CU one workgroup, of a chunk
 // or more, and up to two (float32, whose matrix instructions take most of its
-// time and gain from evener shares: four) while segments stay long.  Measured
+// time and gain from evener shares: four) while segments stay long; and where
+// whole chunks would make two of three, segments of one chunk (float32, up to
+// 255 tokens: 224 of 24 heads of 64 x 128 whole 46 us, in two 44, in four 31;
+// of 85 heads of 64 x 64 59, 54, 38).  Measured
 // against segments of 256 (192) tokens or more alone: one prompt of 512 tokens,
 // 24 heads of 64 x 128, bf16 41 -> 26 us, float32 82 -> 35; 2048 tokens of 8
 // heads of 64 x 64, bf16 30 -> 22; four of 512 tokens, 128 heads, unsplit 45
@@ -354,6 +357,7 @@ int scan_segments(int P, int N, int B, int H, int G, bool bf16, int T, int max_l
     if (n < 3 || longest < (bf16 ? 384 : 192)) n = 1;
     const int64_t len = (longest + n - 1) / n;
     *seg_len = (int)((len + kScanChunk - 1) / kScanChunk * kScanChunk);
+    if (n > 1 && longest <= 2 * *seg_len) *seg_len = kScanChunk;
     return (int)((longest + *seg_len - 1) / *seg_len);
 }
 

@@ -410,3 +410,14 @@ def test_growth_then_a_reset(io, start):
     assert p.run() is not None
     torch.cuda.synchronize()
     p.check()
+
+
+@pytest.mark.parametrize("lens,H,G,P,N", [([255, 64, 65, 0], 3, 1, 64, 128), ([224, 223], 2, 2, 128, 128), ([193, 192], 5, 1, 64, 64)])
+def test_four_segments_of_a_short_prompt(lens, H, G, P, N):
+    """float32, between three chunks and four: a segment a chunk, the last of any length."""
+    gu.note(f"scan four segments {lens} H={H} P={P} N={N}")
+    p = Prompts(lens, H, G, P, N, "f32", seed=sum(lens))
+    ws = p.run()
+    torch.cuda.synchronize()
+    assert ws.numel() == 3 * p.B * H * (P * N + 1)
+    p.check()

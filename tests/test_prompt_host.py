@@ -184,3 +184,14 @@ def test_launch_limits(lad):
     n = ctypes.c_size_t()
     assert lad.lib.replay_sample_workspace(1 << 22, 2, 8, ctypes.byref(n)) == 2
     assert lad.lib.replay_sample_workspace((1 << 23) - 1, 1, 8, ctypes.byref(n)) == 0
+
+
+@pytest.mark.parametrize("io", [0, 1])
+@pytest.mark.parametrize("P,N", [(16, 16), (64, 64), (64, 128), (128, 128)])
+def test_no_scan_in_two_segments(lad, io, P, N):
+    """Two segments take two passes over a half: three are the fewest that a plan may have."""
+    for heads in (1, 2, 7, 24, 64, 85, 86, 128, 340):
+        cfg, slot = _cfg(lad, io_dtype=io, batch=1, heads=heads, groups=1, head_dim=P, state_dim=N), heads * (P * N + 1) * 4
+        for most in (*range(1, 1200), 1300, 2047, 2048, 2049, 4096, 8193):
+            need = lad.replay_scan_workspace(cfg, most, most)
+            assert need % slot == 0 and need != slot, (heads, most)
