@@ -351,6 +351,10 @@ __device__ __forceinline__ int step_of(float x, float top, float rate) {
 }
 
 // Histogram of the row over the steps: of its tokens, or of their weight.
+// Blocks that weigh nothing are not added: on a masked row, or at a low
+// temperature, that is nearly all of it, and would queue for the last step's
+// word (256 rows of 131072, bf16, top-p .98, 99 % masked: 155 -> 70 us; T = .1
+// 153 -> 63).
 template <class R>
 __device__ void histogram(Lds &l, const R &row, bool mass, float top, float rate, double scale) {
     l.count[threadIdx.x] = 0;
@@ -359,8 +363,10 @@ __device__ void histogram(Lds &l, const R &row, bool mass, float top, float rate
     if (mass) {
         row.each([&](int, const float *x, int) {
             uint64_t w[R::E];
+            uint64_t some = 0;
 #pragma unroll
-            for (int e = 0; e < R::E; ++e) w[e] = weight_of(l.fine, x[e], (double)top, scale);
+            for (int e = 0; e < R::E; ++e) some |= w[e] = weight_of(l.fine, x[e], (double)top, scale);
+            if (!some) return;
 #pragma unroll
             for (int e = 0; e < R::E; ++e)
                 atomicAdd((unsigned long long *)&l.mass[step_of(x[e], top, rate)], (unsigned long long)w[e]);

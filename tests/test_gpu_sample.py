@@ -265,3 +265,20 @@ def test_top_k_past_the_list(io, V):
     for k in (2048, 2049, 2500, V // 3, V // 2 + 7, V - 1):
         for T, p, mp in ((1, 1, 0), (0.7, 0.95, 0), (2.5, 0.999, 0), (1.3, 1, 1e-4), (4, 0.5, 1e-3)):
             rows.run(r.uniform(0, 1, n), T, np.full(n, k), p, mp).check((k, T, p, mp))
+
+
+@pytest.mark.parametrize("io,V", [("bf16", 20011), ("f32", 20011), ("bf16", 131072)])
+def test_rows_that_weigh_almost_nothing(io, V):
+    """Top-p, and a k about the number that is left, where nearly all of a row is masked, or far below its largest."""
+    r = np.random.default_rng(V + 7)
+    gu.note(f"sample mostly masked V={V} {io}")
+    x = _logits(r, 6, V)
+    left = 60
+    for b in range(3):
+        x[b, r.permutation(V)[left:]] = -np.inf
+    x[3, r.permutation(V)[3000:]] = -np.inf
+    x[4] = np.where(r.uniform(0, 1, V) < 0.99, x[4] - 500, x[4])
+    rows = Rows(x, io)
+    for T, k, p in ((1, 0, 0.98), (0.01, 0, 0.9), (0.1, 0, 0.98), (1, 50, 1), (0.8, left - 1, 0.95), (1, left, 1), (1, left + 1, 0.9),
+                    (1, 1000, 1), (0.01, 2500, 0.9), (1, 3500, 0.99), (1, 5000, 0.9)):
+        rows.run(r.uniform(0, 1, 6), T, k, p).check((T, k, p))
