@@ -507,9 +507,9 @@ typedef struct {
    as replay_rollback takes it; the sequence goes on with the last kept
    position's token, tokens[b][W - 1 - n_reject[b]].  fed and n_reject: both
    or neither.  Outputs overlap nothing else that the call reads or writes.
-   B W < 2^23.  workspace: device memory of replay_sample_workspace bytes
-   (NULL where that is 0), holding nothing between calls; calls that can
-   overlap need one each. */
+   B W < 2^23.  No workspace is used: replay_sample_workspace gives 0 for
+   every size, and workspace and workspace_bytes, kept beside those of
+   replay_scan, are ignored (NULL and 0). */
 replay_status replay_sample_workspace(int32_t B, int32_t W, int32_t V, size_t *bytes);
 replay_status replay_sample(int32_t B, int32_t W, int32_t V, const void *logits, int32_t logits_dtype,
                             int64_t row_stride, const replay_sampling *opt, const float *u, int32_t *tokens,

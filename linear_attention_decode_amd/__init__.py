@@ -389,7 +389,7 @@ def replay_scan(cfg, T, max_len, cu_seqlens, q, k, v, dt, a, s_in, s_out, y, err
 
 
 def replay_sample_workspace(B, W, V) -> int:
-    """Bytes of workspace that replay_sample needs for B sequences of W positions and V logits."""
+    """Bytes of workspace that replay_sample needs for B sequences of W positions and V logits: always 0."""
     n = ctypes.c_size_t()
     _check(lib.replay_sample_workspace(B, W, V, ctypes.byref(n)), "replay_sample_workspace")
     return n.value

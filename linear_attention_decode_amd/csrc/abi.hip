@@ -879,14 +879,13 @@ replay_status replay_sample_workspace(int32_t B, int32_t W, int32_t V, size_t *b
     replay_status st = check_sample(B, W, V);
     if (st != REPLAY_OK) return st;
     if (!bytes) return REPLAY_ERR_INVALID_ARG;
-    *bytes = sample_workspace(B, W, V);
+    *bytes = 0;   // a row's work stays in its workgroup
     return REPLAY_OK;
 }
 
 replay_status replay_sample(int32_t B, int32_t W, int32_t V, const void *logits, int32_t logits_dtype,
                             int64_t row_stride, const replay_sampling *opt, const float *u, int32_t *tokens,
-                            float *probs, const int32_t *fed, int32_t *n_reject, void *workspace,
-                            size_t workspace_bytes, void *stream) {
+                            float *probs, const int32_t *fed, int32_t *n_reject, void *, size_t, void *stream) {
     replay_status st = check_sample(B, W, V);
     if (st != REPLAY_OK) return st;
     if (logits_dtype != REPLAY_F32 && logits_dtype != REPLAY_BF16) return REPLAY_ERR_UNSUPPORTED;
@@ -905,8 +904,6 @@ replay_status replay_sample(int32_t B, int32_t W, int32_t V, const void *logits,
         a.top_p = opt->top_p;
         a.min_p = opt->min_p;
     }
-    const size_t need = sample_workspace(B, W, V);
-    if (need && (!workspace || !aligned16(workspace) || workspace_bytes < need)) return REPLAY_ERR_INVALID_ARG;
     a.B = B;
     a.W = W;
     a.V = V;
@@ -918,7 +915,6 @@ replay_status replay_sample(int32_t B, int32_t W, int32_t V, const void *logits,
     a.probs = probs;
     a.fed = fed;
     a.n_reject = n_reject;
-    a.ws = workspace;
     return from_hip(launch_sample(a, as_stream(stream)));
 }
 

@@ -60,14 +60,12 @@ struct SampleArgs {
     float *probs;                  // [B][W] or null
     const int32_t *fed;            // [B][W], with
     int32_t *n_reject;             // [B]; both or neither
-    void *ws;
 };
 constexpr int kMaxVocab = 1 << 18;
 constexpr int kSampleNT = 512;   // threads of a row, a workgroup each
 
 // Launchers (return hipSuccess or the launch error).
 hipError_t launch_sample(const SampleArgs &a, hipStream_t s);
-size_t sample_workspace(int B, int W, int V);
 hipError_t launch_scan(int P, int N, const ScanArgs &a, hipStream_t s);
 int scan_segments(int P, int N, int B, int H, int G, bool bf16, int T, int max_len, int *seg_len);   // the number of segments, and their length
 // hipErrorInvalidConfiguration: more workgroups than a launch numbers

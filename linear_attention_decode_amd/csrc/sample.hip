@@ -870,8 +870,6 @@ __global__ __launch_bounds__(256) void reject_kernel(const int32_t *tokens, cons
 
 }  // namespace
 
-size_t sample_workspace(int, int, int) { return 0; }
-
 hipError_t launch_sample(const SampleArgs &a, hipStream_t s) {
     const unsigned rows = (unsigned)((int64_t)a.B * a.W);
     if (a.bf16)

@@ -195,3 +195,7 @@ def test_no_scan_in_two_segments(lad, io, P, N):
         for most in (*range(1, 1200), 1300, 2047, 2048, 2049, 4096, 8193):
             need = lad.replay_scan_workspace(cfg, most, most)
             assert need % slot == 0 and need != slot, (heads, most)
+
+
+def test_sampling_needs_no_workspace(lad):
+    assert {lad.replay_sample_workspace(*s) for s in ((1, 1, 1), (1, 1, 1 << 18), (256, 1, 131072), (48, 5, 50021), (1 << 20, 7, 300))} == {0}
