@@ -807,7 +807,9 @@ __global__ __launch_bounds__(kNT) void sample_kernel(SampleArgs a) {
         const bool past = x < x_last || (x == x_last && (uint32_t)i > (uint32_t)last);   // composite(x, i) > last
         return !past && v >= least ? v : 0;
     };
-    uint64_t *part = l.list;   // [turn][wavefront]
+    // [turn][wavefront]; 2^18 float32 logits off a 16-byte boundary have 129 turns
+    static_assert(((kMaxVocab + R::E) / R::E + kNT - 1) / kNT * kWaves <= kList, "a row's parts fit the list");
+    uint64_t *part = l.list;
     row.each([&](int t, const float *x, int i) {
         uint64_t sum = 0;
 #pragma unroll
@@ -816,7 +818,7 @@ __global__ __launch_bounds__(kNT) void sample_kernel(SampleArgs a) {
         if (lane == 0) part[t * kWaves + w] = sum;
     });
     __syncthreads();
-    // parts in order, kEach a thread (turns of up to 2^18 float32 logits: 65)
+    // parts in order, kEach a thread
     const int parts = (row.blocks + kNT - 1) / kNT * kWaves;
     uint64_t v[kEach], sum = 0, mass;
 #pragma unroll
