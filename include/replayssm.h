@@ -490,7 +490,8 @@ typedef struct {
 } replay_sampling;
 
 /* Weights are whole numbers, w_i = rint(2^45 exp((x_i - max) / T)) of logit
-   x_i, so that sums are exact; the order is by logit, largest first, equal
+   x_i (the exponential in float64: a large one can be one unit off), so that
+   sums are exact; the order is by logit, largest first, equal
    ones by index; the filters keep what all of them keep.  The token is the
    lowest index whose kept weight, with that of the kept ones before it,
    exceeds floor(u Z), Z being all kept weight.  u: [B][W] f32, the caller's

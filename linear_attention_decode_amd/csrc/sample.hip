@@ -3,10 +3,12 @@
 //
 // Weights are whole numbers, w_i = rint(2^45 exp((x_i - max) / T)): their
 // sums in 64 bits are exact (V <= 2^18), so neither the order in which
-// lanes, waves and atomics add nor the split of a row changes a token, and a
-// draw next to a border falls on the side that the definition says.  The
-// exponential is taken in float64: at 2^45 a float32 one would be off by a
-// million units.
+// lanes, waves and atomics add nor the split of a row changes a token.  The
+// exponential is taken in float64, to some 6e-16 of itself: 2 or 3 in 1000 of
+// the largest weights (above 2^43) are one unit off the definition's, all the
+// others are its own; borders between tokens lie where these weights put them,
+// a part in 2^45 of the largest weight a token from the definition's at most.
+// A float32 exponential would be off by a million units.
 //
 // Tokens are ordered by logit, largest first, ties by index: the order of
 // the composite number (~key << 32 | index), key being the logit's bits made
