@@ -504,7 +504,7 @@ typedef struct {
    token's share of Z (1 where T = 0, 0 beside a token of -1), or NULL.
    fed: int32 [B][W], the tokens that this round was given, or NULL:
    position w > 0 of a window stays while the token drawn at w - 1 is
-   fed[w], and n_reject (int32 [B]) receives W minus the number that stays,
+   fed[w] (a -1 is no token, and none stays behind it), and n_reject (int32 [B]) receives W minus the number that stays,
    as replay_rollback takes it; the sequence goes on with the last kept
    position's token, tokens[b][W - 1 - n_reject[b]].  fed and n_reject: both
    or neither.  Outputs overlap nothing else that the call reads or writes.

@@ -862,13 +862,16 @@ __global__ __launch_bounds__(kNT) void sample_kernel(SampleArgs a) {
 }
 
 // Position w of a window stays while the token drawn before it is the one
-// that was fed there.
+// that was fed there; no token (-1) is none that can be fed.
 __global__ __launch_bounds__(256) void reject_kernel(const int32_t *tokens, const int32_t *fed, int32_t *n_reject, int B,
                                                      int W) {
     const int b = blockIdx.x * 256 + threadIdx.x;
     if (b >= B) return;
     int kept = 1;
-    while (kept < W && tokens[(size_t)b * W + kept - 1] == fed[(size_t)b * W + kept]) ++kept;
+    for (; kept < W; ++kept) {
+        const int token = tokens[(size_t)b * W + kept - 1];
+        if (token < 0 || token != fed[(size_t)b * W + kept]) break;
+    }
     n_reject[b] = W - kept;
 }
 

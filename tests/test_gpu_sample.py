@@ -282,3 +282,19 @@ def test_rows_that_weigh_almost_nothing(io, V):
     for T, k, p in ((1, 0, 0.98), (0.01, 0, 0.9), (0.1, 0, 0.98), (1, 50, 1), (0.8, left - 1, 0.95), (1, left, 1), (1, left + 1, 0.9),
                     (1, 1000, 1), (0.01, 2500, 0.9), (1, 3500, 0.99), (1, 5000, 0.9)):
         rows.run(r.uniform(0, 1, 6), T, k, p).check((T, k, p))
+
+
+def test_no_token_matches_no_draft():
+    """A position without an answer (token -1) does not stand for a draft of -1, and nothing behind it stays."""
+    gu.note("sample -1 against a draft of -1")
+    r = np.random.default_rng(6)
+    x = _logits(r, 3 * 4, 300)
+    x[1], x[4 + 0], x[8 + 2] = np.nan, -np.inf, np.inf
+    rows = Rows(x, "f32", W=4)
+    tok = rows.run(0.4).tokens.cpu().numpy()
+    assert (tok == -1).sum() == 3
+    fed = np.full((3, 4), -1)
+    fed[:, 1:] = tok[:, :-1]
+    rows.run(0.4, fed=fed).check()
+    # kept: the position without an answer itself, at most
+    assert rows.rej.cpu().tolist() == [2, 3, 1]
