@@ -279,6 +279,13 @@ def _want(what, t, shape, dtype, gpu):
     return t.data_ptr()
 
 
+def _size(what, n):
+    """n, if the C call's int32 holds it (ctypes would cut it to another size)."""
+    if not -2 ** 31 <= n < 2 ** 31:
+        raise ReplayError(f"{what}: {n} does not fit 32 bits")
+    return n
+
+
 def _rows(what, t, n, width, dtype, gpu):
     """(address, row stride) of a [n, width] tensor whose rows may lie any stride apart (None: (None, 0))."""
     if t is None:
@@ -362,7 +369,8 @@ def replay_conv_step(cfg, conv, W, x, dt_raw, pos, conv_state, q, k, v, dt, a, b
 def replay_scan_workspace(cfg, T, max_len) -> int:
     """Bytes of workspace that replay_scan needs for T rows, up to max_len of them a sequence."""
     n = ctypes.c_size_t()
-    _check(lib.replay_scan_workspace(ctypes.byref(cfg), T, max_len, ctypes.byref(n)), "replay_scan_workspace")
+    _check(lib.replay_scan_workspace(ctypes.byref(cfg), _size("T", T), _size("max_len", max_len), ctypes.byref(n)),
+           "replay_scan_workspace")
     return n.value
 
 
@@ -381,7 +389,7 @@ def replay_scan(cfg, T, max_len, cu_seqlens, q, k, v, dt, a, s_in, s_out, y, err
     f32, i32, io, gpu = torch.float32, torch.int32, _io_type(cfg), _gpu()
     B, H, G, P, N = cfg.batch, cfg.heads, cfg.groups, cfg.head_dim, cfg.state_dim
     _check(lib.replay_scan(
-        ctypes.byref(cfg), T, max_len, _want("cu_seqlens", cu_seqlens, (B + 1,), i32, gpu),
+        ctypes.byref(cfg), _size("T", T), _size("max_len", max_len), _want("cu_seqlens", cu_seqlens, (B + 1,), i32, gpu),
         _want("q", q, (T, G, N), io, gpu), _want("k", k, (T, G, N), io, gpu), _want("v", v, (T, H, P), io, gpu),
         _want("dt", dt, (T, H), f32, gpu), _want("a", a, (T, H), f32, gpu), _want("s_in", s_in, (B, H, P, N), f32, gpu),
         _want("s_out", s_out, (B, H, P, N), f32, gpu), _want("y", y, (T, H, P), io, gpu),
@@ -391,7 +399,8 @@ def replay_scan(cfg, T, max_len, cu_seqlens, q, k, v, dt, a, s_in, s_out, y, err
 def replay_sample_workspace(B, W, V) -> int:
     """Bytes of workspace that replay_sample needs for B sequences of W positions and V logits: always 0."""
     n = ctypes.c_size_t()
-    _check(lib.replay_sample_workspace(B, W, V, ctypes.byref(n)), "replay_sample_workspace")
+    _check(lib.replay_sample_workspace(_size("B", B), _size("W", W), _size("V", V), ctypes.byref(n)),
+           "replay_sample_workspace")
     return n.value
 
 

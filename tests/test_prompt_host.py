@@ -199,3 +199,14 @@ def test_no_scan_in_two_segments(lad, io, P, N):
 
 def test_sampling_needs_no_workspace(lad):
     assert {lad.replay_sample_workspace(*s) for s in ((1, 1, 1), (1, 1, 1 << 18), (256, 1, 131072), (48, 5, 50021), (1 << 20, 7, 300))} == {0}
+
+
+@pytest.mark.parametrize("big", [1 << 31, (1 << 32) + 64, -(1 << 32) + 64])
+def test_sizes_past_32_bits_are_refused(lad, big):
+    """A size that the C call's int32 would cut to another one."""
+    for args in ((big, 64), (64, big)):
+        with pytest.raises(lad.ReplayError, match="32 bits"):
+            lad.replay_scan_workspace(_cfg(lad), *args)
+    for args in ((big, 1, 8), (1, big, 8), (1, 1, big)):
+        with pytest.raises(lad.ReplayError, match="32 bits"):
+            lad.replay_sample_workspace(*args)
