@@ -460,9 +460,10 @@ replay_status replay_conv_step(const replay_config *cfg, const replay_conv_param
    are.  With bf16 io the products run on bf16 operands: inputs are taken as
    they are, the state and the tokens' weights go into y's products as two bf16
    parts that hold them to 2^-15 of each term, s_out is what float32 products
-   give; sums are float32.  y and s_out overlap nothing else
-   that the call reads or writes (s_out over s_in: INVALID_ARG).  T <= 2^30,
-   H P and G N <= 2^24.
+   give; sums are float32.  What is not finite in an input reaches the outputs
+   and states that the recurrence lets it reach, and no others (an infinity may
+   arrive as NaN).  y and s_out overlap nothing else that the call reads or
+   writes (s_out over s_in: INVALID_ARG).  T <= 2^30, H P and G N <= 2^24.
    A sequence whose range decreases, leaves 0..T or is longer than max_len
    gets BAD_RANGE in err (device int32 [B + 1]); its rows and its s_out are
    left as they are.

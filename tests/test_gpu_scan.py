@@ -421,3 +421,31 @@ def test_four_segments_of_a_short_prompt(lens, H, G, P, N):
     torch.cuda.synchronize()
     assert ws.numel() == 3 * p.B * H * (P * N + 1)
     p.check()
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("P,N,H,G,lens", [(64, 128, 4, 2, [90, 20]), (16, 16, 2, 1, [70, 9]), (128, 128, 2, 2, [130]), (64, 64, 3, 1, [500, 70])])
+@pytest.mark.parametrize("name", ["q", "k", "v", "dt", "a", "s_in"])
+def test_what_is_not_finite_reaches_what_the_recurrence_lets_it(io, P, N, H, G, lens, name):
+    """Outputs and states are finite where the float64 recurrence's are, and nowhere else."""
+    gu.note(f"scan not finite {name} P={P} N={N} H={H} {io}")
+    for value in (float("inf"), -float("inf"), float("nan")):
+        p = Prompts(lens, H, G, P, N, io, seed=N + H)
+        for b, at in enumerate((37, 2)[:len(lens)]):
+            t = int(p.ends[b]) - lens[b] + at
+            if name in "qk":
+                getattr(p, name)[t, b % G, 3] = value
+            elif name == "v":
+                p.v[t, H - 1 - b, 9] = value
+            elif name == "s_in":
+                p.s_in[b, b, 2, 7] = value
+            else:
+                getattr(p, name)[t, H - 1 - b] = value
+        p.run()
+        torch.cuda.synchronize()
+        for b, n in enumerate(lens):
+            with np.errstate(invalid="ignore"):
+                y, S = p.reference(b)
+            rows = slice(int(p.ends[b]) - n, int(p.ends[b]))
+            assert np.array_equal(p.y[rows].isfinite().cpu().numpy(), np.isfinite(y)), (value, b)
+            assert np.array_equal(p.s_out[b].isfinite().cpu().numpy(), np.isfinite(S)), (value, b)
