@@ -29,11 +29,12 @@
 //
 // Bound by the chain of steps of a row (two passes, a dozen barriers, sorts of
 // few tokens) and by the float64 exponentials, more than by reading the
-// logits.  Rows of 131072 in bf16, 256 of them, all filters on: 38 us, 1.8
-// TB/s of 67 MB (the copy rate would take 14 us); top-k of 50 alone 27 us, of
-// 1000 34 us, of 5000 113 us; top-p of .98 alone 175 us and no filter 71 us,
-// where every token's weight is computed and every token counts.  One row 24
-// us.  512 threads a row: 1024 leave half the registers, and spill.
+// logits.  Rows of 131072 in bf16, 256 of them, all filters on: 39 us, 1.7
+// TB/s of 67 MB (the copy rate would take 14 us); top-k of 50 alone 29 us, of
+// 1000 35 us, of 5000 120 us; min-p of .05 25 us; greedy 31 us; top-p of .98
+// alone 179 us and no filter 75 us, where every token's weight is computed and
+// every token counts.  One row 22 us.  512 threads a row: 1024 leave half the
+// registers, and spill.
 #include "device_common.h"
 #include "prompt.h"
 
@@ -365,8 +366,7 @@ __device__ void histogram(Lds &l, const R &row, bool mass, float top, float rate
     __syncthreads();
     if (mass) {
         row.each([&](int, const float *x, int) {
-            uint64_t w[R::E];
-            uint64_t some = 0;
+            uint64_t w[R::E], some = 0;
 #pragma unroll
             for (int e = 0; e < R::E; ++e) some |= w[e] = weight_of(l.fine, x[e], (double)top, scale);
             if (!some) return;
