@@ -518,6 +518,32 @@ replay_status replay_sample(int32_t B, int32_t W, int32_t V, const void *logits,
                             float *probs, const int32_t *fed, int32_t *n_reject, void *workspace,
                             size_t workspace_bytes, void *stream);
 
+/* ---- scores of tokens ------------------------------------------------------
+   What a serving loop reports beside the tokens (background to the pages, as
+   sampling): for each of W positions of B sequences, from V logits x_i and T,
+       log p_i = (x_i - m) / T - log Z,  m = max x,  Z = sum_j exp((x_j - m) / T),
+   of n_given tokens (ids, int32 [B][W][n_given]) into logp (f32
+   [B][W][n_given]); the entropy -sum p_i log p_i into entropy (f32 [B][W], or
+   NULL); the n_top most likely tokens, most likely first, equal logits by
+   index, into top_ids (int32 [B][W][n_top]) and top_logp (f32).  n_given and
+   n_top may be 0, n_top <= min(V, 32).  temperature: f32 [B], or NULL for 1.
+   T = 0: the first of the largest logits has all, as replay_sample takes it
+   (log p 0, the others -infinity, entropy 0).  A row that replay_sample gives
+   no token (it holds a NaN or +infinity or nothing but -infinity, or a T that
+   is negative, infinite or NaN): NaN, and top_ids -1.  A given token outside
+   0..V - 1 (a -1 beside no token): NaN.  Logits of -infinity: -infinity.
+   logits as for replay_sample; V <= 2^18.  Sums are float64 over float32
+   exponentials; a token of less than 2^-126 of the likeliest one's share counts
+   as nothing in Z and in the entropy.  workspace: of the size that replay_logprobs_workspace gives
+   for the same B, W, V and n_top, 16-byte aligned; it holds nothing between
+   calls, and calls that can overlap need one each.  Outputs overlap nothing
+   else that the call reads or writes. */
+replay_status replay_logprobs_workspace(int32_t B, int32_t W, int32_t V, int32_t n_top, size_t *bytes);
+replay_status replay_logprobs(int32_t B, int32_t W, int32_t V, const void *logits, int32_t logits_dtype,
+                              int64_t row_stride, const float *temperature, int32_t n_given, const int32_t *ids,
+                              float *logp, float *entropy, int32_t n_top, int32_t *top_ids, float *top_logp,
+                              void *workspace, size_t workspace_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -25,6 +25,7 @@ __all__ = [
     "replay_eager_step", "replay_eager_select", "replay_stream_probe",
     "ReplayConvParams", "ReplayConv", "SEQERR_BAD_RANGE", "replay_conv_prompt", "replay_conv_step",
     "replay_scan_workspace", "replay_scan", "ReplaySampling", "replay_sample_workspace", "replay_sample",
+    "replay_logprobs_workspace", "replay_logprobs",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libreplayssm.so")
@@ -41,7 +42,7 @@ EXPORTS = (
     "replay_verify_step", "replay_rollback_verify_step", "replay_set_flush_skipping", "replay_get_error",
     "replay_eager_step", "replay_eager_select", "replay_stream_probe",
     "replay_conv_prompt", "replay_conv_step", "replay_scan_workspace", "replay_scan",
-    "replay_sample_workspace", "replay_sample",
+    "replay_sample_workspace", "replay_sample", "replay_logprobs_workspace", "replay_logprobs",
 )
 
 _VP = ctypes.c_void_p
@@ -113,6 +114,9 @@ def _load():
     L.replay_sample_workspace.argtypes = [_I32, _I32, _I32, ctypes.POINTER(ctypes.c_size_t)]
     L.replay_sample.argtypes = ([_I32, _I32, _I32, _VP, _I32, _I64, ctypes.POINTER(ReplaySampling)] + [_VP] * 6
                                 + [ctypes.c_size_t, _VP])
+    L.replay_logprobs_workspace.argtypes = [_I32, _I32, _I32, _I32, ctypes.POINTER(ctypes.c_size_t)]
+    L.replay_logprobs.argtypes = ([_I32, _I32, _I32, _VP, _I32, _I64, _VP, _I32, _VP, _VP, _VP, _I32, _VP, _VP, _VP,
+                                   ctypes.c_size_t, _VP])
     for name in EXPORTS:
         if name not in ("replay_status_string", "replay_abi_version"):
             getattr(L, name).restype = ctypes.c_int
@@ -404,6 +408,19 @@ def replay_sample_workspace(B, W, V) -> int:
     return n.value
 
 
+def _logit_rows(logits, gpu):
+    """The row stride of logits [B, W, V]."""
+    import torch
+    B, W, V = logits.shape
+    row = logits.stride(1) if W > 1 else logits.stride(0) if B > 1 else V
+    if (logits.dtype not in (torch.float32, torch.bfloat16) or logits.get_device() != gpu
+            or (V > 1 and logits.stride(2) != 1) or (B > 1 and logits.stride(0) != W * row)):
+        raise ReplayError("logits: want a float32 or bf16 tensor [B, W, V] of evenly spaced rows with unit stride along "
+                          f"them on the current GPU ({gpu}), got {logits.dtype} with strides {logits.stride()} on "
+                          f"{logits.device}")
+    return row
+
+
 def replay_sample(logits, u, tokens, temperature=None, top_k=None, top_p=None, min_p=None, probs=None, fed=None,
                   n_reject=None, workspace=None, stream=None):
     """logits [B, W, V] (float32 or bf16; positions may lie any stride apart), u [B, W] f32, tokens [B, W] int32;
@@ -412,12 +429,7 @@ def replay_sample(logits, u, tokens, temperature=None, top_k=None, top_p=None, m
     import torch
     f32, i32, gpu = torch.float32, torch.int32, _gpu()
     B, W, V = logits.shape
-    row = logits.stride(1) if W > 1 else logits.stride(0) if B > 1 else V
-    if (logits.dtype not in (f32, torch.bfloat16) or logits.get_device() != gpu or (V > 1 and logits.stride(2) != 1)
-            or (B > 1 and logits.stride(0) != W * row)):
-        raise ReplayError("logits: want a float32 or bf16 tensor [B, W, V] of evenly spaced rows with unit stride along "
-                          f"them on the current GPU ({gpu}), got {logits.dtype} with strides {logits.stride()} on "
-                          f"{logits.device}")
+    row = _logit_rows(logits, gpu)
     opt = ReplaySampling(_want("temperature", temperature, (B,), f32, gpu), _want("top_k", top_k, (B,), i32, gpu),
                          _want("top_p", top_p, (B,), f32, gpu), _want("min_p", min_p, (B,), f32, gpu))
     _check(lib.replay_sample(
@@ -425,6 +437,33 @@ def replay_sample(logits, u, tokens, temperature=None, top_k=None, top_p=None, m
         _want("u", u, (B, W), f32, gpu), _want("tokens", tokens, (B, W), i32, gpu), _want("probs", probs, (B, W), f32, gpu),
         _want("fed", fed, (B, W), i32, gpu), _want("n_reject", n_reject, (B,), i32, gpu), *_workspace(workspace, gpu),
         _on(stream, gpu)), "replay_sample")
+
+
+def replay_logprobs_workspace(B, W, V, n_top) -> int:
+    """Bytes of workspace that replay_logprobs needs for B sequences of W positions, V logits and n_top alternatives."""
+    n = ctypes.c_size_t()
+    _check(lib.replay_logprobs_workspace(_size("B", B), _size("W", W), _size("V", V), _size("n_top", n_top), ctypes.byref(n)),
+           "replay_logprobs_workspace")
+    return n.value
+
+
+def replay_logprobs(logits, ids=None, logp=None, entropy=None, top_ids=None, top_logp=None, temperature=None,
+                    workspace=None, stream=None):
+    """logits [B, W, V] as for replay_sample; ids [B, W, M] int32 with logp [B, W, M] f32; entropy [B, W] f32; top_ids
+    [B, W, n] int32 with top_logp [B, W, n] f32; temperature [B] f32 (None: 1).  Any of the outputs may be None."""
+    import torch
+    f32, i32, gpu = torch.float32, torch.int32, _gpu()
+    B, W, V = logits.shape
+    row = _logit_rows(logits, gpu)
+    for what, a, b in (("ids and logp", ids, logp), ("top_ids and top_logp", top_ids, top_logp)):
+        if (a is None) != (b is None) or (a is not None and a.dim() != 3):
+            raise ReplayError(f"{what}: want both, of shape (B, W, count), or neither")
+    M, n = (0 if t is None else t.shape[2] for t in (ids, top_ids))
+    _check(lib.replay_logprobs(
+        B, W, V, logits.data_ptr(), F32 if logits.dtype is f32 else BF16, row, _want("temperature", temperature, (B,), f32, gpu),
+        M, _want("ids", ids, (B, W, M), i32, gpu), _want("logp", logp, (B, W, M), f32, gpu),
+        _want("entropy", entropy, (B, W), f32, gpu), n, _want("top_ids", top_ids, (B, W, n), i32, gpu),
+        _want("top_logp", top_logp, (B, W, n), f32, gpu), *_workspace(workspace, gpu), _on(stream, gpu)), "replay_logprobs")
 
 
 # ---- one layer's state, allocated with torch -------------------------------

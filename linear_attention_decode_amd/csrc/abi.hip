@@ -7,8 +7,8 @@
 // float32 master and of a shared low-precision checkpoint), gdn.hip (Gated
 // DeltaNet layers), ring.hip (append, rollback, fills), conv.hip (the
 // convolution and discretisation ahead of the recurrence), scan.hip (the
-// recurrence over prompts), sample.hip (tokens from logits), eager.hip and
-// probe.hip.
+// recurrence over prompts), sample.hip and logprobs.hip (tokens from logits,
+// and their scores), eager.hip and probe.hip.
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
@@ -916,6 +916,69 @@ replay_status replay_sample(int32_t B, int32_t W, int32_t V, const void *logits,
     a.fed = fed;
     a.n_reject = n_reject;
     return from_hip(launch_sample(a, as_stream(stream)));
+}
+
+}  // extern "C"
+
+namespace {
+
+// The parts of the rows, and the workspace they need.
+replay_status logprob_plan(int32_t B, int32_t W, int32_t V, int32_t n, int *part, int *parts, size_t *bytes) {
+    if (B < 1 || W < 1 || V < 1 || n < 0 || n > V) return REPLAY_ERR_INVALID_ARG;
+    if (V > kMaxVocab || n > kMaxTop) return REPLAY_ERR_UNSUPPORTED;
+    const int64_t rows = (int64_t)B * W;
+    *part = logprob_part(rows, V, parts);
+    if (!launch_fits(rows * *parts, kPartNT)) return REPLAY_ERR_UNSUPPORTED;
+    *bytes = (size_t)rows * *parts * (kPartWords + (n > 0 ? n : 1)) * sizeof(uint64_t);
+    return REPLAY_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+replay_status replay_logprobs_workspace(int32_t B, int32_t W, int32_t V, int32_t n_top, size_t *bytes) {
+    int part, parts;
+    size_t need;
+    const replay_status st = logprob_plan(B, W, V, n_top, &part, &parts, &need);
+    if (st != REPLAY_OK) return st;
+    if (!bytes) return REPLAY_ERR_INVALID_ARG;
+    *bytes = need;
+    return REPLAY_OK;
+}
+
+replay_status replay_logprobs(int32_t B, int32_t W, int32_t V, const void *logits, int32_t logits_dtype,
+                              int64_t row_stride, const float *temperature, int32_t n_given, const int32_t *ids,
+                              float *logp, float *entropy, int32_t n_top, int32_t *top_ids, float *top_logp,
+                              void *workspace, size_t workspace_bytes, void *stream) {
+    LogprobArgs a{};
+    size_t need;
+    const replay_status st = logprob_plan(B, W, V, n_top, &a.part, &a.parts, &need);
+    if (st != REPLAY_OK) return st;
+    if (logits_dtype != REPLAY_F32 && logits_dtype != REPLAY_BF16) return REPLAY_ERR_UNSUPPORTED;
+    const size_t mask = logits_dtype == REPLAY_BF16 ? 1 : 3;
+    if (!logits || (reinterpret_cast<uintptr_t>(logits) & mask) || row_stride < V || !aligned4(temperature))
+        return REPLAY_ERR_INVALID_ARG;
+    if (n_given < 0 || (n_given > 0 && (!ids || !logp)) || !aligned4(ids) || !aligned4(logp) || !aligned4(entropy))
+        return REPLAY_ERR_INVALID_ARG;
+    if ((n_top > 0 && (!top_ids || !top_logp)) || !aligned4(top_ids) || !aligned4(top_logp)) return REPLAY_ERR_INVALID_ARG;
+    if (!workspace || !aligned16(workspace) || workspace_bytes < need) return REPLAY_ERR_INVALID_ARG;
+    a.B = B;
+    a.W = W;
+    a.V = V;
+    a.M = n_given;
+    a.n = n_top;
+    a.bf16 = logits_dtype == REPLAY_BF16;
+    a.logits = logits;
+    a.stride = row_stride;
+    a.temperature = temperature;
+    a.ids = ids;
+    a.logp = logp;
+    a.entropy = entropy;
+    a.top_ids = top_ids;
+    a.top_logp = top_logp;
+    a.ws = static_cast<uint64_t *>(workspace);
+    return from_hip(launch_logprobs(a, as_stream(stream)));
 }
 
 }  // extern "C"

@@ -1,0 +1,394 @@
+// logprobs.hip -- log-probabilities of given tokens, the entropy of the
+// distribution and its most likely tokens, from logits.
+//
+// With m the row's maximum, t_i = (m - x_i) / T >= 0 and Z = sum exp(-t_i),
+//     log p_i = -t_i - log Z,     H = -sum p_i log p_i = log Z + sum exp(-t_i) t_i / Z;
+// all terms of both sums are positive, so nothing cancels.  log Z is taken as
+// log1p(Z - 1), Z - 1 summed without one of the elements that equal m: where
+// one token holds nearly all, its log-probability is the small number that
+// the others leave.
+//
+// A row is cut into parts, a workgroup each, that hold their logits in
+// registers from one reading: the maximum first, then the sums from it, then
+// the part's first n tokens.  A second launch, a workgroup a row, scales the
+// parts' sums to the row's maximum, merges their first tokens and looks up
+// the given ones.
+//
+// The first n of a part: of its threads' own largest keys the n-th bounds the
+// n-th of all from below, so that only tokens from it on (some n of them) are
+// gathered and ranked, each by counting those before it.  Where equal logits
+// make these too many, the n-th token's composite is found by bisection.
+//
+// Sums: a block's 4 or 8 terms in float32, a thread's blocks and all beyond
+// in float64; the exponential is the hardware's, within 2^-22 of a term.
+#include "logits.h"
+
+namespace replay {
+
+namespace {
+
+constexpr int kNT = kPartNT, kWaves = kNT / 64;
+constexpr int kList = 1024;                      // tokens gathered
+constexpr int kMaxParts = kMaxVocab / kPartSmall + 1;
+
+struct Found {
+    uint64_t list[kList];
+    __align__(16) uint32_t key[kNT];
+    uint64_t first[kWaves];
+    double sum[kWaves], spread[kWaves];
+    uint32_t ones[kWaves], bad[kWaves], n, bound;
+};
+
+__device__ __forceinline__ uint64_t wave_min(uint64_t x) {
+#pragma unroll
+    for (int d = 32; d; d >>= 1) {
+        const uint64_t y = (uint64_t)__shfl_xor((long long)x, d);
+        x = x < y ? x : y;
+    }
+    return x;
+}
+__device__ __forceinline__ uint32_t wave_add(uint32_t x) {
+#pragma unroll
+    for (int d = 32; d; d >>= 1) x += (uint32_t)__shfl_xor((int)x, d);
+    return x;
+}
+__device__ __forceinline__ double wave_add(double x) {
+#pragma unroll
+    for (int d = 32; d; d >>= 1) x += __shfl_xor(x, d);
+    return x;
+}
+
+// 1 / T, where T scales a distribution (T = 0 takes the largest alone)
+__device__ __forceinline__ bool scales(float T) { return T > 0.f && T < __builtin_inff(); }
+
+// U blocks of 16 bytes a thread
+template <bool BF16, int U>
+__global__ __launch_bounds__(kNT) void logprobs_part_kernel(LogprobArgs a) {
+    using L = Logits<BF16>;
+    constexpr int E = L::E;
+    __shared__ Found f;
+    const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
+    const int row = blockIdx.x / a.parts, part = blockIdx.x % a.parts;
+    const L l(a.logits, row, a.stride, a.V);
+    const float T = a.temperature ? a.temperature[row / a.W] : 1.f;
+
+    // blocks lo .. hi - 1 of the row are whole
+    const int lo = l.off ? 1 : 0, hi = (l.off + a.V) / E, i0 = part * (kNT * U) + tid;
+    const auto whole = make_rsrc(l.base + 16 * lo, hi > lo ? (uint32_t)(hi - lo) * 16u : 0u);
+    u32x4 r[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) r[u] = __builtin_amdgcn_raw_buffer_load_b128(whole, (uint32_t)(i0 + u * kNT - lo) * 16u, 0, 0);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const int i = i0 + u * kNT;
+        if (i < lo || i >= hi) r[u] = i < l.blocks ? l.load_edge(i) : L::none();
+    }
+
+    // this thread's first token, and whether a value is none of a distribution's
+    float top = -__builtin_inff();
+    int at = 0x7fffffff;
+    bool bad = false;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        float x[E];
+        l.widen(r[u], x);
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            const int i = l.first(i0 + u * kNT) + e;
+            bad |= !(x[e] < __builtin_inff());
+            const bool in = i >= 0 && i < a.V;
+            if (in && (x[e] > top || at == 0x7fffffff)) {
+                top = x[e];
+                at = i;
+            }
+        }
+    }
+    const bool any = at != 0x7fffffff;
+    f.key[tid] = any ? key_of(top) : 0u;
+    const uint64_t first = wave_min(any ? composite(top, at) : ~0ull);
+    const bool wave_bad = __any(bad);
+    if (lane == 0) {
+        f.first[wave] = first;
+        f.bad[wave] = wave_bad;
+    }
+    if (tid == 0) f.n = 0;
+    __syncthreads();
+    uint64_t lead = f.first[0];
+    uint32_t worse = f.bad[0];
+#pragma unroll
+    for (int w = 1; w < kWaves; ++w) {
+        lead = f.first[w] < lead ? f.first[w] : lead;
+        worse |= f.bad[w];
+    }
+    uint64_t *out = a.ws + (size_t)blockIdx.x * (kPartWords + (a.n > 0 ? a.n : 1));
+    const float m = value_at(lead);
+
+    // the sums, from this part's maximum (nothing but -infinity weighs nothing)
+    double sum = 0., spread = 0.;
+    uint32_t ones = 0;
+    if (scales(T) && m > -__builtin_inff()) {
+        const float c = 1.44269504088896340736f / T;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            float x[E], w[E], d[E];
+            l.widen(r[u], x);
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                d[e] = fminf((m - x[e]) * c, 200.f);   // 2^-200 is no float32: -infinity and the far ones weigh nothing
+                w[e] = __builtin_amdgcn_exp2f(-d[e]);
+                d[e] *= w[e];
+                ones += x[e] == m;
+                w[e] = x[e] == m ? 0.f : w[e];
+            }
+#pragma unroll
+            for (int s = E / 2; s; s >>= 1)
+#pragma unroll
+                for (int e = 0; e < s; ++e) {
+                    w[e] += w[e + s];
+                    d[e] += d[e + s];
+                }
+            sum += w[0];
+            spread += d[0];
+        }
+    }
+    sum = wave_add(sum);
+    spread = wave_add(spread);
+    ones = wave_add(ones);
+    if (lane == 0) {
+        f.sum[wave] = sum;
+        f.spread[wave] = spread;
+        f.ones[wave] = ones;
+    }
+
+    // the key that the n-th of the threads' first tokens has
+    const int n = a.n < kNT ? a.n : kNT;
+    uint32_t bound = 0;
+    if (n > 1) {
+        const uint32_t mine = f.key[tid];
+        int rank = 0;
+        for (int o = 0; o < kNT; o += 4) {
+            const u32x4 k = *reinterpret_cast<const u32x4 *>(&f.key[o]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) rank += k[e] > mine || (k[e] == mine && o + e < tid);
+        }
+        if (rank == n - 1) f.bound = mine;
+    }
+    __syncthreads();
+    if (tid == 0) {
+        double s = 0., d = 0.;
+        uint32_t o = 0;
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w) {
+            s += f.sum[w];
+            d += f.spread[w];
+            o += f.ones[w];
+        }
+        out[0] = (uint64_t)__double_as_longlong(s);
+        out[1] = (uint64_t)__double_as_longlong(d);
+        out[2] = (uint64_t)worse << 32 | o;
+        if (n <= 1) out[kPartWords] = lead;
+    }
+    if (n <= 1) return;
+    bound = f.bound;
+
+    // f(composite) for this part's tokens, thread by thread
+    auto each = [&](auto g) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            float x[E];
+            l.widen(r[u], x);
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                const int i = l.first(i0 + u * kNT) + e;
+                if (i >= 0 && i < a.V) g(composite(x[e], i));
+            }
+        }
+    };
+    // (a key below every token's takes all there are; an index has 32 bits)
+    uint64_t upto = ((uint64_t)~bound << 32) | 0xffffffffu;
+    auto gather = [&] {
+        each([&](uint64_t comp) {
+            if (comp <= upto) {
+                const uint32_t k = atomicAdd(&f.n, 1u);
+                if (k < kList) f.list[k] = comp;
+            }
+        });
+        __syncthreads();
+    };
+    gather();
+    if (f.n > kList) {
+        // equal logits: the n-th composite, the least that n are not above
+        uint64_t below = 0, here = upto;   // fewer than n are <= below - 1; n or more are <= here
+        while (below < here) {
+            const uint64_t mid = below + (here - below) / 2;
+            uint32_t count = 0;
+            each([&](uint64_t comp) { count += comp <= mid; });
+            count = wave_add(count);
+            __syncthreads();
+            if (lane == 0) f.ones[wave] = count;
+            __syncthreads();
+            uint32_t all = 0;
+#pragma unroll
+            for (int w = 0; w < kWaves; ++w) all += f.ones[w];
+            if (all >= (uint32_t)n)
+                here = mid;
+            else
+                below = mid + 1;
+        }
+        upto = here;
+        __syncthreads();
+        if (tid == 0) f.n = 0;
+        __syncthreads();
+        gather();
+    }
+    const int c = (int)f.n;
+    for (int i = tid; i < c; i += kNT) {
+        const uint64_t mine = f.list[i];
+        int rank = 0;
+        for (int o = 0; o < c; ++o) rank += f.list[o] < mine;
+        if (rank < n) out[kPartWords + rank] = mine;
+    }
+    for (int i = c + tid; i < n; i += kNT) out[kPartWords + i] = ~0ull;   // a part of fewer tokens
+}
+
+// One workgroup a row: its parts joined.
+__global__ __launch_bounds__(kNT) void logprobs_join_kernel(LogprobArgs a) {
+    __shared__ uint64_t list[kMaxParts * kMaxTop];
+    __shared__ uint64_t keep[kMaxParts * kMaxTop];
+    __shared__ uint64_t lead_of[kWaves];
+    __shared__ double sums[kWaves], spreads[kWaves];
+    __shared__ uint32_t bads[kWaves], kept;
+    __shared__ uint64_t bound;
+    const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, row = blockIdx.x;
+    const int n = a.n > 0 ? a.n : 1, words = kPartWords + n, parts = a.parts;
+    const uint64_t *ws = a.ws + (size_t)row * parts * words;
+    for (int i = tid; i < parts * n; i += kNT) list[i] = ws[i / n * words + kPartWords + i % n];
+    double s = 0., d = 0.;
+    uint64_t head = 0, mine = ~0ull;
+    if (tid < parts) {
+        s = __longlong_as_double((long long)ws[tid * words]);
+        d = __longlong_as_double((long long)ws[tid * words + 1]);
+        head = ws[tid * words + 2];
+        mine = ws[tid * words + kPartWords];
+    }
+    const uint64_t first = wave_min(mine);
+    const bool wave_bad = __any((int)(head >> 32) != 0);
+    if (lane == 0) {
+        lead_of[wave] = first;
+        bads[wave] = wave_bad;
+    }
+    if (tid == 0) kept = 0;
+    __syncthreads();
+    uint64_t lead = lead_of[0];
+    uint32_t worse = bads[0];
+#pragma unroll
+    for (int w = 1; w < kWaves; ++w) {
+        lead = lead_of[w] < lead ? lead_of[w] : lead;
+        worse |= bads[w];
+    }
+    const float T = a.temperature ? a.temperature[row / a.W] : 1.f;
+    const float top = value_at(lead);
+    const bool valid = !worse && top > -__builtin_inff() && (T == 0.f || scales(T));
+    const double per = scales(T) ? 1. / (double)T : 0.;
+
+    // Z - 1 and sum exp(-t) t from the row's maximum: a part's terms, w of its
+    // own, weigh f w there, and its t grow by the maxima's distance
+    double zs = 0., hs = 0.;
+    if (tid < parts && valid && T > 0.f && mine != ~0ull) {
+        const float m = value_at(mine);
+        const double t = ((double)top - (double)m) * per, f = m > -__builtin_inff() ? exp(-t) : 0.;
+        const double ones = (double)(uint32_t)head, all = ones + s;
+        zs = f * s + (mine == lead ? ones - 1. : f * ones);
+        hs = f > 0. ? f * (d * 0.69314718055994530942 + t * all) : 0.;
+    }
+    zs = wave_add(zs);
+    hs = wave_add(hs);
+    if (lane == 0) {
+        sums[wave] = zs;
+        spreads[wave] = hs;
+    }
+    // of entry q of every part the k-th: n tokens at least are not behind it
+    const int q = (n + parts - 1) / parts - 1, k = (n + q) / (q + 1);
+    if (tid < parts) {
+        const uint64_t e = list[tid * n + q];
+        int rank = 0;
+        for (int o = 0; o < parts; ++o) {
+            const uint64_t x = list[o * n + q];
+            rank += x < e || (x == e && o < tid);
+        }
+        if (rank == k - 1) bound = e;
+    }
+    __syncthreads();
+    double z = 0., h = 0.;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) {
+        z += sums[w];
+        h += spreads[w];
+    }
+    const float nan = __builtin_nanf("");
+    const double log_z = log1p(z);
+    if (tid == 0 && a.entropy) a.entropy[row] = valid ? (float)(log_z + h / (1. + z)) : nan;
+    // log p of a logit; T = 0: the first of the largest has all
+    auto score = [&](float x, bool is_lead) {
+        if (!valid) return nan;
+        if (T == 0.f) return is_lead ? 0.f : -__builtin_inff();
+        return (float)(((double)x - (double)top) * per - log_z);
+    };
+    for (int i = tid; i < a.M; i += kNT) {
+        const int id = a.ids[(size_t)row * a.M + i];
+        float lp = nan;
+        if (id >= 0 && id < a.V) {
+            const size_t at = (size_t)((int64_t)row * a.stride + id);
+            const float x = a.bf16 ? load_io1<true>(a.logits, at) : load_io1<false>(a.logits, at);
+            lp = score(x, id == (int)(uint32_t)lead);
+        }
+        a.logp[(size_t)row * a.M + i] = lp;
+    }
+    if (!a.n) return;
+    for (int i = tid; i < parts * n; i += kNT) {
+        const uint64_t e = list[i];
+        if (e <= bound && e != ~0ull) keep[atomicAdd(&kept, 1u)] = e;
+    }
+    __syncthreads();
+    const int c = (int)kept;
+    for (int i = tid; i < c; i += kNT) {
+        const uint64_t e = keep[i];
+        int rank = 0;
+        for (int o = 0; o < c; ++o) rank += keep[o] < e;
+        if (rank < n) {
+            const size_t at = (size_t)row * n + rank;
+            a.top_ids[at] = valid ? (int)(uint32_t)e : -1;
+            a.top_logp[at] = score(value_at(e), e == lead);
+        }
+    }
+}
+
+template <bool BF16, int U>
+void launch_parts(const LogprobArgs &a, hipStream_t s) {
+    logprobs_part_kernel<BF16, U><<<(unsigned)((int64_t)a.B * a.W * a.parts), kNT, 0, s>>>(a);
+}
+
+}  // namespace
+
+// Small parts where big ones would leave CUs without a few workgroups each.
+int logprob_part(int64_t rows, int V, int *parts) {
+    const int part = rows * (V / kPartBig + 1) < 1024 ? kPartSmall : kPartBig;
+    *parts = (V + 7 + part - 1) / part;   // a row may begin up to 7 elements into its first block
+    return part;
+}
+
+hipError_t launch_logprobs(const LogprobArgs &a, hipStream_t s) {
+    if (a.part == kPartBig) {
+        if (a.bf16) launch_parts<true, kPartBig / kNT / 8>(a, s);
+        else launch_parts<false, kPartBig / kNT / 4>(a, s);
+    } else {
+        if (a.bf16) launch_parts<true, kPartSmall / kNT / 8>(a, s);
+        else launch_parts<false, kPartSmall / kNT / 4>(a, s);
+    }
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    logprobs_join_kernel<<<(unsigned)((int64_t)a.B * a.W), kNT, 0, s>>>(a);
+    return hipGetLastError();
+}
+
+}  // namespace replay

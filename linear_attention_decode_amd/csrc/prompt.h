@@ -1,6 +1,6 @@
 // prompt.h -- private declarations of the calls around the recurrence: the
-// inputs' convolution (conv.hip), prompts (scan.hip, scan_mx.hip) and
-// sampling (sample.hip).
+// inputs' convolution (conv.hip), prompts (scan.hip, scan_mx.hip), sampling
+// (sample.hip) and token scores (logprobs.hip).
 #pragma once
 
 #include "internal.h"
@@ -64,7 +64,27 @@ struct SampleArgs {
 constexpr int kMaxVocab = 1 << 18;
 constexpr int kSampleNT = 512;   // threads of a row, a workgroup each
 
+// Scores of tokens (logprobs.hip).
+struct LogprobArgs {
+    int32_t B, W, V, M, n, bf16;   // M given tokens, n alternatives a row
+    const void *logits;            // B W rows of V, stride elements apart
+    int64_t stride;
+    const float *temperature;      // [B] or null
+    const int32_t *ids;            // [B][W][M]
+    float *logp, *entropy;         // [B][W][M]; [B][W] or null
+    int32_t *top_ids;              // [B][W][n], with
+    float *top_logp;               // [B][W][n]
+    uint64_t *ws;                  // [B W][parts][kPartWords + max(n, 1)]
+    int32_t parts, part;           // parts of a row, elements of a part
+};
+constexpr int kMaxTop = 32;
+constexpr int kPartWords = 3;      // a part's sums, ahead of its first tokens
+constexpr int kPartNT = 256;       // threads of a part, and of a row's join
+constexpr int kPartBig = 8192, kPartSmall = 2048;
+int logprob_part(int64_t rows, int V, int *parts);   // elements of a part, and their number
+
 // Launchers (return hipSuccess or the launch error).
+hipError_t launch_logprobs(const LogprobArgs &a, hipStream_t s);
 hipError_t launch_sample(const SampleArgs &a, hipStream_t s);
 hipError_t launch_scan(int P, int N, const ScanArgs &a, hipStream_t s);
 int scan_segments(int P, int N, int B, int H, int G, bool bf16, int T, int max_len, int *seg_len);   // the number of segments, and their length
