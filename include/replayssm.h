@@ -78,6 +78,8 @@ typedef enum {
 #define REPLAY_SEQERR_TOO_FEW        4  /* decode / verify(W) with count < W; y of that sequence is NaN */
 #define REPLAY_SEQERR_POS_OVERFLOW   8  /* append would take pos past 2^31 - 1 */
 #define REPLAY_SEQERR_BAD_RANGE     16  /* prompts: a sequence's range decreases, leaves 0..T or is too long */
+#define REPLAY_SEQERR_BAD_TREE      32  /* trees: a node's parent is no earlier node, a path leaves the nodes, or a
+                                           sequence has less than 0 or more than W of them */
 
 typedef enum {
     REPLAY_NONE = -1,
@@ -543,6 +545,84 @@ replay_status replay_logprobs(int32_t B, int32_t W, int32_t V, const void *logit
                               int64_t row_stride, const float *temperature, int32_t n_given, const int32_t *ids,
                               float *logp, float *entropy, int32_t n_top, int32_t *top_ids, float *top_logp,
                               void *workspace, size_t workspace_bytes, void *stream);
+
+/* ---- Gated DeltaNet layers: from the convolution to the gated delta rule ----
+   What such a layer does with its convolution's queries and keys, and with the
+   two scalars of its projection (background to the pages):
+       q = q_scale q_in / sqrt(q_in . q_in + eps),   k = k_in / sqrt(k_in . k_in + eps),
+       beta = 1 / (1 + exp(-b_raw)),   alpha = exp(-exp(a_log) softplus(a_raw + dt_bias)),
+   for T rows: of packed prompts, or of the B W tokens or nodes of a round.
+   q_in, k_in, q, k: [T][G][N] (io dtype; q may be q_in and k k_in).  b_raw,
+   a_raw: H values a row in the io dtype, rows b_stride and a_stride apart.
+   dt_bias (or NULL) and a_log: [H] f32.  beta, alpha: [T][H] f32, which take
+   the places of dt and a.  Sums are float32, and the squares' sum has to be
+   finite there; every row is written.  Gated DeltaNet layers only. */
+replay_status replay_delta_inputs(const replay_config *cfg, int32_t T, const void *q_in, const void *k_in,
+                                  const void *b_raw, int64_t b_stride, const void *a_raw, int64_t a_stride,
+                                  const float *dt_bias, const float *a_log, float q_scale, float eps, void *q, void *k,
+                                  float *beta, float *alpha, void *stream);
+
+/* ---- trees of drafted tokens -------------------------------------------------
+   A round that drafts alternatives: sequence b has n_nodes[b] <= W nodes (device
+   int32 [B], NULL: W each), node w behind node parent[b][w] < w, or behind the
+   sequence's newest token where that is -1 (device int32 [B][W]).  1 <= W <= 64.
+   A node sees the ring and the nodes on its own path, itself among them (page
+   "ReplaySSM: Cachear Inputs, No Estado", section "Paralelismo": an entry is
+   visible to a position when it lies before it).  The ring does not take the
+   nodes; a round is
+       replay_conv_tree, replay_verify_tree  outputs of all nodes
+       replay_sample                         a token behind each
+       replay_accept_tree                    the path that they confirm
+       replay_conv_path, replay_append_path  that path into the two states
+   with a replay_flush ahead of it where the ring may not hold a whole path.
+   Nodes past n_nodes[b]: their inputs are not used, their outputs left as they
+   are.  A sequence that is no tree (n_nodes outside 0..W, a parent outside
+   -1..w - 1) gets BAD_TREE.
+
+   replay_conv_tree: replay_conv_step for the nodes, each behind its ancestors and, past
+   its path's first, the state's rows before pos[b].  x: [B W] rows, dt_raw
+   likewise or NULL; outputs q, k [B][W][G][N], v [B][W][H][P], dt, a [B][W][H],
+   left as they are for a sequence that is no tree.  conv_state is read alone. */
+replay_status replay_conv_tree(const replay_config *cfg, const replay_conv_params *conv, int32_t W,
+                               const int32_t *parent, const int32_t *n_nodes, const void *x, int64_t x_stride,
+                               const void *dt_raw, int64_t dt_stride, const int32_t *pos, const void *conv_state,
+                               void *q, void *k, void *v, float *dt, float *a, int32_t *err, void *stream);
+
+/* Outputs of all nodes against one read of the checkpoint (or its copy), no
+   state or pointer written.  q, k: [B][W][G][N], v: [B][W][H][P] (io dtype);
+   dt, a: [B][W][H] f32 (beta, alpha for Gated DeltaNet layers); y: [B][W][H][P]
+   f32, 16-byte aligned.  On a chain of nodes this is replay_append(W),
+   replay_verify(W), replay_rollback(W) up to the order of sums.  A node's inputs reach
+   its own and its descendants' outputs alone, whatever they hold.  The ring may be
+   empty.  Sequences with BAD_TREE (or a count outside 0..L: TOO_FEW): y is NaN. */
+replay_status replay_verify_tree(replay_handle *h, int32_t W, const int32_t *parent, const int32_t *n_nodes,
+                                 const void *q, const void *k, const void *v, const float *dt, const float *a, float *y,
+                                 void *stream);
+
+/* The path that sampled tokens confirm: from node 0, which was fed the
+   sequence's last token (fed [B][W]: what the nodes were fed), on to the first
+   child that was fed the token sampled behind its parent (tokens [B][W], as
+   replay_sample gives them for B sequences of W positions; a -1 is no token),
+   while there is one.  path: [B][W] its nodes in order, -1 behind them; n_keep: [B] their number
+   (0 for a sequence of no nodes, or that is no tree).  The sequence goes on
+   with tokens[b][path[b][n_keep[b] - 1]]. */
+replay_status replay_accept_tree(int32_t B, int32_t W, const int32_t *parent, const int32_t *n_nodes,
+                                 const int32_t *tokens, const int32_t *fed, int32_t *path, int32_t *n_keep,
+                                 void *stream);
+
+/* The rows of nodes path[b][0 .. n_keep[b]) into the convolution's state behind
+   its newest, ahead of the replay_append_path that moves pos.  R >= K - 1 serves; R =
+   K - 1 + W keeps the state whole where that append is refused.  A path that leaves
+   0..W - 1 or an n_keep that leaves 0..W: BAD_TREE, the state is left as it is. */
+replay_status replay_conv_path(const replay_config *cfg, const replay_conv_params *conv, int32_t W, const int32_t *path,
+                               const int32_t *n_keep, const void *x, int64_t x_stride, const int32_t *pos,
+                               void *conv_state, int32_t *err, void *stream);
+
+/* replay_append of nodes path[b][0 .. n_keep[b]) in that order, of the arguments
+   that replay_verify_tree had.  BAD_TREE as for replay_conv_path; RING_OVERFLOW and
+   POS_OVERFLOW as for replay_append.  Such a sequence is left unchanged. */
+replay_status replay_append_path(replay_handle *h, int32_t W, const int32_t *path, const int32_t *n_keep, const void *q,
+                                 const void *k, const void *v, const float *dt, const float *a, void *stream);
 
 #ifdef __cplusplus
 }

@@ -25,14 +25,15 @@ __all__ = [
     "replay_eager_step", "replay_eager_select", "replay_stream_probe",
     "ReplayConvParams", "ReplayConv", "SEQERR_BAD_RANGE", "replay_conv_prompt", "replay_conv_step",
     "replay_scan_workspace", "replay_scan", "ReplaySampling", "replay_sample_workspace", "replay_sample",
-    "replay_logprobs_workspace", "replay_logprobs",
+    "replay_logprobs_workspace", "replay_logprobs", "SEQERR_BAD_TREE", "replay_delta_inputs", "replay_conv_tree",
+    "replay_verify_tree", "replay_accept_tree", "replay_conv_path", "replay_append_path",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libreplayssm.so")
 
 NONE, F32, BF16, FP8_E4M3, FP4_E2M1 = -1, 0, 1, 2, 3
 SEQERR_RING_OVERFLOW, SEQERR_ROLLBACK_RANGE, SEQERR_TOO_FEW, SEQERR_POS_OVERFLOW = 1, 2, 4, 8
-SEQERR_BAD_RANGE = 16
+SEQERR_BAD_RANGE, SEQERR_BAD_TREE = 16, 32
 
 # every symbol include/replayssm.h declares
 EXPORTS = (
@@ -43,6 +44,8 @@ EXPORTS = (
     "replay_eager_step", "replay_eager_select", "replay_stream_probe",
     "replay_conv_prompt", "replay_conv_step", "replay_scan_workspace", "replay_scan",
     "replay_sample_workspace", "replay_sample", "replay_logprobs_workspace", "replay_logprobs",
+    "replay_delta_inputs", "replay_conv_tree", "replay_verify_tree", "replay_accept_tree", "replay_conv_path",
+    "replay_append_path",
 )
 
 _VP = ctypes.c_void_p
@@ -117,6 +120,15 @@ def _load():
     L.replay_logprobs_workspace.argtypes = [_I32, _I32, _I32, _I32, ctypes.POINTER(ctypes.c_size_t)]
     L.replay_logprobs.argtypes = ([_I32, _I32, _I32, _VP, _I32, _I64, _VP, _I32, _VP, _VP, _VP, _I32, _VP, _VP, _VP,
                                    ctypes.c_size_t, _VP])
+    L.replay_delta_inputs.argtypes = [ctypes.POINTER(ReplayConfig), _I32, _VP, _VP, _VP, _I64, _VP, _I64, _VP, _VP,
+                                      ctypes.c_float, ctypes.c_float] + [_VP] * 5
+    L.replay_conv_tree.argtypes = ([ctypes.POINTER(ReplayConfig), ctypes.POINTER(ReplayConvParams), _I32, _VP, _VP, _VP,
+                                    _I64, _VP, _I64] + [_VP] * 9)
+    L.replay_verify_tree.argtypes = [_VP, _I32] + [_VP] * 9
+    L.replay_accept_tree.argtypes = [_I32, _I32] + [_VP] * 7
+    L.replay_conv_path.argtypes = [ctypes.POINTER(ReplayConfig), ctypes.POINTER(ReplayConvParams), _I32, _VP, _VP, _VP,
+                                   _I64, _VP, _VP, _VP, _VP]
+    L.replay_append_path.argtypes = [_VP, _I32] + [_VP] * 8
     for name in EXPORTS:
         if name not in ("replay_status_string", "replay_abi_version"):
             getattr(L, name).restype = ctypes.c_int
@@ -466,6 +478,95 @@ def replay_logprobs(logits, ids=None, logp=None, entropy=None, top_ids=None, top
         _want("top_logp", top_logp, (B, W, n), f32, gpu), *_workspace(workspace, gpu), _on(stream, gpu)), "replay_logprobs")
 
 
+# ---- Gated DeltaNet layers' inputs; trees of drafted tokens -------------------
+
+def replay_delta_inputs(cfg, T, q_in, k_in, b_raw, a_raw, dt_bias, a_log, q_scale, eps, q, k, beta, alpha, stream=None):
+    """T rows: q_in, k_in, q, k [T, G, N] (q may be q_in, k k_in); b_raw, a_raw [T, H] may be views into wider rows;
+    dt_bias (or None) and a_log [H] f32; beta, alpha [T, H] f32."""
+    import torch
+    f32, io, gpu = torch.float32, _io_type(cfg), _gpu()
+    H, qk = cfg.heads, (T, cfg.groups, cfg.state_dim)
+    _check(lib.replay_delta_inputs(
+        ctypes.byref(cfg), _size("T", T), _want("q_in", q_in, qk, io, gpu), _want("k_in", k_in, qk, io, gpu),
+        *_rows("b_raw", b_raw, T, H, io, gpu), *_rows("a_raw", a_raw, T, H, io, gpu), _want("dt_bias", dt_bias, (H,), f32, gpu),
+        _want("a_log", a_log, (H,), f32, gpu), q_scale, eps, _want("q", q, qk, io, gpu), _want("k", k, qk, io, gpu),
+        _want("beta", beta, (T, H), f32, gpu), _want("alpha", alpha, (T, H), f32, gpu), _on(stream, gpu)),
+        "replay_delta_inputs")
+
+
+def _tree(parent, n_nodes, B, W, gpu):
+    import torch
+    return _want("parent", parent, (B, W), torch.int32, gpu), _want("n_nodes", n_nodes, (B,), torch.int32, gpu)
+
+
+def _path(path, n_keep, B, W, gpu):
+    import torch
+    return _want("path", path, (B, W), torch.int32, gpu), _want("n_keep", n_keep, (B,), torch.int32, gpu)
+
+
+def _nodes(cfg, W, q, k, v, dt, a, gpu):
+    import torch
+    f32, io, B, H = torch.float32, _io_type(cfg), cfg.batch, cfg.heads
+    qk = (B, W, cfg.groups, cfg.state_dim)
+    return (_want("q", q, qk, io, gpu), _want("k", k, qk, io, gpu), _want("v", v, (B, W, H, cfg.head_dim), io, gpu),
+            _want("dt", dt, (B, W, H), f32, gpu), _want("a", a, (B, W, H), f32, gpu))
+
+
+def replay_conv_tree(cfg, conv, W, parent, x, dt_raw, pos, conv_state, q, k, v, dt, a, err, n_nodes=None, stream=None):
+    """parent [B, W] int32, n_nodes [B] int32 (None: W each); x [B W, C] and dt_raw [B W, H] may be views into wider rows;
+    conv: ReplayConv; dt_raw may be None."""
+    import torch
+    i32, io, gpu, B = torch.int32, _io_type(cfg), _gpu(), cfg.batch
+    rows, outs = _conv_call("replay_conv_tree", cfg, conv, B * W, (B, W), x, dt_raw, q, k, v, dt, a, io, torch.float32,
+                            gpu)
+    _check(lib.replay_conv_tree(
+        ctypes.byref(cfg), ctypes.byref(conv.params), W, *_tree(parent, n_nodes, B, W, gpu), *rows,
+        _want("pos", pos, (B,), i32, gpu), _want("conv_state", conv_state, (B, conv.slots, conv.channels), io, gpu), *outs,
+        _want("err", err, (B + 1,), i32, gpu), _on(stream, gpu)), "replay_conv_tree")
+
+
+def replay_conv_path(cfg, conv, W, path, n_keep, x, pos, conv_state, err, stream=None):
+    """path [B, W] and n_keep [B] as replay_accept_tree gives them; x as for replay_conv_tree."""
+    import torch
+    i32, io, gpu, B = torch.int32, _io_type(cfg), _gpu(), cfg.batch
+    C = cfg.heads * cfg.head_dim + 2 * cfg.groups * cfg.state_dim
+    if conv.channels != C or conv.gpu != gpu:
+        raise ReplayError(f"replay_conv_path: a convolution of {conv.channels} channels on GPU {conv.gpu} for a layer of {C} "
+                          f"on the current one, {gpu}")
+    _check(lib.replay_conv_path(
+        ctypes.byref(cfg), ctypes.byref(conv.params), W, *_path(path, n_keep, B, W, gpu), *_rows("x", x, B * W, C, io, gpu),
+        _want("pos", pos, (B,), i32, gpu), _want("conv_state", conv_state, (B, conv.slots, C), io, gpu),
+        _want("err", err, (B + 1,), i32, gpu), _on(stream, gpu)), "replay_conv_path")
+
+
+def replay_accept_tree(parent, tokens, fed, path, n_keep, n_nodes=None, stream=None):
+    """parent, tokens, fed, path [B, W] and n_keep, n_nodes [B], all int32 (n_nodes None: W each)."""
+    import torch
+    i32, gpu = torch.int32, _gpu()
+    B, W = parent.shape
+    up, n = _tree(parent, n_nodes, B, W, gpu)
+    _check(lib.replay_accept_tree(B, W, up, n, _want("tokens", tokens, (B, W), i32, gpu), _want("fed", fed, (B, W), i32, gpu),
+                                  *_path(path, n_keep, B, W, gpu), _on(stream, gpu)), "replay_accept_tree")
+
+
+# The handle does not tell its shapes: cfg is its layer's.
+
+def replay_verify_tree(h, cfg, W, parent, q, k, v, dt, a, y, n_nodes=None, stream=None):
+    """q, k [B, W, G, N], v [B, W, H, P], dt, a [B, W, H], y [B, W, H, P] f32; cfg: the layer's, its shapes are checked."""
+    import torch
+    gpu = _gpu()
+    _check(lib.replay_verify_tree(h, W, *_tree(parent, n_nodes, cfg.batch, W, gpu), *_nodes(cfg, W, q, k, v, dt, a, gpu),
+                                  _want("y", y, (cfg.batch, W, cfg.heads, cfg.head_dim), torch.float32, gpu),
+                                  _on(stream, gpu)), "replay_verify_tree")
+
+
+def replay_append_path(h, cfg, W, path, n_keep, q, k, v, dt, a, stream=None):
+    """Nodes path[b, :n_keep[b]] of replay_verify_tree's arguments into the ring; cfg: the layer's, its shapes are checked."""
+    gpu = _gpu()
+    _check(lib.replay_append_path(h, W, *_path(path, n_keep, cfg.batch, W, gpu), *_nodes(cfg, W, q, k, v, dt, a, gpu),
+                                  _on(stream, gpu)), "replay_append_path")
+
+
 # ---- one layer's state, allocated with torch -------------------------------
 
 _DTYPE_CODE = {"f32": F32, "bf16": BF16, "fp8": FP8_E4M3, "fp4": FP4_E2M1, None: NONE, "none": NONE}
@@ -574,6 +675,23 @@ class ReplayLayer:
     def scan(self, T, max_len, cu_seqlens, q, k, v, dt, a, s_in, s_out, y, workspace=None, stream=None):
         """The recurrence over packed prompts (replay_scan); load_checkpoint(s_out) makes its states this layer's."""
         replay_scan(self.cfg, T, max_len, cu_seqlens, q, k, v, dt, a, s_in, s_out, y, self.t["err"], workspace, stream)
+
+    def conv_tree(self, conv, W, parent, x, dt_raw, conv_state, q, k, v, dt, a, n_nodes=None, stream=None):
+        """The inputs of a tree of drafts (replay_conv_tree)."""
+        replay_conv_tree(self.cfg, conv, W, parent, x, dt_raw, self.t["pos"], conv_state, q, k, v, dt, a, self.t["err"], n_nodes,
+                         stream)
+
+    def verify_tree(self, W, parent, q, k, v, dt, a, y, n_nodes=None, stream=None):
+        """Outputs of a tree of drafts; the ring and the pointers stay as they are."""
+        replay_verify_tree(self.h, self.cfg, W, parent, q, k, v, dt, a, y, n_nodes, stream)
+
+    def conv_path(self, conv, W, path, n_keep, x, conv_state, stream=None):
+        """The kept path's rows into the convolution's state, ahead of append_path."""
+        replay_conv_path(self.cfg, conv, W, path, n_keep, x, self.t["pos"], conv_state, self.t["err"], stream)
+
+    def append_path(self, W, path, n_keep, q, k, v, dt, a, stream=None):
+        """The kept path of a tree into the ring."""
+        replay_append_path(self.h, self.cfg, W, path, n_keep, q, k, v, dt, a, stream)
 
     def load_checkpoint(self, s_src, stream=None):
         replay_load_checkpoint(self.h, s_src, stream)

@@ -6,7 +6,8 @@
 // fused speculative round), flush.hip and flush_shared.hip (the folds of a
 // float32 master and of a shared low-precision checkpoint), gdn.hip (Gated
 // DeltaNet layers), ring.hip (append, rollback, fills), conv.hip (the
-// convolution and discretisation ahead of the recurrence), scan.hip (the
+// convolution and discretisation ahead of the recurrence), delta_inputs.hip
+// (what a Gated DeltaNet layer has there), tree*.hip (trees of drafts), scan.hip (the
 // recurrence over prompts), sample.hip and logprobs.hip (tokens from logits,
 // and their scores), eager.hip and probe.hip.
 #include <hip/hip_runtime.h>
@@ -19,6 +20,7 @@
 #include "count_bound.h"
 #include "internal.h"
 #include "prompt.h"
+#include "tree.h"
 
 using namespace replay;
 
@@ -979,6 +981,166 @@ replay_status replay_logprobs(int32_t B, int32_t W, int32_t V, const void *logit
     a.top_logp = top_logp;
     a.ws = static_cast<uint64_t *>(workspace);
     return from_hip(launch_logprobs(a, as_stream(stream)));
+}
+
+}  // extern "C"
+
+namespace {
+
+// What the tree calls ask of a tree's arguments.
+bool tree_args_ok(int32_t W, const int32_t *parent, const int32_t *n_nodes) {
+    return W >= 1 && parent && aligned4(parent) && aligned4(n_nodes);
+}
+
+}  // namespace
+
+extern "C" {
+
+replay_status replay_conv_tree(const replay_config *cfg, const replay_conv_params *conv, int32_t W,
+                               const int32_t *parent, const int32_t *n_nodes, const void *x, int64_t x_stride,
+                               const void *dt_raw, int64_t dt_stride, const int32_t *pos, const void *conv_state,
+                               void *q, void *k, void *v, float *dt, float *a, int32_t *err, void *stream) {
+    ConvArgs c;
+    const replay_status st = conv_args(cfg, conv, x, x_stride, dt_raw, dt_stride, q, k, v, dt, a, &c);
+    if (st != REPLAY_OK) return st;
+    if (!tree_args_ok(W, parent, n_nodes) || !pos || !aligned4(pos) || !conv_state || !aligned16(conv_state) || !err ||
+        !aligned4(err))
+        return REPLAY_ERR_INVALID_ARG;
+    if (W > kMaxTree || (int64_t)cfg->batch * W > INT32_MAX) return REPLAY_ERR_UNSUPPORTED;
+    c.W = W;
+    c.pos = pos;
+    c.state_out = const_cast<void *>(conv_state);   // (read only)
+    c.err = err;
+    c.parent = parent;
+    c.n_nodes = n_nodes;
+    return from_conv(launch_conv_tree(c, as_stream(stream)));
+}
+
+replay_status replay_conv_path(const replay_config *cfg, const replay_conv_params *conv, int32_t W, const int32_t *path,
+                               const int32_t *n_keep, const void *x, int64_t x_stride, const int32_t *pos,
+                               void *conv_state, int32_t *err, void *stream) {
+    ConvArgs c;
+    // (the outputs are not written: the state stands in for them in the checks)
+    const replay_status st =
+        conv_args(cfg, conv, x, x_stride, nullptr, 0, conv_state, conv_state, conv_state, nullptr, nullptr, &c);
+    if (st != REPLAY_OK) return st;
+    if (!tree_args_ok(W, path, n_keep) || !n_keep || !pos || !aligned4(pos) || !err || !aligned4(err))
+        return REPLAY_ERR_INVALID_ARG;
+    if (W > kMaxTree || (int64_t)cfg->batch * W > INT32_MAX) return REPLAY_ERR_UNSUPPORTED;
+    c.W = W;
+    c.pos = pos;
+    c.state_out = conv_state;
+    c.err = err;
+    c.path = path;
+    c.n_keep = n_keep;
+    return from_conv(launch_conv_tree(c, as_stream(stream)));
+}
+
+replay_status replay_accept_tree(int32_t B, int32_t W, const int32_t *parent, const int32_t *n_nodes,
+                                 const int32_t *tokens, const int32_t *fed, int32_t *path, int32_t *n_keep,
+                                 void *stream) {
+    if (B < 1 || !tree_args_ok(W, parent, n_nodes)) return REPLAY_ERR_INVALID_ARG;
+    for (const int32_t *p : {tokens, fed, static_cast<const int32_t *>(path), static_cast<const int32_t *>(n_keep)})
+        if (!p || !aligned4(p)) return REPLAY_ERR_INVALID_ARG;
+    if (W > kMaxTree || !launch_fits(B, 64)) return REPLAY_ERR_UNSUPPORTED;
+    return from_hip(launch_accept_tree(B, W, parent, n_nodes, tokens, fed, path, n_keep, as_stream(stream)));
+}
+
+replay_status replay_verify_tree(replay_handle *h, int32_t W, const int32_t *parent, const int32_t *n_nodes,
+                                 const void *q, const void *k, const void *v, const float *dt, const float *a, float *y,
+                                 void *stream) {
+    if (!h || !tree_args_ok(W, parent, n_nodes)) return REPLAY_ERR_INVALID_ARG;
+    for (const void *p : {q, k, v, static_cast<const void *>(y)})
+        if (!p || !aligned16(p)) return REPLAY_ERR_INVALID_ARG;
+    for (const float *p : {dt, a})
+        if (!p || !aligned4(p)) return REPLAY_ERR_INVALID_ARG;
+    const replay_config &c = h->cfg;
+    if (W > kMaxTree || !launch_fits((int64_t)c.batch * c.heads, 4 * c.head_dim)) return REPLAY_ERR_UNSUPPORTED;
+    TreeArgs t{};
+    t.r = ring_view(h);
+    t.S = c.read_copy == REPLAY_NONE ? static_cast<const void *>(h->bufs.s_master) : h->bufs.s_copy;
+    t.scale = h->bufs.s_scale;
+    t.parent = parent;
+    t.n_nodes = n_nodes;
+    t.q = q;
+    t.k = k;
+    t.v = v;
+    t.dt = dt;
+    t.a = a;
+    t.y = y;
+    t.W = W;
+    const bool delta = c.rule == REPLAY_RULE_GATED_DELTA, bf16 = c.io_dtype == REPLAY_BF16;
+    auto *launch = delta ? (bf16 ? launch_tree_delta_bf16 : launch_tree_delta_f32)
+                         : (bf16 ? launch_tree_mamba2_bf16 : launch_tree_mamba2_f32);
+    return from_hip(launch(c.head_dim, c.state_dim, state_kind(c.read_copy), t, as_stream(stream)));
+}
+
+replay_status replay_append_path(replay_handle *h, int32_t W, const int32_t *path, const int32_t *n_keep, const void *q,
+                                 const void *k, const void *v, const float *dt, const float *a, void *stream) {
+    if (!h || !h->bufs.sync || !tree_args_ok(W, path, n_keep) || !n_keep) return REPLAY_ERR_INVALID_ARG;
+    for (const void *p : {q, k, v})
+        if (!p || !aligned16(p)) return REPLAY_ERR_INVALID_ARG;
+    for (const float *p : {dt, a})
+        if (!p || !aligned4(p)) return REPLAY_ERR_INVALID_ARG;
+    if (W > kMaxTree) return REPLAY_ERR_UNSUPPORTED;
+    hipStream_t s = as_stream(stream);
+    note_capture(h, s);
+    TreeArgs t{};
+    t.r = ring_view(h);
+    t.q = q;
+    t.k = k;
+    t.v = v;
+    t.dt = dt;
+    t.a = a;
+    t.W = W;
+    const hipError_t e = launch_append_path(h->cfg.head_dim, h->cfg.state_dim, t, path, n_keep, h->bufs.ring_q,
+                                            h->bufs.ring_k, h->bufs.ring_v, h->bufs.ring_dt, h->bufs.ring_a,
+                                            h->bufs.pos, h->bufs.sync, s);
+    if (e != hipSuccess) {
+        h->bound.unknown();
+        return REPLAY_ERR_HIP;
+    }
+    h->bound.append_some(W < h->cfg.ring_len ? W : h->cfg.ring_len);
+    return REPLAY_OK;
+}
+
+replay_status replay_delta_inputs(const replay_config *cfg, int32_t T, const void *q_in, const void *k_in,
+                                  const void *b_raw, int64_t b_stride, const void *a_raw, int64_t a_stride,
+                                  const float *dt_bias, const float *a_log, float q_scale, float eps, void *q, void *k,
+                                  float *beta, float *alpha, void *stream) {
+    const replay_status st = check_shape(cfg);
+    if (st != REPLAY_OK) return st;
+    if (cfg->rule != REPLAY_RULE_GATED_DELTA) return REPLAY_ERR_UNSUPPORTED;
+    if (T < 1 || !(eps >= 0.f) || !(q_scale - q_scale == 0.f) || !(eps - eps == 0.f)) return REPLAY_ERR_INVALID_ARG;
+    for (const void *p : {q_in, k_in, static_cast<const void *>(q), static_cast<const void *>(k)})
+        if (!p || !aligned16(p)) return REPLAY_ERR_INVALID_ARG;
+    const size_t io_mask = io_bytes(*cfg) - 1;
+    for (const void *p : {b_raw, a_raw})
+        if (!p || (reinterpret_cast<uintptr_t>(p) & io_mask)) return REPLAY_ERR_INVALID_ARG;
+    if (b_stride < cfg->heads || a_stride < cfg->heads || !a_log || !aligned4(a_log) || !aligned4(dt_bias) || !beta ||
+        !alpha || !aligned4(beta) || !aligned4(alpha))
+        return REPLAY_ERR_INVALID_ARG;
+    DeltaInputsArgs d{};
+    d.T = T;
+    d.H = cfg->heads;
+    d.G = cfg->groups;
+    d.N = cfg->state_dim;
+    d.io_bf16 = cfg->io_dtype == REPLAY_BF16;
+    d.q_in = q_in;
+    d.k_in = k_in;
+    d.q = q;
+    d.k = k;
+    d.b_raw = b_raw;
+    d.a_raw = a_raw;
+    d.b_stride = b_stride;
+    d.a_stride = a_stride;
+    d.dt_bias = dt_bias;
+    d.a_log = a_log;
+    d.q_scale = q_scale;
+    d.eps = eps;
+    d.beta = beta;
+    d.alpha = alpha;
+    return from_conv(launch_delta_inputs(d, as_stream(stream)));
 }
 
 }  // extern "C"

@@ -21,8 +21,7 @@
 // sequences 9.3 us, 3.4 TB/s of 32 MB (float32: 12.8 us, 64 MB), and of one 3.7
 // us, a launch and one chain of loads; windows of 5 drafts, 64 heads, 15.6 us
 // (float32 20).
-#include "device_common.h"
-#include "prompt.h"
+#include "tree_common.h"
 
 namespace replay {
 
@@ -40,6 +39,8 @@ constexpr int kAhead = 8;     // rows a thread loads before it uses the first
 // its exponentials and logarithms are a chain, and 32 of them (64 tokens of
 // 128 heads) took 25 us, the whole time of a short prompt.
 constexpr int kGates = 1024;
+constexpr int kTreeGates = 256;        // (node, head) pairs of a workgroup that makes dt and a
+constexpr int kManyTreeBlocks = 2048;  // workgroups of 16 nodes from which on they need not be split
 
 // 16 bytes of io elements as floats, by one load where the row is 16-byte
 // aligned and element by element otherwise.
@@ -376,6 +377,94 @@ __global__ __launch_bounds__(kStepNT) void conv_step_kernel(ConvArgs a, int CB) 
     }
 }
 
+// The nodes of a tree: workgroups [0, B CB NB) take `per` nodes' channels of
+// a sequence each, the rest 64 (node, head) pairs' dt and a a thread block.  A
+// node's K rows are read where they lie, its own and its ancestors' in x and
+// those before the tree in the state: neighbours in a tree find them in the
+// caches, and no load waits for another.
+template <bool BF16, bool AL, int K>
+__global__ __launch_bounds__(kStepNT) void conv_tree_kernel(ConvArgs a, int CB, int NB, int per, int gates) {
+    constexpr int E = BF16 ? 8 : 4, U = 4;
+    const int lane = threadIdx.x;
+    int id = blockIdx.x;
+    const bool gate = id >= a.B * CB * NB;
+    if (gate) id -= a.B * CB * NB;
+    const int b = gate ? id / gates : id / (CB * NB);
+    Tree tree;
+    tree.load(a.parent, a.n_nodes, b, a.W, lane);
+    if (!tree.ok) {
+        if (!gate && id % (CB * NB) == 0 && lane == 0) raise_seq_error(a.err, b, REPLAY_SEQERR_BAD_TREE);
+        return;
+    }
+    if (gate) {
+        for (int i = id % gates * kTreeGates + lane; i < (id % gates + 1) * kTreeGates && i < tree.n * a.H; i += kStepNT)
+            discretise<BF16>(a, (size_t)b * a.W + i / a.H, i % a.H);
+        return;
+    }
+    int from[K];   // lane w: where the K rows of node w are
+    from[0] = lane;
+#pragma unroll
+    for (int d = 1; d < K; ++d) from[d] = tree.up(from[d - 1]);
+    const int w0 = id % NB * per, c0 = (id / NB % CB * kStepNT + lane) * E;
+    const bool in = c0 < a.C;
+    Channels<BF16, K> ch;
+    if (in) ch.init(a, c0);
+    const int pm = (int)((uint32_t)a.pos[b] % (uint32_t)a.R);
+    for (int i0 = w0; i0 < w0 + per && i0 < tree.n; i0 += U) {
+        Row<BF16, AL> rows[U][K];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int w = i0 + u < tree.n ? i0 + u : tree.n - 1;
+#pragma unroll
+            for (int d = 0; d < K; ++d) {
+                const int f = __builtin_amdgcn_readlane(from[d], w);
+                int slot = pm + f;
+                slot += slot < 0 ? a.R : 0;
+                if (in) {
+                    if (f >= 0)
+                        rows[u][d].load(a.x, ((size_t)b * a.W + f) * a.x_stride + c0);
+                    else
+                        rows[u][d].load(a.state_out, ((size_t)b * a.R + slot) * a.C + c0);
+                }
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (!in || i0 + u >= tree.n || i0 + u >= w0 + per) break;
+            float hist[K - 1][E], x[E];
+#pragma unroll
+            for (int d = 1; d < K; ++d) rows[u][d].widen(hist[K - 1 - d]);
+            rows[u][0].widen(x);
+            ch.apply(hist, x, (size_t)b * a.W + i0 + u);
+        }
+    }
+}
+
+// The rows of a tree's kept path into the state, behind its newest.
+template <bool BF16, bool AL>
+__global__ __launch_bounds__(kStepNT) void conv_path_kernel(ConvArgs a, int CB) {
+    constexpr int E = BF16 ? 8 : 4;
+    const int b = blockIdx.x / CB, lane = threadIdx.x, c0 = (blockIdx.x % CB * kStepNT + lane) * E;
+    const int n = a.n_keep[b];
+    const int node = lane < a.W ? a.path[(size_t)b * a.W + lane] : 0;
+    if (n < 0 || n > a.W || __any(lane < n && (node < 0 || node >= a.W))) {
+        if (blockIdx.x % CB == 0 && lane == 0) raise_seq_error(a.err, b, REPLAY_SEQERR_BAD_TREE);
+        return;
+    }
+    int slot = (int)((uint32_t)a.pos[b] % (uint32_t)a.R);
+    for (int i = 0; i < n; ++i) {
+        const int f = __builtin_amdgcn_readlane(node, i);
+        if (i + a.R >= n && c0 < a.C) {   // no later row takes this slot
+            Row<BF16, AL> r;
+            float x[E];
+            r.load(a.x, ((size_t)b * a.W + f) * a.x_stride + c0);
+            r.widen(x);
+            store_row<BF16, E>(a.state_out, ((size_t)b * a.R + slot) * a.C + c0, x);
+        }
+        slot = slot + 1 == a.R ? 0 : slot + 1;
+    }
+}
+
 bool rows_aligned(const ConvArgs &a) {
     const size_t esz = a.io_bf16 ? 2 : 4;
     return (reinterpret_cast<uintptr_t>(a.x) & 15u) == 0 && (a.x_stride * esz) % 16 == 0;
@@ -384,6 +473,33 @@ bool rows_aligned(const ConvArgs &a) {
 // Sequences a thread of the step takes: several where one each makes more
 // workgroups of single tokens than the card holds at a time (32 a CU).
 constexpr int kShare = 4, kManyGroups = 2048;
+
+template <bool BF16, bool AL, int K>
+hipError_t launch_tree(const ConvArgs &a, hipStream_t s) {
+    constexpr int E = BF16 ? 8 : 4;
+    const int64_t cb = (a.C / E + kStepNT - 1) / kStepNT;
+    const int per = (int64_t)a.B * cb * ((a.W + 15) / 16) < kManyTreeBlocks ? 4 : 16;
+    const int64_t nb = (a.W + per - 1) / per;
+    const int64_t gates = a.dt_raw ? ((int64_t)a.W * a.H + kTreeGates - 1) / kTreeGates : 0;
+    const int64_t blocks = a.B * (cb * nb + gates);
+    if (!launch_fits(blocks, kStepNT)) return hipErrorInvalidConfiguration;
+    conv_tree_kernel<BF16, AL, K><<<(unsigned)blocks, kStepNT, 0, s>>>(a, (int)cb, (int)nb, per, (int)gates);
+    return hipGetLastError();
+}
+
+template <bool BF16, bool AL>
+hipError_t launch_tree_width(const ConvArgs &a, hipStream_t s) {
+    if (a.path) {
+        const int64_t cb = (a.C / (BF16 ? 8 : 4) + kStepNT - 1) / kStepNT;
+        if (!launch_fits(a.B * cb, kStepNT)) return hipErrorInvalidConfiguration;
+        conv_path_kernel<BF16, AL><<<(unsigned)(a.B * cb), kStepNT, 0, s>>>(a, (int)cb);
+        return hipGetLastError();
+    }
+    if (a.K == 2) return launch_tree<BF16, AL, 2>(a, s);
+    if (a.K == 3) return launch_tree<BF16, AL, 3>(a, s);
+    if (a.K == 4) return launch_tree<BF16, AL, 4>(a, s);
+    return hipErrorInvalidValue;
+}
 
 template <bool BF16, bool AL, int K>
 hipError_t launch_one(const ConvArgs &a, bool step, hipStream_t s) {
@@ -425,5 +541,11 @@ hipError_t launch_conv(const ConvArgs &a, bool step, hipStream_t s) {
 
 hipError_t launch_conv_prompt(const ConvArgs &a, hipStream_t s) { return launch_conv(a, false, s); }
 hipError_t launch_conv_step(const ConvArgs &a, hipStream_t s) { return launch_conv(a, true, s); }
+
+hipError_t launch_conv_tree(const ConvArgs &a, hipStream_t s) {
+    const bool al = rows_aligned(a);
+    if (a.io_bf16) return al ? launch_tree_width<true, true>(a, s) : launch_tree_width<true, false>(a, s);
+    return al ? launch_tree_width<false, true>(a, s) : launch_tree_width<false, false>(a, s);
+}
 
 }  // namespace replay

@@ -69,6 +69,12 @@ struct CountBound {
         pos += W;
     }
 
+    // append of 0 to W tokens, as many as the device knows
+    void append_some(int32_t W) {
+        hi = min2(hi + W, L);
+        pos += W;
+    }
+
     // flush(m): sequences with count >= max(m, 1) fold (count 0)
     bool flush_may_fold(int32_t min_count) const { return hi >= need(min_count); }
     void flush(int32_t min_count) {

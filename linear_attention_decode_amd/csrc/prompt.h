@@ -31,6 +31,21 @@ struct ConvArgs {
     void *q, *k, *v;
     float *dt, *a;
     int32_t *err;
+    const int32_t *parent, *n_nodes;   // trees: [B][W], [B] or null
+    const int32_t *path, *n_keep;      // a kept path into the state: [B][W], [B]
+};
+constexpr int kMaxTree = 64;   // nodes of a tree: a lane each
+
+// A Gated DeltaNet layer's inputs (delta_inputs.hip): T rows.
+struct DeltaInputsArgs {
+    int32_t T, H, G, N, io_bf16;
+    const void *q_in, *k_in;           // [T][G][N]
+    void *q, *k;
+    const void *b_raw, *a_raw;         // T rows of H, b_stride, a_stride elements apart
+    int64_t b_stride, a_stride;
+    const float *dt_bias, *a_log;      // [H]
+    float q_scale, eps;
+    float *beta, *alpha;               // [T][H]
 };
 
 // The recurrence over packed prompts (scan.hip).
@@ -91,5 +106,10 @@ int scan_segments(int P, int N, int B, int H, int G, bool bf16, int T, int max_l
 // hipErrorInvalidConfiguration: more workgroups than a launch numbers
 hipError_t launch_conv_prompt(const ConvArgs &a, hipStream_t s);
 hipError_t launch_conv_step(const ConvArgs &a, hipStream_t s);
+hipError_t launch_conv_tree(const ConvArgs &a, hipStream_t s);   // with path: the kept rows into the state
+hipError_t launch_delta_inputs(const DeltaInputsArgs &a, hipStream_t s);
+// the path that sampled tokens confirm (tree.hip)
+hipError_t launch_accept_tree(int B, int W, const int32_t *parent, const int32_t *n_nodes, const int32_t *tokens,
+                              const int32_t *fed, int32_t *path, int32_t *n_keep, hipStream_t s);
 
 }  // namespace replay

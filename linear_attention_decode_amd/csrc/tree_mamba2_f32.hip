@@ -1,0 +1,8 @@
+// tree_mamba2_f32.hip -- the tree kernels of Mamba-2 layers with float32 io.
+#include "tree_impl.h"
+
+namespace replay {
+hipError_t launch_tree_mamba2_f32(int P, int N, int st, const TreeArgs &a, hipStream_t s) {
+    return launch_tree<false, false>(P, N, st, a, s);
+}
+}  // namespace replay

@@ -88,3 +88,40 @@ def sample(x, u, T=1.0, top_k=0, top_p=1.0, min_p=0.0):
         if upto > target:
             return i, w[i] / total
     raise AssertionError("no token")
+
+
+def unit(x, eps, scale=1.0):
+    """Rows to unit length."""
+    return scale * x / np.sqrt((x * x).sum(-1, keepdims=True) + eps)
+
+
+def delta_gates(b_raw, a_raw, dt_bias, a_log):
+    """beta = sigmoid(b_raw), alpha = exp(-exp(a_log) softplus(a_raw + dt_bias))."""
+    return 1 / (1 + np.exp(-b_raw)), discretise(a_raw, dt_bias, a_log)[1]
+
+
+def delta_scan(q, k, v, beta, alpha, S):
+    """The gated delta rule over one sequence, token after token; shapes as for scan()."""
+    H, G = v.shape[1], q.shape[1]
+    y = np.zeros(v.shape)
+    S = S.copy()
+    for t in range(len(v)):
+        kk, qq = np.repeat(k[t], H // G, 0), np.repeat(q[t], H // G, 0)
+        S = alpha[t][:, None, None] * S
+        miss = v[t] - np.einsum("hpn,hn->hp", S, kk)
+        S = S + (beta[t][:, None] * miss)[:, :, None] * kk[:, None, :]
+        y[t] = np.einsum("hpn,hn->hp", S, qq)
+    return y, S
+
+
+def delta_size(q, k, v, beta, alpha, S):
+    """A bound on |y| and on the rows' norms of S where |k| <= 1 and 0 <= beta <= 1: the rule's erasure, I - beta k k^T,
+    lengthens no row, so a row's norm is at most |alpha| of what it was and beta |v| |k| more.  (y [n, H, P], rows [H, P])"""
+    H, G = v.shape[1], q.shape[1]
+    y = np.zeros(v.shape)
+    z = np.sqrt((S * S).sum(-1))
+    for t in range(len(v)):
+        kn, qn = (np.repeat(np.sqrt((x[t] ** 2).sum(-1)), H // G)[:, None] for x in (k, q))
+        z = np.abs(alpha[t])[:, None] * z + np.abs(beta[t][:, None] * v[t]) * kn
+        y[t] = z * qn
+    return y, z
