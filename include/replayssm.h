@@ -562,6 +562,24 @@ replay_status replay_delta_inputs(const replay_config *cfg, int32_t T, const voi
                                   const float *dt_bias, const float *a_log, float q_scale, float eps, void *q, void *k,
                                   float *beta, float *alpha, void *stream);
 
+/* ---- Gated DeltaNet layers: prompts --------------------------------------------
+   The gated delta rule (replay_rule) over packed prompts, as replay_scan runs
+   the Mamba-2 recurrence: the same arguments, layouts, ranges and errors, dt and
+   a carrying beta and alpha.  Keys of at most unit length, 0 <= beta <= 2 and
+   |alpha| <= 1 keep the rule from growing and are always right; beyond them the
+   corrections of 64 consecutive tokens and the products of their alphas have
+   to be finite in float32.  Sums, corrections and states are float32 (with bf16 io
+   products take parts that hold 24 bits of them), y is rounded once to the io dtype.
+   What is not finite in an input reaches the outputs and states that the rule lets
+   it reach, and no others (an infinity may arrive as NaN).
+   workspace: as for replay_scan, by replay_delta_scan_workspace.  Gated DeltaNet
+   layers only (Mamba-2: UNSUPPORTED). */
+replay_status replay_delta_scan_workspace(const replay_config *cfg, int32_t T, int32_t max_len, size_t *bytes);
+replay_status replay_delta_scan(const replay_config *cfg, int32_t T, int32_t max_len, const int32_t *cu_seqlens,
+                                const void *q, const void *k, const void *v, const float *beta, const float *alpha,
+                                const float *s_in, float *s_out, void *y, int32_t *err, void *workspace,
+                                size_t workspace_bytes, void *stream);
+
 /* ---- trees of drafted tokens -------------------------------------------------
    A round that drafts alternatives: sequence b has n_nodes[b] <= W nodes (device
    int32 [B], NULL: W each), node w behind node parent[b][w] < w, or behind the

@@ -27,6 +27,7 @@ __all__ = [
     "replay_scan_workspace", "replay_scan", "ReplaySampling", "replay_sample_workspace", "replay_sample",
     "replay_logprobs_workspace", "replay_logprobs", "SEQERR_BAD_TREE", "replay_delta_inputs", "replay_conv_tree",
     "replay_verify_tree", "replay_accept_tree", "replay_conv_path", "replay_append_path",
+    "replay_delta_scan_workspace", "replay_delta_scan",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libreplayssm.so")
@@ -45,7 +46,7 @@ EXPORTS = (
     "replay_conv_prompt", "replay_conv_step", "replay_scan_workspace", "replay_scan",
     "replay_sample_workspace", "replay_sample", "replay_logprobs_workspace", "replay_logprobs",
     "replay_delta_inputs", "replay_conv_tree", "replay_verify_tree", "replay_accept_tree", "replay_conv_path",
-    "replay_append_path",
+    "replay_append_path", "replay_delta_scan_workspace", "replay_delta_scan",
 )
 
 _VP = ctypes.c_void_p
@@ -122,6 +123,8 @@ def _load():
                                    ctypes.c_size_t, _VP])
     L.replay_delta_inputs.argtypes = [ctypes.POINTER(ReplayConfig), _I32, _VP, _VP, _VP, _I64, _VP, _I64, _VP, _VP,
                                       ctypes.c_float, ctypes.c_float] + [_VP] * 5
+    L.replay_delta_scan_workspace.argtypes = L.replay_scan_workspace.argtypes
+    L.replay_delta_scan.argtypes = L.replay_scan.argtypes
     L.replay_conv_tree.argtypes = ([ctypes.POINTER(ReplayConfig), ctypes.POINTER(ReplayConvParams), _I32, _VP, _VP, _VP,
                                     _I64, _VP, _I64] + [_VP] * 9)
     L.replay_verify_tree.argtypes = [_VP, _I32] + [_VP] * 9
@@ -382,12 +385,15 @@ def replay_conv_step(cfg, conv, W, x, dt_raw, pos, conv_state, q, k, v, dt, a, b
         "replay_conv_step")
 
 
+def _scan_workspace(what, cfg, T, max_len) -> int:
+    n = ctypes.c_size_t()
+    _check(getattr(lib, what)(ctypes.byref(cfg), _size("T", T), _size("max_len", max_len), ctypes.byref(n)), what)
+    return n.value
+
+
 def replay_scan_workspace(cfg, T, max_len) -> int:
     """Bytes of workspace that replay_scan needs for T rows, up to max_len of them a sequence."""
-    n = ctypes.c_size_t()
-    _check(lib.replay_scan_workspace(ctypes.byref(cfg), _size("T", T), _size("max_len", max_len), ctypes.byref(n)),
-           "replay_scan_workspace")
-    return n.value
+    return _scan_workspace("replay_scan_workspace", cfg, T, max_len)
 
 
 def _workspace(t, gpu):
@@ -399,17 +405,22 @@ def _workspace(t, gpu):
     return t.data_ptr(), t.numel() * t.element_size()
 
 
-def replay_scan(cfg, T, max_len, cu_seqlens, q, k, v, dt, a, s_in, s_out, y, err, workspace=None, stream=None):
-    """Packed prompts: q, k [T, G, N], v and y [T, H, P], dt, a [T, H]; s_in may be None (zeros)."""
+def _scan(what, cfg, T, max_len, cu_seqlens, q, k, v, dt, a, s_in, s_out, y, err, workspace, stream, names):
     import torch
     f32, i32, io, gpu = torch.float32, torch.int32, _io_type(cfg), _gpu()
     B, H, G, P, N = cfg.batch, cfg.heads, cfg.groups, cfg.head_dim, cfg.state_dim
-    _check(lib.replay_scan(
+    _check(getattr(lib, what)(
         ctypes.byref(cfg), _size("T", T), _size("max_len", max_len), _want("cu_seqlens", cu_seqlens, (B + 1,), i32, gpu),
         _want("q", q, (T, G, N), io, gpu), _want("k", k, (T, G, N), io, gpu), _want("v", v, (T, H, P), io, gpu),
-        _want("dt", dt, (T, H), f32, gpu), _want("a", a, (T, H), f32, gpu), _want("s_in", s_in, (B, H, P, N), f32, gpu),
-        _want("s_out", s_out, (B, H, P, N), f32, gpu), _want("y", y, (T, H, P), io, gpu),
-        _want("err", err, (B + 1,), i32, gpu), *_workspace(workspace, gpu), _on(stream, gpu)), "replay_scan")
+        _want(names[0], dt, (T, H), f32, gpu), _want(names[1], a, (T, H), f32, gpu),
+        _want("s_in", s_in, (B, H, P, N), f32, gpu), _want("s_out", s_out, (B, H, P, N), f32, gpu),
+        _want("y", y, (T, H, P), io, gpu), _want("err", err, (B + 1,), i32, gpu), *_workspace(workspace, gpu),
+        _on(stream, gpu)), what)
+
+
+def replay_scan(cfg, T, max_len, cu_seqlens, q, k, v, dt, a, s_in, s_out, y, err, workspace=None, stream=None):
+    """Packed prompts: q, k [T, G, N], v and y [T, H, P], dt, a [T, H]; s_in may be None (zeros)."""
+    _scan("replay_scan", cfg, T, max_len, cu_seqlens, q, k, v, dt, a, s_in, s_out, y, err, workspace, stream, ("dt", "a"))
 
 
 def replay_sample_workspace(B, W, V) -> int:
@@ -492,6 +503,17 @@ def replay_delta_inputs(cfg, T, q_in, k_in, b_raw, a_raw, dt_bias, a_log, q_scal
         _want("a_log", a_log, (H,), f32, gpu), q_scale, eps, _want("q", q, qk, io, gpu), _want("k", k, qk, io, gpu),
         _want("beta", beta, (T, H), f32, gpu), _want("alpha", alpha, (T, H), f32, gpu), _on(stream, gpu)),
         "replay_delta_inputs")
+
+
+def replay_delta_scan_workspace(cfg, T, max_len) -> int:
+    """Bytes of workspace that replay_delta_scan needs for T rows, up to max_len of them a sequence."""
+    return _scan_workspace("replay_delta_scan_workspace", cfg, T, max_len)
+
+
+def replay_delta_scan(cfg, T, max_len, cu_seqlens, q, k, v, beta, alpha, s_in, s_out, y, err, workspace=None, stream=None):
+    """Packed prompts of a Gated DeltaNet layer: q, k [T, G, N], v and y [T, H, P], beta, alpha [T, H]; s_in may be None."""
+    _scan("replay_delta_scan", cfg, T, max_len, cu_seqlens, q, k, v, beta, alpha, s_in, s_out, y, err, workspace, stream,
+          ("beta", "alpha"))
 
 
 def _tree(parent, n_nodes, B, W, gpu):
@@ -673,8 +695,10 @@ class ReplayLayer:
                          n_reject, stream)
 
     def scan(self, T, max_len, cu_seqlens, q, k, v, dt, a, s_in, s_out, y, workspace=None, stream=None):
-        """The recurrence over packed prompts (replay_scan); load_checkpoint(s_out) makes its states this layer's."""
-        replay_scan(self.cfg, T, max_len, cu_seqlens, q, k, v, dt, a, s_in, s_out, y, self.t["err"], workspace, stream)
+        """The recurrence over packed prompts (replay_scan, or replay_delta_scan: dt is beta, a alpha);
+        load_checkpoint(s_out) makes its states this layer's."""
+        scan = replay_delta_scan if self.cfg.rule == GATED_DELTA else replay_scan
+        scan(self.cfg, T, max_len, cu_seqlens, q, k, v, dt, a, s_in, s_out, y, self.t["err"], workspace, stream)
 
     def conv_tree(self, conv, W, parent, x, dt_raw, conv_state, q, k, v, dt, a, n_nodes=None, stream=None):
         """The inputs of a tree of drafts (replay_conv_tree)."""

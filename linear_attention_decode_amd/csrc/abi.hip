@@ -7,7 +7,7 @@
 // float32 master and of a shared low-precision checkpoint), gdn.hip (Gated
 // DeltaNet layers), ring.hip (append, rollback, fills), conv.hip (the
 // convolution and discretisation ahead of the recurrence), delta_inputs.hip
-// (what a Gated DeltaNet layer has there), tree*.hip (trees of drafts), scan.hip (the
+// (what a Gated DeltaNet layer has there), tree*.hip (trees of drafts), scan.hip and delta_scan.hip (the
 // recurrence over prompts), sample.hip and logprobs.hip (tokens from logits,
 // and their scores), eager.hip and probe.hip.
 #include <hip/hip_runtime.h>
@@ -809,6 +809,38 @@ bool scan_plan(const replay_config &c, int32_t T, int32_t max_len, int *nseg, in
     return launch_fits((bh + 8 * (int64_t)c.heads) * *nseg, 4 * c.head_dim);   // a wavefront 16 columns of a head, or more
 }
 
+// What the two scans check and fill alike.
+replay_status scan_args(const replay_config *cfg, int32_t T, int32_t max_len, const int32_t *cu_seqlens, const void *q,
+                        const void *k, const void *v, const float *dt, const float *a, const float *s_in, float *s_out,
+                        void *y, int32_t *err, ScanArgs *r) {
+    if (T < 1 || max_len < 1 || !cu_seqlens || !aligned4(cu_seqlens) || !err || !aligned4(err) || !aligned16(s_in))
+        return REPLAY_ERR_INVALID_ARG;
+    for (const void *p : {q, k, v, static_cast<const void *>(s_out), static_cast<const void *>(y)})
+        if (!p || !aligned16(p)) return REPLAY_ERR_INVALID_ARG;
+    for (const void *p : {dt, a})
+        if (!p || !aligned4(p)) return REPLAY_ERR_INVALID_ARG;
+    const size_t state = (size_t)cfg->batch * cfg->heads * cfg->head_dim * cfg->state_dim;
+    const uintptr_t in = reinterpret_cast<uintptr_t>(s_in), out = reinterpret_cast<uintptr_t>(s_out);
+    if (s_in && in < out + state * sizeof(float) && out < in + state * sizeof(float)) return REPLAY_ERR_INVALID_ARG;
+    r->B = cfg->batch;
+    r->H = cfg->heads;
+    r->G = cfg->groups;
+    r->T = T;
+    r->max_len = max_len;
+    r->io_bf16 = cfg->io_dtype == REPLAY_BF16;
+    r->cu = cu_seqlens;
+    r->q = q;
+    r->k = k;
+    r->v = v;
+    r->dt = dt;
+    r->a = a;
+    r->s_in = s_in;
+    r->s_out = s_out;
+    r->y = y;
+    r->err = err;
+    return REPLAY_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -829,35 +861,12 @@ replay_status replay_scan(const replay_config *cfg, int32_t T, int32_t max_len, 
     replay_status st = check_shape(cfg);
     if (st != REPLAY_OK) return st;
     if (cfg->rule == REPLAY_RULE_GATED_DELTA) return REPLAY_ERR_UNSUPPORTED;
-    if (T < 1 || max_len < 1 || !cu_seqlens || !aligned4(cu_seqlens) || !err || !aligned4(err) || !aligned16(s_in))
-        return REPLAY_ERR_INVALID_ARG;
-    for (const void *p : {q, k, v, static_cast<const void *>(s_out), static_cast<const void *>(y)})
-        if (!p || !aligned16(p)) return REPLAY_ERR_INVALID_ARG;
-    for (const void *p : {dt, a})
-        if (!p || !aligned4(p)) return REPLAY_ERR_INVALID_ARG;
-    const size_t state = (size_t)cfg->batch * cfg->heads * cfg->head_dim * cfg->state_dim;
-    const uintptr_t in = reinterpret_cast<uintptr_t>(s_in), out = reinterpret_cast<uintptr_t>(s_out);
-    if (s_in && in < out + state * sizeof(float) && out < in + state * sizeof(float)) return REPLAY_ERR_INVALID_ARG;
     ScanArgs r{};
+    const replay_status filled = scan_args(cfg, T, max_len, cu_seqlens, q, k, v, dt, a, s_in, s_out, y, err, &r);
+    if (filled != REPLAY_OK) return filled;
     size_t need;
     if (!scan_plan(*cfg, T, max_len, &r.nseg, &r.seg_len, &need)) return REPLAY_ERR_UNSUPPORTED;
     if (need && (!workspace || !aligned16(workspace) || workspace_bytes < need)) return REPLAY_ERR_INVALID_ARG;
-    r.B = cfg->batch;
-    r.H = cfg->heads;
-    r.G = cfg->groups;
-    r.T = T;
-    r.max_len = max_len;
-    r.io_bf16 = cfg->io_dtype == REPLAY_BF16;
-    r.cu = cu_seqlens;
-    r.q = q;
-    r.k = k;
-    r.v = v;
-    r.dt = dt;
-    r.a = a;
-    r.s_in = s_in;
-    r.s_out = s_out;
-    r.y = y;
-    r.err = err;
     r.ws = static_cast<float *>(workspace);
     r.ws_decay = need ? r.ws + need / sizeof(float) - (size_t)r.B * r.H * (r.nseg - 1) : nullptr;
     return from_hip(launch_scan(cfg->head_dim, cfg->state_dim, r, as_stream(stream)));
@@ -1141,6 +1150,49 @@ replay_status replay_delta_inputs(const replay_config *cfg, int32_t T, const voi
     d.beta = beta;
     d.alpha = alpha;
     return from_conv(launch_delta_inputs(d, as_stream(stream)));
+}
+
+}  // extern "C"
+
+namespace {
+
+// As scan_plan, for the gated delta rule: a sequence is one segment.
+bool delta_plan(const replay_config &c, int32_t T, int32_t max_len, int *nseg, int *seg_len, size_t *bytes) {
+    if ((int64_t)c.heads * c.head_dim > kMaxRow || (int64_t)c.groups * c.state_dim > kMaxRow || T > 1 << 30) return false;
+    *nseg = 1;
+    *seg_len = max_len < T ? max_len : T;
+    *bytes = 0;
+    return launch_fits((int64_t)c.batch * c.heads + 8 * (int64_t)c.heads, 4 * c.head_dim);
+}
+
+}  // namespace
+
+extern "C" {
+
+replay_status replay_delta_scan_workspace(const replay_config *cfg, int32_t T, int32_t max_len, size_t *bytes) {
+    const replay_status st = check_shape(cfg);
+    if (st != REPLAY_OK) return st;
+    if (!bytes || T < 1 || max_len < 1) return REPLAY_ERR_INVALID_ARG;
+    if (cfg->rule != REPLAY_RULE_GATED_DELTA) return REPLAY_ERR_UNSUPPORTED;
+    int nseg, seg_len;
+    return delta_plan(*cfg, T, max_len, &nseg, &seg_len, bytes) ? REPLAY_OK : REPLAY_ERR_UNSUPPORTED;
+}
+
+replay_status replay_delta_scan(const replay_config *cfg, int32_t T, int32_t max_len, const int32_t *cu_seqlens,
+                                const void *q, const void *k, const void *v, const float *beta, const float *alpha,
+                                const float *s_in, float *s_out, void *y, int32_t *err, void *workspace,
+                                size_t workspace_bytes, void *stream) {
+    const replay_status st = check_shape(cfg);
+    if (st != REPLAY_OK) return st;
+    if (cfg->rule != REPLAY_RULE_GATED_DELTA) return REPLAY_ERR_UNSUPPORTED;
+    ScanArgs r{};
+    const replay_status filled = scan_args(cfg, T, max_len, cu_seqlens, q, k, v, beta, alpha, s_in, s_out, y, err, &r);
+    if (filled != REPLAY_OK) return filled;
+    size_t need;
+    if (!delta_plan(*cfg, T, max_len, &r.nseg, &r.seg_len, &need)) return REPLAY_ERR_UNSUPPORTED;
+    if (need && (!workspace || !aligned16(workspace) || workspace_bytes < need)) return REPLAY_ERR_INVALID_ARG;
+    r.ws = static_cast<float *>(workspace);
+    return from_hip(launch_delta_scan(cfg->head_dim, cfg->state_dim, r, as_stream(stream)));
 }
 
 }  // extern "C"

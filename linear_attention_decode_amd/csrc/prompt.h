@@ -102,6 +102,8 @@ int logprob_part(int64_t rows, int V, int *parts);   // elements of a part, and 
 hipError_t launch_logprobs(const LogprobArgs &a, hipStream_t s);
 hipError_t launch_sample(const SampleArgs &a, hipStream_t s);
 hipError_t launch_scan(int P, int N, const ScanArgs &a, hipStream_t s);
+// the gated delta rule (delta_scan.hip): dt carries beta, a alpha
+hipError_t launch_delta_scan(int P, int N, const ScanArgs &a, hipStream_t s);
 int scan_segments(int P, int N, int B, int H, int G, bool bf16, int T, int max_len, int *seg_len);   // the number of segments, and their length
 // hipErrorInvalidConfiguration: more workgroups than a launch numbers
 hipError_t launch_conv_prompt(const ConvArgs &a, hipStream_t s);

@@ -140,3 +140,30 @@ def test_accept_tree_refusals(lad, at, value, status):
 def test_handle_calls_without_a_handle(lad):
     assert lad.lib.replay_verify_tree(None, 4, *[P16] * 8, None) == 1
     assert lad.lib.replay_append_path(None, 4, *[P16] * 7, None) == 1
+
+
+def _delta_scan(lad, cfg=None, T=64, most=64, **kw):
+    a = dict(cu=P16, q=P16, k=P16, v=P16, dt=P16, a=P16, s_in=P16, s_out=0x10000000, y=P16, err=P16, ws=None, ws_bytes=0) | kw
+    cfg = cfg or _cfg(lad, rule=1)
+    return lad.lib.replay_delta_scan(ctypes.byref(cfg), T, most, a["cu"], a["q"], a["k"], a["v"], a["dt"], a["a"], a["s_in"],
+                                     a["s_out"], a["y"], a["err"], a["ws"], a["ws_bytes"], None)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(T=0), 1), (dict(most=0), 1), (dict(cu=None), 1), (dict(cu=0x1002), 1), (dict(q=None), 1), (dict(k=0x1008), 1),
+    (dict(v=None), 1), (dict(dt=None), 1), (dict(a=0x1001), 1), (dict(s_in=0x1004), 1), (dict(s_out=None), 1),
+    (dict(s_out=P16), 1), (dict(s_out=P16 + 2 * 4 * 64 * 128 * 4 - 16), 1), (dict(y=None), 1), (dict(err=None), 1),
+    (dict(T=(1 << 30) + 1), 2),
+])
+def test_delta_scan_refusals(lad, kw, status):
+    assert _delta_scan(lad, **kw) == status
+
+
+@pytest.mark.parametrize("kw,status", [(dict(batch=0), 1), (dict(head_dim=32), 2), (dict(rule=0), 2), (dict(io_dtype=3), 2),
+                                       (dict(batch=1 << 20, heads=512), 2), (dict(heads=1 << 19, groups=1 << 19), 2)])
+def test_delta_scan_shapes(lad, kw, status):
+    cfg = _cfg(lad, **({"rule": 1} | kw))
+    assert _delta_scan(lad, cfg=cfg, s_in=None) == status
+    n = ctypes.c_size_t()
+    assert lad.lib.replay_delta_scan_workspace(ctypes.byref(cfg), 64, 64, ctypes.byref(n)) == status
+    assert lad.lib.replay_delta_scan_workspace(ctypes.byref(_cfg(lad, rule=1)), 64, 64, None) == 1
