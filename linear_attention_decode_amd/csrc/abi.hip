@@ -1157,12 +1157,13 @@ replay_status replay_delta_inputs(const replay_config *cfg, int32_t T, const voi
 namespace {
 
 // As scan_plan, for the gated delta rule: a sequence is one segment.
-bool delta_plan(const replay_config &c, int32_t T, int32_t max_len, int *nseg, int *seg_len, size_t *bytes) {
+bool delta_plan(const replay_config &c, int32_t T, int32_t max_len, ScanArgs *r, size_t *bytes) {
     if ((int64_t)c.heads * c.head_dim > kMaxRow || (int64_t)c.groups * c.state_dim > kMaxRow || T > 1 << 30) return false;
-    *nseg = 1;
-    *seg_len = max_len < T ? max_len : T;
-    *bytes = 0;
-    return launch_fits((int64_t)c.batch * c.heads + 8 * (int64_t)c.heads, 4 * c.head_dim);
+    r->nseg = 1;
+    r->seg_len = max_len < T ? max_len : T;
+    r->window = delta_window(c.head_dim, c.state_dim, c.batch, c.heads, c.io_dtype == REPLAY_BF16, r->seg_len, bytes);
+    const int64_t bh = (int64_t)c.batch * c.heads;
+    return launch_fits((bh + 8 * (int64_t)c.heads) * (c.head_dim / 16), 256) && launch_fits(bh * r->window, 256);
 }
 
 }  // namespace
@@ -1174,8 +1175,8 @@ replay_status replay_delta_scan_workspace(const replay_config *cfg, int32_t T, i
     if (st != REPLAY_OK) return st;
     if (!bytes || T < 1 || max_len < 1) return REPLAY_ERR_INVALID_ARG;
     if (cfg->rule != REPLAY_RULE_GATED_DELTA) return REPLAY_ERR_UNSUPPORTED;
-    int nseg, seg_len;
-    return delta_plan(*cfg, T, max_len, &nseg, &seg_len, bytes) ? REPLAY_OK : REPLAY_ERR_UNSUPPORTED;
+    ScanArgs r{};
+    return delta_plan(*cfg, T, max_len, &r, bytes) ? REPLAY_OK : REPLAY_ERR_UNSUPPORTED;
 }
 
 replay_status replay_delta_scan(const replay_config *cfg, int32_t T, int32_t max_len, const int32_t *cu_seqlens,
@@ -1189,7 +1190,7 @@ replay_status replay_delta_scan(const replay_config *cfg, int32_t T, int32_t max
     const replay_status filled = scan_args(cfg, T, max_len, cu_seqlens, q, k, v, beta, alpha, s_in, s_out, y, err, &r);
     if (filled != REPLAY_OK) return filled;
     size_t need;
-    if (!delta_plan(*cfg, T, max_len, &r.nseg, &r.seg_len, &need)) return REPLAY_ERR_UNSUPPORTED;
+    if (!delta_plan(*cfg, T, max_len, &r, &need)) return REPLAY_ERR_UNSUPPORTED;
     if (need && (!workspace || !aligned16(workspace) || workspace_bytes < need)) return REPLAY_ERR_INVALID_ARG;
     r.ws = static_cast<float *>(workspace);
     return from_hip(launch_delta_scan(cfg->head_dim, cfg->state_dim, r, as_stream(stream)));

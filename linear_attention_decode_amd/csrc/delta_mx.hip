@@ -1,0 +1,824 @@
+// delta_mx.hip -- the gated delta rule over packed prompts for bf16 inputs on
+// the bf16 matrix instructions; delta_scan.hip has the mathematics.
+//
+// What a chunk of 64 tokens needs of k, q, alpha and beta alone does not wait
+// for a state, so it comes first and for all chunks at once: delta_prep_kernel
+// makes T = (I + A)^-1 diag(beta) and G, and writes them to the workspace as
+// operands, in the order in which lanes take them.  delta_mx_kernel then goes
+// from chunk to chunk:
+//   R = V - diag(g) K S^T,  U = T R,  Y = diag(g) Q S^T + G U,  S <- g_last S + (e U)^T K.
+// A chain of chunks has little to spread over the card (32 heads of 128 columns
+// are 256 tiles of 16 columns), so two wavefronts share 16 columns: each has
+// half of a chunk's tokens, and half of S^T's rows, which stay in its accumulators.
+// What bounds it: the chain of a chunk's steps, four barriers apart.  One
+// sequence of 8192 tokens (32 heads of 128 x 128): 55 us for T and G, 345 for 128
+// chunks, two wavefronts a CU.  Sixteen ragged ones of 15013 tokens: 103 and 335
+// us, eight wavefronts a CU that wait for LDS, for the matrix instructions and for each
+// other in turn.  The float32 kernel takes 3410 and 889 us.
+//
+// What bf16 operands leave out: k and q are bf16 as they are; S, R, T and e U
+// go into the products that make the state as three parts of 8 bits, which
+// hold their 24 (of T R the six products that weigh 2^-16 or more), so U and
+// the state are what float32 products give; S, U and G enter y's products as two
+// parts, so that a term lacks 2^-15 of itself at most, and y is rounded once.
+//
+// Layouts (16 x 16 x 32 products).  An accumulator tile holds in lane (column
+// c, group lg) rows 4 lg .. 4 lg + 3; an operand of 32 steps in lane (row or
+// column c, group lg) eight of them, which eight is free as long as both
+// operands agree: steps 4 lg .. + 3 and 16 + 4 lg .. + 3 are what two tiles of 16
+// rows hold there.  So S^T, R and U are operands as they are, and what meets them
+// (k, q, T, G) is read in that order, as two 8-byte pieces.  k^T comes
+// through the transposing LDS read.  y is made transposed, a lane 4 neighbouring
+// columns of one token.
+//
+// A chunk that holds a value that is no number (k, alpha, beta: noted by the
+// first kernel; v: seen by the wavefront) is run token by token, by the rule
+// itself.
+#include "scan_common.h"
+
+namespace replay {
+
+namespace {
+
+constexpr int kQ = kScanChunk;
+static_assert(kQ == 64, "two blocks of 32 tokens");
+
+typedef __bf16 bf8 __attribute__((ext_vector_type(8)));
+typedef float acc4 __attribute__((ext_vector_type(4)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+
+// A head's chunk in the workspace: T's operands (tiles of 16 tokens by steps of
+// 32, three parts each), G's (two parts), g and e, and whether the chunk holds a value
+// that is no number.  Operand x < 4 is tile x at the step its tokens are in,
+// the two behind them are tiles 2 and 3 at step 0.
+constexpr int kFrag = 1024, kFrags = 6;
+constexpr int kTBytes = kFrags * 3 * kFrag, kGBytes = kFrags * 2 * kFrag;
+constexpr int kImage = kTBytes + kGBytes + 2 * kQ * 4;
+constexpr int kSlot = (kImage + 16 + 255) / 256 * 256;
+static_assert(kImage % 16 == 0, "whole pieces");
+__host__ __device__ constexpr int frag(int tile, int step) { return step == tile >> 1 ? tile : tile + 2; }
+
+__device__ __forceinline__ acc4 mma16(bf8 a, bf8 b, acc4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+}
+__device__ __forceinline__ acc4 mma4(float a, float b, acc4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x4f32(a, b, c, 0, 0, 0);
+}
+__device__ __forceinline__ bool odd_pair(uint32_t w) {   // a bf16 pair with a value that is no number
+    return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
+}
+
+// Eight floats as one, two or three operands that hold 8 bits each, the last one rounded.
+template <int PARTS>
+__device__ __forceinline__ void split(const acc4 &lo, const acc4 &hi, bf8 *out) {
+    float x[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+#pragma unroll
+    for (int z = 0; z < PARTS; ++z) {
+        u32x4 w;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            if (z + 1 < PARTS) {
+                w[r] = upper_pair(x[2 * r], x[2 * r + 1]);
+                x[2 * r] = below_upper(x[2 * r]);
+                x[2 * r + 1] = below_upper(x[2 * r + 1]);
+            } else {
+                w[r] = f32x2_to_bf16_pair(x[2 * r], x[2 * r + 1]);
+            }
+        }
+        out[z] = __builtin_bit_cast(bf8, w);
+    }
+}
+
+// ---- T and G of every chunk and head ----------------------------------------
+
+constexpr int kPrepNT = 256;
+
+struct Decays {
+    float alpha[kQ], beta[kQ];
+    float pre[kQ], suf[kQ];   // products of alpha within a tile of 16: up to and with i; behind j
+    float tot[4];             // a tile's whole product
+};
+// A, whose place T takes block by block
+struct PrepTile {
+    float a[kQ][kQ + 4];
+    Decays d;
+};
+
+// The lower left corner of the inverse of rows and columns r0 .. r0 + 2 SIZE -
+// 1, a wavefront for 16 columns j of it: T10 = -T11 (A10 T00).
+template <int SIZE>
+__device__ __forceinline__ void invert_corner(float (*m)[kQ + 4], int r0, int j, int lane) {
+    constexpr int TL = SIZE / 16;
+    const int c = lane & 15, lg = lane >> 4, c0 = r0 + 16 * j + c;
+    acc4 x[TL];
+#pragma unroll
+    for (int i = 0; i < TL; ++i) x[i] = acc4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int k = 0; k < TL; ++k) {
+        if (k < j) continue;   // T00 is zero there
+        float t[4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) t[r] = m[r0 + 16 * k + 4 * lg + r][c0];
+#pragma unroll
+        for (int i = 0; i < TL; ++i) {
+            const f32x4 a = *reinterpret_cast<const f32x4 *>(&m[r0 + SIZE + 16 * i + c][r0 + 16 * k + 4 * lg]);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) x[i] = mma4(a[r], t[r], x[i]);
+        }
+    }
+    acc4 o[TL];
+#pragma unroll
+    for (int i = 0; i < TL; ++i) {
+        o[i] = acc4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int k = 0; k <= i; ++k) {
+            const f32x4 t = *reinterpret_cast<const f32x4 *>(&m[r0 + SIZE + 16 * i + c][r0 + SIZE + 16 * k + 4 * lg]);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) o[i] = mma4(t[r], x[k][r], o[i]);
+        }
+    }
+    if constexpr (TL > 1) __syncthreads();   // A10 is read by both wavefronts
+#pragma unroll
+    for (int i = 0; i < TL; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) m[r0 + SIZE + 16 * i + 4 * lg + r][c0] = -o[i][r];
+}
+
+// D over tile (ti, tj) of one head, lane (column i = 16 ti + c, rows j = 16 tj
+// + 4 lg + r): alpha_{j+1} ... alpha_i; nothing above the diagonal.
+__device__ __forceinline__ f32x4 decays_of(const Decays &d, int ti, int tj, int c, int lg) {
+    const int i = 16 * ti + c, j0 = 16 * tj + 4 * lg;
+    if (ti == tj) {
+        // blocks of 4: alpha over those between j's and i, times what is behind j in its block
+        const f32x4 aa = *reinterpret_cast<const f32x4 *>(&d.alpha[j0]);
+        const float R = row_upto(c >= 4 * (lg + 1) ? d.alpha[i] : 1.f);
+        f32x4 D = {R, R, R, R};
+        float f = 1.f;
+#pragma unroll
+        for (int r = 2; r >= 0; --r) {
+            f = j0 + r + 1 <= i ? f * aa[r + 1] : 1.f;
+            D[r] *= f;
+        }
+        return D;
+    }
+    // the nearest first: every product is one of consecutive tokens
+    float p = d.pre[i];
+    p *= ti - tj > 1 ? d.tot[(ti - 1) & 3] : 1.f;
+    p *= ti - tj > 2 ? d.tot[(ti - 2) & 3] : 1.f;
+    return p * *reinterpret_cast<const f32x4 *>(&d.suf[j0]);
+}
+
+// A workgroup makes a chunk of HP heads of a group, which share k . k and k . q.
+template <int N, int HP>
+__global__ __launch_bounds__(kPrepNT) void delta_prep_kernel(ScanArgs s) {
+    __shared__ __align__(16) PrepTile m[HP];
+    __shared__ uint32_t odd[HP];
+    const int tid = threadIdx.x, lane = tid & 63, c = lane & 15, lg = lane >> 4;
+    const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int h0 = blockIdx.x % (s.H / HP) * HP, slot = blockIdx.x / (s.H / HP), b = slot / s.window, g = h0 / (s.H / s.G);
+    const Span sp = find_span(s, b, 0);
+    const int first = (s.chunk0 + slot % s.window) * kQ;
+    if (!sp.run || first >= sp.n) return;
+    const int n = sp.n - first < kQ ? sp.n - first : kQ, t0 = sp.t0 + first;
+    uint8_t *out = reinterpret_cast<uint8_t *>(s.ws) + ((size_t)slot * s.H + h0) * kSlot;
+
+    // tiles (ti, tj) of K K^T and K Q^T, lane (column i = c, rows j = 4 lg + r):
+    // a wavefront's diagonal one, two below the diagonal, and for w < 2 one
+    // above it, G's zeros.  Rows past the chunk's tokens read zero.
+    const int ti[3] = {w, w == 0 ? 1 : (w == 1 ? 2 : 3), w == 0 ? 0 : (w == 1 ? 2 : (w == 2 ? 2 : 3))};
+    const int tj[3] = {w, w == 0 ? 0 : (w == 3 ? 1 : 0), w == 0 ? 1 : (w == 1 ? 1 : (w == 2 ? 3 : 2))};
+    acc4 kk[3], qk[3];
+    const uint32_t rqk = (uint32_t)s.G * N * 2;
+    {
+        const size_t base = (size_t)t0 * rqk + (size_t)g * N * 2;
+        const auto rk = make_rsrc(static_cast<const char *>(s.k) + base, (uint32_t)(n - 1) * rqk + N * 2);
+        const auto rq = make_rsrc(static_cast<const char *>(s.q) + base, (uint32_t)(n - 1) * rqk + N * 2);
+        const uint32_t o = c * rqk + 16 * lg;
+        u32x4 kj[3][N / 32], ki[3][N / 32], qi[3][N / 32];
+#pragma unroll
+        for (int z = 0; z < 3; ++z)
+#pragma unroll
+            for (int st = 0; st < N / 32; ++st) {
+                kj[z][st] = __builtin_amdgcn_raw_buffer_load_b128(rk, o, 16 * tj[z] * rqk + 64 * st, 0);
+                ki[z][st] = z == 0 ? kj[0][st] : __builtin_amdgcn_raw_buffer_load_b128(rk, o, 16 * ti[z] * rqk + 64 * st, 0);
+                qi[z][st] = __builtin_amdgcn_raw_buffer_load_b128(rq, o, 16 * ti[z] * rqk + 64 * st, 0);
+            }
+        if (w < HP) {   // the decays of head w, while the rows are on their way
+            const int h = h0 + w;
+            Decays &d = m[w].d;
+            float al = 1.f, be = 0.f;
+            if (lane < n) {
+                al = s.a[(size_t)(t0 + lane) * s.H + h];
+                be = s.dt[(size_t)(t0 + lane) * s.H + h];
+            }
+            const float pre = row_upto(al), suf = row_move<0x101>(row_from(al));
+            const float p0 = lane_value(pre, 15), p1 = lane_value(pre, 31), p2 = lane_value(pre, 47), p3 = lane_value(pre, 63);
+            const int tile = lane >> 4;
+            const float ahead = tile == 0 ? 1.f : (tile == 1 ? p0 : (tile == 2 ? p0 * p1 : p0 * p1 * p2));
+            const float behind = tile == 3 ? 1.f : (tile == 2 ? p3 : (tile == 1 ? p2 * p3 : p1 * p2 * p3));
+            d.alpha[lane] = al;
+            d.beta[lane] = be;
+            d.pre[lane] = pre;
+            d.suf[lane] = suf;
+            if (lane < 4) d.tot[lane] = lane == 0 ? p0 : (lane == 1 ? p1 : (lane == 2 ? p2 : p3));
+            float *decay = reinterpret_cast<float *>(out + (size_t)w * kSlot + kTBytes + kGBytes);
+            decay[lane] = ahead * pre;
+            decay[kQ + lane] = suf * behind;
+            const bool bad = __any(!(finite(al) && finite(be)));
+            if (lane == 0) odd[w] = bad;
+        }
+        bool bad = false;
+#pragma unroll
+        for (int z = 0; z < 3; ++z) {
+            kk[z] = qk[z] = acc4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int st = 0; st < N / 32; ++st) {
+                kk[z] = mma16(__builtin_bit_cast(bf8, kj[z][st]), __builtin_bit_cast(bf8, ki[z][st]), kk[z]);
+                qk[z] = mma16(__builtin_bit_cast(bf8, kj[z][st]), __builtin_bit_cast(bf8, qi[z][st]), qk[z]);
+                if (z == 0)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) bad |= odd_pair(ki[z][st][r]);
+            }
+        }
+        bad = __any(bad);
+        __syncthreads();   // the decays
+        if (bad && lane < HP) odd[lane] = 1;
+    }
+#pragma unroll
+    for (int y = 0; y < HP; ++y) {
+        uint8_t *to_head = out + (size_t)y * kSlot + kTBytes;
+#pragma unroll
+        for (int z = 0; z < 3; ++z) {
+            const int i = 16 * ti[z] + c, j0 = 16 * tj[z] + 4 * lg;
+            const bool below = ti[z] >= tj[z];
+            f32x4 D = {0.f, 0.f, 0.f, 0.f};
+            if (below) D = decays_of(m[y].d, ti[z], tj[z], c, lg);
+            const float be = m[y].d.beta[i];
+            f32x4 a, o;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                a[r] = j0 + r < i ? be * (kk[z][r] * D[r]) : 0.f;
+                o[r] = j0 + r <= i ? qk[z][r] * D[r] : 0.f;
+            }
+            *reinterpret_cast<f32x4 *>(&m[y].a[i][j0]) = a;   // (zeros above the diagonal are T's too)
+            uint8_t *to = to_head + frag(ti[z], tj[z] >> 1) * 2 * kFrag + lane * 16 + (tj[z] & 1) * 8;
+            *reinterpret_cast<u32x2 *>(to) = u32x2{upper_pair(o[0], o[1]), upper_pair(o[2], o[3])};
+            *reinterpret_cast<u32x2 *>(to + kFrag) = u32x2{lower_pair(o[0], o[1]), lower_pair(o[2], o[3])};
+        }
+    }
+    __syncthreads();
+    if (w < HP) {
+        // the diagonal blocks by substitution: lane (block lg, column c) a column
+        float(*a)[kQ + 4] = m[w].a;
+        const int b0 = 16 * lg;
+        float x[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            x[i] = i == c ? 1.f : 0.f;
+#pragma unroll
+            for (int j4 = 0; j4 < i; j4 += 4) {
+                const f32x4 r4 = *reinterpret_cast<const f32x4 *>(&a[b0 + i][b0 + j4]);
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    if (j4 + r < i) x[i] = fmaf(-r4[r], x[j4 + r], x[i]);
+            }
+        }
+        wave_lds_sync();
+#pragma unroll
+        for (int i = 0; i < 16; ++i) a[b0 + i][b0 + c] = x[i];
+    }
+    __syncthreads();
+    if (w < 2 * HP) invert_corner<16>(m[w >> 1].a, 32 * (w & 1), 0, lane);
+    __syncthreads();
+    if (w < 2 * HP) {
+        invert_corner<32>(m[w >> 1].a, 0, w & 1, lane);
+    } else {
+        __syncthreads();   // the one in there
+    }
+    __syncthreads();
+    for (int x = tid; x < HP * kFrags * 64; x += kPrepNT) {
+        const int y = x / (kFrags * 64), f = x / 64 % kFrags, tile = f < 4 ? f : f - 2, step = f < 4 ? tile >> 1 : 0;
+        const int l = x & 63, i = 16 * tile + (l & 15), j0 = 32 * step + 4 * (l >> 4);
+        acc4 v[2];
+#pragma unroll
+        for (int z = 0; z < 2; ++z)
+            v[z] = *reinterpret_cast<const acc4 *>(&m[y].a[i][j0 + 16 * z]) * *reinterpret_cast<const acc4 *>(&m[y].d.beta[j0 + 16 * z]);
+        bf8 parts[3];
+        split<3>(v[0], v[1], parts);
+        uint8_t *to = out + (size_t)y * kSlot + f * 3 * kFrag + l * 16;
+#pragma unroll
+        for (int z = 0; z < 3; ++z) *reinterpret_cast<u32x4 *>(to + z * kFrag) = __builtin_bit_cast(u32x4, parts[z]);
+    }
+    if (tid < HP) *reinterpret_cast<uint32_t *>(out + (size_t)tid * kSlot + kImage) = odd[tid];
+}
+
+// ---- from chunk to chunk ----------------------------------------------------
+
+__device__ __forceinline__ bf8 frag16(const uint8_t *m) { return __builtin_bit_cast(bf8, *reinterpret_cast<const u32x4 *>(m)); }
+// Rows of k and q in LDS: the sixteen 8-byte pieces of 128 bytes are permuted by the
+// row's number, so that 16 rows' equal pieces, and 4 rows' 4 neighbouring ones, lie
+// in distinct banks.
+__device__ __forceinline__ int turn(int row) { return (row & 3) << 2 | (row >> 2 & 3); }
+// an operand's two pieces
+__device__ __forceinline__ bf8 row8(const uint8_t *first, const uint8_t *second) {
+    const u32x2 lo = *reinterpret_cast<const u32x2 *>(first), hi = *reinterpret_cast<const u32x2 *>(second);
+    return __builtin_bit_cast(bf8, u32x4{lo[0], lo[1], hi[0], hi[1]});
+}
+__device__ __forceinline__ s16x4 col4(const uint8_t *m) {
+    typedef __attribute__((address_space(3))) s16x4 lds4;
+    return __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4 *)m);
+}
+
+template <int P, int N, int CW>
+struct Shape {
+    static constexpr int NT = 128 * CW, PC = 16 * CW, CB = P / PC;   // threads, columns, workgroups a head
+    static constexpr int QB = 2 * N, KN = N / 32, KH = KN / 2;       // bytes of a row; steps over it, a wavefront's own
+    static constexpr int IQ = kQ * QB / 16 / NT;                     // 16-byte pieces of k, and of q, that a thread stages
+    // Several pairs of wavefronts share T and G through LDS (their own loads of
+    // them would be 120 KB a chunk, and what a CU gets from its L2 is some 18 bytes a clock);
+    // a pair alone takes its own straight into registers.
+    static constexpr bool SHARE = CW > 1;
+    static constexpr int IT = (kImage + 16) / 16 / NT + 1;           // pieces of the chunk's slot
+    static_assert(P % PC == 0 && kQ * QB / 16 % NT == 0, "whole pieces");
+};
+
+// What the two wavefronts of 16 columns hand each other, as operands.
+template <int KN>
+struct Exchange {
+    uint8_t s[KN][3][kFrag], e[2][3][kFrag], r[3][kFrag], u[2][kFrag];
+};
+template <int P, int N, int CW>
+struct Tile {
+    using Sh = Shape<P, N, CW>;
+    __align__(16) uint8_t k[kQ * Sh::QB], q[kQ * Sh::QB];
+    uint8_t odd[16];
+    __align__(16) Exchange<Sh::KN> x[CW];
+    __align__(16) uint8_t slot[Sh::SHARE ? kImage + 16 : 16];
+};
+
+// The next chunk's k and q on their way to LDS: rows past its n tokens read zero.
+template <int P, int N, int CW>
+struct Ahead {
+    using Sh = Shape<P, N, CW>;
+    u32x4 q[Sh::IQ], k[Sh::IQ], slot[Sh::SHARE ? Sh::IT : 1];
+    // n <= 0: nothing is read (no load is conditional, here and below: a
+    // wait could not tell it from those behind it)
+    __device__ __forceinline__ void load(const char *kp, const char *qp, uint32_t rqk, int n, const uint8_t *from) {
+        const uint32_t bytes = n > 0 ? (uint32_t)(n < kQ ? n - 1 : kQ - 1) * rqk + Sh::QB : 0, tid = threadIdx.x;
+        const auto rk = make_rsrc(kp, bytes), rq = make_rsrc(qp, bytes);
+        const uint32_t o = tid / (Sh::QB / 16) * rqk + tid % (Sh::QB / 16) * 16, step = Sh::NT / (Sh::QB / 16) * rqk;
+#pragma unroll
+        for (int i = 0; i < Sh::IQ; ++i) {
+            k[i] = __builtin_amdgcn_raw_buffer_load_b128(rk, o, i * step, 0);
+            q[i] = __builtin_amdgcn_raw_buffer_load_b128(rq, o, i * step, 0);
+        }
+        if constexpr (Sh::SHARE) {
+            const auto rs = make_rsrc(from, n > 0 ? kImage + 16 : 0);
+#pragma unroll
+            for (int i = 0; i < Sh::IT; ++i) slot[i] = __builtin_amdgcn_raw_buffer_load_b128(rs, tid * 16, i * Sh::NT * 16, 0);
+        }
+    }
+    __device__ __forceinline__ void store(Tile<P, N, CW> &m) const {
+        constexpr int PR = Sh::QB / 16, RS = Sh::NT / PR;   // pieces of a row; rows from one of a thread's to the next
+        static_assert(RS % 8 == 0, "their permutations differ by exchanges of 16-byte pieces alone");
+        const int tid = threadIdx.x, row = tid / PR, f = turn(row);
+        const int o = row * Sh::QB + ((tid % PR * 16) ^ ((f & 14) << 3));
+        const bool swap = f & 1;
+        auto put = [&](uint8_t *to, u32x4 x) { *reinterpret_cast<u32x4 *>(to) = swap ? u32x4{x[2], x[3], x[0], x[1]} : x; };
+#pragma unroll
+        for (int i = 0; i < Sh::IQ; ++i) {
+            const int to = (o ^ ((turn(i * RS) & 14) << 3)) + i * Sh::NT * 16;
+            put(m.k + to, k[i]);
+            put(m.q + to, q[i]);
+        }
+        if constexpr (Sh::SHARE) {
+#pragma unroll
+            for (int i = 0; i < Sh::IT; ++i)
+                if ((i * Sh::NT + tid) * 16 < kImage + 16) *reinterpret_cast<u32x4 *>(m.slot + (i * Sh::NT + tid) * 16) = slot[i];
+        }
+    }
+};
+
+// v: column c, tokens 32 th + 16 x + 4 lg + r of the next chunk
+struct Values {
+    uint32_t v[8];
+    __device__ __forceinline__ void load(const char *vp, uint32_t rv, int n, uint32_t o) {
+        const auto r = make_rsrc(vp, n > 0 ? (uint32_t)(n - 1) * rv + 32 : 0);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(r, o, (i & 3) * rv + (i >> 2) * 16 * rv, 0);
+    }
+};
+
+// What a wavefront takes of a chunk's slot: registers, loaded a chunk ahead.
+// (slot null: nothing is read)
+template <bool SHARE>
+struct Slot {
+    bf8 t_[2][3], tx_[2][3];   // T: its own step, and (th = 1; else unused) step 0
+    bf8 g_[2][2], gx_[2][2];   // G likewise
+    f32x4 d_[2], e_[2];        // g and e of the tokens of v
+    float dn_[2], all_;        // g of tokens 32 th + 16 x + c; of the last
+    uint32_t odd_;
+    __device__ __forceinline__ void load_decays(const uint8_t *slot, int th, int lane) {
+        const auto ws = make_rsrc(slot, slot ? kSlot : 0);
+        const uint32_t o = (32 * th + 4 * (lane >> 4)) * 4, on = (32 * th + (lane & 15)) * 4, s = kTBytes + kGBytes;
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            d_[x] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(ws, o + 64 * x, s, 0));
+            e_[x] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(ws, o + 4 * kQ + 64 * x, s, 0));
+            dn_[x] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(ws, on + 64 * x, s, 0));
+        }
+        all_ = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(ws, 4 * (kQ - 1), s, 0));
+        odd_ = __builtin_amdgcn_raw_buffer_load_b32(ws, 2 * 4 * kQ, s, 0);
+    }
+    __device__ __forceinline__ void load_t(const uint8_t *slot, int th, int lane) {
+        const auto ws = make_rsrc(slot, slot ? kSlot : 0), wx = make_rsrc(slot, slot && th ? kSlot : 0);
+        const uint32_t o = lane * 16, s = 6 * kFrag * th;
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+#pragma unroll
+            for (int z = 0; z < 3; ++z) {
+                t_[x][z] = __builtin_bit_cast(bf8, __builtin_amdgcn_raw_buffer_load_b128(ws, o, s + (3 * x + z) * kFrag, 0));
+                tx_[x][z] = __builtin_bit_cast(bf8, __builtin_amdgcn_raw_buffer_load_b128(wx, o, (12 + 3 * x + z) * kFrag, 0));
+            }
+    }
+    __device__ __forceinline__ void load_g(const uint8_t *slot, int th, int lane) {
+        const auto ws = make_rsrc(slot, slot ? kSlot : 0), wx = make_rsrc(slot, slot && th ? kSlot : 0);
+        const uint32_t o = lane * 16, s = kTBytes + 4 * kFrag * th;
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+#pragma unroll
+            for (int z = 0; z < 2; ++z) {
+                g_[x][z] = __builtin_bit_cast(bf8, __builtin_amdgcn_raw_buffer_load_b128(ws, o, s + (2 * x + z) * kFrag, 0));
+                gx_[x][z] = __builtin_bit_cast(bf8, __builtin_amdgcn_raw_buffer_load_b128(wx, o, kTBytes + (8 + 2 * x + z) * kFrag, 0));
+            }
+    }
+    __device__ __forceinline__ bf8 t(int x, int z) const { return t_[x][z]; }
+    __device__ __forceinline__ bf8 tx(int x, int z) const { return tx_[x][z]; }
+    __device__ __forceinline__ bf8 g(int x, int z) const { return g_[x][z]; }
+    __device__ __forceinline__ bf8 gx(int x, int z) const { return gx_[x][z]; }
+    __device__ __forceinline__ f32x4 d(int x) const { return d_[x]; }
+    __device__ __forceinline__ f32x4 e(int x) const { return e_[x]; }
+    __device__ __forceinline__ float dn(int x) const { return dn_[x]; }
+    __device__ __forceinline__ float all() const { return all_; }
+    __device__ __forceinline__ uint32_t odd() const { return odd_; }
+};
+// The same from the workgroup's copy in LDS.
+template <>
+struct Slot<true> {
+    const uint8_t *frags, *decay, *natural, *base;
+    int step;
+    __device__ __forceinline__ void init(const uint8_t *m, int th, int lane) {
+        base = m;
+        frags = m + 16 * lane;
+        decay = m + kTBytes + kGBytes + (32 * th + 4 * (lane >> 4)) * 4;
+        natural = m + kTBytes + kGBytes + (32 * th + (lane & 15)) * 4;
+        step = th;
+    }
+    __device__ __forceinline__ bf8 t(int x, int z) const { return frag16(frags + (6 * step + 3 * x + z) * kFrag); }
+    __device__ __forceinline__ bf8 tx(int x, int z) const { return frag16(frags + (12 + 3 * x + z) * kFrag); }
+    __device__ __forceinline__ bf8 g(int x, int z) const { return frag16(frags + kTBytes + (4 * step + 2 * x + z) * kFrag); }
+    __device__ __forceinline__ bf8 gx(int x, int z) const { return frag16(frags + kTBytes + (8 + 2 * x + z) * kFrag); }
+    __device__ __forceinline__ f32x4 d(int x) const { return *reinterpret_cast<const f32x4 *>(decay + 64 * x); }
+    __device__ __forceinline__ f32x4 e(int x) const { return *reinterpret_cast<const f32x4 *>(decay + 4 * kQ + 64 * x); }
+    __device__ __forceinline__ float dn(int x) const { return *reinterpret_cast<const float *>(natural + 64 * x); }
+    __device__ __forceinline__ float all() const { return *reinterpret_cast<const float *>(base + kTBytes + kGBytes + 4 * (kQ - 1)); }
+    __device__ __forceinline__ uint32_t odd() const { return *reinterpret_cast<const uint32_t *>(base + kImage); }
+};
+
+__device__ __forceinline__ void put_frag(uint8_t *to, bf8 x) { *reinterpret_cast<u32x4 *>(to) = __builtin_bit_cast(u32x4, x); }
+
+// A chunk token by token, by a wavefront for 16 columns.  The state stays in
+// s_out, S this lane's first place there (columns 16 t + 4 lg ..).
+template <int P, int N, int CW>
+__device__ __forceinline__ void by_token(const ScanArgs &s, const Tile<P, N, CW> &m, float *S, int t0, int n, int h, int p, int lane) {
+    using Sh = Shape<P, N, CW>;
+    const int lg = lane >> 4;
+#pragma unroll 1
+    for (int t = 0; t < n; ++t) {
+        const float al = s.a[(size_t)(t0 + t) * s.H + h], be = s.dt[(size_t)(t0 + t) * s.H + h];
+        const size_t o = ((size_t)(t0 + t) * s.H + h) * P + p;
+        const uint8_t *k = m.k + t * Sh::QB, *q = m.q + t * Sh::QB;
+        const int f = turn(t) << 3;
+        float dot = 0.f, y = 0.f;
+#pragma unroll 1
+        for (int i = 0; i < N / 4; ++i) dot = fmaf(S[16 * (i / 4) + i % 4], load_io1<true>(k + ((32 * (i / 4) + 8 * lg) ^ f), i % 4), dot);
+        dot += __shfl_xor(dot, 16);
+        dot += __shfl_xor(dot, 32);
+        const float u = be * fmaf(-al, dot, load_io1<true>(s.v, o));
+#pragma unroll 1
+        for (int i = 0; i < N / 4; ++i) {
+            const float x = fmaf(u, load_io1<true>(k + ((32 * (i / 4) + 8 * lg) ^ f), i % 4), al * S[16 * (i / 4) + i % 4]);
+            S[16 * (i / 4) + i % 4] = x;
+            y = fmaf(x, load_io1<true>(q + ((32 * (i / 4) + 8 * lg) ^ f), i % 4), y);
+        }
+        y += __shfl_xor(y, 16);
+        y += __shfl_xor(y, 32);
+        if (lg == 0) static_cast<uint16_t *>(s.y)[o] = (uint16_t)f32_to_bf16_bits(y);
+    }
+}
+
+// Two wavefronts take 16 columns: th = 0, 1 have the chunk's tokens 32 th ..
+// in R, U and y, and the state's rows N / 2 th .. in S^T.  The system is lower
+// triangular, so that th = 0 needs nothing of th = 1 for R, U and y.
+template <int P, int N, int CW>
+__global__ __launch_bounds__((Shape<P, N, CW>::NT), 2) void delta_mx_kernel(ScanArgs s) {
+    using Sh = Shape<P, N, CW>;
+    constexpr int KN = Sh::KN, KH = Sh::KH, QB = Sh::QB;
+    __shared__ Tile<P, N, CW> m;
+
+    Place place;
+    if (!find_place(s, 1, &place, Sh::CB)) return;
+    const int h = place.h, b = place.b, g = place.g;
+    const Span sp = find_span(s, b, 0);
+    const int tid = threadIdx.x, lane = tid & 63, c = lane & 15, lg = lane >> 4;
+    const int w = __builtin_amdgcn_readfirstlane(tid >> 6), th = w & 1;
+    if (s.chunk0 == 0 && h == 0 && place.cb == 0 && !sp.run && tid == 0) raise_seq_error(s.err, b, REPLAY_SEQERR_BAD_RANGE);
+    const int from = s.chunk0 * kQ, upto = sp.n < from + s.window * kQ ? sp.n : from + s.window * kQ;
+    if (!sp.run || (from > 0 && from >= sp.n)) return;
+    Exchange<KN> &ex = m.x[w >> 1];
+    uint8_t &odd_chunk = m.odd[w >> 1];   // of the two wavefronts'
+
+    const int p0 = Sh::PC * place.cb + 16 * (w >> 1);   // the wavefront's columns
+    const size_t bh = (size_t)b * s.H + h;
+    float *const state = s.s_out + (bh * P + p0 + c) * N + 4 * lg;          // columns 16 t + 4 lg ..
+    const float *in = from > 0 ? s.s_out : s.s_in;
+    // tile t of the wavefront's half of S^T: n = N / 2 th + 16 t + 4 lg + r
+    acc4 S[2 * KH];
+    auto get_state = [&](const float *from_) {
+#pragma unroll
+        for (int t = 0; t < 2 * KH; ++t) {
+            S[t] = acc4{0.f, 0.f, 0.f, 0.f};
+            if (from_) S[t] = *reinterpret_cast<const acc4 *>(from_ + N / 2 * th + 16 * t);
+        }
+    };
+    auto put_state = [&] {
+#pragma unroll
+        for (int t = 0; t < 2 * KH; ++t) *reinterpret_cast<acc4 *>(state + N / 2 * th + 16 * t) = S[t];
+    };
+    auto hand_state = [&] {
+        uint8_t *to = ex.s[KH * th][0] + 16 * lane;
+#pragma unroll
+        for (int i = 0; i < KH; ++i) {
+            bf8 part[3];
+            split<3>(S[2 * i], S[2 * i + 1], part);
+#pragma unroll
+            for (int z = 0; z < 3; ++z) put_frag(to + (3 * i + z) * kFrag, part[z]);
+        }
+    };
+    get_state(in ? in + (bh * P + p0 + c) * N + 4 * lg : nullptr);
+    if (upto == from) {   // no tokens: the state as it is
+        put_state();
+        return;
+    }
+    const uint32_t rv = (uint32_t)s.H * P * 2, rqk = (uint32_t)s.G * QB;
+    const size_t t0 = (size_t)(sp.t0 + from);
+    const char *kp = static_cast<const char *>(s.k) + t0 * rqk + (size_t)g * QB;
+    const char *qp = static_cast<const char *>(s.q) + t0 * rqk + (size_t)g * QB;
+    const char *vp = static_cast<const char *>(s.v) + t0 * rv + ((size_t)h * P + p0) * 2;
+    char *yp = static_cast<char *>(s.y) + t0 * rv + ((size_t)h * P + p0) * 2;
+    const uint8_t *slot = reinterpret_cast<const uint8_t *>(s.ws) + ((size_t)b * s.window * s.H + h) * kSlot;
+    const size_t next_slot = (size_t)s.H * kSlot;
+    const uint32_t vo = (32 * th + 4 * lg) * rv + 2 * c, yo = (32 * th + c) * rv + 8 * lg;
+    // places in a row's 128 bytes of the four pieces 4 i + lg, and of k^T's 4 i + c % 4
+    int piece[4], col[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        piece[i] = (32 * th + c) * QB + (((4 * i + lg) ^ turn(c)) << 3);
+        col[i] = (4 * lg + (c >> 2)) * QB + (((4 * i + (c & 3)) ^ turn(4 * lg + (c >> 2))) << 3);
+    }
+    auto operand = [&](const uint8_t *rows, int x, int st) {   // of tokens 32 th + 16 x + c, step st
+        const int o = 16 * QB * x + 128 * (st >> 1), i = 2 * (st & 1);
+        return row8(rows + piece[i] + o, rows + piece[i + 1] + o);
+    };
+    const uint8_t *const xl = reinterpret_cast<const uint8_t *>(&ex) + 16 * lane;
+    constexpr int kE = KN * 3 * kFrag, kR = kE + 6 * kFrag, kU = kR + 3 * kFrag;       // places in Exchange
+    Ahead<P, N, CW> ahead;
+    Values val;
+    Slot<Sh::SHARE> my;
+    ahead.load(kp, qp, rqk, upto - from, slot);
+    val.load(vp, rv, sp.n - from < kQ ? sp.n - from : kQ, vo);
+    if constexpr (Sh::SHARE) {
+        my.init(m.slot, th, lane);
+    } else {
+        my.load_decays(slot, th, lane);
+        my.load_t(slot, th, lane);
+        my.load_g(slot, th, lane);
+    }
+    hand_state();
+    if (th == 0 && lane == 0) odd_chunk = 0;
+    ahead.store(m);
+    for (int done = from; done < upto; done += kQ) {
+        const int n = sp.n - done < kQ ? sp.n - done : kQ, left = upto - done - kQ;   // of this chunk; behind it
+        lds_barrier();   // k, q and the operands of S^T
+        kp += (size_t)kQ * rqk;
+        qp += (size_t)kQ * rqk;
+        vp += (size_t)kQ * rv;
+        slot += next_slot;
+        ahead.load(kp, qp, rqk, left, slot);
+        [[maybe_unused]] const uint8_t *const next = left > 0 ? slot : nullptr;
+        // K S^T, rows token 32 th + 16 x + 4 lg + r, column c.  S Q^T, rows p = 4
+        // lg + r, column token 32 th + 16 x + c, comes behind U where all wavefronts of
+        // a full CU would read k, q and S at once here.
+        acc4 ks[2], y[2];
+        bf8 part[KN][2];   // S's first two parts, kept for S Q^T
+#pragma unroll
+        for (int st = 0; st < KN; ++st) {
+            bf8 k[2];
+#pragma unroll
+            for (int x = 0; x < 2; ++x) k[x] = operand(m.k, x, st);
+#pragma unroll
+            for (int z = 2; z >= 0; --z) {
+                const bf8 p = frag16(xl + (3 * st + z) * kFrag);
+                if (z < 2) part[st][z] = p;
+#pragma unroll
+                for (int x = 0; x < 2; ++x) ks[x] = mma16(k[x], p, st == 0 && z == 2 ? acc4{0.f, 0.f, 0.f, 0.f} : ks[x]);
+            }
+        }
+        auto read_state = [&] {
+#pragma unroll
+            for (int st = 0; st < KN; ++st) {
+                bf8 q[2];
+#pragma unroll
+                for (int x = 0; x < 2; ++x) q[x] = operand(m.q, x, st);
+#pragma unroll
+                for (int z = 1; z >= 0; --z)
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) y[x] = mma16(part[st][z], q[x], st == 0 && z == 1 ? acc4{0.f, 0.f, 0.f, 0.f} : y[x]);
+            }
+#pragma unroll
+            for (int x = 0; x < 2; ++x) y[x] *= my.dn(x);
+        };
+        if constexpr (!Sh::SHARE) read_state();
+        // (0 v is a NaN where v is no number)
+        float none = my.odd() ? __builtin_nanf("") : 0.f;
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            const f32x4 d = my.d(x);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const float v = bf16_bits_to_f32(val.v[4 * x + r]);
+                none = fmaf(v, 0.f, none);
+                ks[x][r] = fmaf(-d[r], ks[x][r], v);
+            }
+        }
+        if (__any(none != none) && lane == 0) odd_chunk = 1;
+        bf8 rp[3];
+        split<3>(ks[0], ks[1], rp);
+        if (th == 0)
+#pragma unroll
+            for (int z = 0; z < 3; ++z) put_frag(ex.r[z] + 16 * lane, rp[z]);
+        lds_barrier();   // R of the first tokens
+        const bool odd = odd_chunk != 0;
+        val.load(vp, rv, left < kQ ? left : kQ, vo);
+        bf8 up[2], ep[3];
+        if (!odd) {
+            acc4 u[2];
+#pragma unroll
+            for (int x = 0; x < 2; ++x) u[x] = acc4{0.f, 0.f, 0.f, 0.f};
+            constexpr int a[6] = {0, 0, 1, 1, 0, 2}, o[6] = {0, 1, 0, 1, 2, 0};   // parts of T and R, the largest first
+            if (th) {
+                bf8 rx[3];
+#pragma unroll
+                for (int z = 0; z < 3; ++z) rx[z] = frag16(xl + kR + z * kFrag);
+#pragma unroll
+                for (int z = 5; z >= 0; --z)
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) u[x] = mma16(my.tx(x, a[z]), rx[o[z]], u[x]);
+            }
+#pragma unroll
+            for (int z = 5; z >= 0; --z)
+#pragma unroll
+                for (int x = 0; x < 2; ++x) u[x] = mma16(my.t(x, a[z]), rp[o[z]], u[x]);
+            split<2>(u[0], u[1], up);
+            if (th == 0)
+#pragma unroll
+                for (int z = 0; z < 2; ++z) put_frag(ex.u[z] + 16 * lane, up[z]);
+#pragma unroll
+            for (int x = 0; x < 2; ++x) u[x] *= my.e(x);
+            split<3>(u[0], u[1], ep);
+#pragma unroll
+            for (int z = 0; z < 3; ++z) put_frag(ex.e[th][z] + 16 * lane, ep[z]);
+            if constexpr (Sh::SHARE) read_state();
+        } else {
+            put_state();
+            __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup");
+        }
+        const float all = my.all();   // (before the slot's next chunk is loaded)
+        if constexpr (!Sh::SHARE) {
+            my.load_decays(next, th, lane);
+            my.load_t(next, th, lane);
+        }
+        lds_barrier();   // U of the first tokens, e U of all
+        if (!odd) {
+            // y^T: + U^T G^T
+            if (th) {
+                bf8 ux[2];
+#pragma unroll
+                for (int z = 0; z < 2; ++z) ux[z] = frag16(xl + kU + z * kFrag);
+#pragma unroll
+                for (int z = 2; z >= 0; --z)
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) y[x] = mma16(ux[z == 2], my.gx(x, z == 1), y[x]);
+            }
+#pragma unroll
+            for (int z = 2; z >= 0; --z)
+#pragma unroll
+                for (int x = 0; x < 2; ++x) y[x] = mma16(up[z == 2], my.g(x, z == 1), y[x]);
+            const auto ys = make_rsrc(yp, (uint32_t)(n - 1) * rv + 32);
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+                __builtin_amdgcn_raw_buffer_store_b64(
+                    u32x2{f32x2_to_bf16_pair(y[x][0], y[x][1]), f32x2_to_bf16_pair(y[x][2], y[x][3])}, ys, yo, 16 * x * rv, 0);
+            // S^T <- (whole decay) S^T + K^T (e U), the wavefront's own tokens first
+            bf8 ox[3];
+#pragma unroll
+            for (int z = 0; z < 3; ++z) ox[z] = frag16(xl + kE + 3 * kFrag * (1 - th) + z * kFrag);
+#pragma unroll
+            for (int t = 0; t < 2 * KH; ++t) S[t] *= all;
+#pragma unroll
+            for (int st = 0; st < 2; ++st) {
+                const uint8_t *const from_k = m.k + 32 * QB * (st ? 1 - th : th) + (KH == 2 ? 128 * th : 0);
+                bf8 k[2 * KH];
+#pragma unroll
+                for (int t = 0; t < 2 * KH; ++t) {
+                    const uint8_t *const kt = from_k + (KH == 2 ? col[t] : (th ? col[t + 2] : col[t]));
+                    const s16x4 lo = col4(kt), hi = col4(kt + 16 * QB);
+                    k[t] = __builtin_bit_cast(bf8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+                }
+#pragma unroll
+                for (int z = 2; z >= 0; --z)
+#pragma unroll
+                    for (int t = 0; t < 2 * KH; ++t) S[t] = mma16(k[t], st ? ox[z] : ep[z], S[t]);
+            }
+            hand_state();
+        } else if (th == 0) {
+            __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup");
+            by_token<P, N, CW>(s, m, state, sp.t0 + done, n, h, p0 + c, lane);
+            __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup");
+        }
+        yp += (size_t)kQ * rv;
+        if constexpr (!Sh::SHARE) my.load_g(next, th, lane);
+        lds_barrier();   // k, q and what was handed over are read to their end
+        if (odd) {
+            __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup");
+            get_state(state);
+            hand_state();
+        }
+        if (th == 0 && lane == 0) odd_chunk = 0;
+        ahead.store(m);
+    }
+    put_state();
+}
+
+template <int P, int N, int CW>
+hipError_t launch_chain(const ScanArgs &a, hipStream_t s) {
+    using Sh = Shape<P, N, CW>;
+    delta_mx_kernel<P, N, CW><<<scan_blocks(a, 1, Sh::CB), Sh::NT, 0, s>>>(a);
+    return hipGetLastError();
+}
+
+template <int P, int N>
+hipError_t launch_pn(ScanArgs a, hipStream_t s) {
+    const int chunks = ((a.seg_len < a.max_len ? a.seg_len : a.max_len) + kQ - 1) / kQ;
+    for (a.chunk0 = 0; a.chunk0 < chunks; a.chunk0 += a.window) {
+        const int64_t units = (int64_t)a.B * a.window * a.H;
+        if (a.H / a.G % 2 == 0)
+            delta_prep_kernel<N, 2><<<(unsigned)(units / 2), kPrepNT, 0, s>>>(a);
+        else
+            delta_prep_kernel<N, 1><<<(unsigned)units, kPrepNT, 0, s>>>(a);
+        hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+        e = (int64_t)a.B * a.H * P / 64 >= 128 ? launch_chain<P, N, 4>(a, s) : launch_chain<P, N, 1>(a, s);
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
+}
+
+// More than this and the workspace is used again, window after window.
+constexpr size_t kMostWorkspace = (size_t)512 << 20;
+
+}  // namespace
+
+bool delta_mx_supported(int P, int N, const ScanArgs &a) {
+    return a.io_bf16 && a.window > 0;
+}
+
+int delta_window(int P, int N, int B, int H, bool bf16, int longest, size_t *bytes) {
+    *bytes = 0;
+    if (!bf16 || P < 64) return 0;
+    const size_t each = (size_t)B * H * kSlot;   // a chunk of every sequence
+    const size_t chunks = ((size_t)longest + kQ - 1) / kQ;
+    size_t n = kMostWorkspace / each;
+    n = n < 1 ? 1 : (n > chunks ? chunks : n);
+    *bytes = n * each;
+    return (int)n;
+}
+
+hipError_t launch_delta_mx(int P, int N, const ScanArgs &a, hipStream_t s) {
+    if (P == 64 && N == 64) return launch_pn<64, 64>(a, s);
+    if (P == 64 && N == 128) return launch_pn<64, 128>(a, s);
+    if (P == 128 && N == 128) return launch_pn<128, 128>(a, s);
+    return hipErrorInvalidValue;
+}
+
+}  // namespace replay

@@ -23,6 +23,10 @@
 // product before left in accumulators, (column l % 16, rows 4 (l / 16) + r):
 // neither S nor U passes through LDS.
 //
+// Bound by the chain of a chunk's steps, one workgroup's behind the other: three
+// prompts of 97 tokens in all, 4 heads of 64 x 128, 26 us for 2 chunks.  bf16 io
+// with heads of 64 or 128 columns takes delta_mx.hip.
+//
 // A value that is no number: one of v is to reach its column alone, from its
 // token on, and one of k, beta or alpha nothing before its token; but the
 // products run over the whole chunk, and 0 NaN is NaN.  So a chunk ends ahead
@@ -358,6 +362,7 @@ hipError_t launch_io(int P, int N, const ScanArgs &a, hipStream_t s) {
 }  // namespace
 
 hipError_t launch_delta_scan(int P, int N, const ScanArgs &a, hipStream_t s) {
+    if (delta_mx_supported(P, N, a)) return launch_delta_mx(P, N, a, s);
     return a.io_bf16 ? launch_io<true>(P, N, a, s) : launch_io<false>(P, N, a, s);
 }
 

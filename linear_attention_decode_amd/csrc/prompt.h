@@ -61,6 +61,9 @@ struct ScanArgs {
     int32_t nseg, seg_len;         // segments of a sequence, tokens of a segment
     float *ws;                     // nseg > 1: states [B][H][nseg - 1][P][N], then
     float *ws_decay;               // decays [B][H][nseg - 1]
+    // the gated delta rule's bf16 kernels: chunks of a sequence in the
+    // workspace at a time, and the first of them
+    int32_t window, chunk0;
 };
 
 // Sampling (sample.hip).
@@ -104,6 +107,8 @@ hipError_t launch_sample(const SampleArgs &a, hipStream_t s);
 hipError_t launch_scan(int P, int N, const ScanArgs &a, hipStream_t s);
 // the gated delta rule (delta_scan.hip): dt carries beta, a alpha
 hipError_t launch_delta_scan(int P, int N, const ScanArgs &a, hipStream_t s);
+// chunks of a sequence that the workspace holds at a time (0: it needs none), and its bytes
+int delta_window(int P, int N, int B, int H, bool bf16, int longest, size_t *bytes);
 int scan_segments(int P, int N, int B, int H, int G, bool bf16, int T, int max_len, int *seg_len);   // the number of segments, and their length
 // hipErrorInvalidConfiguration: more workgroups than a launch numbers
 hipError_t launch_conv_prompt(const ConvArgs &a, hipStream_t s);

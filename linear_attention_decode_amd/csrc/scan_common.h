@@ -16,11 +16,12 @@ constexpr int kScanChunk = 64;   // segments are whole chunks of either kernel
 // where lengths differ.  Of up to 64 sequences the longest go first (a lane
 // each, ranked by 64 comparisons): the last workgroups to start are then the
 // shortest.  False for the places that fill up the last round.
+// CB workgroups share a head, each with its columns of v: block cb of them.
 struct Place {
-    int b, seg, h, g;
+    int b, seg, h, g, cb;
 };
-__device__ __forceinline__ bool find_place(const ScanArgs &a, int HB, Place *p) {
-    const int per = a.H / a.G / HB, x = blockIdx.x & 7, j = blockIdx.x >> 3;
+__device__ __forceinline__ bool find_place(const ScanArgs &a, int HB, Place *p, int CB = 1) {
+    const int per = a.H / a.G / HB * CB, x = blockIdx.x & 7, j = blockIdx.x >> 3;
     const int64_t unit = (int64_t)(j / per) * 8 + x;
     if (unit >= (int64_t)a.B * a.nseg * a.G) return false;
     p->g = (int)(unit % a.G);
@@ -36,12 +37,13 @@ __device__ __forceinline__ bool find_place(const ScanArgs &a, int HB, Place *p) 
         }
         p->b = __builtin_ctzll(__ballot(lane < a.B && rank == p->b));
     }
-    p->h = p->g * (a.H / a.G) + j % per * HB;
+    p->h = p->g * (a.H / a.G) + j % per / CB * HB;
+    p->cb = j % per % CB;
     return true;
 }
-inline unsigned scan_blocks(const ScanArgs &a, int HB) {
+inline unsigned scan_blocks(const ScanArgs &a, int HB, int CB = 1) {
     const int64_t units = (int64_t)a.B * a.nseg * a.G;
-    return (unsigned)((units + 7) / 8 * 8 * (a.H / a.G / HB));
+    return (unsigned)((units + 7) / 8 * 8 * (a.H / a.G / HB * CB));
 }
 
 // Where a workgroup's tokens are.
@@ -61,11 +63,48 @@ __device__ __forceinline__ Span find_span(const ScanArgs &a, int b, int seg) {
 
 __device__ __forceinline__ bool finite(float x) { return (__float_as_uint(x) & 0x7f800000u) != 0x7f800000u; }
 
+// The value of the lane d before (behind) this one in its row of 16, 1 past the row's end.
+template <int CTRL>
+__device__ __forceinline__ float row_move(float x) {
+    return __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp(0x3f800000, (int)__float_as_uint(x), CTRL, 0xf, 0xf, false));
+}
+__device__ __forceinline__ float row_upto(float x) {
+    x *= row_move<0x111>(x);
+    x *= row_move<0x112>(x);
+    x *= row_move<0x114>(x);
+    x *= row_move<0x118>(x);
+    return x;
+}
+__device__ __forceinline__ float row_from(float x) {
+    x *= row_move<0x101>(x);
+    x *= row_move<0x102>(x);
+    x *= row_move<0x104>(x);
+    x *= row_move<0x108>(x);
+    return x;
+}
+
+__device__ __forceinline__ float lane_value(float x, int lane) {
+    return __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(x), lane));
+}
+
+// x's upper bits and y's as a bf16 pair
+__device__ __forceinline__ uint32_t upper_pair(float x, float y) {
+    return __builtin_amdgcn_perm(__float_as_uint(y), __float_as_uint(x), 0x07060302u);
+}
+// what these leave of x
+__device__ __forceinline__ float below_upper(float x) { return x - __uint_as_float(__float_as_uint(x) & 0xffff0000u); }
+// ... of both, as a bf16 pair
+__device__ __forceinline__ uint32_t lower_pair(float x, float y) { return f32x2_to_bf16_pair(below_upper(x), below_upper(y)); }
+
 // The bf16 kernel's part of launch_scan: whether it covers the shape, the
 // heads it gives a workgroup, and its launch (state_only: the segments' own
 // states into the workspace).
 bool scan_mx_supported(int P, int N, const ScanArgs &a);
 int scan_mx_heads(int P, int H, int G);
+// The same of launch_delta_scan (delta_mx.hip), with the bytes of workspace it
+// needs and the chunks of a sequence that it covers at a time.
+bool delta_mx_supported(int P, int N, const ScanArgs &a);
+hipError_t launch_delta_mx(int P, int N, const ScanArgs &a, hipStream_t s);
 hipError_t launch_scan_mx(int P, int N, const ScanArgs &a, bool state_only, hipStream_t s);
 
 }  // namespace replay

@@ -101,30 +101,6 @@ __device__ __forceinline__ int pi(int c) {
     return (c & ~12) | ((x == 1 ? 2 : (x == 2 ? 1 : x)) << 2);
 }
 
-// The value of the lane d before (behind) this one in its row of 16, 1 past the row's end.
-template <int CTRL>
-__device__ __forceinline__ float row_move(float x) {
-    return __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp(0x3f800000, (int)__float_as_uint(x), CTRL, 0xf, 0xf, false));
-}
-__device__ __forceinline__ float row_upto(float x) {
-    x *= row_move<0x111>(x);
-    x *= row_move<0x112>(x);
-    x *= row_move<0x114>(x);
-    x *= row_move<0x118>(x);
-    return x;
-}
-__device__ __forceinline__ float row_from(float x) {
-    x *= row_move<0x101>(x);
-    x *= row_move<0x102>(x);
-    x *= row_move<0x104>(x);
-    x *= row_move<0x108>(x);
-    return x;
-}
-
-__device__ __forceinline__ float lane_value(float x, int lane) {
-    return __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(x), lane));
-}
-
 template <int P, int N, int VW>
 struct Shape {
     static constexpr int NW = VW / 32, NT = 64 * NW, HB = VW / P;   // wavefronts, threads, heads
@@ -229,15 +205,6 @@ struct Ahead {
         }
     }
 };
-
-// x's upper bits and y's as a bf16 pair
-__device__ __forceinline__ uint32_t upper_pair(float x, float y) {
-    return __builtin_amdgcn_perm(__float_as_uint(y), __float_as_uint(x), 0x07060302u);
-}
-// what these leave of x
-__device__ __forceinline__ float below_upper(float x) { return x - __uint_as_float(__float_as_uint(x) & 0xffff0000u); }
-// ... of both, as a bf16 pair
-__device__ __forceinline__ uint32_t lower_pair(float x, float y) { return f32x2_to_bf16_pair(below_upper(x), below_upper(y)); }
 
 // G = the weighted scores, in 16 x 16 tiles (ti, tj) of K Q^T, lane (column i
 // = l % 16, rows j = 4 (l / 16) + r).  A fourth of the work is the diagonal
