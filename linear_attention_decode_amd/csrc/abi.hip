@@ -1064,7 +1064,9 @@ replay_status replay_verify_tree(replay_handle *h, int32_t W, const int32_t *par
     for (const float *p : {dt, a})
         if (!p || !aligned4(p)) return REPLAY_ERR_INVALID_ARG;
     const replay_config &c = h->cfg;
-    if (W > kMaxTree || !launch_fits((int64_t)c.batch * c.heads, 4 * c.head_dim)) return REPLAY_ERR_UNSUPPORTED;
+    if (W > kMaxTree || !launch_fits((int64_t)c.batch * c.heads, 4 * c.head_dim) || (int64_t)c.heads * c.head_dim > kMaxTreeRow ||
+        (int64_t)c.groups * c.state_dim > kMaxTreeRow)
+        return REPLAY_ERR_UNSUPPORTED;
     TreeArgs t{};
     t.r = ring_view(h);
     t.S = c.read_copy == REPLAY_NONE ? static_cast<const void *>(h->bufs.s_master) : h->bufs.s_copy;

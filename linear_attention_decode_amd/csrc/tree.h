@@ -5,6 +5,9 @@
 
 namespace replay {
 
+// Most values in a node's rows of q, k or v: 64 of them then stay within 31-bit byte offsets.
+constexpr int64_t kMaxTreeRow = 1 << 23;
+
 // Outputs of a tree of W nodes a sequence, and its accepted path's append.
 struct TreeArgs {
     RingView r;

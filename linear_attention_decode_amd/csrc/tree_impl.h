@@ -14,10 +14,14 @@
 //     which is the recurrence solved for its corrections, as over a prompt's
 //     chunk, with "before" read off the tree.
 //
+// The system is solved in blocks of 16 entries from the last one back: C_J^T =
+// T_JJ^T (G_J^T - sum_{I > J} A_IJ^T C_I^T), T_JJ the inverse of a diagonal block by
+// substitution, all of them at once.
+//
 // A workgroup takes one (sequence, head), a wavefront 16 of its rows: their
-// tile of S0 is on its way while the workgroup forms the weights C (and x) in
-// LDS; then S0 x^T and V^T C^T go into one accumulator, both on
-// v_mfma_f32_16x16x4_f32, 16 nodes at a time.
+// tile of S0, and the columns of v that meet it, are on their way while the
+// workgroup forms the weights C (and x) in LDS; then S0 x^T and V^T C^T go into one
+// accumulator, both on v_mfma_f32_16x16x4_f32, 16 nodes at a time.
 #pragma once
 
 #include "tree.h"
@@ -34,65 +38,61 @@ struct TreeShape {
     static constexpr int ME = (kMaxRing + kMaxTree) / 4;   // entries a lane of the V product holds
 };
 
-// LDS, in floats: weights C [WP][CS]; then the decays D [WP][WP] (gated delta
-// rule: and A^T [ES][CS], the ring's own decays [LP][LP]), which the queries
-// [WP][XS] replace.
+// LDS, in floats: weights C [WP][CS], decays D [WP][WP]; then the queries
+// [WP][XS], which for the gated delta rule take the place of A^T [ES][CS], the diagonal
+// blocks' inverses [ES][16] (transposed) and the ring's own decays [LP][LP].
 struct TreeLds {
-    int WP, LP, ES, CS, a, rr, total;
+    int WP, LP, ES, CS, x, inv, rr, total;
     __host__ __device__ TreeLds(int W, int L, int N, bool delta) {
         WP = (W + 15) / 16 * 16;
         LP = (L + 15) / 16 * 16;
         ES = LP + WP;
         CS = ES + 4;
-        a = WP * CS + WP * WP;
-        rr = a + ES * CS;
-        const int first = delta ? rr + LP * LP : a, second = WP * (CS + N + 4);
+        x = WP * CS + WP * WP;
+        inv = x + ES * CS;
+        rr = inv + ES * 16;
+        const int first = delta ? rr + LP * LP : 0, second = x + WP * (N + 4);
         total = first > second ? first : second;
     }
 };
 
-// Entry e's row: ring entries 0 .. LP - 1 (there are count), then the nodes.
-// False: there is none.
+// The rows of k (or v) of the entries, in bytes: ring entries 0 .. LP - 1 (there
+// are count), then the nodes.  Loads of a row that is none read zero.
 struct Entries {
-    const TreeArgs &t;
-    int b, g, h, bmod, count, n, LP;
-    __device__ __forceinline__ bool at(int e, bool v, const void **base, size_t *row) const {
-        const RingView &r = t.r;
-        if (e < LP) {
-            if (e >= count) return false;
-            *base = v ? r.v : r.k;
-            *row = (v ? (size_t)b * r.H + h : (size_t)b * r.G + g) * r.L + ring_slot(bmod, e, r.L);
-            return true;
-        }
-        if (e - LP >= n) return false;
-        *base = v ? t.v : t.k;
-        const size_t token = (size_t)b * t.W + (e - LP);
-        *row = v ? token * r.H + h : token * r.G + g;
-        return true;
+    __amdgpu_buffer_rsrc_t ring, nodes;
+    uint32_t row, stride;   // bytes of a row; from a node to the next
+    int bmod, L, count, LP;
+    __device__ __forceinline__ Entries(const void *ring0, const void *node0, uint32_t row_, uint32_t stride_, int base, int L_,
+                                       int count_, int n, int LP_)
+        : ring(make_rsrc(ring0, (uint32_t)L_ * row_)), nodes(make_rsrc(node0, (uint32_t)(n - 1) * stride_ + row_)), row(row_),
+          stride(stride_), bmod(base % L_), L(L_), count(count_), LP(LP_) {}
+    __device__ __forceinline__ uint32_t ring_at(int e) const {
+        return e < count ? (uint32_t)ring_slot(bmod, e, L) * row : 0x80000000u;
+    }
+    // element `col` of entry e, of a tile of entries that are all the ring's or all nodes
+    template <bool IOB>
+    __device__ __forceinline__ uint32_t value(int e, bool of_ring, int col) const {
+        const uint32_t o = (of_ring ? ring_at(e) : (uint32_t)(e - LP) * stride) + col * (IOB ? 2 : 4);
+        if constexpr (IOB) return of_ring ? (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(ring, o, 0, 0) : (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(nodes, o, 0, 0);
+        return of_ring ? __builtin_amdgcn_raw_buffer_load_b32(ring, o, 0, 0) : __builtin_amdgcn_raw_buffer_load_b32(nodes, o, 0, 0);
     }
 };
+template <bool IOB>
+__device__ __forceinline__ float entry_value(uint32_t raw) { return IOB ? bf16_bits_to_f32(raw) : __uint_as_float(raw); }
 
 // A lane's part of an operand of k . k or k . q: 8 of every 32 columns of a row.
 template <int N, bool IOB>
 struct DotRow {
     static constexpr int KB = (N + 31) / 32;
-    uint4 b[IOB ? KB : 1];
-    f32x4 f[IOB ? 1 : KB][2];
-    __device__ __forceinline__ void load(const void *base, size_t row, bool there, int lane) {
+    u32x4 b[KB][IOB ? 1 : 2];
+    // the row at byte o; columns past N (only where N < 32) read zero
+    __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t rows, uint32_t o, int lane) {
 #pragma unroll
         for (int kb = 0; kb < KB; ++kb) {
             const int c = 32 * kb + 8 * (lane >> 4);
-            const bool in = there && c < N;
-            if constexpr (IOB) {
-                b[kb] = uint4{0u, 0u, 0u, 0u};
-                if (in) b[kb] = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(base) + row * N + c);
-            } else {
+            const uint32_t at = c < N ? o + c * (IOB ? 2 : 4) : 0x80000000u;
 #pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    f[kb][x] = f32x4{0.f, 0.f, 0.f, 0.f};
-                    if (in) f[kb][x] = *reinterpret_cast<const f32x4 *>(static_cast<const float *>(base) + row * N + c + 4 * x);
-                }
-            }
+            for (int x = 0; x < (IOB ? 1 : 2); ++x) b[kb][x] = __builtin_amdgcn_raw_buffer_load_b128(rows, at + 16 * x, 0, 0);
         }
     }
     // rows of this (M) by rows of o (N): register r is (4 (lane / 16) + r, lane % 16)
@@ -101,10 +101,11 @@ struct DotRow {
 #pragma unroll
         for (int kb = 0; kb < KB; ++kb) {
             if constexpr (IOB) {
-                d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(b[kb]), as_bf16x8(o.b[kb]), d, 0, 0, 0);
+                d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, b[kb][0]), __builtin_bit_cast(bf16x8_t, o.b[kb][0]), d, 0, 0, 0);
             } else {
 #pragma unroll
-                for (int t = 0; t < 8; ++t) d = __builtin_amdgcn_mfma_f32_16x16x4f32(f[kb][t >> 2][t & 3], o.f[kb][t >> 2][t & 3], d, 0, 0, 0);
+                for (int t = 0; t < 8; ++t)
+                    d = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(b[kb][t >> 2][t & 3]), __uint_as_float(o.b[kb][t >> 2][t & 3]), d, 0, 0, 0);
             }
         }
         return d;
@@ -149,45 +150,80 @@ __global__ __launch_bounds__((TreeShape<P, N>::NT)) void verify_tree_kernel(Tree
     if (n == 0) return;
     const TreeLds at(W, L, N, DELTA);
     const int WP = at.WP, LP = at.LP, ES = at.ES, CS = at.CS;
-    float *s_C = lds, *s_D = lds + WP * CS, *s_A = lds + at.a, *s_RR = lds + at.rr, *s_X = lds + WP * CS;
+    float *s_C = lds, *s_D = lds + WP * CS, *s_X = lds + at.x, *s_A = s_X, *s_inv = lds + at.inv, *s_RR = lds + at.rr;
     const int wt_n = (n + 15) / 16, et_n = LP / 16 + wt_n, e_end = LP + n;
-    const Entries ent{t, b, g, h, base % L, count, n, LP};
+    constexpr uint32_t ESZ = IOB ? 2 : 4;
+    const Entries ks(static_cast<const char *>(r.k) + ((size_t)b * r.G + g) * L * N * ESZ,
+                     static_cast<const char *>(t.k) + ((size_t)b * W * r.G + g) * N * ESZ, N * ESZ, (uint32_t)r.G * N * ESZ, base,
+                     L, count, n, LP);
+    const Entries vs(static_cast<const char *>(r.v) + bh * L * P * ESZ, static_cast<const char *>(t.v) + ((size_t)b * W * H + h) * P * ESZ,
+                     P * ESZ, (uint32_t)H * P * ESZ, base, L, count, n, LP);
+    const auto qs = make_rsrc(static_cast<const char *>(t.q) + ((size_t)b * W * r.G + g) * N * ESZ, (uint32_t)(n - 1) * ks.stride + N * ESZ);
 
-    // raw dots: C[w][e] = k_e . q_w, and A^T[j][i] = k_j . k_i of tiles i >= j
+    // column p0 + lr of v of entries 4 s + lg
+    uint32_t vc[Sh::ME];
+#pragma unroll
+    for (int s = 0; s < Sh::ME; ++s) {
+        vc[s] = 0;
+        if (4 * s < e_end) vc[s] = vs.template value<IOB>(4 * s + lg, 4 * s < LP, p0 + lr);
+    }
+    if constexpr (!DELTA) {   // the queries, 4 columns a thread and turn
+        for (int i = tid; i < 16 * wt_n * (N / 4); i += NT) {
+            const int w = i / (N / 4), c = i % (N / 4) * 4;
+            f32x4 q;
+            if constexpr (IOB) {
+                const u32x2 x = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(qs, (uint32_t)w * ks.stride + c * 2, 0, 0));
+                q = f32x4{bf16_bits_to_f32(x[0] & 0xffffu), bf16_bits_to_f32(x[0] >> 16), bf16_bits_to_f32(x[1] & 0xffffu), bf16_bits_to_f32(x[1] >> 16)};
+            } else {
+                q = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(qs, (uint32_t)w * ks.stride + c * 4, 0, 0));
+            }
+            *reinterpret_cast<f32x4 *>(&s_X[w * XS + c]) = q;
+        }
+    }
+
+    // raw dots: C[w][e] = k_e . q_w, and A^T[j][i] = k_j . k_i of tiles i >= j;
+    // the next tile's rows are on their way during a product
     {
         const int cq = et_n * wt_n, total = cq + (DELTA ? et_n * (et_n + 1) / 2 : 0);
-        for (int x = wave; x < total; x += NW) {
+        auto place = [&](int x, int *et, int *ot) {
+            if (x < cq) {
+                *et = x / wt_n;
+                *ot = x % wt_n;
+                return;
+            }
+            int o = 0, left = x - cq;
+            while (left > o) left -= ++o;
+            *et = left;   // <= ot
+            *ot = o;
+        };
+        auto rows_of = [&](DotRow<N, IOB> &d, int tile) {
+            if (16 * tile < LP) d.load(ks.ring, ks.ring_at(16 * tile + lr), lane);
+            else d.load(ks.nodes, (uint32_t)(16 * tile + lr - LP) * ks.stride, lane);
+        };
+        auto load = [&](int x, DotRow<N, IOB> &A, DotRow<N, IOB> &B) {
             int et, ot;
-            const bool kk = x >= cq;
-            if (!kk) {
-                et = x / wt_n;
-                ot = x % wt_n;
-            } else {
-                ot = 0;
-                int left = x - cq;
-                while (left > ot) left -= ++ot;
-                et = left;   // et <= ot
-            }
-            DotRow<N, IOB> A, B;
-            const void *src = nullptr;
-            size_t row = 0;
-            bool there = ent.at(16 * et + lr, false, &src, &row);
-            A.load(src, row, there, lane);
-            if (kk) {
-                there = ent.at(16 * ot + lr, false, &src, &row);
-            } else {
-                const int w = 16 * ot + lr;
-                there = w < n;
-                src = t.q;
-                row = ((size_t)b * W + w) * r.G + g;
-            }
-            B.load(src, row, there, lane);
+            place(x, &et, &ot);
+            rows_of(A, et);
+            if (x < cq) B.load(qs, (uint32_t)(16 * ot + lr) * ks.stride, lane);
+            else rows_of(B, ot);
+        };
+        DotRow<N, IOB> A, B;
+        if (wave < total) load(wave, A, B);
+        for (int x = wave; x < total; x += NW) {
+            DotRow<N, IOB> nextA, nextB;
+            if (x + NW < total) load(x + NW, nextA, nextB);
+            int et, ot;
+            place(x, &et, &ot);
             const f32x4 d = A.dots(B);
-            if (!kk) {
+            if (x < cq) {
                 *reinterpret_cast<f32x4 *>(&s_C[(16 * ot + lr) * CS + 16 * et + 4 * lg]) = d;
             } else {
 #pragma unroll
                 for (int rr = 0; rr < 4; ++rr) s_A[(16 * et + 4 * lg + rr) * CS + 16 * ot + lr] = d[rr];
+            }
+            if (x + NW < total) {
+                A = nextA;
+                B = nextB;
             }
         }
     }
@@ -240,15 +276,20 @@ __global__ __launch_bounds__((TreeShape<P, N>::NT)) void verify_tree_kernel(Tree
             s_gam[LP + lane] = path * all;
             s_dt[LP + lane] = ndt;
         }
-        // D[w][j], row by row: the parent's, one factor more
-        float cur = 0.f;
-        for (int w = 0; w < n; ++w) {
-            const int pw = __builtin_amdgcn_readlane(tree.parent, w);
-            const float aw = bcast(na, w);
-            float prev = 0.f;
-            if (pw >= 0) prev = pw == w - 1 ? cur : (lane < WP ? s_D[pw * WP + lane] : 0.f);
-            cur = lane == w ? 1.f : prev * aw;
-            if (lane < WP) s_D[w * WP + lane] = cur;
+        // D[w][j] for the j on w's way up, a lane a node: the nearest first
+        {
+            float p = 1.f;
+            int x = lane < n ? lane : -1;
+            while (__any(x >= 0)) {
+                const int from = x < 0 ? 0 : x;
+                const float f = __shfl(na, from);
+                const int u = __shfl(tree.parent, from);
+                if (x >= 0) {
+                    s_D[lane * WP + x] = p;
+                    p *= f;
+                    x = u;
+                }
+            }
         }
         if constexpr (DELTA) {
             float p = 1.f;
@@ -258,74 +299,88 @@ __global__ __launch_bounds__((TreeShape<P, N>::NT)) void verify_tree_kernel(Tree
             }
         }
     }
-    __syncthreads();
+    lds_barrier();
 
     // weights: the dots of what lies on the node's path, decayed (selects, not
     // factors of 0: another branch's NaN stays there)
     auto on_path = [&](int w, int e) { return w < n && (e < LP ? e < count : (s_anc[w] >> (e - LP) & 1) != 0); };
     auto decay = [&](int w, int e) { return e < LP ? s_R[e] * s_path[w] : s_D[w * WP + e - LP]; };
-    for (int i = tid; i < 16 * wt_n * ES; i += NT) {
-        const int w = i / ES, e = i % ES;
-        float *c = s_C + w * CS + e;
-        *c = on_path(w, e) ? decay(w, e) * *c * (DELTA ? 1.f : s_dt[e]) : 0.f;
-    }
-    if constexpr (DELTA) {
-        for (int x = tid; x < ES * ES; x += NT) {
-            const int j = x / ES, i = x % ES;
-            if (i >= LP + 16 * wt_n) continue;
-            float c = 0.f;
-            if (i > j && (i < LP ? i < count : on_path(i - LP, j)))
-                c = (i < LP ? s_RR[j * LP + i] : decay(i - LP, j)) * s_A[j * CS + i] * s_dt[i];
-            s_A[j * CS + i] = c;
+    for (int w = tid / 16; w < 16 * wt_n; w += NT / 16)   // 16 threads a row
+        for (int e = tid % 16; e < ES; e += 16) {
+            float *c = s_C + w * CS + e;
+            *c = on_path(w, e) ? decay(w, e) * *c * (DELTA ? 1.f : s_dt[e]) : 0.f;
         }
-        __syncthreads();
-        // C (I + A) = G, a node's row from its last entry back: four lanes a
-        // node, each a quarter of the sum
-        const int part = lane & 3;
-        for (int wt = wave; wt < wt_n; wt += NW) {
-            float *row = s_C + (16 * wt + (lane >> 2)) * CS;
-            for (int j = e_end - 2; j >= 0; --j) {
-                if (j >= count && j < LP) j = count - 1;   // (count = 0: -1, none is left)
-                if (j < 0) break;
-                const float *col = s_A + j * CS;
-                float sum = 0.f;
-                for (int i = (j + 1 & ~3) + part; i < e_end; i += 4) {
-                    const float c = row[i];
-                    if (i > j && c != 0.f) sum = fmaf(c, col[i], sum);   // (0: not on the path, or without part in it)
+    if constexpr (DELTA) {
+        // A^T; of values that are no numbers nothing: what they have to reach, G, beta
+        // and the decays carry
+        for (int j = tid / 16; j < ES; j += NT / 16)
+            for (int i = tid % 16; i < ES; i += 16) {
+                float c = 0.f;
+                if (i > j && i < e_end && (i < LP ? i < count : on_path(i - LP, j)))
+                    c = (i < LP ? s_RR[j * LP + i] : decay(i - LP, j)) * s_A[j * CS + i] * s_dt[i];
+                s_A[j * CS + i] = tree_finite(c) ? c : 0.f;
+            }
+        lds_barrier();
+        // rows of the diagonal blocks' inverses T, a lane a row: y (I + A) = e_r from the last column back
+        for (int x = tid; x < 16 * et_n; x += NT) {
+            const int b0 = x & ~15, row = x & 15;
+            float y[16];
+#pragma unroll
+            for (int j = 15; j >= 0; --j) {
+                y[j] = j == row ? 1.f : 0.f;
+#pragma unroll
+                for (int i4 = j & ~3; i4 < 16; i4 += 4) {
+                    const f32x4 c = *reinterpret_cast<const f32x4 *>(&s_A[(b0 + j) * CS + b0 + i4]);
+#pragma unroll
+                    for (int u = 0; u < 4; ++u)
+                        if (i4 + u > j) y[j] = fmaf(-c[u], y[i4 + u], y[j]);
                 }
-                sum += lane_partner(sum, 0);
-                sum += lane_partner(sum, 1);
-                if (part == 0 && sum != 0.f) row[j] -= sum;
-                wave_lds_sync();
+                s_inv[(b0 + j) * 16 + row] = y[j];   // T^T
             }
         }
-        __syncthreads();
-        for (int i = tid; i < 16 * wt_n * ES; i += NT) {
-            const int w = i / ES, e = i % ES;
-            s_C[w * CS + e] = on_path(w, e) ? s_C[w * CS + e] * s_dt[e] : 0.f;
+        lds_barrier();
+        // C_J^T = T_JJ^T (G_J^T - sum A_IJ^T C_I^T), lane (node lr, entries 4 lg + u), a wavefront 16 nodes
+        for (int wt = wave; wt < wt_n; wt += NW) {
+            float *row = s_C + (16 * wt + lr) * CS + 4 * lg;
+            for (int J = et_n - 1; J >= 0; --J) {
+                f32x4 c = *reinterpret_cast<const f32x4 *>(row + 16 * J);
+                f32x4 sum = {0.f, 0.f, 0.f, 0.f};
+                for (int I = J + 1; I < et_n; ++I) {
+                    const f32x4 m = *reinterpret_cast<const f32x4 *>(&s_A[(16 * J + lr) * CS + 16 * I + 4 * lg]);
+                    const f32x4 o = *reinterpret_cast<const f32x4 *>(row + 16 * I);
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) sum = __builtin_amdgcn_mfma_f32_16x16x4f32(m[u], o[u], sum, 0, 0, 0);
+                }
+                c -= sum;
+                const f32x4 m = *reinterpret_cast<const f32x4 *>(&s_inv[(16 * J + lr) * 16 + 4 * lg]);
+                sum = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int u = 0; u < 4; ++u) sum = __builtin_amdgcn_mfma_f32_16x16x4f32(m[u], c[u], sum, 0, 0, 0);
+                *reinterpret_cast<f32x4 *>(row + 16 * J) = sum;
+                wave_lds_sync();
+            }
+#pragma unroll 1
+            for (int J = 0; J < et_n; ++J) {
+                f32x4 c = *reinterpret_cast<const f32x4 *>(row + 16 * J);
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    const int e = 16 * J + 4 * lg + u;
+                    c[u] = on_path(16 * wt + lr, e) ? c[u] * s_dt[e] : 0.f;
+                }
+                *reinterpret_cast<f32x4 *>(row + 16 * J) = c;
+            }
         }
     }
-    __syncthreads();
+    lds_barrier();
 
-    // the queries, which take the place of the decays
-    if constexpr (!DELTA) {
-        for (int i = tid; i < 16 * wt_n * (N / 4); i += NT) {
-            const int w = i / (N / 4), c = i % (N / 4) * 4;
-            float q[4] = {0.f, 0.f, 0.f, 0.f};
-            if (w < n) load_io4<IOB>(t.q, (((size_t)b * W + w) * r.G + g) * N + c, q);
-            *reinterpret_cast<f32x4 *>(&s_X[w * XS + c]) = f32x4{q[0], q[1], q[2], q[3]};
-        }
-    } else {
+    if constexpr (DELTA) {   // the queries, which take the place of A
         for (int nt = wave; nt < N / 16; nt += NW) {
             float kc[Sh::ME];   // column 16 nt + lr of entries 4 s + lg
 #pragma unroll
             for (int s = 0; s < Sh::ME; ++s) {
                 kc[s] = 0.f;
-                const int e = 4 * s + lg;
-                const void *src;
-                size_t row;
-                if (e < e_end && ent.at(e, false, &src, &row)) {
-                    const float k = load_io1<IOB>(src, row * N + 16 * nt + lr);
+                if (4 * s < e_end) {
+                    const float k = entry_value<IOB>(ks.template value<IOB>(4 * s + lg, 4 * s < LP, 16 * nt + lr));
                     if (tree_finite(k)) kc[s] = k;   // another's weight makes its nodes NaN as it is
                 }
             }
@@ -349,22 +404,18 @@ __global__ __launch_bounds__((TreeShape<P, N>::NT)) void verify_tree_kernel(Tree
             }
         }
     }
-    __syncthreads();
+    if constexpr (DELTA) lds_barrier();
 
     // y^T: rows p0 + 4 lg + rr, nodes 16 wt + lr
     rows.transpose(s_T[WT::COAL ? wave : 0], lane);
-    float vc[Sh::ME];   // column p0 + lr of entries 4 s + lg
+    float vf[Sh::ME];
     bool odd = false;
 #pragma unroll
     for (int s = 0; s < Sh::ME; ++s) {
-        vc[s] = 0.f;
-        const int e = 4 * s + lg;
-        const void *src;
-        size_t row;
-        if (e < e_end && ent.at(e, true, &src, &row)) {
-            const float v = load_io1<IOB>(src, row * P + p0 + lr);
-            if (tree_finite(v)) vc[s] = v;
-            else odd = true;
+        vf[s] = entry_value<IOB>(vc[s]);
+        if (!tree_finite(vf[s])) {
+            vf[s] = 0.f;
+            odd = true;
         }
     }
     odd = __any(odd);
@@ -377,17 +428,15 @@ __global__ __launch_bounds__((TreeShape<P, N>::NT)) void verify_tree_kernel(Tree
 #pragma unroll
         for (int s = 0; s < Sh::ME; ++s) {
             if (4 * s >= e_end) break;
-            y = __builtin_amdgcn_mfma_f32_16x16x4f32(vc[s], s_C[w * CS + 4 * s + lg], y, 0, 0, 0);
+            y = __builtin_amdgcn_mfma_f32_16x16x4f32(vf[s], s_C[w * CS + 4 * s + lg], y, 0, 0, 0);
         }
         if (w >= n) continue;
         if (odd) {   // a value that is no number, for the nodes behind it alone
             for (int e = 0; e < e_end; ++e) {
-                const void *src;
-                size_t row;
-                if (!ent.at(e, true, &src, &row) || (e >= LP && !(s_anc[w] >> (e - LP) & 1))) continue;
+                if (!on_path(w, e)) continue;
 #pragma unroll
                 for (int rr = 0; rr < 4; ++rr) {
-                    const float v = load_io1<IOB>(src, row * P + p0 + 4 * lg + rr);
+                    const float v = entry_value<IOB>(vs.template value<IOB>(e, e < LP, p0 + 4 * lg + rr));
                     if (!tree_finite(v)) y[rr] = fmaf(s_C[w * CS + e], v, y[rr]);
                 }
             }
