@@ -20,6 +20,12 @@ struct Tree {
         n = __builtin_amdgcn_readfirstlane(ok ? n : 0);
         parent = lane < n ? p : -1;
     }
+    // of count nodes, 0 <= count <= W, p loaded already
+    __device__ __forceinline__ void set(int p, int count, int lane) {
+        ok = !__any(lane < count && (p < -1 || p >= lane));
+        n = count;
+        parent = lane < count ? p : -1;
+    }
     // one step up from x: a node, or -s for the s-th token before the tree
     __device__ __forceinline__ int up(int x) const {
         const int p = __shfl(parent, x < 0 ? 0 : x);

@@ -34,16 +34,23 @@ template <int P, int N>
 struct TreeShape {
     static constexpr int NW = P / 16, NT = 64 * NW;
     static constexpr int XS = N + 4;      // LDS row stride of the queries, floats
-    static constexpr int KB = (N + 31) / 32;
-    static constexpr int ME = (kMaxRing + kMaxTree) / 4;   // entries a lane of the V product holds
+    static constexpr int MT = (kMaxRing + kMaxTree) / 16;   // tiles of entries
+    static constexpr int QU = 4 * N / NT;                   // units of 4 columns of 16 queries, by thread
+    static_assert(4 * N % NT == 0, "queries by thread");
+    template <bool IOB>
+    static constexpr int KS = N * (IOB ? 2 : 4) / 4 + 4;    // LDS row stride of the keys, floats
+    template <int ST>
+    static constexpr int TILE = WideTile<P, N, ST>::COAL ? NW * 16 * WideTile<P, N, ST>::TROW : 0;
 };
 
 // LDS, in floats: weights C [WP][CS], decays D [WP][WP]; then the queries
 // [WP][XS], which for the gated delta rule take the place of A^T [ES][CS], the diagonal
-// blocks' inverses [ES][16] (transposed) and the ring's own decays [LP][LP].
+// blocks' inverses [ES][16] (transposed) and the ring's own decays [LP][LP]; then the
+// gated delta rule's keys [ES][KS], whose place the tile of S0 takes on its
+// way into operands (`tile` floats).
 struct TreeLds {
-    int WP, LP, ES, CS, x, inv, rr, total;
-    __host__ __device__ TreeLds(int W, int L, int N, bool delta) {
+    int WP, LP, ES, CS, x, inv, rr, k, total;
+    __host__ __device__ TreeLds(int W, int L, int N, bool delta, int KS, int tile) {
         WP = (W + 15) / 16 * 16;
         LP = (L + 15) / 16 * 16;
         ES = LP + WP;
@@ -52,31 +59,37 @@ struct TreeLds {
         inv = x + ES * CS;
         rr = inv + ES * 16;
         const int first = delta ? rr + LP * LP : 0, second = x + WP * (N + 4);
-        total = first > second ? first : second;
+        k = first > second ? first : second;
+        const int keys = delta ? ES * KS : 0;
+        total = k + (keys > tile ? keys : tile);
     }
 };
 
-// The rows of k (or v) of the entries, in bytes: ring entries 0 .. LP - 1 (there
-// are count), then the nodes.  Loads of a row that is none read zero.
+// The rows of k (or v) of the entries: ring entries 0 .. LP - 1 (there are
+// count), then the nodes.  Loads of a row that is none read zero.
 struct Entries {
-    __amdgpu_buffer_rsrc_t ring, nodes;
-    uint32_t row, stride;   // bytes of a row; from a node to the next
+    const char *ring, *nodes;
+    uint32_t ring_bytes, node_bytes, row, stride;   // bytes in all, of a row, from a node to the next
     int bmod, L, count, LP;
-    __device__ __forceinline__ Entries(const void *ring0, const void *node0, uint32_t row_, uint32_t stride_, int base, int L_,
+    __device__ __forceinline__ Entries(const void *ring0, const void *node0, uint32_t row_, uint32_t stride_, int bmod_, int L_,
                                        int count_, int n, int LP_)
-        : ring(make_rsrc(ring0, (uint32_t)L_ * row_)), nodes(make_rsrc(node0, (uint32_t)(n - 1) * stride_ + row_)), row(row_),
-          stride(stride_), bmod(base % L_), L(L_), count(count_), LP(LP_) {}
-    __device__ __forceinline__ uint32_t ring_at(int e) const {
-        return e < count ? (uint32_t)ring_slot(bmod, e, L) * row : 0x80000000u;
+        : ring(static_cast<const char *>(ring0)), nodes(static_cast<const char *>(node0)), ring_bytes((uint32_t)L_ * row_),
+          node_bytes((uint32_t)(n - 1) * stride_ + row_), row(row_), stride(stride_), bmod(bmod_), L(L_), count(count_), LP(LP_) {}
+    // of the tile of 16 entries from e0 on (all the ring's, or all nodes)
+    __device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_of(int e0) const {
+        return make_rsrc(e0 < LP ? ring : nodes, e0 < LP ? ring_bytes : node_bytes);
     }
-    // element `col` of entry e, of a tile of entries that are all the ring's or all nodes
-    template <bool IOB>
-    __device__ __forceinline__ uint32_t value(int e, bool of_ring, int col) const {
-        const uint32_t o = (of_ring ? ring_at(e) : (uint32_t)(e - LP) * stride) + col * (IOB ? 2 : 4);
-        if constexpr (IOB) return of_ring ? (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(ring, o, 0, 0) : (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(nodes, o, 0, 0);
-        return of_ring ? __builtin_amdgcn_raw_buffer_load_b32(ring, o, 0, 0) : __builtin_amdgcn_raw_buffer_load_b32(nodes, o, 0, 0);
+    __device__ __forceinline__ uint32_t at(int e0, int i) const {
+        const int e = e0 + i;
+        const uint32_t in_ring = e < count ? (uint32_t)ring_slot(bmod, e, L) * row : 0x80000000u;
+        return e0 < LP ? in_ring : (uint32_t)(e - LP) * stride;
     }
 };
+template <bool IOB>
+__device__ __forceinline__ uint32_t load_raw(__amdgpu_buffer_rsrc_t rows, uint32_t o, int col) {
+    if constexpr (IOB) return (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(rows, o + 2 * col, 0, 0);
+    return __builtin_amdgcn_raw_buffer_load_b32(rows, o + 4 * col, 0, 0);
+}
 template <bool IOB>
 __device__ __forceinline__ float entry_value(uint32_t raw) { return IOB ? bf16_bits_to_f32(raw) : __uint_as_float(raw); }
 
@@ -93,6 +106,18 @@ struct DotRow {
             const uint32_t at = c < N ? o + c * (IOB ? 2 : 4) : 0x80000000u;
 #pragma unroll
             for (int x = 0; x < (IOB ? 1 : 2); ++x) b[kb][x] = __builtin_amdgcn_raw_buffer_load_b128(rows, at + 16 * x, 0, 0);
+        }
+    }
+    __device__ __forceinline__ void load(const float *rows, int stride, int lane) {   // from LDS
+        const char *row = reinterpret_cast<const char *>(rows + (lane & 15) * stride);
+#pragma unroll
+        for (int kb = 0; kb < KB; ++kb) {
+            const int c = 32 * kb + 8 * (lane >> 4);
+#pragma unroll
+            for (int x = 0; x < (IOB ? 1 : 2); ++x) {
+                b[kb][x] = u32x4{0, 0, 0, 0};
+                if (c < N) b[kb][x] = *reinterpret_cast<const u32x4 *>(row + c * (IOB ? 2 : 4) + 16 * x);
+            }
         }
     }
     // rows of this (M) by rows of o (N): register r is (4 (lane / 16) + r, lane % 16)
@@ -119,12 +144,13 @@ __global__ __launch_bounds__((TreeShape<P, N>::NT)) void verify_tree_kernel(Tree
     using Sh = TreeShape<P, N>;
     using WT = WideTile<P, N, ST>;
     constexpr int NW = Sh::NW, NT = Sh::NT, XS = Sh::XS;
+    constexpr int KS = Sh::template KS<IOB>;
     extern __shared__ __align__(16) float lds[];
-    __shared__ __align__(16) uint32_t s_T[WT::COAL ? NW : 1][16][WT::TROW];   // per-wavefront staging
     __shared__ uint64_t s_anc[kMaxTree];            // ancestors of a node, itself among them
     // products of a: of a node's path; from the checkpoint up to and with an
     // entry; of the ring behind an entry.  An entry's dt (beta), 0 where there is none
-    __shared__ float s_path[kMaxTree], s_gam[kMaxRing + kMaxTree], s_R[kMaxRing], s_dt[kMaxRing + kMaxTree];
+    __shared__ __align__(16) float s_gam[kMaxRing + kMaxTree], s_dt[kMaxRing + kMaxTree];
+    __shared__ float s_path[kMaxTree], s_R[kMaxRing];
 
     const RingView &r = t.r;
     const int lid = xcd_remap(blockIdx.x, gridDim.x);
@@ -136,108 +162,163 @@ __global__ __launch_bounds__((TreeShape<P, N>::NT)) void verify_tree_kernel(Tree
     const size_t bh = (size_t)b * H + h;
     const int p0 = 16 * wave;
 
-    const int base = r.base[b], count = r.pos[b] - base;
-    WideRows<P, N, ST> rows;
-    rows.load(t.S, bh * (size_t)(P * N), p0, lane, t.scale);
+    const int base = r.base[b], count = r.pos[b] - base, n = t.n_nodes ? t.n_nodes[b] : W;
     Tree tree;
-    tree.load(t.parent, t.n_nodes, b, W, lane);
-    if (!tree.ok || count < 0 || count > L) {   // uniform over the workgroup
+    auto fail = [&] {
         for (int i = tid; i < W * P; i += NT) t.y[(((size_t)b * W + i / P) * H + h) * P + i % P] = __builtin_nanf("");
         if (tid == 0 && h == 0) raise_seq_error(r.err, b, tree.ok ? REPLAY_SEQERR_TOO_FEW : REPLAY_SEQERR_BAD_TREE);
+    };
+    if (count < 0 || count > L || n < 0 || n > W) {   // uniform over the workgroup, as every check here
+        tree.load(t.parent, t.n_nodes, b, W, lane);
+        fail();
         return;
     }
-    const int n = tree.n;
     if (n == 0) return;
-    const TreeLds at(W, L, N, DELTA);
-    const int WP = at.WP, LP = at.LP, ES = at.ES, CS = at.CS;
+
+    // Every load that the weights wait for, then V and the tile of S0: loads
+    // return in the order in which they were sent.
+    const int parent = t.parent[(size_t)b * W + (lane < n ? lane : 0)];
+    const int bmod = base % L, last = lane < count ? ring_slot(bmod, lane, L) : 0;
+    float ra = r.a[dta_index(b, bh, H, L, last)], rdt = r.dt[dta_index(b, bh, H, L, last)];
+    const size_t node = ((size_t)b * W + (lane < n ? lane : 0)) * H + h;
+    float na = t.a[node], ndt = t.dt[node];
+    const float sc = ST == ST_FP8 ? static_cast<const float *>(t.scale)[bh] : 1.f;
+
+    const TreeLds at(W, L, N, DELTA, KS, Sh::template TILE<ST>);
+    const int WP = at.WP, LP = at.LP, CS = at.CS;
     float *s_C = lds, *s_D = lds + WP * CS, *s_X = lds + at.x, *s_A = s_X, *s_inv = lds + at.inv, *s_RR = lds + at.rr;
+    float *s_K = lds + at.k;
     const int wt_n = (n + 15) / 16, et_n = LP / 16 + wt_n, e_end = LP + n;
     constexpr uint32_t ESZ = IOB ? 2 : 4;
     const Entries ks(static_cast<const char *>(r.k) + ((size_t)b * r.G + g) * L * N * ESZ,
-                     static_cast<const char *>(t.k) + ((size_t)b * W * r.G + g) * N * ESZ, N * ESZ, (uint32_t)r.G * N * ESZ, base,
+                     static_cast<const char *>(t.k) + ((size_t)b * W * r.G + g) * N * ESZ, N * ESZ, (uint32_t)r.G * N * ESZ, bmod,
                      L, count, n, LP);
     const Entries vs(static_cast<const char *>(r.v) + bh * L * P * ESZ, static_cast<const char *>(t.v) + ((size_t)b * W * H + h) * P * ESZ,
-                     P * ESZ, (uint32_t)H * P * ESZ, base, L, count, n, LP);
+                     P * ESZ, (uint32_t)H * P * ESZ, bmod, L, count, n, LP);
     const auto qs = make_rsrc(static_cast<const char *>(t.q) + ((size_t)b * W * r.G + g) * N * ESZ, (uint32_t)(n - 1) * ks.stride + N * ESZ);
 
-    // column p0 + lr of v of entries 4 s + lg
-    uint32_t vc[Sh::ME];
+    // k . q: a wavefront has one tile of queries (every NW-th, where there are more
+    // of them than wavefronts) and every `ways`-th tile of entries
+    const int ways = NW > wt_n ? NW / wt_n : 1;
+    const int ot0 = ways > 1 ? wave % wt_n : wave, et0 = ways > 1 ? wave / wt_n : 0;
+    const bool dots = et0 < ways && ot0 < wt_n;
+    DotRow<N, IOB> Q, K;
+    Q.load(qs, dots ? (uint32_t)(16 * ot0 + lr) * ks.stride : 0x80000000u, lane);
+    // the gated delta rule's keys, 64 units of 16 bytes (8 where a row has but two of 16) by wavefront and turn
+    constexpr int UB = N * ESZ / 4 < 16 ? 8 : 16, UR = N * ESZ / UB, TU = 16 * UR / 64;   // turns a tile
+    constexpr int KT = DELTA ? (Sh::MT * TU + NW - 1) / NW : 1;
+    static_assert(16 * UR % 64 == 0, "a turn within a tile");
+    u32x4 kraw[KT];
+    u32x2 qraw[Sh::QU][IOB ? 1 : 2];
+    auto load_queries = [&](int wt) {
 #pragma unroll
-    for (int s = 0; s < Sh::ME; ++s) {
-        vc[s] = 0;
-        if (4 * s < e_end) vc[s] = vs.template value<IOB>(4 * s + lg, 4 * s < LP, p0 + lr);
-    }
-    if constexpr (!DELTA) {   // the queries, 4 columns a thread and turn
-        for (int i = tid; i < 16 * wt_n * (N / 4); i += NT) {
-            const int w = i / (N / 4), c = i % (N / 4) * 4;
+        for (int i = 0; i < Sh::QU; ++i) {
+            const int x = tid + i * NT, w = 16 * wt + x / (N / 4);
+            const uint32_t o = (uint32_t)w * ks.stride + x % (N / 4) * 4 * ESZ;
+#pragma unroll
+            for (int y = 0; y < (IOB ? 1 : 2); ++y) qraw[i][y] = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(qs, o + 8 * y, 0, 0));
+        }
+    };
+    auto store_queries = [&](int wt) {
+#pragma unroll
+        for (int i = 0; i < Sh::QU; ++i) {
+            const int x = tid + i * NT;
+            const u32x2 u = qraw[i][0], v = qraw[i][IOB ? 0 : 1];
             f32x4 q;
-            if constexpr (IOB) {
-                const u32x2 x = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(qs, (uint32_t)w * ks.stride + c * 2, 0, 0));
-                q = f32x4{bf16_bits_to_f32(x[0] & 0xffffu), bf16_bits_to_f32(x[0] >> 16), bf16_bits_to_f32(x[1] & 0xffffu), bf16_bits_to_f32(x[1] >> 16)};
+            if constexpr (IOB) q = f32x4{bf16_bits_to_f32(u.x & 0xffffu), bf16_bits_to_f32(u.x >> 16), bf16_bits_to_f32(u.y & 0xffffu), bf16_bits_to_f32(u.y >> 16)};
+            else q = f32x4{__uint_as_float(u.x), __uint_as_float(u.y), __uint_as_float(v.x), __uint_as_float(v.y)};
+            *reinterpret_cast<f32x4 *>(&s_X[(16 * wt + x / (N / 4)) * XS + x % (N / 4) * 4]) = q;
+        }
+    };
+    if constexpr (DELTA) {
+#pragma unroll
+        for (int i = 0; i < KT; ++i) {
+            const int turn = i * NW + wave, e0 = turn / TU * 16, x = turn % TU * 64 + lane;
+            const auto rows_k = ks.rows_of(e0);
+            const uint32_t o = e0 < e_end ? ks.at(e0, x / UR) + x % UR * UB : 0x80000000u;
+            if constexpr (UB == 16) {
+                kraw[i] = __builtin_amdgcn_raw_buffer_load_b128(rows_k, o, 0, 0);
             } else {
-                q = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(qs, (uint32_t)w * ks.stride + c * 4, 0, 0));
+                const u32x2 u = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(rows_k, o, 0, 0));
+                kraw[i] = u32x4{u.x, u.y, 0, 0};
             }
-            *reinterpret_cast<f32x4 *>(&s_X[w * XS + c]) = q;
+        }
+    } else {
+        const bool first = dots && et0 < et_n;
+        K.load(ks.rows_of(first ? 16 * et0 : 0), first ? ks.at(16 * et0, lr) : 0x80000000u, lane);
+        load_queries(0);
+    }
+    // column p0 + lr of v of entries 16 i + 4 lg + u
+    uint32_t vc[Sh::MT][4];
+#pragma unroll
+    for (int i = 0; i < Sh::MT; ++i) {
+#pragma unroll
+        for (int u = 0; u < 4; ++u) vc[i][u] = 0;
+        if (16 * i < e_end) {
+            const auto rows_v = vs.rows_of(16 * i);
+#pragma unroll
+            for (int u = 0; u < 4; ++u) vc[i][u] = load_raw<IOB>(rows_v, vs.at(16 * i, 4 * lg + u), p0 + lr);
         }
     }
+    __builtin_amdgcn_sched_barrier(0);
+    WideRows<P, N, ST> rows;
+    rows.load(t.S, bh * (size_t)(P * N), p0, lane, t.scale);
+    __builtin_amdgcn_sched_barrier(0);
 
-    // raw dots: C[w][e] = k_e . q_w, and A^T[j][i] = k_j . k_i of tiles i >= j;
-    // the next tile's rows are on their way during a product
-    {
-        const int cq = et_n * wt_n, total = cq + (DELTA ? et_n * (et_n + 1) / 2 : 0);
-        auto place = [&](int x, int *et, int *ot) {
-            if (x < cq) {
-                *et = x / wt_n;
-                *ot = x % wt_n;
-                return;
-            }
-            int o = 0, left = x - cq;
-            while (left > o) left -= ++o;
-            *et = left;   // <= ot
-            *ot = o;
-        };
-        auto rows_of = [&](DotRow<N, IOB> &d, int tile) {
-            if (16 * tile < LP) d.load(ks.ring, ks.ring_at(16 * tile + lr), lane);
-            else d.load(ks.nodes, (uint32_t)(16 * tile + lr - LP) * ks.stride, lane);
-        };
-        auto load = [&](int x, DotRow<N, IOB> &A, DotRow<N, IOB> &B) {
-            int et, ot;
-            place(x, &et, &ot);
-            rows_of(A, et);
-            if (x < cq) B.load(qs, (uint32_t)(16 * ot + lr) * ks.stride, lane);
-            else rows_of(B, ot);
-        };
-        DotRow<N, IOB> A, B;
-        if (wave < total) load(wave, A, B);
-        for (int x = wave; x < total; x += NW) {
-            DotRow<N, IOB> nextA, nextB;
-            if (x + NW < total) load(x + NW, nextA, nextB);
-            int et, ot;
-            place(x, &et, &ot);
-            const f32x4 d = A.dots(B);
-            if (x < cq) {
-                *reinterpret_cast<f32x4 *>(&s_C[(16 * ot + lr) * CS + 16 * et + 4 * lg]) = d;
-            } else {
+    tree.set(parent, n, lane);
+    if (!tree.ok) {
+        fail();
+        return;
+    }
+
+    // raw dots: C[w][e] = k_e . q_w, and A^T[j][i] = k_j . k_i of tiles i >= j
+    if constexpr (DELTA) {
 #pragma unroll
-                for (int rr = 0; rr < 4; ++rr) s_A[(16 * et + 4 * lg + rr) * CS + 16 * ot + lr] = d[rr];
+        for (int i = 0; i < KT; ++i) {
+            const int turn = i * NW + wave, e0 = turn / TU * 16, x = turn % TU * 64 + lane;
+            char *to = reinterpret_cast<char *>(s_K + (e0 + x / UR) * KS) + x % UR * UB;
+            if (e0 < e_end) {
+                if constexpr (UB == 16) *reinterpret_cast<u32x4 *>(to) = kraw[i];
+                else *reinterpret_cast<u32x2 *>(to) = u32x2{kraw[i].x, kraw[i].y};
             }
-            if (x + NW < total) {
-                A = nextA;
-                B = nextB;
+        }
+        lds_barrier();
+        for (int x = NW - 1 - wave; x < et_n * (et_n + 1) / 2; x += NW) {
+            int ot = 0, et = x;
+            while (et > ot) et -= ++ot;   // et <= ot
+            DotRow<N, IOB> A, B;
+            A.load(s_K + 16 * et * KS, KS, lane);
+            B.load(s_K + 16 * ot * KS, KS, lane);
+            const f32x4 d = A.dots(B);
+#pragma unroll
+            for (int rr = 0; rr < 4; ++rr) s_A[(16 * et + 4 * lg + rr) * CS + 16 * ot + lr] = d[rr];
+        }
+    }
+    if (dots)
+        for (int ot = ot0; ot < wt_n; ot += ways > 1 ? wt_n : NW) {
+            if (ot != ot0) Q.load(qs, (uint32_t)(16 * ot + lr) * ks.stride, lane);
+            for (int et = et0; et < et_n; et += ways) {
+                if constexpr (DELTA) K.load(s_K + 16 * et * KS, KS, lane);
+                else if (et != et0 || ot != ot0) K.load(ks.rows_of(16 * et), ks.at(16 * et, lr), lane);
+                *reinterpret_cast<f32x4 *>(&s_C[(16 * ot + lr) * CS + 16 * et + 4 * lg]) = K.dots(Q);
             }
+        }
+    if constexpr (!DELTA) {
+        store_queries(0);
+        for (int wt = 1; wt < wt_n; ++wt) {
+            load_queries(wt);
+            store_queries(wt);
         }
     }
     // the decays, by the last wavefront: lane j has ring entry j and node j
     if (wave == NW - 1) {
-        float ra = 1.f, rdt = 0.f, na = 1.f, ndt = 0.f;
-        if (lane < count) {
-            const int sl = ring_slot(base % L, lane, L);
-            ra = r.a[dta_index(b, bh, H, L, sl)];
-            rdt = r.dt[dta_index(b, bh, H, L, sl)];
+        if (lane >= count) {
+            ra = 1.f;
+            rdt = 0.f;
         }
-        if (lane < n) {
-            na = t.a[((size_t)b * W + lane) * H + h];
-            ndt = t.dt[((size_t)b * W + lane) * H + h];
+        if (lane >= n) {
+            na = 1.f;
+            ndt = 0.f;
         }
         float pre = ra, suf = ra;   // of the ring, up to and with j; from j on
 #pragma unroll
@@ -306,15 +387,15 @@ __global__ __launch_bounds__((TreeShape<P, N>::NT)) void verify_tree_kernel(Tree
     auto on_path = [&](int w, int e) { return w < n && (e < LP ? e < count : (s_anc[w] >> (e - LP) & 1) != 0); };
     auto decay = [&](int w, int e) { return e < LP ? s_R[e] * s_path[w] : s_D[w * WP + e - LP]; };
     for (int w = tid / 16; w < 16 * wt_n; w += NT / 16)   // 16 threads a row
-        for (int e = tid % 16; e < ES; e += 16) {
+        for (int e = tid % 16; e < 16 * et_n; e += 16) {
             float *c = s_C + w * CS + e;
             *c = on_path(w, e) ? decay(w, e) * *c * (DELTA ? 1.f : s_dt[e]) : 0.f;
         }
     if constexpr (DELTA) {
         // A^T; of values that are no numbers nothing: what they have to reach, G, beta
         // and the decays carry
-        for (int j = tid / 16; j < ES; j += NT / 16)
-            for (int i = tid % 16; i < ES; i += 16) {
+        for (int j = tid / 16; j < 16 * et_n; j += NT / 16)
+            for (int i = (j & ~15) + tid % 16; i < 16 * et_n; i += 16) {
                 float c = 0.f;
                 if (i > j && i < e_end && (i < LP ? i < count : on_path(i - LP, j)))
                     c = (i < LP ? s_RR[j * LP + i] : decay(i - LP, j)) * s_A[j * CS + i] * s_dt[i];
@@ -375,31 +456,51 @@ __global__ __launch_bounds__((TreeShape<P, N>::NT)) void verify_tree_kernel(Tree
 
     if constexpr (DELTA) {   // the queries, which take the place of A
         for (int nt = wave; nt < N / 16; nt += NW) {
-            float kc[Sh::ME];   // column 16 nt + lr of entries 4 s + lg
+            float q[kMaxTree / 16][4];
 #pragma unroll
-            for (int s = 0; s < Sh::ME; ++s) {
-                kc[s] = 0.f;
-                if (4 * s < e_end) {
-                    const float k = entry_value<IOB>(ks.template value<IOB>(4 * s + lg, 4 * s < LP, 16 * nt + lr));
-                    if (tree_finite(k)) kc[s] = k;   // another's weight makes its nodes NaN as it is
+            for (int wt = 0; wt < kMaxTree / 16; ++wt)
+                if (16 * wt < n) {
+                    const uint32_t o = (uint32_t)(16 * wt + lr) * ks.stride + (16 * nt + 4 * lg) * ESZ;
+                    if constexpr (IOB) {
+                        const u32x2 u = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(qs, o, 0, 0));
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) q[wt][x] = bf16_bits_to_f32(u[x >> 1] >> (16 * (x & 1)) & 0xffffu);
+                    } else {
+                        const u32x4 u = __builtin_amdgcn_raw_buffer_load_b128(qs, o, 0, 0);
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) q[wt][x] = __uint_as_float(u[x]);
+                    }
                 }
-            }
-            for (int wt = 0; wt < wt_n; ++wt) {
+            float kc[Sh::MT][4];   // column 16 nt + lr of entries 16 i + 4 lg + u
+#pragma unroll
+            for (int i = 0; i < Sh::MT; ++i)
+                if (16 * i < e_end)
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) {
+                        const float *row = s_K + (16 * i + 4 * lg + u) * KS;
+                        float k;
+                        if constexpr (IOB) k = bf16_bits_to_f32(reinterpret_cast<const uint16_t *>(row)[16 * nt + lr]);
+                        else k = row[16 * nt + lr];
+                        kc[i][u] = tree_finite(k) ? k : 0.f;   // another's weight makes its nodes NaN as it is
+                    }
+#pragma unroll
+            for (int wt = 0; wt < kMaxTree / 16; ++wt) {
+                if (16 * wt >= n) break;
                 const int w = 16 * wt + lr;
                 f32x4 x = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                for (int s = 0; s < Sh::ME; ++s) {
-                    if (4 * s >= e_end) break;
-                    const int e = 4 * s + lg;
-                    const float c = s_C[w * CS + e];
-                    x = __builtin_amdgcn_mfma_f32_16x16x4f32(kc[s], c == 0.f ? 0.f : c * s_gam[e], x, 0, 0, 0);
-                }
-                float q[4] = {0.f, 0.f, 0.f, 0.f};
-                if (w < n) load_io4<IOB>(t.q, (((size_t)b * W + w) * r.G + g) * N + 16 * nt + 4 * lg, q);
+                for (int i = 0; i < Sh::MT; ++i)
+                    if (16 * i < e_end) {
+                        const f32x4 c = *reinterpret_cast<const f32x4 *>(&s_C[w * CS + 16 * i + 4 * lg]);
+                        const f32x4 gam = *reinterpret_cast<const f32x4 *>(&s_gam[16 * i + 4 * lg]);
+#pragma unroll
+                        for (int u = 0; u < 4; ++u)
+                            x = __builtin_amdgcn_mfma_f32_16x16x4f32(kc[i][u], c[u] == 0.f ? 0.f : c[u] * gam[u], x, 0, 0, 0);
+                    }
                 const float gw = s_gam[LP + w];
                 f32x4 o;
 #pragma unroll
-                for (int rr = 0; rr < 4; ++rr) o[rr] = w < n ? fmaf(gw, q[rr], -x[rr]) : 0.f;
+                for (int rr = 0; rr < 4; ++rr) o[rr] = w < n ? fmaf(gw, q[wt][rr], -x[rr]) : 0.f;
                 *reinterpret_cast<f32x4 *>(&s_X[w * XS + 16 * nt + 4 * lg]) = o;
             }
         }
@@ -407,36 +508,39 @@ __global__ __launch_bounds__((TreeShape<P, N>::NT)) void verify_tree_kernel(Tree
     if constexpr (DELTA) lds_barrier();
 
     // y^T: rows p0 + 4 lg + rr, nodes 16 wt + lr
-    rows.transpose(s_T[WT::COAL ? wave : 0], lane);
-    float vf[Sh::ME];
+    rows.transpose(reinterpret_cast<uint32_t (*)[WT::TROW]>(s_K + (WT::COAL ? wave * 16 * WT::TROW : 0)), lane);
+    float vf[Sh::MT][4];
     bool odd = false;
 #pragma unroll
-    for (int s = 0; s < Sh::ME; ++s) {
-        vf[s] = entry_value<IOB>(vc[s]);
-        if (!tree_finite(vf[s])) {
-            vf[s] = 0.f;
-            odd = true;
+    for (int i = 0; i < Sh::MT; ++i)
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            vf[i][u] = entry_value<IOB>(vc[i][u]);
+            if (!tree_finite(vf[i][u])) {
+                vf[i][u] = 0.f;
+                odd = true;
+            }
         }
-    }
     odd = __any(odd);
     const uint8_t *rsc = static_cast<const uint8_t *>(t.scale) + (bh * P + p0 + 4 * lg) * WT::NB;   // FP4 rows
-    const float sc = ST == ST_FP8 ? static_cast<const float *>(t.scale)[bh] : 1.f;
     for (int wt = 0; wt < wt_n; ++wt) {
         const int w = 16 * wt + lr;
         f32x4 y = rows.dot_f32q(reinterpret_cast<const float (*)[XS]>(s_X + 16 * wt * XS), lane, rsc);
         y *= DELTA ? sc : sc * s_gam[LP + w];
 #pragma unroll
-        for (int s = 0; s < Sh::ME; ++s) {
-            if (4 * s >= e_end) break;
-            y = __builtin_amdgcn_mfma_f32_16x16x4f32(vf[s], s_C[w * CS + 4 * s + lg], y, 0, 0, 0);
-        }
+        for (int i = 0; i < Sh::MT; ++i)
+            if (16 * i < e_end) {
+                const f32x4 c = *reinterpret_cast<const f32x4 *>(&s_C[w * CS + 16 * i + 4 * lg]);
+#pragma unroll
+                for (int u = 0; u < 4; ++u) y = __builtin_amdgcn_mfma_f32_16x16x4f32(vf[i][u], c[u], y, 0, 0, 0);
+            }
         if (w >= n) continue;
         if (odd) {   // a value that is no number, for the nodes behind it alone
             for (int e = 0; e < e_end; ++e) {
                 if (!on_path(w, e)) continue;
 #pragma unroll
                 for (int rr = 0; rr < 4; ++rr) {
-                    const float v = entry_value<IOB>(vs.template value<IOB>(e, e < LP, p0 + 4 * lg + rr));
+                    const float v = entry_value<IOB>(load_raw<IOB>(vs.rows_of(e & ~15), vs.at(e & ~15, e & 15), p0 + 4 * lg + rr));
                     if (!tree_finite(v)) y[rr] = fmaf(s_C[w * CS + e], v, y[rr]);
                 }
             }
@@ -447,7 +551,8 @@ __global__ __launch_bounds__((TreeShape<P, N>::NT)) void verify_tree_kernel(Tree
 
 template <int P, int N, int ST, bool IOB, bool DELTA>
 hipError_t launch_tree_one(const TreeArgs &a, hipStream_t s) {
-    const TreeLds at(a.W, a.r.L, N, DELTA);
+    using Sh = TreeShape<P, N>;
+    const TreeLds at(a.W, a.r.L, N, DELTA, Sh::template KS<IOB>, Sh::template TILE<ST>);
     verify_tree_kernel<P, N, ST, IOB, DELTA>
         <<<(unsigned)((int64_t)a.r.B * a.r.H), TreeShape<P, N>::NT, at.total * sizeof(float), s>>>(a);
     return hipGetLastError();
