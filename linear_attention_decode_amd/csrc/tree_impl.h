@@ -33,32 +33,40 @@ namespace replay {
 template <int P, int N>
 struct TreeShape {
     static constexpr int NW = P / 16, NT = 64 * NW;
-    static constexpr int XS = N + 4;      // LDS row stride of the queries, floats
     static constexpr int MT = (kMaxRing + kMaxTree) / 16;   // tiles of entries
     static constexpr int QU = 4 * N / NT;                   // units of 4 columns of 16 queries, by thread
     static_assert(4 * N % NT == 0, "queries by thread");
+    // The queries: float32, rows of XS floats; or, where S0 is of fewer bits, as the
+    // bf16 numbers that they are the sum of (one for bf16 queries, else three of 8
+    // bits each, which is exact), [part][row] of XB.
+    static constexpr int XS = N + 4, XB = N + 8;
+    template <int ST, bool IOB, bool DELTA>
+    static constexpr int PARTS = !WideTile<P, N, ST>::BF ? 0 : (IOB && !DELTA ? 1 : 3);
+    template <int ST, bool IOB, bool DELTA>
+    static constexpr int XF = PARTS<ST, IOB, DELTA> ? PARTS<ST, IOB, DELTA> * XB / 2 : XS;
     template <bool IOB>
     static constexpr int KS = N * (IOB ? 2 : 4) / 4 + 4;    // LDS row stride of the keys, floats
     template <int ST>
     static constexpr int TILE = WideTile<P, N, ST>::COAL ? NW * 16 * WideTile<P, N, ST>::TROW : 0;
 };
 
-// LDS, in floats: weights C [WP][CS], decays D [WP][WP]; then the queries
-// [WP][XS], which for the gated delta rule take the place of A^T [ES][CS], the diagonal
-// blocks' inverses [ES][16] (transposed) and the ring's own decays [LP][LP]; then the
-// gated delta rule's keys [ES][KS], whose place the tile of S0 takes on its
-// way into operands (`tile` floats).
+// LDS, in floats: weights C [WP][CS], decays D [WP][WP] and the queries (XF a
+// row); for the gated delta rule A^T [ES][CS], the diagonal blocks' inverses [ES][16]
+// (transposed) and the ring's own decays [LP][LP] lie behind D, and the queries take the
+// place of all four; then its keys [ES][KS], whose place the tile of S0 takes
+// on its way into operands (`tile` floats).
 struct TreeLds {
-    int WP, LP, ES, CS, x, inv, rr, k, total;
-    __host__ __device__ TreeLds(int W, int L, int N, bool delta, int KS, int tile) {
+    int WP, LP, ES, CS, x, A, inv, rr, k, total;
+    __host__ __device__ TreeLds(int W, int L, bool delta, int XF, int KS, int tile) {
         WP = (W + 15) / 16 * 16;
         LP = (L + 15) / 16 * 16;
         ES = LP + WP;
         CS = ES + 4;
-        x = WP * CS + WP * WP;
-        inv = x + ES * CS;
+        A = WP * CS + WP * WP;
+        inv = A + ES * CS;
         rr = inv + ES * 16;
-        const int first = delta ? rr + LP * LP : 0, second = x + WP * (N + 4);
+        x = delta ? WP * CS : A;
+        const int first = delta ? rr + LP * LP : 0, second = x + WP * XF;
         k = first > second ? first : second;
         const int keys = delta ? ES * KS : 0;
         total = k + (keys > tile ? keys : tile);
@@ -139,12 +147,72 @@ struct DotRow {
 
 __device__ __forceinline__ bool tree_finite(float x) { return (__float_as_uint(x) & 0x7f800000u) != 0x7f800000u; }
 
+// 4 values as PARTS bf16 numbers each, `part` elements apart
+template <int PARTS>
+__device__ __forceinline__ void put_parts(uint16_t *to, int part, f32x4 x) {
+#pragma unroll
+    for (int z = 0; z < PARTS; ++z) {
+        uint32_t hi[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t u = __float_as_uint(x[i]);
+            const bool fin = tree_finite(x[i]);
+            hi[i] = fin || !(u & 0x007fffffu) ? u : u | 0x00400000u;   // a NaN stays one
+            x[i] = fin ? x[i] - __uint_as_float(u & 0xffff0000u) : 0.f;
+        }
+        *reinterpret_cast<u32x2 *>(to + z * part) = u32x2{hi[0] >> 16 | (hi[1] & 0xffff0000u), hi[2] >> 16 | (hi[3] & 0xffff0000u)};
+    }
+}
+
+// S0 x^T over 16 rows and 16 queries in PARTS bf16 numbers, on v_mfma_f32_16x16x32_bf16:
+// bf16, e4m3 (unscaled) and MX FP4 values are bf16 numbers, and every product is exact.
+// At 128 columns 12 products (16 cycles each) take the place of 32 of 32 cycles.
+template <int PARTS, int P, int N, int ST>
+__device__ __forceinline__ f32x4 dot_parts(const WideRows<P, N, ST> &rows, const uint16_t *x, int part, int stride, int lane,
+                                           const uint8_t *rsc) {
+    using WT = WideTile<P, N, ST>;
+    const int lg = lane >> 4;
+    const uint16_t *row = x + (lane & 15) * stride;
+    f32x4 out = {0.f, 0.f, 0.f, 0.f};
+    uint32_t sw[ST == ST_FP4 ? WT::NB : 1];   // the 4 rows' scale bytes, rr NB + st
+    if constexpr (ST == ST_FP4)
+#pragma unroll
+        for (int i = 0; i < WT::NB; ++i) sw[i] = reinterpret_cast<const uint32_t *>(rsc)[i];
+#pragma unroll
+    for (int st = 0; st < WT::STEPS; ++st) {
+        constexpr int HALVES = WT::CVEC / 8;
+#pragma unroll
+        for (int hh = 0; hh < HALVES; ++hh) {
+            uint4 a;
+            if constexpr (ST == ST_BF16) a = rows.at[st].v;
+            else if constexpr (ST == ST_FP8) a = rows.at[st].bf16_half(hh);
+            else a = rows.at[st].bf16x8();
+            f32x4 acc = ST == ST_FP4 ? f32x4{0.f, 0.f, 0.f, 0.f} : out;
+#pragma unroll
+            for (int z = PARTS - 1; z >= 0; --z) {
+                const uint4 q = *reinterpret_cast<const uint4 *>(row + z * part + (4 * st + lg) * WT::CVEC + 8 * hh);
+                acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(a), as_bf16x8(q), acc, 0, 0, 0);
+            }
+            if constexpr (ST == ST_FP4) {
+#pragma unroll
+                for (int rr = 0; rr < 4; ++rr) {
+                    const int i = rr * WT::NB + st;
+                    out[rr] += ldexpf(acc[rr], (int)((sw[i >> 2] >> (8 * (i & 3))) & 0xffu) - 127);
+                }
+            } else {
+                out = acc;
+            }
+        }
+    }
+    return out;
+}
+
 template <int P, int N, int ST, bool IOB, bool DELTA>
-__global__ __launch_bounds__((TreeShape<P, N>::NT)) void verify_tree_kernel(TreeArgs t) {
+__global__ __launch_bounds__((TreeShape<P, N>::NT), IOB ? 4 : 3) void verify_tree_kernel(TreeArgs t) {
     using Sh = TreeShape<P, N>;
     using WT = WideTile<P, N, ST>;
     constexpr int NW = Sh::NW, NT = Sh::NT, XS = Sh::XS;
-    constexpr int KS = Sh::template KS<IOB>;
+    constexpr int KS = Sh::template KS<IOB>, PARTS = Sh::template PARTS<ST, IOB, DELTA>, XF = Sh::template XF<ST, IOB, DELTA>;
     extern __shared__ __align__(16) float lds[];
     __shared__ uint64_t s_anc[kMaxTree];            // ancestors of a node, itself among them
     // products of a: of a node's path; from the checkpoint up to and with an
@@ -184,10 +252,15 @@ __global__ __launch_bounds__((TreeShape<P, N>::NT)) void verify_tree_kernel(Tree
     float na = t.a[node], ndt = t.dt[node];
     const float sc = ST == ST_FP8 ? static_cast<const float *>(t.scale)[bh] : 1.f;
 
-    const TreeLds at(W, L, N, DELTA, KS, Sh::template TILE<ST>);
+    const TreeLds at(W, L, DELTA, XF, KS, Sh::template TILE<ST>);
     const int WP = at.WP, LP = at.LP, CS = at.CS;
-    float *s_C = lds, *s_D = lds + WP * CS, *s_X = lds + at.x, *s_A = s_X, *s_inv = lds + at.inv, *s_RR = lds + at.rr;
+    float *s_C = lds, *s_D = lds + WP * CS, *s_X = lds + at.x, *s_A = lds + at.A, *s_inv = lds + at.inv, *s_RR = lds + at.rr;
     float *s_K = lds + at.k;
+    const int part = WP * Sh::XB;   // elements
+    auto put_query = [&](int w, int c, f32x4 x) {   // columns c .. c + 3
+        if constexpr (PARTS) put_parts<PARTS>(reinterpret_cast<uint16_t *>(s_X) + w * Sh::XB + c, part, x);
+        else *reinterpret_cast<f32x4 *>(&s_X[w * XS + c]) = x;
+    };
     const int wt_n = (n + 15) / 16, et_n = LP / 16 + wt_n, e_end = LP + n;
     constexpr uint32_t ESZ = IOB ? 2 : 4;
     const Entries ks(static_cast<const char *>(r.k) + ((size_t)b * r.G + g) * L * N * ESZ,
@@ -197,11 +270,12 @@ __global__ __launch_bounds__((TreeShape<P, N>::NT)) void verify_tree_kernel(Tree
                      P * ESZ, (uint32_t)H * P * ESZ, bmod, L, count, n, LP);
     const auto qs = make_rsrc(static_cast<const char *>(t.q) + ((size_t)b * W * r.G + g) * N * ESZ, (uint32_t)(n - 1) * ks.stride + N * ESZ);
 
-    // k . q: a wavefront has one tile of queries (every NW-th, where there are more
+    // k . q: a wavefront has one tile of queries (every ND-th, where there are more
     // of them than wavefronts) and every `ways`-th tile of entries
-    const int ways = NW > wt_n ? NW / wt_n : 1;
+    constexpr int ND = DELTA && NW >= 4 ? NW - 1 : NW;   // the last one has the decays to do
+    const int ways = ND > wt_n ? ND / wt_n : 1;
     const int ot0 = ways > 1 ? wave % wt_n : wave, et0 = ways > 1 ? wave / wt_n : 0;
-    const bool dots = et0 < ways && ot0 < wt_n;
+    const bool dots = wave < ND && et0 < ways && ot0 < wt_n;
     DotRow<N, IOB> Q, K;
     Q.load(qs, dots ? (uint32_t)(16 * ot0 + lr) * ks.stride : 0x80000000u, lane);
     // the gated delta rule's keys, 64 units of 16 bytes (8 where a row has but two of 16) by wavefront and turn
@@ -227,7 +301,7 @@ __global__ __launch_bounds__((TreeShape<P, N>::NT)) void verify_tree_kernel(Tree
             f32x4 q;
             if constexpr (IOB) q = f32x4{bf16_bits_to_f32(u.x & 0xffffu), bf16_bits_to_f32(u.x >> 16), bf16_bits_to_f32(u.y & 0xffffu), bf16_bits_to_f32(u.y >> 16)};
             else q = f32x4{__uint_as_float(u.x), __uint_as_float(u.y), __uint_as_float(v.x), __uint_as_float(v.y)};
-            *reinterpret_cast<f32x4 *>(&s_X[(16 * wt + x / (N / 4)) * XS + x % (N / 4) * 4]) = q;
+            put_query(16 * wt + x / (N / 4), x % (N / 4) * 4, q);
         }
     };
     if constexpr (DELTA) {
@@ -283,7 +357,7 @@ __global__ __launch_bounds__((TreeShape<P, N>::NT)) void verify_tree_kernel(Tree
             }
         }
         lds_barrier();
-        for (int x = NW - 1 - wave; x < et_n * (et_n + 1) / 2; x += NW) {
+        for (int x = ND - 1 - wave; x >= 0 && x < et_n * (et_n + 1) / 2; x += ND) {
             int ot = 0, et = x;
             while (et > ot) et -= ++ot;   // et <= ot
             DotRow<N, IOB> A, B;
@@ -295,7 +369,7 @@ __global__ __launch_bounds__((TreeShape<P, N>::NT)) void verify_tree_kernel(Tree
         }
     }
     if (dots)
-        for (int ot = ot0; ot < wt_n; ot += ways > 1 ? wt_n : NW) {
+        for (int ot = ot0; ot < wt_n; ot += ways > 1 ? wt_n : ND) {
             if (ot != ot0) Q.load(qs, (uint32_t)(16 * ot + lr) * ks.stride, lane);
             for (int et = et0; et < et_n; et += ways) {
                 if constexpr (DELTA) K.load(s_K + 16 * et * KS, KS, lane);
@@ -410,66 +484,68 @@ __global__ __launch_bounds__((TreeShape<P, N>::NT)) void verify_tree_kernel(Tree
             for (int j = 15; j >= 0; --j) {
                 y[j] = j == row ? 1.f : 0.f;
 #pragma unroll
-                for (int i4 = j & ~3; i4 < 16; i4 += 4) {
+                for (int i4 = 12; i4 >= (j & ~3); i4 -= 4) {
                     const f32x4 c = *reinterpret_cast<const f32x4 *>(&s_A[(b0 + j) * CS + b0 + i4]);
 #pragma unroll
-                    for (int u = 0; u < 4; ++u)
+                    for (int u = 3; u >= 0; --u)
                         if (i4 + u > j) y[j] = fmaf(-c[u], y[i4 + u], y[j]);
                 }
                 s_inv[(b0 + j) * 16 + row] = y[j];   // T^T
+                __builtin_amdgcn_sched_barrier(0);
             }
         }
         lds_barrier();
-        // C_J^T = T_JJ^T (G_J^T - sum A_IJ^T C_I^T), lane (node lr, entries 4 lg + u), a wavefront 16 nodes
+        // C^T by blocks, lane (node lr, entries 4 lg + u), a wavefront 16 nodes: C_J^T = T_JJ^T (what is left of
+        // G_J^T), and what C_J takes from the blocks before it
         for (int wt = wave; wt < wt_n; wt += NW) {
+            asm volatile("" ::: "memory");   // A and T stay in LDS
             float *row = s_C + (16 * wt + lr) * CS + 4 * lg;
-            for (int J = et_n - 1; J >= 0; --J) {
-                f32x4 c = *reinterpret_cast<const f32x4 *>(row + 16 * J);
-                f32x4 sum = {0.f, 0.f, 0.f, 0.f};
-                for (int I = J + 1; I < et_n; ++I) {
-                    const f32x4 m = *reinterpret_cast<const f32x4 *>(&s_A[(16 * J + lr) * CS + 16 * I + 4 * lg]);
-                    const f32x4 o = *reinterpret_cast<const f32x4 *>(row + 16 * I);
+            const int w = 16 * wt + lr;   // the entries on its path, from 4 lg on
+            const uint64_t nodes = w < n ? s_anc[w] >> 4 * lg : 0;
+            const uint32_t in_ring = w < n ? (uint32_t)((1ull << count) - 1) >> 4 * lg : 0;
+            f32x4 c[Sh::MT];
 #pragma unroll
-                    for (int u = 0; u < 4; ++u) sum = __builtin_amdgcn_mfma_f32_16x16x4f32(m[u], o[u], sum, 0, 0, 0);
+            for (int J = 0; J < Sh::MT; ++J)
+                if (J < et_n) c[J] = *reinterpret_cast<const f32x4 *>(row + 16 * J);
+#pragma unroll
+            for (int J = Sh::MT - 1; J >= 0; --J)
+                if (J < et_n) {
+                    const f32x4 T = *reinterpret_cast<const f32x4 *>(&s_inv[(16 * J + lr) * 16 + 4 * lg]);
+                    f32x4 sum = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) sum = __builtin_amdgcn_mfma_f32_16x16x4f32(T[u], c[J][u], sum, 0, 0, 0);
+                    c[J] = sum;
+                    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                    for (int I = J - 1; I >= 0; --I) {
+                        const f32x4 m = *reinterpret_cast<const f32x4 *>(&s_A[(16 * I + lr) * CS + 16 * J + 4 * lg]);
+#pragma unroll
+                        for (int u = 0; u < 4; ++u) c[I] = __builtin_amdgcn_mfma_f32_16x16x4f32(-m[u], c[J][u], c[I], 0, 0, 0);
+                    }
                 }
-                c -= sum;
-                const f32x4 m = *reinterpret_cast<const f32x4 *>(&s_inv[(16 * J + lr) * 16 + 4 * lg]);
-                sum = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                for (int u = 0; u < 4; ++u) sum = __builtin_amdgcn_mfma_f32_16x16x4f32(m[u], c[u], sum, 0, 0, 0);
-                *reinterpret_cast<f32x4 *>(row + 16 * J) = sum;
-                wave_lds_sync();
-            }
-#pragma unroll 1
-            for (int J = 0; J < et_n; ++J) {
-                f32x4 c = *reinterpret_cast<const f32x4 *>(row + 16 * J);
+            for (int J = 0; J < Sh::MT; ++J)
+                if (J < et_n) {
+                    const f32x4 beta = *reinterpret_cast<const f32x4 *>(&s_dt[16 * J + 4 * lg]);
+                    const uint32_t on = 16 * J < LP ? in_ring >> 16 * J : (uint32_t)(nodes >> (16 * J - LP));
 #pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    const int e = 16 * J + 4 * lg + u;
-                    c[u] = on_path(16 * wt + lr, e) ? c[u] * s_dt[e] : 0.f;
+                    for (int u = 0; u < 4; ++u) c[J][u] = on >> u & 1 ? c[J][u] * beta[u] : 0.f;
+                    *reinterpret_cast<f32x4 *>(row + 16 * J) = c[J];
                 }
-                *reinterpret_cast<f32x4 *>(row + 16 * J) = c;
-            }
         }
     }
     lds_barrier();
 
     if constexpr (DELTA) {   // the queries, which take the place of A
         for (int nt = wave; nt < N / 16; nt += NW) {
-            float q[kMaxTree / 16][4];
+            u32x2 q[kMaxTree / 16][IOB ? 1 : 2];
 #pragma unroll
             for (int wt = 0; wt < kMaxTree / 16; ++wt)
-                if (16 * wt < n) {
-                    const uint32_t o = (uint32_t)(16 * wt + lr) * ks.stride + (16 * nt + 4 * lg) * ESZ;
-                    if constexpr (IOB) {
-                        const u32x2 u = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(qs, o, 0, 0));
 #pragma unroll
-                        for (int x = 0; x < 4; ++x) q[wt][x] = bf16_bits_to_f32(u[x >> 1] >> (16 * (x & 1)) & 0xffffu);
-                    } else {
-                        const u32x4 u = __builtin_amdgcn_raw_buffer_load_b128(qs, o, 0, 0);
-#pragma unroll
-                        for (int x = 0; x < 4; ++x) q[wt][x] = __uint_as_float(u[x]);
-                    }
+                for (int x = 0; x < (IOB ? 1 : 2); ++x) {
+                    q[wt][x] = u32x2{0, 0};
+                    if (16 * wt < n)
+                        q[wt][x] = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(qs, (uint32_t)(16 * wt + lr) * ks.stride + (16 * nt + 4 * lg) * ESZ + 8 * x, 0, 0));
                 }
             float kc[Sh::MT][4];   // column 16 nt + lr of entries 16 i + 4 lg + u
 #pragma unroll
@@ -500,8 +576,13 @@ __global__ __launch_bounds__((TreeShape<P, N>::NT)) void verify_tree_kernel(Tree
                 const float gw = s_gam[LP + w];
                 f32x4 o;
 #pragma unroll
-                for (int rr = 0; rr < 4; ++rr) o[rr] = w < n ? fmaf(gw, q[wt][rr], -x[rr]) : 0.f;
-                *reinterpret_cast<f32x4 *>(&s_X[w * XS + 16 * nt + 4 * lg]) = o;
+                for (int rr = 0; rr < 4; ++rr) {
+                    uint32_t u = q[wt][IOB ? 0 : rr >> 1][IOB ? rr >> 1 : rr & 1];
+                    asm volatile("" : "+v"(u));   // as with v
+                    if (IOB) u = rr & 1 ? u >> 16 : u & 0xffffu;
+                    o[rr] = w < n ? fmaf(gw, entry_value<IOB>(u), -x[rr]) : 0.f;
+                }
+                put_query(w, 16 * nt + 4 * lg, o);
             }
         }
     }
@@ -515,6 +596,7 @@ __global__ __launch_bounds__((TreeShape<P, N>::NT)) void verify_tree_kernel(Tree
     for (int i = 0; i < Sh::MT; ++i)
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
+            asm volatile("" : "+v"(vc[i][u]));   // its load ends here, not where it was sent
             vf[i][u] = entry_value<IOB>(vc[i][u]);
             if (!tree_finite(vf[i][u])) {
                 vf[i][u] = 0.f;
@@ -525,7 +607,9 @@ __global__ __launch_bounds__((TreeShape<P, N>::NT)) void verify_tree_kernel(Tree
     const uint8_t *rsc = static_cast<const uint8_t *>(t.scale) + (bh * P + p0 + 4 * lg) * WT::NB;   // FP4 rows
     for (int wt = 0; wt < wt_n; ++wt) {
         const int w = 16 * wt + lr;
-        f32x4 y = rows.dot_f32q(reinterpret_cast<const float (*)[XS]>(s_X + 16 * wt * XS), lane, rsc);
+        f32x4 y;
+        if constexpr (PARTS) y = dot_parts<PARTS>(rows, reinterpret_cast<const uint16_t *>(s_X) + 16 * wt * Sh::XB, part, Sh::XB, lane, rsc);
+        else y = rows.dot_f32q(reinterpret_cast<const float (*)[XS]>(s_X + 16 * wt * XS), lane, rsc);
         y *= DELTA ? sc : sc * s_gam[LP + w];
 #pragma unroll
         for (int i = 0; i < Sh::MT; ++i)
@@ -552,7 +636,7 @@ __global__ __launch_bounds__((TreeShape<P, N>::NT)) void verify_tree_kernel(Tree
 template <int P, int N, int ST, bool IOB, bool DELTA>
 hipError_t launch_tree_one(const TreeArgs &a, hipStream_t s) {
     using Sh = TreeShape<P, N>;
-    const TreeLds at(a.W, a.r.L, N, DELTA, Sh::template KS<IOB>, Sh::template TILE<ST>);
+    const TreeLds at(a.W, a.r.L, DELTA, Sh::template XF<ST, IOB, DELTA>, Sh::template KS<IOB>, Sh::template TILE<ST>);
     verify_tree_kernel<P, N, ST, IOB, DELTA>
         <<<(unsigned)((int64_t)a.r.B * a.r.H), TreeShape<P, N>::NT, at.total * sizeof(float), s>>>(a);
     return hipGetLastError();
