@@ -50,24 +50,32 @@ struct TreeShape {
     static constexpr int TILE = WideTile<P, N, ST>::COAL ? NW * 16 * WideTile<P, N, ST>::TROW : 0;
 };
 
-// LDS, in floats: weights C [WP][CS], decays D [WP][WP] and the queries (XF a
-// row); for the gated delta rule A^T [ES][CS], the diagonal blocks' inverses [ES][16]
-// (transposed) and the ring's own decays [LP][LP] lie behind D, and the queries take the
-// place of all four; then its keys [ES][KS], whose place the tile of S0 takes
-// on its way into operands (`tile` floats).
+// LDS, in floats: weights C [WP][CS] and decays D [WP][WP]; for the gated delta rule
+// also A^T [ES][CS], the diagonal blocks' inverses [ES][16] (transposed) and the
+// ring's own decays [LP][LP].  The queries (XF a row) lie behind C and D, or for the
+// gated delta rule in place of what is not needed any more when they are formed: all
+// but C, or all (`parts`: C then goes on as [3][WP][CB] bf16, which lie in place of D
+// and the ring's decays).  Then the gated delta rule's keys [ES][KS], whose place
+// the tile of S0 takes on its way into operands (`tile` floats).
 struct TreeLds {
-    int WP, LP, ES, CS, x, A, inv, rr, k, total;
-    __host__ __device__ TreeLds(int W, int L, bool delta, int XF, int KS, int tile) {
+    int WP, LP, ES, CS, CB, D, x, A, inv, rr, parts, k, total;
+    __host__ __device__ TreeLds(int W, int L, bool delta, bool in_parts, int XF, int KS, int tile) {
         WP = (W + 15) / 16 * 16;
         LP = (L + 15) / 16 * 16;
         ES = LP + WP;
         CS = ES + 4;
-        A = WP * CS + WP * WP;
-        inv = A + ES * CS;
-        rr = inv + ES * 16;
-        x = delta ? WP * CS : A;
-        const int first = delta ? rr + LP * LP : 0, second = x + WP * XF;
-        k = first > second ? first : second;
+        CB = (ES + 31) / 32 * 32 + 8;
+        A = WP * CS;
+        inv = A + (delta ? ES * CS : 0);
+        parts = inv + (delta ? ES * 16 : 0);
+        const int queries = WP * XF;
+        x = in_parts ? 0 : delta ? A : A + WP * WP;
+        if (in_parts && queries > parts) parts = queries;
+        D = parts;
+        rr = D + WP * WP;
+        k = rr + (delta ? LP * LP : 0);
+        if (in_parts && parts + 3 * WP * CB / 2 > k) k = parts + 3 * WP * CB / 2;
+        if (x + queries > k) k = x + queries;
         const int keys = delta ? ES * KS : 0;
         total = k + (keys > tile ? keys : tile);
     }
@@ -147,9 +155,9 @@ struct DotRow {
 
 __device__ __forceinline__ bool tree_finite(float x) { return (__float_as_uint(x) & 0x7f800000u) != 0x7f800000u; }
 
-// 4 values as PARTS bf16 numbers each, `part` elements apart
+// 4 values as PARTS bf16 numbers each: 8 bits, then what is left
 template <int PARTS>
-__device__ __forceinline__ void put_parts(uint16_t *to, int part, f32x4 x) {
+__device__ __forceinline__ void split_parts(f32x4 x, u32x2 *out) {
 #pragma unroll
     for (int z = 0; z < PARTS; ++z) {
         uint32_t hi[4];
@@ -160,8 +168,27 @@ __device__ __forceinline__ void put_parts(uint16_t *to, int part, f32x4 x) {
             hi[i] = fin || !(u & 0x007fffffu) ? u : u | 0x00400000u;   // a NaN stays one
             x[i] = fin ? x[i] - __uint_as_float(u & 0xffff0000u) : 0.f;
         }
-        *reinterpret_cast<u32x2 *>(to + z * part) = u32x2{hi[0] >> 16 | (hi[1] & 0xffff0000u), hi[2] >> 16 | (hi[3] & 0xffff0000u)};
+        out[z] = u32x2{hi[0] >> 16 | (hi[1] & 0xffff0000u), hi[2] >> 16 | (hi[3] & 0xffff0000u)};
     }
+}
+template <int PARTS>   // `part` elements apart
+__device__ __forceinline__ void put_parts(uint16_t *to, int part, f32x4 x) {
+    u32x2 p[PARTS];
+    split_parts<PARTS>(x, p);
+#pragma unroll
+    for (int z = 0; z < PARTS; ++z) *reinterpret_cast<u32x2 *>(to + z * part) = p[z];
+}
+
+// An operand of 16 columns (16 nt on) of bf16 rows in LDS: column lane % 16 of rows 4 lg + u
+// of the first 16 rows, then of those `second` floats on, each by one transposing read.
+__device__ __forceinline__ bf16x8_t cols8(const float *rows, int second, int stride, int nt, int lane) {
+    typedef short s16x4 __attribute__((ext_vector_type(4)));
+    typedef __attribute__((address_space(3))) s16x4 lds4;
+    const int lr = lane & 15, lg = lane >> 4;
+    const float *at = rows + (4 * lg + (lr >> 2)) * stride + 8 * nt + 2 * (lr & 3);
+    const u32x2 a = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4 *)at));
+    const u32x2 b = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4 *)(at + second)));
+    return __builtin_bit_cast(bf16x8_t, u32x4{a.x, a.y, b.x, b.y});
 }
 
 // S0 x^T over 16 rows and 16 queries in PARTS bf16 numbers, on v_mfma_f32_16x16x32_bf16:
@@ -213,12 +240,14 @@ __global__ __launch_bounds__((TreeShape<P, N>::NT), IOB ? 4 : 3) void verify_tre
     using WT = WideTile<P, N, ST>;
     constexpr int NW = Sh::NW, NT = Sh::NT, XS = Sh::XS;
     constexpr int KS = Sh::template KS<IOB>, PARTS = Sh::template PARTS<ST, IOB, DELTA>, XF = Sh::template XF<ST, IOB, DELTA>;
+    constexpr bool CP = DELTA && IOB;   // C as bf16 parts
     extern __shared__ __align__(16) float lds[];
     __shared__ uint64_t s_anc[kMaxTree];            // ancestors of a node, itself among them
     // products of a: of a node's path; from the checkpoint up to and with an
     // entry; of the ring behind an entry.  An entry's dt (beta), 0 where there is none
     __shared__ __align__(16) float s_gam[kMaxRing + kMaxTree], s_dt[kMaxRing + kMaxTree];
-    __shared__ float s_path[kMaxTree], s_R[kMaxRing];
+    __shared__ __align__(16) float s_path[kMaxTree], s_R[kMaxRing];
+    __shared__ uint32_t s_odd[NW];   // a wavefront's keys hold a value that is no number
 
     const RingView &r = t.r;
     const int lid = xcd_remap(blockIdx.x, gridDim.x);
@@ -252,11 +281,12 @@ __global__ __launch_bounds__((TreeShape<P, N>::NT), IOB ? 4 : 3) void verify_tre
     float na = t.a[node], ndt = t.dt[node];
     const float sc = ST == ST_FP8 ? static_cast<const float *>(t.scale)[bh] : 1.f;
 
-    const TreeLds at(W, L, DELTA, XF, KS, Sh::template TILE<ST>);
+    const TreeLds at(W, L, DELTA, CP, XF, KS, Sh::template TILE<ST>);
     const int WP = at.WP, LP = at.LP, CS = at.CS;
-    float *s_C = lds, *s_D = lds + WP * CS, *s_X = lds + at.x, *s_A = lds + at.A, *s_inv = lds + at.inv, *s_RR = lds + at.rr;
+    float *s_C = lds, *s_D = lds + at.D, *s_X = lds + at.x, *s_A = lds + at.A, *s_inv = lds + at.inv, *s_RR = lds + at.rr;
     float *s_K = lds + at.k;
-    const int part = WP * Sh::XB;   // elements
+    uint16_t *s_P = reinterpret_cast<uint16_t *>(lds + at.parts);   // C's parts
+    const int part = WP * Sh::XB, cpart = WP * at.CB;   // elements
     auto put_query = [&](int w, int c, f32x4 x) {   // columns c .. c + 3
         if constexpr (PARTS) put_parts<PARTS>(reinterpret_cast<uint16_t *>(s_X) + w * Sh::XB + c, part, x);
         else *reinterpret_cast<f32x4 *>(&s_X[w * XS + c]) = x;
@@ -347,6 +377,16 @@ __global__ __launch_bounds__((TreeShape<P, N>::NT), IOB ? 4 : 3) void verify_tre
 
     // raw dots: C[w][e] = k_e . q_w, and A^T[j][i] = k_j . k_i of tiles i >= j
     if constexpr (DELTA) {
+        if constexpr (CP) {
+            bool bad = false;
+#pragma unroll
+            for (int i = 0; i < KT; ++i)
+#pragma unroll
+                for (int u = 0; u < UB / 4; ++u)
+                    bad |= (kraw[i][u] & 0x7f80u) == 0x7f80u || (kraw[i][u] & 0x7f800000u) == 0x7f800000u;
+            bad = __any(bad);
+            if (lane == 0) s_odd[wave] = bad;
+        }
 #pragma unroll
         for (int i = 0; i < KT; ++i) {
             const int turn = i * NW + wave, e0 = turn / TU * 16, x = turn % TU * 64 + lane;
@@ -446,35 +486,101 @@ __global__ __launch_bounds__((TreeShape<P, N>::NT), IOB ? 4 : 3) void verify_tre
                 }
             }
         }
-        if constexpr (DELTA) {
+    }
+    if constexpr (DELTA)
+        if (wave == ND - 1) {
             float p = 1.f;
             for (int i = 0; i < count; ++i) {   // a behind j up to and with i
                 if (i > lane) p *= bcast(ra, i);
                 if (lane < LP) s_RR[lane * LP + i] = p;
             }
         }
-    }
     lds_barrier();
 
-    // weights: the dots of what lies on the node's path, decayed (selects, not
-    // factors of 0: another branch's NaN stays there)
-    auto on_path = [&](int w, int e) { return w < n && (e < LP ? e < count : (s_anc[w] >> (e - LP) & 1) != 0); };
-    auto decay = [&](int w, int e) { return e < LP ? s_R[e] * s_path[w] : s_D[w * WP + e - LP]; };
-    for (int w = tid / 16; w < 16 * wt_n; w += NT / 16)   // 16 threads a row
-        for (int e = tid % 16; e < 16 * et_n; e += 16) {
-            float *c = s_C + w * CS + e;
-            *c = on_path(w, e) ? decay(w, e) * *c * (DELTA ? 1.f : s_dt[e]) : 0.f;
-        }
-    if constexpr (DELTA) {
-        // A^T; of values that are no numbers nothing: what they have to reach, G, beta
-        // and the decays carry
-        for (int j = tid / 16; j < 16 * et_n; j += NT / 16)
-            for (int i = (j & ~15) + tid % 16; i < 16 * et_n; i += 16) {
-                float c = 0.f;
-                if (i > j && i < e_end && (i < LP ? i < count : on_path(i - LP, j)))
-                    c = (i < LP ? s_RR[j * LP + i] : decay(i - LP, j)) * s_A[j * CS + i] * s_dt[i];
-                s_A[j * CS + i] = tree_finite(c) ? c : 0.f;
+    // v, where it is no number 0: what such a value has to reach is added at the end
+    float vf[Sh::MT][4];
+    bf16x8_t vp[Sh::MT / 2];   // C in parts: entries 32 i + 4 lg + u, then 32 i + 16 + 4 lg + u
+    bool odd = false;
+#pragma unroll
+    for (int i = 0; i < Sh::MT; ++i)
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            asm volatile("" : "+v"(vc[i][u]));   // its load ends here, not where it was sent
+            vf[i][u] = entry_value<IOB>(vc[i][u]);
+            if (!tree_finite(vf[i][u])) {
+                vf[i][u] = 0.f;
+                vc[i][u] = 0;
+                odd = true;
             }
+        }
+    if constexpr (CP) {
+#pragma unroll
+        for (int i = 0; i < Sh::MT / 2; ++i) {
+            u32x4 x;
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                uint32_t two = vc[2 * i + u / 2][2 * u % 4] | vc[2 * i + u / 2][2 * u % 4 + 1] << 16;
+                asm volatile("" : "+v"(two));   // one register from here on
+                x[u] = two;
+            }
+            vp[i] = __builtin_bit_cast(bf16x8_t, x);
+        }
+    }
+    odd = __any(odd);
+
+    // weights: the dots of what lies on the node's path, decayed (selects, not
+    // factors of 0: another branch's NaN stays there), by tiles, lane (column lr, entries or nodes 4 lg + u)
+    auto on_path = [&](int w, int e) { return w < n && (e < LP ? e < count : (s_anc[w] >> (e - LP) & 1) != 0); };
+    auto vec = [](const float *p) { return *reinterpret_cast<const f32x4 *>(p); };
+    for (int x = wave; x < et_n * wt_n; x += NW) {
+        const int e = x / wt_n * 16 + 4 * lg, w = x % wt_n * 16 + lr;
+        const bool of_ring = x / wt_n * 16 < LP;   // uniform
+        const uint32_t on = w >= n ? 0u : of_ring ? (uint32_t)((1ull << count) - 1) >> e : (uint32_t)(s_anc[w] >> (e - LP));
+        f32x4 c = vec(s_C + w * CS + e) * (of_ring ? vec(s_R + e) * s_path[w] : vec(s_D + w * WP + e - LP));
+        if constexpr (!DELTA) c *= vec(s_dt + e);
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+            if (!(on >> u & 1)) c[u] = 0.f;
+        *reinterpret_cast<f32x4 *>(s_C + w * CS + e) = c;
+    }
+    if constexpr (DELTA) {
+        // A^T, tiles i >= j; of values that are no numbers nothing: what they have to
+        // reach, G, beta and the decays carry
+        for (int x = NW - 1 - wave; x < et_n * (et_n + 1) / 2; x += NW) {
+            int ot = 0, et = x;
+            while (et > ot) et -= ++ot;
+            const int j = 16 * et + lr, i = 16 * ot + 4 * lg;
+            f32x4 d;
+            uint32_t on = 0;
+            if (16 * ot < LP) {
+                d = vec(s_RR + j * LP + i);
+                on = (uint32_t)((1ull << count) - 1) >> i;
+            } else if (16 * et < LP) {
+                d = vec(s_path + i - LP) * s_R[j];
+                on = j < count ? 15 : 0;
+            } else {
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    d[u] = s_D[(i + u - LP) * WP + j - LP];
+                    on |= (uint32_t)(s_anc[i + u - LP] >> (j - LP) & 1) << u;
+                }
+            }
+            f32x4 c = d * vec(s_A + j * CS + i) * vec(s_dt + i);
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+                if (!(on >> u & 1) || i + u <= j || i + u >= e_end || !tree_finite(c[u])) c[u] = 0.f;
+            *reinterpret_cast<f32x4 *>(s_A + j * CS + i) = c;
+        }
+        if constexpr (CP) {
+            uint32_t bad = 0;
+#pragma unroll
+            for (int i = 0; i < NW; ++i) bad |= s_odd[i];
+            if (bad)   // the products take 0 for such values: another's weight makes its nodes NaN as it is
+                for (int x = tid; x < 16 * et_n * (N / 2); x += NT) {
+                    uint32_t *u = reinterpret_cast<uint32_t *>(s_K + x / (N / 2) * KS) + x % (N / 2);
+                    *u &= ((*u & 0x7f80u) == 0x7f80u ? 0u : 0xffffu) | ((*u & 0x7f800000u) == 0x7f800000u ? 0u : 0xffff0000u);
+                }
+        }
         lds_barrier();
         // rows of the diagonal blocks' inverses T, a lane a row: y (I + A) = e_r from the last column back
         for (int x = tid; x < 16 * et_n; x += NT) {
@@ -506,7 +612,7 @@ __global__ __launch_bounds__((TreeShape<P, N>::NT), IOB ? 4 : 3) void verify_tre
             f32x4 c[Sh::MT];
 #pragma unroll
             for (int J = 0; J < Sh::MT; ++J)
-                if (J < et_n) c[J] = *reinterpret_cast<const f32x4 *>(row + 16 * J);
+                c[J] = *reinterpret_cast<const f32x4 *>(row + 16 * (J < et_n ? J : 0));
 #pragma unroll
             for (int J = Sh::MT - 1; J >= 0; --J)
                 if (J < et_n) {
@@ -526,37 +632,93 @@ __global__ __launch_bounds__((TreeShape<P, N>::NT), IOB ? 4 : 3) void verify_tre
 #pragma unroll
             for (int J = 0; J < Sh::MT; ++J)
                 if (J < et_n) {
+                    f32x4 o;
                     const f32x4 beta = *reinterpret_cast<const f32x4 *>(&s_dt[16 * J + 4 * lg]);
                     const uint32_t on = 16 * J < LP ? in_ring >> 16 * J : (uint32_t)(nodes >> (16 * J - LP));
 #pragma unroll
-                    for (int u = 0; u < 4; ++u) c[J][u] = on >> u & 1 ? c[J][u] * beta[u] : 0.f;
-                    *reinterpret_cast<f32x4 *>(row + 16 * J) = c[J];
+                    for (int u = 0; u < 4; ++u) o[u] = on >> u & 1 ? c[J][u] * beta[u] : 0.f;
+                    if constexpr (CP) put_parts<3>(s_P + w * at.CB + 16 * J + 4 * lg, cpart, o);
+                    else *reinterpret_cast<f32x4 *>(row + 16 * J) = o;
                 }
+            if constexpr (CP)
+                if (et_n & 1)   // the other half of the last 32
+#pragma unroll
+                    for (int z = 0; z < 3; ++z) *reinterpret_cast<u32x2 *>(s_P + z * cpart + w * at.CB + 16 * et_n + 4 * lg) = u32x2{0, 0};
         }
     }
     lds_barrier();
 
-    if constexpr (DELTA) {   // the queries, which take the place of A
-        for (int nt = wave; nt < N / 16; nt += NW) {
-            u32x2 q[kMaxTree / 16][IOB ? 1 : 2];
+    if constexpr (CP) {   // the queries: a wavefront has 16 nodes and every `turns`-th 16 columns
+        const int turns = NW > wt_n ? NW / wt_n : 1;
+        const int first = turns > 1 ? wave / wt_n : 0;
+        if (first < turns)
+            for (int wt = turns > 1 ? wave % wt_n : wave; wt < wt_n; wt += turns > 1 ? wt_n : NW) {
+                asm volatile("" ::: "memory");   // gamma stays in LDS
+                const int w = 16 * wt + lr;
+                bf16x8_t c[Sh::MT / 2][3];   // C gamma of entries 32 i + 4 lg + u and 32 i + 16 + 4 lg + u
 #pragma unroll
-            for (int wt = 0; wt < kMaxTree / 16; ++wt)
+                for (int i = 0; i < Sh::MT / 2; ++i)
+                    if (32 * i < e_end) {
+                        u32x2 o[2][3];
 #pragma unroll
-                for (int x = 0; x < (IOB ? 1 : 2); ++x) {
-                    q[wt][x] = u32x2{0, 0};
-                    if (16 * wt < n)
-                        q[wt][x] = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(qs, (uint32_t)(16 * wt + lr) * ks.stride + (16 * nt + 4 * lg) * ESZ + 8 * x, 0, 0));
+                        for (int hh = 0; hh < 2; ++hh) {
+                            const int e = 32 * i + 16 * hh + 4 * lg;
+                            u32x2 in[3];
+#pragma unroll
+                            for (int z = 0; z < 3; ++z) in[z] = *reinterpret_cast<const u32x2 *>(s_P + z * cpart + w * at.CB + e);
+                            const f32x4 gam = vec(s_gam + e);
+                            f32x4 x;
+#pragma unroll
+                            for (int u = 0; u < 4; ++u) {
+                                float v[3];
+#pragma unroll
+                                for (int z = 0; z < 3; ++z) v[z] = bf16_bits_to_f32(u & 1 ? in[z][u >> 1] >> 16 : in[z][u >> 1] & 0xffffu);
+                                const float f = v[2] + v[1] + v[0];
+                                x[u] = f == 0.f || 16 * (2 * i + hh) >= e_end ? 0.f : f * gam[u];
+                            }
+                            split_parts<3>(x, o[hh]);
+                        }
+#pragma unroll
+                        for (int z = 0; z < 3; ++z) c[i][z] = __builtin_bit_cast(bf16x8_t, u32x4{o[0][z].x, o[0][z].y, o[1][z].x, o[1][z].y});
+                    }
+                const float gw = s_gam[LP + w];
+                auto query = [&](int nt) {
+                    return __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(qs, nt < N / 16 ? (uint32_t)w * ks.stride + (16 * nt + 4 * lg) * ESZ : 0x80000000u, 0, 0));
+                };
+                u32x2 q = query(first);
+                for (int nt = first; nt < N / 16; nt += turns) {
+                    const u32x2 next = query(nt + turns);
+                    f32x4 x = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int i = 0; i < Sh::MT / 2; ++i)
+                        if (32 * i < e_end) {
+                            const bf16x8_t k = cols8(s_K + 32 * i * KS, 32 * i + 16 < e_end ? 16 * KS : 0, KS, nt, lane);
+#pragma unroll
+                            for (int z = 2; z >= 0; --z) x = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k, c[i][z], x, 0, 0, 0);
+                        }
+                    f32x4 o;
+#pragma unroll
+                    for (int rr = 0; rr < 4; ++rr)
+                        o[rr] = w < n ? fmaf(gw, bf16_bits_to_f32(rr & 1 ? q[rr >> 1] >> 16 : q[rr >> 1] & 0xffffu), -x[rr]) : 0.f;
+                    put_query(w, 16 * nt + 4 * lg, o);
+                    q = next;
                 }
+            }
+    } else if constexpr (DELTA) {
+        for (int nt = wave; nt < N / 16; nt += NW) {
+            u32x4 q[kMaxTree / 16];
+#pragma unroll
+            for (int wt = 0; wt < kMaxTree / 16; ++wt) {
+                q[wt] = u32x4{0, 0, 0, 0};
+                if (16 * wt < n) q[wt] = __builtin_amdgcn_raw_buffer_load_b128(qs, (uint32_t)(16 * wt + lr) * ks.stride + (16 * nt + 4 * lg) * ESZ, 0, 0);
+            }
             float kc[Sh::MT][4];   // column 16 nt + lr of entries 16 i + 4 lg + u
 #pragma unroll
             for (int i = 0; i < Sh::MT; ++i)
                 if (16 * i < e_end)
 #pragma unroll
                     for (int u = 0; u < 4; ++u) {
-                        const float *row = s_K + (16 * i + 4 * lg + u) * KS;
-                        float k;
-                        if constexpr (IOB) k = bf16_bits_to_f32(reinterpret_cast<const uint16_t *>(row)[16 * nt + lr]);
-                        else k = row[16 * nt + lr];
+                        const float k = s_K[(16 * i + 4 * lg + u) * KS + 16 * nt + lr];
                         kc[i][u] = tree_finite(k) ? k : 0.f;   // another's weight makes its nodes NaN as it is
                     }
 #pragma unroll
@@ -577,10 +739,7 @@ __global__ __launch_bounds__((TreeShape<P, N>::NT), IOB ? 4 : 3) void verify_tre
                 f32x4 o;
 #pragma unroll
                 for (int rr = 0; rr < 4; ++rr) {
-                    uint32_t u = q[wt][IOB ? 0 : rr >> 1][IOB ? rr >> 1 : rr & 1];
-                    asm volatile("" : "+v"(u));   // as with v
-                    if (IOB) u = rr & 1 ? u >> 16 : u & 0xffffu;
-                    o[rr] = w < n ? fmaf(gw, entry_value<IOB>(u), -x[rr]) : 0.f;
+                    o[rr] = w < n ? fmaf(gw, __uint_as_float(q[wt][rr]), -x[rr]) : 0.f;
                 }
                 put_query(w, 16 * nt + 4 * lg, o);
             }
@@ -590,20 +749,6 @@ __global__ __launch_bounds__((TreeShape<P, N>::NT), IOB ? 4 : 3) void verify_tre
 
     // y^T: rows p0 + 4 lg + rr, nodes 16 wt + lr
     rows.transpose(reinterpret_cast<uint32_t (*)[WT::TROW]>(s_K + (WT::COAL ? wave * 16 * WT::TROW : 0)), lane);
-    float vf[Sh::MT][4];
-    bool odd = false;
-#pragma unroll
-    for (int i = 0; i < Sh::MT; ++i)
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            asm volatile("" : "+v"(vc[i][u]));   // its load ends here, not where it was sent
-            vf[i][u] = entry_value<IOB>(vc[i][u]);
-            if (!tree_finite(vf[i][u])) {
-                vf[i][u] = 0.f;
-                odd = true;
-            }
-        }
-    odd = __any(odd);
     const uint8_t *rsc = static_cast<const uint8_t *>(t.scale) + (bh * P + p0 + 4 * lg) * WT::NB;   // FP4 rows
     for (int wt = 0; wt < wt_n; ++wt) {
         const int w = 16 * wt + lr;
@@ -611,6 +756,17 @@ __global__ __launch_bounds__((TreeShape<P, N>::NT), IOB ? 4 : 3) void verify_tre
         if constexpr (PARTS) y = dot_parts<PARTS>(rows, reinterpret_cast<const uint16_t *>(s_X) + 16 * wt * Sh::XB, part, Sh::XB, lane, rsc);
         else y = rows.dot_f32q(reinterpret_cast<const float (*)[XS]>(s_X + 16 * wt * XS), lane, rsc);
         y *= DELTA ? sc : sc * s_gam[LP + w];
+        if constexpr (CP) {
+#pragma unroll
+            for (int i = 0; i < Sh::MT / 2; ++i)
+                if (32 * i < e_end)
+#pragma unroll
+                    for (int z = 2; z >= 0; --z) {
+                        const uint16_t *c = s_P + z * cpart + w * at.CB + 32 * i + 4 * lg;
+                        const u32x2 c0 = *reinterpret_cast<const u32x2 *>(c), c1 = *reinterpret_cast<const u32x2 *>(c + 16);
+                        y = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vp[i], __builtin_bit_cast(bf16x8_t, u32x4{c0.x, c0.y, c1.x, c1.y}), y, 0, 0, 0);
+                    }
+        } else
 #pragma unroll
         for (int i = 0; i < Sh::MT; ++i)
             if (16 * i < e_end) {
@@ -625,7 +781,9 @@ __global__ __launch_bounds__((TreeShape<P, N>::NT), IOB ? 4 : 3) void verify_tre
 #pragma unroll
                 for (int rr = 0; rr < 4; ++rr) {
                     const float v = entry_value<IOB>(load_raw<IOB>(vs.rows_of(e & ~15), vs.at(e & ~15, e & 15), p0 + 4 * lg + rr));
-                    if (!tree_finite(v)) y[rr] = fmaf(s_C[w * CS + e], v, y[rr]);
+                    if (tree_finite(v)) continue;
+                    if constexpr (CP) y[rr] = fmaf(bf16_bits_to_f32(s_P[w * at.CB + e]), v, y[rr]);   // its sign and whether it is 0
+                    else y[rr] = fmaf(s_C[w * CS + e], v, y[rr]);
                 }
             }
         }
@@ -636,7 +794,7 @@ __global__ __launch_bounds__((TreeShape<P, N>::NT), IOB ? 4 : 3) void verify_tre
 template <int P, int N, int ST, bool IOB, bool DELTA>
 hipError_t launch_tree_one(const TreeArgs &a, hipStream_t s) {
     using Sh = TreeShape<P, N>;
-    const TreeLds at(a.W, a.r.L, DELTA, Sh::template XF<ST, IOB, DELTA>, Sh::template KS<IOB>, Sh::template TILE<ST>);
+    const TreeLds at(a.W, a.r.L, DELTA, DELTA && IOB, Sh::template XF<ST, IOB, DELTA>, Sh::template KS<IOB>, Sh::template TILE<ST>);
     verify_tree_kernel<P, N, ST, IOB, DELTA>
         <<<(unsigned)((int64_t)a.r.B * a.r.H), TreeShape<P, N>::NT, at.total * sizeof(float), s>>>(a);
     return hipGetLastError();
