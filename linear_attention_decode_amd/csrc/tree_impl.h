@@ -160,15 +160,16 @@ template <int PARTS>
 __device__ __forceinline__ void split_parts(f32x4 x, u32x2 *out) {
 #pragma unroll
     for (int z = 0; z < PARTS; ++z) {
-        uint32_t hi[4];
+        uint32_t u[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const uint32_t u = __float_as_uint(x[i]);
-            const bool fin = tree_finite(x[i]);
-            hi[i] = fin || !(u & 0x007fffffu) ? u : u | 0x00400000u;   // a NaN stays one
-            x[i] = fin ? x[i] - __uint_as_float(u & 0xffff0000u) : 0.f;
+            u[i] = __float_as_uint(z == 0 ? __builtin_canonicalizef(x[i]) : x[i]);   // a NaN stays one
+            if (z + 1 < PARTS) {
+                const float left = x[i] - __uint_as_float(u[i] & 0xffff0000u);
+                x[i] = z > 0 || tree_finite(x[i]) ? left : 0.f;
+            }
         }
-        out[z] = u32x2{hi[0] >> 16 | (hi[1] & 0xffff0000u), hi[2] >> 16 | (hi[3] & 0xffff0000u)};
+        out[z] = u32x2{u[0] >> 16 | (u[1] & 0xffff0000u), u[2] >> 16 | (u[3] & 0xffff0000u)};
     }
 }
 template <int PARTS>   // `part` elements apart
@@ -235,7 +236,7 @@ __device__ __forceinline__ f32x4 dot_parts(const WideRows<P, N, ST> &rows, const
 }
 
 template <int P, int N, int ST, bool IOB, bool DELTA>
-__global__ __launch_bounds__((TreeShape<P, N>::NT), IOB ? 4 : 3) void verify_tree_kernel(TreeArgs t) {
+__global__ __launch_bounds__((TreeShape<P, N>::NT), DELTA ? (IOB ? 4 : 3) : 1) void verify_tree_kernel(TreeArgs t) {
     using Sh = TreeShape<P, N>;
     using WT = WideTile<P, N, ST>;
     constexpr int NW = Sh::NW, NT = Sh::NT, XS = Sh::XS;
@@ -436,26 +437,27 @@ __global__ __launch_bounds__((TreeShape<P, N>::NT), IOB ? 4 : 3) void verify_tre
         }
         float pre = ra, suf = ra;   // of the ring, up to and with j; from j on
 #pragma unroll
-        for (int d = 1; d < kMaxRing; d <<= 1) {
-            const float u = __shfl_up(pre, d), o = __shfl_down(suf, d);
-            if (lane >= d) pre *= u;
-            if (lane + d < 64) suf *= o;
-        }
-        const float all = __shfl(pre, kMaxRing - 1);
+        for (int d = 1; d < kMaxRing; d <<= 1)
+            if (d < LP) {
+                const float u = __shfl_up(pre, d), o = __shfl_down(suf, d);
+                if (lane >= d) pre *= u;
+                if (lane + d < 64) suf *= o;
+            }
+        const float all = __shfl(pre, LP - 1);
         suf = __shfl_down(suf, 1);
-        uint64_t anc = 1ull << lane;
-        float path = na;
-        int up = tree.parent;
-#pragma unroll
-        for (int d = 1; d < kMaxTree; d <<= 1) {   // what lies 2^d steps up
-            const int from = up < 0 ? 0 : up;
-            const uint64_t m = (uint64_t)__shfl((long long)anc, from);
-            const float f = __shfl(path, from);
-            const int u = __shfl(up, from);
-            if (up >= 0) {
-                anc |= m;
+        // up from node `lane`, the nearest first: D[w][j] for the j on the way, and who they are
+        uint64_t anc = 0;
+        float path = 1.f;
+        int x = lane < n ? lane : -1;
+        while (__any(x >= 0)) {
+            const int from = x < 0 ? 0 : x;
+            const float f = __shfl(na, from);
+            const int u = __shfl(tree.parent, from);
+            if (x >= 0) {
+                s_D[lane * WP + x] = path;
                 path *= f;
-                up = u;
+                anc |= 1ull << x;
+                x = u;
             }
         }
         if (lane < kMaxRing) {
@@ -470,21 +472,6 @@ __global__ __launch_bounds__((TreeShape<P, N>::NT), IOB ? 4 : 3) void verify_tre
             s_path[lane] = path;
             s_gam[LP + lane] = path * all;
             s_dt[LP + lane] = ndt;
-        }
-        // D[w][j] for the j on w's way up, a lane a node: the nearest first
-        {
-            float p = 1.f;
-            int x = lane < n ? lane : -1;
-            while (__any(x >= 0)) {
-                const int from = x < 0 ? 0 : x;
-                const float f = __shfl(na, from);
-                const int u = __shfl(tree.parent, from);
-                if (x >= 0) {
-                    s_D[lane * WP + x] = p;
-                    p *= f;
-                    x = u;
-                }
-            }
         }
     }
     if constexpr (DELTA)
