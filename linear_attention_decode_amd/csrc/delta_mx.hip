@@ -521,7 +521,7 @@ __device__ __forceinline__ void by_token(const ScanArgs &s, const Tile<P, N, CW>
 // in R, U and y, and the state's rows N / 2 th .. in S^T.  The system is lower
 // triangular, so that th = 0 needs nothing of th = 1 for R, U and y.
 template <int P, int N, int CW>
-__global__ __launch_bounds__((Shape<P, N, CW>::NT), 2) void delta_mx_kernel(ScanArgs s) {
+__global__ __launch_bounds__((Shape<P, N, CW>::NT), CW == 1 ? 1 : 2) void delta_mx_kernel(ScanArgs s) {
     using Sh = Shape<P, N, CW>;
     constexpr int KN = Sh::KN, KH = Sh::KH, QB = Sh::QB;
     __shared__ Tile<P, N, CW> m;
@@ -788,7 +788,11 @@ hipError_t launch_pn(ScanArgs a, hipStream_t s) {
             delta_prep_kernel<N, 1><<<(unsigned)units, kPrepNT, 0, s>>>(a);
         hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
-        e = (int64_t)a.B * a.H * P / 64 >= 128 ? launch_chain<P, N, 4>(a, s) : launch_chain<P, N, 1>(a, s);
+        // With 16 columns a workgroup reads k, q and T four times as often, but there are
+        // four times as many to keep the card busy.  2048 tokens, 64 columns of a
+        // head counted as one: 64 of them 110 us against 152 (four shares of 16), 128: 141
+        // and 160, 192: 271 and 200, 512: 267 and 203.
+        e = (int64_t)a.B * a.H * P / 64 > 128 ? launch_chain<P, N, 4>(a, s) : launch_chain<P, N, 1>(a, s);
         if (e != hipSuccess) return e;
     }
     return hipSuccess;
