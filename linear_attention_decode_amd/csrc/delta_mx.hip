@@ -11,8 +11,8 @@
 // are 256 tiles of 16 columns), so two wavefronts share 16 columns: each has
 // half of a chunk's tokens, and half of S^T's rows, which stay in its accumulators.
 // What bounds it: the chain of a chunk's steps, four barriers apart.  One
-// sequence of 8192 tokens (32 heads of 128 x 128): 55 us for T and G, 345 for 128
-// chunks, two wavefronts a CU.  Sixteen ragged ones of 15013 tokens: 103 and 335
+// sequence of 8192 tokens (32 heads of 128 x 128): 55 us for T and G, 343 for 128
+// chunks, two wavefronts a CU.  Sixteen ragged ones of 15013 tokens: 108 and 329
 // us, eight wavefronts a CU that wait for LDS, for the matrix instructions and for each
 // other in turn.  The float32 kernel takes 3410 and 889 us.
 //
@@ -168,7 +168,10 @@ __device__ __forceinline__ f32x4 decays_of(const Decays &d, int ti, int tj, int 
     return p * *reinterpret_cast<const f32x4 *>(&d.suf[j0]);
 }
 
-// A workgroup makes a chunk of HP heads of a group, which share k . k and k . q.
+// A workgroup makes a chunk of HP heads of a group, which share k . k and k . q.  Bound
+// by its own chain (products, decays, the inverse by blocks of 16, their products)
+// and by what it writes: 8192 tokens of 32 heads 55 us, of which a copy of the
+// 129 MB would take 27.
 template <int N, int HP>
 __global__ __launch_bounds__(kPrepNT) void delta_prep_kernel(ScanArgs s) {
     __shared__ __align__(16) PrepTile m[HP];

