@@ -334,28 +334,29 @@ __device__ __forceinline__ s16x4 col4(const uint8_t *m) {
 
 template <int P, int N, int CW>
 struct Shape {
-    static constexpr int NT = 128 * CW, PC = 16 * CW, CB = P / PC;   // threads, columns, workgroups a head
+    // A pair of wavefronts alone has a second one beside it that makes y.
+    static constexpr bool SHARE = CW > 1;
+    static constexpr int NT = SHARE ? 128 * CW : 256, PC = 16 * CW, CB = P / PC;   // threads, columns, workgroups a head
     static constexpr int QB = 2 * N, KN = N / 32, KH = KN / 2;       // bytes of a row; steps over it, a wavefront's own
     static constexpr int IQ = kQ * QB / 16 / NT;                     // 16-byte pieces of k, and of q, that a thread stages
     // Several pairs of wavefronts share T and G through LDS (their own loads of
     // them would be 120 KB a chunk, and what a CU gets from its L2 is some 18 bytes a clock);
     // a pair alone takes its own straight into registers.
-    static constexpr bool SHARE = CW > 1;
     static constexpr int IT = (kImage + 16) / 16 / NT + 1;           // pieces of the chunk's slot
     static_assert(P % PC == 0 && kQ * QB / 16 % NT == 0, "whole pieces");
 };
 
 // What the two wavefronts of 16 columns hand each other, as operands.
-template <int KN>
+template <int KN, bool SHARE>
 struct Exchange {
-    uint8_t s[KN][3][kFrag], e[2][3][kFrag], r[3][kFrag], u[2][kFrag];
+    uint8_t s[KN][3][kFrag], e[2][3][kFrag], r[3][kFrag], u[SHARE ? 1 : 2][2][kFrag];
 };
 template <int P, int N, int CW>
 struct Tile {
     using Sh = Shape<P, N, CW>;
     __align__(16) uint8_t k[kQ * Sh::QB], q[kQ * Sh::QB];
     uint8_t odd[16];
-    __align__(16) Exchange<Sh::KN> x[CW];
+    __align__(16) Exchange<Sh::KN, Sh::SHARE> x[CW];
     __align__(16) uint8_t slot[Sh::SHARE ? kImage + 16 : 16];
 };
 
@@ -534,14 +535,15 @@ __global__ __launch_bounds__((Shape<P, N, CW>::NT), CW == 1 ? 1 : 2) void delta_
     const int h = place.h, b = place.b, g = place.g;
     const Span sp = find_span(s, b, 0);
     const int tid = threadIdx.x, lane = tid & 63, c = lane & 15, lg = lane >> 4;
-    const int w = __builtin_amdgcn_readfirstlane(tid >> 6), th = w & 1;
+    const int w = __builtin_amdgcn_readfirstlane(tid >> 6), th = w & 1, pair = Sh::SHARE ? w >> 1 : 0;
+    const bool makes_y = !Sh::SHARE && w > 1;   // and does not have S^T
     if (s.chunk0 == 0 && h == 0 && place.cb == 0 && !sp.run && tid == 0) raise_seq_error(s.err, b, REPLAY_SEQERR_BAD_RANGE);
     const int from = s.chunk0 * kQ, upto = sp.n < from + s.window * kQ ? sp.n : from + s.window * kQ;
     if (!sp.run || (from > 0 && from >= sp.n)) return;
-    Exchange<KN> &ex = m.x[w >> 1];
-    uint8_t &odd_chunk = m.odd[w >> 1];   // of the two wavefronts'
+    Exchange<KN, Sh::SHARE> &ex = m.x[pair];
+    uint8_t &odd_chunk = m.odd[pair];   // of the two wavefronts'
 
-    const int p0 = Sh::PC * place.cb + 16 * (w >> 1);   // the wavefront's columns
+    const int p0 = Sh::PC * place.cb + 16 * pair;   // the wavefront's columns
     const size_t bh = (size_t)b * s.H + h;
     float *const state = s.s_out + (bh * P + p0 + c) * N + 4 * lg;          // columns 16 t + 4 lg ..
     const float *in = from > 0 ? s.s_out : s.s_in;
@@ -568,9 +570,9 @@ __global__ __launch_bounds__((Shape<P, N, CW>::NT), CW == 1 ? 1 : 2) void delta_
             for (int z = 0; z < 3; ++z) put_frag(to + (3 * i + z) * kFrag, part[z]);
         }
     };
-    get_state(in ? in + (bh * P + p0 + c) * N + 4 * lg : nullptr);
+    if (!makes_y) get_state(in ? in + (bh * P + p0 + c) * N + 4 * lg : nullptr);
     if (upto == from) {   // no tokens: the state as it is
-        put_state();
+        if (!makes_y) put_state();
         return;
     }
     const uint32_t rv = (uint32_t)s.H * P * 2, rqk = (uint32_t)s.G * QB;
@@ -599,13 +601,81 @@ __global__ __launch_bounds__((Shape<P, N, CW>::NT), CW == 1 ? 1 : 2) void delta_
     Values val;
     Slot<Sh::SHARE> my;
     ahead.load(kp, qp, rqk, upto - from, slot);
+    // y^T, rows p = 4 lg + r, column token 32 th + 16 x + c: a half of U's tokens by G, then the store
+    auto add_corrections = [&](acc4 *y, const bf8 *up, const bf8 *ux) {
+        if (th)
+#pragma unroll
+            for (int z = 2; z >= 0; --z)
+#pragma unroll
+                for (int x = 0; x < 2; ++x) y[x] = mma16(ux[z == 2], my.gx(x, z == 1), y[x]);
+#pragma unroll
+        for (int z = 2; z >= 0; --z)
+#pragma unroll
+            for (int x = 0; x < 2; ++x) y[x] = mma16(up[z == 2], my.g(x, z == 1), y[x]);
+    };
+    auto store_y = [&](const acc4 *y, int n) {
+        const auto ys = make_rsrc(yp, (uint32_t)(n - 1) * rv + 32);
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+            __builtin_amdgcn_raw_buffer_store_b64(
+                u32x2{f32x2_to_bf16_pair(y[x][0], y[x][1]), f32x2_to_bf16_pair(y[x][2], y[x][3])}, ys, yo, 16 * x * rv, 0);
+    };
+    if constexpr (!Sh::SHARE) {
+        if (makes_y) {   // the same barriers as in the loop below
+            my.load_decays(slot, th, lane);
+            my.load_g(slot, th, lane);
+            ahead.store(m);
+            for (int done = from; done < upto; done += kQ) {
+                const int n = sp.n - done < kQ ? sp.n - done : kQ, left = upto - done - kQ;
+                lds_barrier();   // q and the operands of S^T
+                kp += (size_t)kQ * rqk;
+                qp += (size_t)kQ * rqk;
+                slot += next_slot;
+                ahead.load(kp, qp, rqk, left, slot);
+                const uint8_t *const next = left > 0 ? slot : nullptr;
+                acc4 y[2];
+#pragma unroll
+                for (int st = 0; st < KN; ++st) {
+                    bf8 q[2];
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) q[x] = operand(m.q, x, st);
+#pragma unroll
+                    for (int z = 1; z >= 0; --z) {
+                        const bf8 p = frag16(xl + (3 * st + z) * kFrag);
+#pragma unroll
+                        for (int x = 0; x < 2; ++x) y[x] = mma16(p, q[x], st == 0 && z == 1 ? acc4{0.f, 0.f, 0.f, 0.f} : y[x]);
+                    }
+                }
+#pragma unroll
+                for (int x = 0; x < 2; ++x) y[x] *= my.dn(x);
+                lds_barrier();   // (R of the first tokens)
+                const bool odd = odd_chunk != 0;
+                lds_barrier();   // U
+                if (!odd) {
+                    bf8 up[2], ux[2];
+#pragma unroll
+                    for (int z = 0; z < 2; ++z) {
+                        up[z] = frag16(xl + kU + (2 * th + z) * kFrag);
+                        ux[z] = frag16(xl + kU + z * kFrag);
+                    }
+                    add_corrections(y, up, ux);
+                    store_y(y, n);
+                }
+                yp += (size_t)kQ * rv;
+                my.load_decays(next, th, lane);
+                my.load_g(next, th, lane);
+                lds_barrier();   // k, q and what was handed over are read to their end
+                ahead.store(m);
+            }
+            return;
+        }
+    }
     val.load(vp, rv, sp.n - from < kQ ? sp.n - from : kQ, vo);
     if constexpr (Sh::SHARE) {
         my.init(m.slot, th, lane);
     } else {
         my.load_decays(slot, th, lane);
         my.load_t(slot, th, lane);
-        my.load_g(slot, th, lane);
     }
     hand_state();
     if (th == 0 && lane == 0) odd_chunk = 0;
@@ -619,9 +689,9 @@ __global__ __launch_bounds__((Shape<P, N, CW>::NT), CW == 1 ? 1 : 2) void delta_
         slot += next_slot;
         ahead.load(kp, qp, rqk, left, slot);
         [[maybe_unused]] const uint8_t *const next = left > 0 ? slot : nullptr;
-        // K S^T, rows token 32 th + 16 x + 4 lg + r, column c.  S Q^T, rows p = 4
-        // lg + r, column token 32 th + 16 x + c, comes behind U where all wavefronts of
-        // a full CU would read k, q and S at once here.
+        // K S^T, rows token 32 th + 16 x + 4 lg + r, column c.  S Q^T, where it is
+        // not another pair's, comes behind U: here all wavefronts of a full CU would
+        // read k, q and S at once.
         acc4 ks[2], y[2];
         bf8 part[KN][2];   // S's first two parts, kept for S Q^T
 #pragma unroll
@@ -632,7 +702,7 @@ __global__ __launch_bounds__((Shape<P, N, CW>::NT), CW == 1 ? 1 : 2) void delta_
 #pragma unroll
             for (int z = 2; z >= 0; --z) {
                 const bf8 p = frag16(xl + (3 * st + z) * kFrag);
-                if (z < 2) part[st][z] = p;
+                if (Sh::SHARE && z < 2) part[st][z] = p;
 #pragma unroll
                 for (int x = 0; x < 2; ++x) ks[x] = mma16(k[x], p, st == 0 && z == 2 ? acc4{0.f, 0.f, 0.f, 0.f} : ks[x]);
             }
@@ -651,7 +721,6 @@ __global__ __launch_bounds__((Shape<P, N, CW>::NT), CW == 1 ? 1 : 2) void delta_
 #pragma unroll
             for (int x = 0; x < 2; ++x) y[x] *= my.dn(x);
         };
-        if constexpr (!Sh::SHARE) read_state();
         // (0 v is a NaN where v is no number)
         float none = my.odd() ? __builtin_nanf("") : 0.f;
 #pragma unroll
@@ -693,9 +762,9 @@ __global__ __launch_bounds__((Shape<P, N, CW>::NT), CW == 1 ? 1 : 2) void delta_
 #pragma unroll
                 for (int x = 0; x < 2; ++x) u[x] = mma16(my.t(x, a[z]), rp[o[z]], u[x]);
             split<2>(u[0], u[1], up);
-            if (th == 0)
+            if (th == 0 || !Sh::SHARE)
 #pragma unroll
-                for (int z = 0; z < 2; ++z) put_frag(ex.u[z] + 16 * lane, up[z]);
+                for (int z = 0; z < 2; ++z) put_frag(ex.u[Sh::SHARE ? 0 : th][z] + 16 * lane, up[z]);
 #pragma unroll
             for (int x = 0; x < 2; ++x) u[x] *= my.e(x);
             split<3>(u[0], u[1], ep);
@@ -713,25 +782,13 @@ __global__ __launch_bounds__((Shape<P, N, CW>::NT), CW == 1 ? 1 : 2) void delta_
         }
         lds_barrier();   // U of the first tokens, e U of all
         if (!odd) {
-            // y^T: + U^T G^T
-            if (th) {
+            if constexpr (Sh::SHARE) {
                 bf8 ux[2];
 #pragma unroll
                 for (int z = 0; z < 2; ++z) ux[z] = frag16(xl + kU + z * kFrag);
-#pragma unroll
-                for (int z = 2; z >= 0; --z)
-#pragma unroll
-                    for (int x = 0; x < 2; ++x) y[x] = mma16(ux[z == 2], my.gx(x, z == 1), y[x]);
+                add_corrections(y, up, ux);
+                store_y(y, n);
             }
-#pragma unroll
-            for (int z = 2; z >= 0; --z)
-#pragma unroll
-                for (int x = 0; x < 2; ++x) y[x] = mma16(up[z == 2], my.g(x, z == 1), y[x]);
-            const auto ys = make_rsrc(yp, (uint32_t)(n - 1) * rv + 32);
-#pragma unroll
-            for (int x = 0; x < 2; ++x)
-                __builtin_amdgcn_raw_buffer_store_b64(
-                    u32x2{f32x2_to_bf16_pair(y[x][0], y[x][1]), f32x2_to_bf16_pair(y[x][2], y[x][3])}, ys, yo, 16 * x * rv, 0);
             // S^T <- (whole decay) S^T + K^T (e U), the wavefront's own tokens first
             bf8 ox[3];
 #pragma unroll
@@ -760,7 +817,6 @@ __global__ __launch_bounds__((Shape<P, N, CW>::NT), CW == 1 ? 1 : 2) void delta_
             __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup");
         }
         yp += (size_t)kQ * rv;
-        if constexpr (!Sh::SHARE) my.load_g(next, th, lane);
         lds_barrier();   // k, q and what was handed over are read to their end
         if (odd) {
             __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup");
