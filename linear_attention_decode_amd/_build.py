@@ -27,10 +27,10 @@ CFLAGS = ["-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}", "-Wall",
 # readfirstlane waits for the atomic (and every load before it) where it is issued.
 EXTRA = {f: ["-mllvm", "-amdgpu-atomic-optimizer-strategy=None"]
          for f in ("step.hip", "step_copy.hip", "verify_step.hip", "flush.hip", "flush_shared.hip", "gdn.hip")}
-# flush_shared.hip, delta_mx.hip, tree_delta_*.hip: MFMA accumulators in VGPRs (the AGPR form copied every
+# flush_shared.hip, delta_mx.hip, delta_few.hip, tree_delta_*.hip: MFMA accumulators in VGPRs (the AGPR form copied every
 # element in and out of the accumulators).
 EXTRA["flush_shared.hip"] += ["-mllvm", "-amdgpu-mfma-vgpr-form"]
-for f in ("delta_mx.hip", "tree_delta_bf16.hip", "tree_delta_f32.hip"):
+for f in ("delta_mx.hip", "delta_few.hip", "tree_delta_bf16.hip", "tree_delta_f32.hip"):
     EXTRA[f] = ["-mllvm", "-amdgpu-mfma-vgpr-form"]
 
 

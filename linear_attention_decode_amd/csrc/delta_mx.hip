@@ -7,14 +7,14 @@
 // operands, in the order in which lanes take them.  delta_mx_kernel then goes
 // from chunk to chunk:
 //   R = V - diag(g) K S^T,  U = T R,  Y = diag(g) Q S^T + G U,  S <- g_last S + (e U)^T K.
-// A chain of chunks has little to spread over the card (32 heads of 128 columns
-// are 256 tiles of 16 columns), so two wavefronts share 16 columns: each has
-// half of a chunk's tokens, and half of S^T's rows, which stay in its accumulators.
-// What bounds it: the chain of a chunk's steps, four barriers apart.  One
-// sequence of 8192 tokens (32 heads of 128 x 128): 55 us for T and G, 343 for 128
-// chunks, two wavefronts a CU.  Sixteen ragged ones of 15013 tokens: 108 and 329
-// us, eight wavefronts a CU that wait for LDS, for the matrix instructions and for each
-// other in turn.  The float32 kernel takes 3410 and 889 us.
+// A chain of chunks has little to spread over the card, so two wavefronts share 16
+// columns: each has half of a chunk's tokens, and half of S^T's rows, which stay in
+// its accumulators; where heads are fewer still, delta_few.hip has more of them.
+// What bounds it: the chain of a chunk's steps, four barriers apart.  Sixteen
+// ragged sequences of 15013 tokens (32 heads of 128 x 128): 108 us for T and G, 329 for
+// the chunks, eight wavefronts a CU that wait for LDS, for the matrix instructions
+// and for each other in turn; one of 8192 tokens 55, and 255 in delta_few.hip.  The
+// float32 kernel takes 889 and 3410 us.
 //
 // What bf16 operands leave out: k and q are bf16 as they are; S, R, T and e U
 // go into the products that make the state as three parts of 8 bits, which
@@ -34,60 +34,11 @@
 // A chunk that holds a value that is no number (k, alpha, beta: noted by the
 // first kernel; v: seen by the wavefront) is run token by token, by the rule
 // itself.
-#include "scan_common.h"
+#include "delta_mx.h"
 
 namespace replay {
 
 namespace {
-
-constexpr int kQ = kScanChunk;
-static_assert(kQ == 64, "two blocks of 32 tokens");
-
-typedef __bf16 bf8 __attribute__((ext_vector_type(8)));
-typedef float acc4 __attribute__((ext_vector_type(4)));
-typedef short s16x4 __attribute__((ext_vector_type(4)));
-
-// A head's chunk in the workspace: T's operands (tiles of 16 tokens by steps of
-// 32, three parts each), G's (two parts), g and e, and whether the chunk holds a value
-// that is no number.  Operand x < 4 is tile x at the step its tokens are in,
-// the two behind them are tiles 2 and 3 at step 0.
-constexpr int kFrag = 1024, kFrags = 6;
-constexpr int kTBytes = kFrags * 3 * kFrag, kGBytes = kFrags * 2 * kFrag;
-constexpr int kImage = kTBytes + kGBytes + 2 * kQ * 4;
-constexpr int kSlot = (kImage + 16 + 255) / 256 * 256;
-static_assert(kImage % 16 == 0, "whole pieces");
-__host__ __device__ constexpr int frag(int tile, int step) { return step == tile >> 1 ? tile : tile + 2; }
-
-__device__ __forceinline__ acc4 mma16(bf8 a, bf8 b, acc4 c) {
-    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
-}
-__device__ __forceinline__ acc4 mma4(float a, float b, acc4 c) {
-    return __builtin_amdgcn_mfma_f32_16x16x4f32(a, b, c, 0, 0, 0);
-}
-__device__ __forceinline__ bool odd_pair(uint32_t w) {   // a bf16 pair with a value that is no number
-    return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
-}
-
-// Eight floats as one, two or three operands that hold 8 bits each, the last one rounded.
-template <int PARTS>
-__device__ __forceinline__ void split(const acc4 &lo, const acc4 &hi, bf8 *out) {
-    float x[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-#pragma unroll
-    for (int z = 0; z < PARTS; ++z) {
-        u32x4 w;
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            if (z + 1 < PARTS) {
-                w[r] = upper_pair(x[2 * r], x[2 * r + 1]);
-                x[2 * r] = below_upper(x[2 * r]);
-                x[2 * r + 1] = below_upper(x[2 * r + 1]);
-            } else {
-                w[r] = f32x2_to_bf16_pair(x[2 * r], x[2 * r + 1]);
-            }
-        }
-        out[z] = __builtin_bit_cast(bf8, w);
-    }
-}
 
 // ---- T and G of every chunk and head ----------------------------------------
 
@@ -317,54 +268,36 @@ __global__ __launch_bounds__(kPrepNT) void delta_prep_kernel(ScanArgs s) {
 
 // ---- from chunk to chunk ----------------------------------------------------
 
-__device__ __forceinline__ bf8 frag16(const uint8_t *m) { return __builtin_bit_cast(bf8, *reinterpret_cast<const u32x4 *>(m)); }
-// Rows of k and q in LDS: the sixteen 8-byte pieces of 128 bytes are permuted by the
-// row's number, so that 16 rows' equal pieces, and 4 rows' 4 neighbouring ones, lie
-// in distinct banks.
-__device__ __forceinline__ int turn(int row) { return (row & 3) << 2 | (row >> 2 & 3); }
-// an operand's two pieces
-__device__ __forceinline__ bf8 row8(const uint8_t *first, const uint8_t *second) {
-    const u32x2 lo = *reinterpret_cast<const u32x2 *>(first), hi = *reinterpret_cast<const u32x2 *>(second);
-    return __builtin_bit_cast(bf8, u32x4{lo[0], lo[1], hi[0], hi[1]});
-}
-__device__ __forceinline__ s16x4 col4(const uint8_t *m) {
-    typedef __attribute__((address_space(3))) s16x4 lds4;
-    return __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4 *)m);
-}
-
-template <int P, int N, int CW>
+template <int P, int N>
 struct Shape {
-    // A pair of wavefronts alone has a second one beside it that makes y.
-    static constexpr bool SHARE = CW > 1;
-    static constexpr int NT = SHARE ? 128 * CW : 256, PC = 16 * CW, CB = P / PC;   // threads, columns, workgroups a head
+    static constexpr int CW = 4, NT = 128 * CW, PC = 16 * CW, CB = P / PC;   // pairs of wavefronts, threads, columns, workgroups a head
     static constexpr int QB = 2 * N, KN = N / 32, KH = KN / 2;       // bytes of a row; steps over it, a wavefront's own
     static constexpr int IQ = kQ * QB / 16 / NT;                     // 16-byte pieces of k, and of q, that a thread stages
-    // Several pairs of wavefronts share T and G through LDS (their own loads of
-    // them would be 120 KB a chunk, and what a CU gets from its L2 is some 18 bytes a clock);
-    // a pair alone takes its own straight into registers.
+    // T and G come through LDS too: the wavefronts' own loads of them would be 120
+    // KB a chunk, and what a CU gets from its L2 is some 18 bytes a clock.
     static constexpr int IT = (kImage + 16) / 16 / NT + 1;           // pieces of the chunk's slot
     static_assert(P % PC == 0 && kQ * QB / 16 % NT == 0, "whole pieces");
 };
 
 // What the two wavefronts of 16 columns hand each other, as operands.
-template <int KN, bool SHARE>
+template <int KN>
 struct Exchange {
-    uint8_t s[KN][3][kFrag], e[2][3][kFrag], r[3][kFrag], u[SHARE ? 1 : 2][2][kFrag];
+    uint8_t s[KN][3][kFrag], e[2][3][kFrag], r[3][kFrag], u[2][kFrag];
 };
-template <int P, int N, int CW>
+template <int P, int N>
 struct Tile {
-    using Sh = Shape<P, N, CW>;
+    using Sh = Shape<P, N>;
     __align__(16) uint8_t k[kQ * Sh::QB], q[kQ * Sh::QB];
     uint8_t odd[16];
-    __align__(16) Exchange<Sh::KN, Sh::SHARE> x[CW];
-    __align__(16) uint8_t slot[Sh::SHARE ? kImage + 16 : 16];
+    __align__(16) Exchange<Sh::KN> x[Sh::CW];
+    __align__(16) uint8_t slot[kImage + 16];
 };
 
 // The next chunk's k and q on their way to LDS: rows past its n tokens read zero.
-template <int P, int N, int CW>
+template <int P, int N>
 struct Ahead {
-    using Sh = Shape<P, N, CW>;
-    u32x4 q[Sh::IQ], k[Sh::IQ], slot[Sh::SHARE ? Sh::IT : 1];
+    using Sh = Shape<P, N>;
+    u32x4 q[Sh::IQ], k[Sh::IQ], slot[Sh::IT];
     // n <= 0: nothing is read (no load is conditional, here and below: a
     // wait could not tell it from those behind it)
     __device__ __forceinline__ void load(const char *kp, const char *qp, uint32_t rqk, int n, const uint8_t *from) {
@@ -376,13 +309,11 @@ struct Ahead {
             k[i] = __builtin_amdgcn_raw_buffer_load_b128(rk, o, i * step, 0);
             q[i] = __builtin_amdgcn_raw_buffer_load_b128(rq, o, i * step, 0);
         }
-        if constexpr (Sh::SHARE) {
-            const auto rs = make_rsrc(from, n > 0 ? kImage + 16 : 0);
+        const auto rs = make_rsrc(from, n > 0 ? kImage + 16 : 0);
 #pragma unroll
-            for (int i = 0; i < Sh::IT; ++i) slot[i] = __builtin_amdgcn_raw_buffer_load_b128(rs, tid * 16, i * Sh::NT * 16, 0);
-        }
+        for (int i = 0; i < Sh::IT; ++i) slot[i] = __builtin_amdgcn_raw_buffer_load_b128(rs, tid * 16, i * Sh::NT * 16, 0);
     }
-    __device__ __forceinline__ void store(Tile<P, N, CW> &m) const {
+    __device__ __forceinline__ void store(Tile<P, N> &m) const {
         constexpr int PR = Sh::QB / 16, RS = Sh::NT / PR;   // pieces of a row; rows from one of a thread's to the next
         static_assert(RS % 8 == 0, "their permutations differ by exchanges of 16-byte pieces alone");
         const int tid = threadIdx.x, row = tid / PR, f = turn(row);
@@ -395,11 +326,9 @@ struct Ahead {
             put(m.k + to, k[i]);
             put(m.q + to, q[i]);
         }
-        if constexpr (Sh::SHARE) {
 #pragma unroll
-            for (int i = 0; i < Sh::IT; ++i)
-                if ((i * Sh::NT + tid) * 16 < kImage + 16) *reinterpret_cast<u32x4 *>(m.slot + (i * Sh::NT + tid) * 16) = slot[i];
-        }
+        for (int i = 0; i < Sh::IT; ++i)
+            if ((i * Sh::NT + tid) * 16 < kImage + 16) *reinterpret_cast<u32x4 *>(m.slot + (i * Sh::NT + tid) * 16) = slot[i];
     }
 };
 
@@ -413,62 +342,9 @@ struct Values {
     }
 };
 
-// What a wavefront takes of a chunk's slot: registers, loaded a chunk ahead.
-// (slot null: nothing is read)
-template <bool SHARE>
+// What a wavefront takes of a chunk's slot, from the copy in LDS: T and G at its own
+// step and (th = 1) at step 0, g and e of the tokens of v, g of tokens 32 th + 16 x + c and of the last.
 struct Slot {
-    bf8 t_[2][3], tx_[2][3];   // T: its own step, and (th = 1; else unused) step 0
-    bf8 g_[2][2], gx_[2][2];   // G likewise
-    f32x4 d_[2], e_[2];        // g and e of the tokens of v
-    float dn_[2], all_;        // g of tokens 32 th + 16 x + c; of the last
-    uint32_t odd_;
-    __device__ __forceinline__ void load_decays(const uint8_t *slot, int th, int lane) {
-        const auto ws = make_rsrc(slot, slot ? kSlot : 0);
-        const uint32_t o = (32 * th + 4 * (lane >> 4)) * 4, on = (32 * th + (lane & 15)) * 4, s = kTBytes + kGBytes;
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-            d_[x] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(ws, o + 64 * x, s, 0));
-            e_[x] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(ws, o + 4 * kQ + 64 * x, s, 0));
-            dn_[x] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(ws, on + 64 * x, s, 0));
-        }
-        all_ = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(ws, 4 * (kQ - 1), s, 0));
-        odd_ = __builtin_amdgcn_raw_buffer_load_b32(ws, 2 * 4 * kQ, s, 0);
-    }
-    __device__ __forceinline__ void load_t(const uint8_t *slot, int th, int lane) {
-        const auto ws = make_rsrc(slot, slot ? kSlot : 0), wx = make_rsrc(slot, slot && th ? kSlot : 0);
-        const uint32_t o = lane * 16, s = 6 * kFrag * th;
-#pragma unroll
-        for (int x = 0; x < 2; ++x)
-#pragma unroll
-            for (int z = 0; z < 3; ++z) {
-                t_[x][z] = __builtin_bit_cast(bf8, __builtin_amdgcn_raw_buffer_load_b128(ws, o, s + (3 * x + z) * kFrag, 0));
-                tx_[x][z] = __builtin_bit_cast(bf8, __builtin_amdgcn_raw_buffer_load_b128(wx, o, (12 + 3 * x + z) * kFrag, 0));
-            }
-    }
-    __device__ __forceinline__ void load_g(const uint8_t *slot, int th, int lane) {
-        const auto ws = make_rsrc(slot, slot ? kSlot : 0), wx = make_rsrc(slot, slot && th ? kSlot : 0);
-        const uint32_t o = lane * 16, s = kTBytes + 4 * kFrag * th;
-#pragma unroll
-        for (int x = 0; x < 2; ++x)
-#pragma unroll
-            for (int z = 0; z < 2; ++z) {
-                g_[x][z] = __builtin_bit_cast(bf8, __builtin_amdgcn_raw_buffer_load_b128(ws, o, s + (2 * x + z) * kFrag, 0));
-                gx_[x][z] = __builtin_bit_cast(bf8, __builtin_amdgcn_raw_buffer_load_b128(wx, o, kTBytes + (8 + 2 * x + z) * kFrag, 0));
-            }
-    }
-    __device__ __forceinline__ bf8 t(int x, int z) const { return t_[x][z]; }
-    __device__ __forceinline__ bf8 tx(int x, int z) const { return tx_[x][z]; }
-    __device__ __forceinline__ bf8 g(int x, int z) const { return g_[x][z]; }
-    __device__ __forceinline__ bf8 gx(int x, int z) const { return gx_[x][z]; }
-    __device__ __forceinline__ f32x4 d(int x) const { return d_[x]; }
-    __device__ __forceinline__ f32x4 e(int x) const { return e_[x]; }
-    __device__ __forceinline__ float dn(int x) const { return dn_[x]; }
-    __device__ __forceinline__ float all() const { return all_; }
-    __device__ __forceinline__ uint32_t odd() const { return odd_; }
-};
-// The same from the workgroup's copy in LDS.
-template <>
-struct Slot<true> {
     const uint8_t *frags, *decay, *natural, *base;
     int step;
     __device__ __forceinline__ void init(const uint8_t *m, int th, int lane) {
@@ -489,58 +365,25 @@ struct Slot<true> {
     __device__ __forceinline__ uint32_t odd() const { return *reinterpret_cast<const uint32_t *>(base + kImage); }
 };
 
-__device__ __forceinline__ void put_frag(uint8_t *to, bf8 x) { *reinterpret_cast<u32x4 *>(to) = __builtin_bit_cast(u32x4, x); }
-
-// A chunk token by token, by a wavefront for 16 columns.  The state stays in
-// s_out, S this lane's first place there (columns 16 t + 4 lg ..).
-template <int P, int N, int CW>
-__device__ __forceinline__ void by_token(const ScanArgs &s, const Tile<P, N, CW> &m, float *S, int t0, int n, int h, int p, int lane) {
-    using Sh = Shape<P, N, CW>;
-    const int lg = lane >> 4;
-#pragma unroll 1
-    for (int t = 0; t < n; ++t) {
-        const float al = s.a[(size_t)(t0 + t) * s.H + h], be = s.dt[(size_t)(t0 + t) * s.H + h];
-        const size_t o = ((size_t)(t0 + t) * s.H + h) * P + p;
-        const uint8_t *k = m.k + t * Sh::QB, *q = m.q + t * Sh::QB;
-        const int f = turn(t) << 3;
-        float dot = 0.f, y = 0.f;
-#pragma unroll 1
-        for (int i = 0; i < N / 4; ++i) dot = fmaf(S[16 * (i / 4) + i % 4], load_io1<true>(k + ((32 * (i / 4) + 8 * lg) ^ f), i % 4), dot);
-        dot += __shfl_xor(dot, 16);
-        dot += __shfl_xor(dot, 32);
-        const float u = be * fmaf(-al, dot, load_io1<true>(s.v, o));
-#pragma unroll 1
-        for (int i = 0; i < N / 4; ++i) {
-            const float x = fmaf(u, load_io1<true>(k + ((32 * (i / 4) + 8 * lg) ^ f), i % 4), al * S[16 * (i / 4) + i % 4]);
-            S[16 * (i / 4) + i % 4] = x;
-            y = fmaf(x, load_io1<true>(q + ((32 * (i / 4) + 8 * lg) ^ f), i % 4), y);
-        }
-        y += __shfl_xor(y, 16);
-        y += __shfl_xor(y, 32);
-        if (lg == 0) static_cast<uint16_t *>(s.y)[o] = (uint16_t)f32_to_bf16_bits(y);
-    }
-}
-
 // Two wavefronts take 16 columns: th = 0, 1 have the chunk's tokens 32 th ..
 // in R, U and y, and the state's rows N / 2 th .. in S^T.  The system is lower
 // triangular, so that th = 0 needs nothing of th = 1 for R, U and y.
-template <int P, int N, int CW>
-__global__ __launch_bounds__((Shape<P, N, CW>::NT), CW == 1 ? 1 : 2) void delta_mx_kernel(ScanArgs s) {
-    using Sh = Shape<P, N, CW>;
+template <int P, int N>
+__global__ __launch_bounds__((Shape<P, N>::NT), 2) void delta_mx_kernel(ScanArgs s) {
+    using Sh = Shape<P, N>;
     constexpr int KN = Sh::KN, KH = Sh::KH, QB = Sh::QB;
-    __shared__ Tile<P, N, CW> m;
+    __shared__ Tile<P, N> m;
 
     Place place;
     if (!find_place(s, 1, &place, Sh::CB)) return;
     const int h = place.h, b = place.b, g = place.g;
     const Span sp = find_span(s, b, 0);
     const int tid = threadIdx.x, lane = tid & 63, c = lane & 15, lg = lane >> 4;
-    const int w = __builtin_amdgcn_readfirstlane(tid >> 6), th = w & 1, pair = Sh::SHARE ? w >> 1 : 0;
-    const bool makes_y = !Sh::SHARE && w > 1;   // and does not have S^T
+    const int w = __builtin_amdgcn_readfirstlane(tid >> 6), th = w & 1, pair = w >> 1;
     if (s.chunk0 == 0 && h == 0 && place.cb == 0 && !sp.run && tid == 0) raise_seq_error(s.err, b, REPLAY_SEQERR_BAD_RANGE);
     const int from = s.chunk0 * kQ, upto = sp.n < from + s.window * kQ ? sp.n : from + s.window * kQ;
     if (!sp.run || (from > 0 && from >= sp.n)) return;
-    Exchange<KN, Sh::SHARE> &ex = m.x[pair];
+    Exchange<KN> &ex = m.x[pair];
     uint8_t &odd_chunk = m.odd[pair];   // of the two wavefronts'
 
     const int p0 = Sh::PC * place.cb + 16 * pair;   // the wavefront's columns
@@ -570,9 +413,9 @@ __global__ __launch_bounds__((Shape<P, N, CW>::NT), CW == 1 ? 1 : 2) void delta_
             for (int z = 0; z < 3; ++z) put_frag(to + (3 * i + z) * kFrag, part[z]);
         }
     };
-    if (!makes_y) get_state(in ? in + (bh * P + p0 + c) * N + 4 * lg : nullptr);
+    get_state(in ? in + (bh * P + p0 + c) * N + 4 * lg : nullptr);
     if (upto == from) {   // no tokens: the state as it is
-        if (!makes_y) put_state();
+        put_state();
         return;
     }
     const uint32_t rv = (uint32_t)s.H * P * 2, rqk = (uint32_t)s.G * QB;
@@ -597,86 +440,12 @@ __global__ __launch_bounds__((Shape<P, N, CW>::NT), CW == 1 ? 1 : 2) void delta_
     };
     const uint8_t *const xl = reinterpret_cast<const uint8_t *>(&ex) + 16 * lane;
     constexpr int kE = KN * 3 * kFrag, kR = kE + 6 * kFrag, kU = kR + 3 * kFrag;       // places in Exchange
-    Ahead<P, N, CW> ahead;
+    Ahead<P, N> ahead;
     Values val;
-    Slot<Sh::SHARE> my;
+    Slot my;
     ahead.load(kp, qp, rqk, upto - from, slot);
-    // y^T, rows p = 4 lg + r, column token 32 th + 16 x + c: a half of U's tokens by G, then the store
-    auto add_corrections = [&](acc4 *y, const bf8 *up, const bf8 *ux) {
-        if (th)
-#pragma unroll
-            for (int z = 2; z >= 0; --z)
-#pragma unroll
-                for (int x = 0; x < 2; ++x) y[x] = mma16(ux[z == 2], my.gx(x, z == 1), y[x]);
-#pragma unroll
-        for (int z = 2; z >= 0; --z)
-#pragma unroll
-            for (int x = 0; x < 2; ++x) y[x] = mma16(up[z == 2], my.g(x, z == 1), y[x]);
-    };
-    auto store_y = [&](const acc4 *y, int n) {
-        const auto ys = make_rsrc(yp, (uint32_t)(n - 1) * rv + 32);
-#pragma unroll
-        for (int x = 0; x < 2; ++x)
-            __builtin_amdgcn_raw_buffer_store_b64(
-                u32x2{f32x2_to_bf16_pair(y[x][0], y[x][1]), f32x2_to_bf16_pair(y[x][2], y[x][3])}, ys, yo, 16 * x * rv, 0);
-    };
-    if constexpr (!Sh::SHARE) {
-        if (makes_y) {   // the same barriers as in the loop below
-            my.load_decays(slot, th, lane);
-            my.load_g(slot, th, lane);
-            ahead.store(m);
-            for (int done = from; done < upto; done += kQ) {
-                const int n = sp.n - done < kQ ? sp.n - done : kQ, left = upto - done - kQ;
-                lds_barrier();   // q and the operands of S^T
-                kp += (size_t)kQ * rqk;
-                qp += (size_t)kQ * rqk;
-                slot += next_slot;
-                ahead.load(kp, qp, rqk, left, slot);
-                const uint8_t *const next = left > 0 ? slot : nullptr;
-                acc4 y[2];
-#pragma unroll
-                for (int st = 0; st < KN; ++st) {
-                    bf8 q[2];
-#pragma unroll
-                    for (int x = 0; x < 2; ++x) q[x] = operand(m.q, x, st);
-#pragma unroll
-                    for (int z = 1; z >= 0; --z) {
-                        const bf8 p = frag16(xl + (3 * st + z) * kFrag);
-#pragma unroll
-                        for (int x = 0; x < 2; ++x) y[x] = mma16(p, q[x], st == 0 && z == 1 ? acc4{0.f, 0.f, 0.f, 0.f} : y[x]);
-                    }
-                }
-#pragma unroll
-                for (int x = 0; x < 2; ++x) y[x] *= my.dn(x);
-                lds_barrier();   // (R of the first tokens)
-                const bool odd = odd_chunk != 0;
-                lds_barrier();   // U
-                if (!odd) {
-                    bf8 up[2], ux[2];
-#pragma unroll
-                    for (int z = 0; z < 2; ++z) {
-                        up[z] = frag16(xl + kU + (2 * th + z) * kFrag);
-                        ux[z] = frag16(xl + kU + z * kFrag);
-                    }
-                    add_corrections(y, up, ux);
-                    store_y(y, n);
-                }
-                yp += (size_t)kQ * rv;
-                my.load_decays(next, th, lane);
-                my.load_g(next, th, lane);
-                lds_barrier();   // k, q and what was handed over are read to their end
-                ahead.store(m);
-            }
-            return;
-        }
-    }
     val.load(vp, rv, sp.n - from < kQ ? sp.n - from : kQ, vo);
-    if constexpr (Sh::SHARE) {
-        my.init(m.slot, th, lane);
-    } else {
-        my.load_decays(slot, th, lane);
-        my.load_t(slot, th, lane);
-    }
+    my.init(m.slot, th, lane);
     hand_state();
     if (th == 0 && lane == 0) odd_chunk = 0;
     ahead.store(m);
@@ -688,9 +457,8 @@ __global__ __launch_bounds__((Shape<P, N, CW>::NT), CW == 1 ? 1 : 2) void delta_
         vp += (size_t)kQ * rv;
         slot += next_slot;
         ahead.load(kp, qp, rqk, left, slot);
-        [[maybe_unused]] const uint8_t *const next = left > 0 ? slot : nullptr;
-        // K S^T, rows token 32 th + 16 x + 4 lg + r, column c.  S Q^T, where it is
-        // not another pair's, comes behind U: here all wavefronts of a full CU would
+        // K S^T, rows token 32 th + 16 x + 4 lg + r, column c.  S Q^T, rows p = 4
+        // lg + r, column token 32 th + 16 x + c, comes behind U: here all wavefronts would
         // read k, q and S at once.
         acc4 ks[2], y[2];
         bf8 part[KN][2];   // S's first two parts, kept for S Q^T
@@ -702,25 +470,11 @@ __global__ __launch_bounds__((Shape<P, N, CW>::NT), CW == 1 ? 1 : 2) void delta_
 #pragma unroll
             for (int z = 2; z >= 0; --z) {
                 const bf8 p = frag16(xl + (3 * st + z) * kFrag);
-                if (Sh::SHARE && z < 2) part[st][z] = p;
+                if (z < 2) part[st][z] = p;
 #pragma unroll
                 for (int x = 0; x < 2; ++x) ks[x] = mma16(k[x], p, st == 0 && z == 2 ? acc4{0.f, 0.f, 0.f, 0.f} : ks[x]);
             }
         }
-        auto read_state = [&] {
-#pragma unroll
-            for (int st = 0; st < KN; ++st) {
-                bf8 q[2];
-#pragma unroll
-                for (int x = 0; x < 2; ++x) q[x] = operand(m.q, x, st);
-#pragma unroll
-                for (int z = 1; z >= 0; --z)
-#pragma unroll
-                    for (int x = 0; x < 2; ++x) y[x] = mma16(part[st][z], q[x], st == 0 && z == 1 ? acc4{0.f, 0.f, 0.f, 0.f} : y[x]);
-            }
-#pragma unroll
-            for (int x = 0; x < 2; ++x) y[x] *= my.dn(x);
-        };
         // (0 v is a NaN where v is no number)
         float none = my.odd() ? __builtin_nanf("") : 0.f;
 #pragma unroll
@@ -762,33 +516,52 @@ __global__ __launch_bounds__((Shape<P, N, CW>::NT), CW == 1 ? 1 : 2) void delta_
 #pragma unroll
                 for (int x = 0; x < 2; ++x) u[x] = mma16(my.t(x, a[z]), rp[o[z]], u[x]);
             split<2>(u[0], u[1], up);
-            if (th == 0 || !Sh::SHARE)
+            if (th == 0)
 #pragma unroll
-                for (int z = 0; z < 2; ++z) put_frag(ex.u[Sh::SHARE ? 0 : th][z] + 16 * lane, up[z]);
+                for (int z = 0; z < 2; ++z) put_frag(ex.u[z] + 16 * lane, up[z]);
 #pragma unroll
             for (int x = 0; x < 2; ++x) u[x] *= my.e(x);
             split<3>(u[0], u[1], ep);
 #pragma unroll
             for (int z = 0; z < 3; ++z) put_frag(ex.e[th][z] + 16 * lane, ep[z]);
-            if constexpr (Sh::SHARE) read_state();
+#pragma unroll
+            for (int st = 0; st < KN; ++st) {
+                bf8 q[2];
+#pragma unroll
+                for (int x = 0; x < 2; ++x) q[x] = operand(m.q, x, st);
+#pragma unroll
+                for (int z = 1; z >= 0; --z)
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) y[x] = mma16(part[st][z], q[x], st == 0 && z == 1 ? acc4{0.f, 0.f, 0.f, 0.f} : y[x]);
+            }
+#pragma unroll
+            for (int x = 0; x < 2; ++x) y[x] *= my.dn(x);
         } else {
             put_state();
             __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup");
         }
         const float all = my.all();   // (before the slot's next chunk is loaded)
-        if constexpr (!Sh::SHARE) {
-            my.load_decays(next, th, lane);
-            my.load_t(next, th, lane);
-        }
         lds_barrier();   // U of the first tokens, e U of all
         if (!odd) {
-            if constexpr (Sh::SHARE) {
+            // y^T: + U^T G^T
+            if (th) {
                 bf8 ux[2];
 #pragma unroll
                 for (int z = 0; z < 2; ++z) ux[z] = frag16(xl + kU + z * kFrag);
-                add_corrections(y, up, ux);
-                store_y(y, n);
+#pragma unroll
+                for (int z = 2; z >= 0; --z)
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) y[x] = mma16(ux[z == 2], my.gx(x, z == 1), y[x]);
             }
+#pragma unroll
+            for (int z = 2; z >= 0; --z)
+#pragma unroll
+                for (int x = 0; x < 2; ++x) y[x] = mma16(up[z == 2], my.g(x, z == 1), y[x]);
+            const auto ys = make_rsrc(yp, (uint32_t)(n - 1) * rv + 32);
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+                __builtin_amdgcn_raw_buffer_store_b64(
+                    u32x2{f32x2_to_bf16_pair(y[x][0], y[x][1]), f32x2_to_bf16_pair(y[x][2], y[x][3])}, ys, yo, 16 * x * rv, 0);
             // S^T <- (whole decay) S^T + K^T (e U), the wavefront's own tokens first
             bf8 ox[3];
 #pragma unroll
@@ -813,7 +586,7 @@ __global__ __launch_bounds__((Shape<P, N, CW>::NT), CW == 1 ? 1 : 2) void delta_
             hand_state();
         } else if (th == 0) {
             __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup");
-            by_token<P, N, CW>(s, m, state, sp.t0 + done, n, h, p0 + c, lane);
+            by_token<P, N>(s, m.k, m.q, state, sp.t0 + done, n, h, p0 + c, lane);
             __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup");
         }
         yp += (size_t)kQ * rv;
@@ -829,10 +602,10 @@ __global__ __launch_bounds__((Shape<P, N, CW>::NT), CW == 1 ? 1 : 2) void delta_
     put_state();
 }
 
-template <int P, int N, int CW>
+template <int P, int N>
 hipError_t launch_chain(const ScanArgs &a, hipStream_t s) {
-    using Sh = Shape<P, N, CW>;
-    delta_mx_kernel<P, N, CW><<<scan_blocks(a, 1, Sh::CB), Sh::NT, 0, s>>>(a);
+    using Sh = Shape<P, N>;
+    delta_mx_kernel<P, N><<<scan_blocks(a, 1, Sh::CB), Sh::NT, 0, s>>>(a);
     return hipGetLastError();
 }
 
@@ -847,11 +620,11 @@ hipError_t launch_pn(ScanArgs a, hipStream_t s) {
             delta_prep_kernel<N, 1><<<(unsigned)units, kPrepNT, 0, s>>>(a);
         hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
-        // With 16 columns a workgroup reads k, q and T four times as often, but there are
-        // four times as many to keep the card busy.  2048 tokens, 64 columns of a
-        // head counted as one: 64 of them 110 us against 152 (four shares of 16), 128: 141
-        // and 160, 192: 271 and 200, 512: 267 and 203.
-        e = (int64_t)a.B * a.H * P / 64 > 128 ? launch_chain<P, N, 4>(a, s) : launch_chain<P, N, 1>(a, s);
+        // delta_few.hip's workgroups of 16 columns read k, q and T four times as often,
+        // but there are four times as many to keep the card busy.  2048 tokens, 64
+        // columns of a head counted as one, state of 128 columns: 128 of them 131 us there,
+        // 160 here; 192: 207 and 200; state of 64: 128 of them 109 and 143, 192: 193 and 171.
+        e = (int64_t)a.B * a.H * P / 64 > 128 ? launch_chain<P, N>(a, s) : launch_delta_few(P, N, a, s);
         if (e != hipSuccess) return e;
     }
     return hipSuccess;
