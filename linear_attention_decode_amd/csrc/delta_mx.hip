@@ -11,9 +11,9 @@
 // columns: each has half of a chunk's tokens, and half of S^T's rows, which stay in
 // its accumulators; where heads are fewer still, delta_few.hip has more of them.
 // What bounds it: the chain of a chunk's steps, four barriers apart.  Sixteen
-// ragged sequences of 15013 tokens (32 heads of 128 x 128): 108 us for T and G, 329 for
+// ragged sequences of 15013 tokens (32 heads of 128 x 128): 88 us for T and G, 329 for
 // the chunks, eight wavefronts a CU that wait for LDS, for the matrix instructions
-// and for each other in turn; one of 8192 tokens 55, and 255 in delta_few.hip.  The
+// and for each other in turn; one of 8192 tokens 44, and 255 in delta_few.hip.  The
 // float32 kernel takes 889 and 3410 us.
 //
 // What bf16 operands leave out: k and q are bf16 as they are; S, R, T and e U
@@ -88,7 +88,7 @@ __device__ __forceinline__ void invert_corner(float (*m)[kQ + 4], int r0, int j,
             for (int r = 0; r < 4; ++r) o[i] = mma4(t[r], x[k][r], o[i]);
         }
     }
-    if constexpr (TL > 1) __syncthreads();   // A10 is read by both wavefronts
+    if constexpr (TL > 1) lds_barrier();   // A10 is read by both wavefronts
 #pragma unroll
     for (int i = 0; i < TL; ++i)
 #pragma unroll
@@ -121,8 +121,7 @@ __device__ __forceinline__ f32x4 decays_of(const Decays &d, int ti, int tj, int 
 
 // A workgroup makes a chunk of HP heads of a group, which share k . k and k . q.  Bound
 // by its own chain (products, decays, the inverse by blocks of 16, their products)
-// and by what it writes: 8192 tokens of 32 heads 55 us, of which a copy of the
-// 129 MB would take 27.
+// and by what it writes: 8192 tokens of 32 heads 44 us, 2.9 TB/s of the 129 MB.
 template <int N, int HP>
 __global__ __launch_bounds__(kPrepNT) void delta_prep_kernel(ScanArgs s) {
     __shared__ __align__(16) PrepTile m[HP];
@@ -136,30 +135,34 @@ __global__ __launch_bounds__(kPrepNT) void delta_prep_kernel(ScanArgs s) {
     const int n = sp.n - first < kQ ? sp.n - first : kQ, t0 = sp.t0 + first;
     uint8_t *out = reinterpret_cast<uint8_t *>(s.ws) + ((size_t)slot * s.H + h0) * kSlot;
 
-    // tiles (ti, tj) of K K^T and K Q^T, lane (column i = c, rows j = 4 lg + r):
-    // a wavefront's diagonal one, two below the diagonal, and for w < 2 one
-    // above it, G's zeros.  Rows past the chunk's tokens read zero.
-    const int ti[3] = {w, w == 0 ? 1 : (w == 1 ? 2 : 3), w == 0 ? 0 : (w == 1 ? 2 : (w == 2 ? 2 : 3))};
-    const int tj[3] = {w, w == 0 ? 0 : (w == 3 ? 1 : 0), w == 0 ? 1 : (w == 1 ? 1 : (w == 2 ? 3 : 2))};
-    acc4 kk[3], qk[3];
+    // tiles (ti, tj) of K K^T and K Q^T, lane (column i = c, rows j = 4 lg + r): a
+    // wavefront has one ti and the pairs of tj that make G's operands of it, so that
+    // it writes them whole (written half by half all takes 55 us for 44).  Two of the tiles lie above the
+    // diagonal, zeros of T and G.  Rows past the chunk's tokens read zero.
+    const int ti = w < 2 ? w + 2 : w - 2, pairs = w < 2 ? 2 : 1;
+    acc4 kk[4], qk[4];
     const uint32_t rqk = (uint32_t)s.G * N * 2;
     {
         const size_t base = (size_t)t0 * rqk + (size_t)g * N * 2;
-        const auto rk = make_rsrc(static_cast<const char *>(s.k) + base, (uint32_t)(n - 1) * rqk + N * 2);
-        const auto rq = make_rsrc(static_cast<const char *>(s.q) + base, (uint32_t)(n - 1) * rqk + N * 2);
+        const uint32_t bytes = (uint32_t)(n - 1) * rqk + N * 2;
+        const auto rk = make_rsrc(static_cast<const char *>(s.k) + base, bytes);
+        const auto rq = make_rsrc(static_cast<const char *>(s.q) + base, bytes);
         const uint32_t o = c * rqk + 16 * lg;
-        u32x4 kj[3][N / 32], ki[3][N / 32], qi[3][N / 32];
+        u32x4 kj[4][N / 32], ki[N / 32], qi[N / 32];
 #pragma unroll
-        for (int z = 0; z < 3; ++z)
+        for (int st = 0; st < N / 32; ++st) {
+            ki[st] = __builtin_amdgcn_raw_buffer_load_b128(rk, o, 16 * ti * rqk + 64 * st, 0);
+            qi[st] = __builtin_amdgcn_raw_buffer_load_b128(rq, o, 16 * ti * rqk + 64 * st, 0);
+        }
 #pragma unroll
-            for (int st = 0; st < N / 32; ++st) {
-                kj[z][st] = __builtin_amdgcn_raw_buffer_load_b128(rk, o, 16 * tj[z] * rqk + 64 * st, 0);
-                ki[z][st] = z == 0 ? kj[0][st] : __builtin_amdgcn_raw_buffer_load_b128(rk, o, 16 * ti[z] * rqk + 64 * st, 0);
-                qi[z][st] = __builtin_amdgcn_raw_buffer_load_b128(rq, o, 16 * ti[z] * rqk + 64 * st, 0);
-            }
-        if (w < HP) {   // the decays of head w, while the rows are on their way
-            const int h = h0 + w;
-            Decays &d = m[w].d;
+        for (int z = 0; z < 4; ++z) {
+            const auto rz = make_rsrc(static_cast<const char *>(s.k) + base, z <= ti ? bytes : 0);
+#pragma unroll
+            for (int st = 0; st < N / 32; ++st) kj[z][st] = __builtin_amdgcn_raw_buffer_load_b128(rz, o, 16 * z * rqk + 64 * st, 0);
+        }
+        if (w >= 4 - HP) {   // a head's decays, while the rows are on their way
+            const int y = w - (4 - HP), h = h0 + y;
+            Decays &d = m[y].d;
             float al = 1.f, be = 0.f;
             if (lane < n) {
                 al = s.a[(size_t)(t0 + lane) * s.H + h];
@@ -175,52 +178,62 @@ __global__ __launch_bounds__(kPrepNT) void delta_prep_kernel(ScanArgs s) {
             d.pre[lane] = pre;
             d.suf[lane] = suf;
             if (lane < 4) d.tot[lane] = lane == 0 ? p0 : (lane == 1 ? p1 : (lane == 2 ? p2 : p3));
-            float *decay = reinterpret_cast<float *>(out + (size_t)w * kSlot + kTBytes + kGBytes);
+            float *decay = reinterpret_cast<float *>(out + (size_t)y * kSlot + kTBytes + kGBytes);
             decay[lane] = ahead * pre;
             decay[kQ + lane] = suf * behind;
             const bool bad = __any(!(finite(al) && finite(be)));
-            if (lane == 0) odd[w] = bad;
+            if (lane == 0) odd[y] = bad;
         }
         bool bad = false;
 #pragma unroll
-        for (int z = 0; z < 3; ++z) {
+        for (int st = 0; st < N / 32; ++st)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) bad |= odd_pair(ki[st][r]);
+#pragma unroll
+        for (int z = 0; z < 4; ++z) {
             kk[z] = qk[z] = acc4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int st = 0; st < N / 32; ++st) {
-                kk[z] = mma16(__builtin_bit_cast(bf8, kj[z][st]), __builtin_bit_cast(bf8, ki[z][st]), kk[z]);
-                qk[z] = mma16(__builtin_bit_cast(bf8, kj[z][st]), __builtin_bit_cast(bf8, qi[z][st]), qk[z]);
-                if (z == 0)
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) bad |= odd_pair(ki[z][st][r]);
+                kk[z] = mma16(__builtin_bit_cast(bf8, kj[z][st]), __builtin_bit_cast(bf8, ki[st]), kk[z]);
+                qk[z] = mma16(__builtin_bit_cast(bf8, kj[z][st]), __builtin_bit_cast(bf8, qi[st]), qk[z]);
             }
         }
         bad = __any(bad);
-        __syncthreads();   // the decays
+        lds_barrier();   // the decays
         if (bad && lane < HP) odd[lane] = 1;
     }
 #pragma unroll
     for (int y = 0; y < HP; ++y) {
         uint8_t *to_head = out + (size_t)y * kSlot + kTBytes;
+        const int i = 16 * ti + c;
+        const float be = m[y].d.beta[i];
 #pragma unroll
-        for (int z = 0; z < 3; ++z) {
-            const int i = 16 * ti[z] + c, j0 = 16 * tj[z] + 4 * lg;
-            const bool below = ti[z] >= tj[z];
-            f32x4 D = {0.f, 0.f, 0.f, 0.f};
-            if (below) D = decays_of(m[y].d, ti[z], tj[z], c, lg);
-            const float be = m[y].d.beta[i];
-            f32x4 a, o;
+        for (int x = 0; x < 2; ++x) {
+            if (x == pairs) break;
+            u32x4 hi, lo;   // G's operand, upper and lower parts
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                a[r] = j0 + r < i ? be * (kk[z][r] * D[r]) : 0.f;
-                o[r] = j0 + r <= i ? qk[z][r] * D[r] : 0.f;
+            for (int half = 0; half < 2; ++half) {
+                const int z = 2 * x + half, j0 = 16 * z + 4 * lg;
+                f32x4 D = {0.f, 0.f, 0.f, 0.f};
+                if (z <= ti) D = decays_of(m[y].d, ti, z, c, lg);
+                f32x4 a, o;
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    a[r] = j0 + r < i ? be * (kk[z][r] * D[r]) : 0.f;
+                    o[r] = j0 + r <= i ? qk[z][r] * D[r] : 0.f;
+                }
+                *reinterpret_cast<f32x4 *>(&m[y].a[i][j0]) = a;   // (zeros above the diagonal are T's too)
+                hi[2 * half] = upper_pair(o[0], o[1]);
+                hi[2 * half + 1] = upper_pair(o[2], o[3]);
+                lo[2 * half] = lower_pair(o[0], o[1]);
+                lo[2 * half + 1] = lower_pair(o[2], o[3]);
             }
-            *reinterpret_cast<f32x4 *>(&m[y].a[i][j0]) = a;   // (zeros above the diagonal are T's too)
-            uint8_t *to = to_head + frag(ti[z], tj[z] >> 1) * 2 * kFrag + lane * 16 + (tj[z] & 1) * 8;
-            *reinterpret_cast<u32x2 *>(to) = u32x2{upper_pair(o[0], o[1]), upper_pair(o[2], o[3])};
-            *reinterpret_cast<u32x2 *>(to + kFrag) = u32x2{lower_pair(o[0], o[1]), lower_pair(o[2], o[3])};
+            uint8_t *to = to_head + frag(ti, x) * 2 * kFrag + lane * 16;
+            *reinterpret_cast<u32x4 *>(to) = hi;
+            *reinterpret_cast<u32x4 *>(to + kFrag) = lo;
         }
     }
-    __syncthreads();
+    lds_barrier();
     if (w < HP) {
         // the diagonal blocks by substitution: lane (block lg, column c) a column
         float(*a)[kQ + 4] = m[w].a;
@@ -241,15 +254,15 @@ __global__ __launch_bounds__(kPrepNT) void delta_prep_kernel(ScanArgs s) {
 #pragma unroll
         for (int i = 0; i < 16; ++i) a[b0 + i][b0 + c] = x[i];
     }
-    __syncthreads();
+    lds_barrier();
     if (w < 2 * HP) invert_corner<16>(m[w >> 1].a, 32 * (w & 1), 0, lane);
-    __syncthreads();
+    lds_barrier();
     if (w < 2 * HP) {
         invert_corner<32>(m[w >> 1].a, 0, w & 1, lane);
     } else {
-        __syncthreads();   // the one in there
+        lds_barrier();   // the one in there
     }
-    __syncthreads();
+    lds_barrier();
     for (int x = tid; x < HP * kFrags * 64; x += kPrepNT) {
         const int y = x / (kFrags * 64), f = x / 64 % kFrags, tile = f < 4 ? f : f - 2, step = f < 4 ? tile >> 1 : 0;
         const int l = x & 63, i = 16 * tile + (l & 15), j0 = 32 * step + 4 * (l >> 4);
