@@ -204,7 +204,8 @@ __device__ __forceinline__ bf16x8_t cols8(const float *rows, int second, int str
 }
 
 // S0 x^T over 16 rows and 16 queries in PARTS bf16 numbers, on v_mfma_f32_16x16x32_bf16:
-// bf16, e4m3 (unscaled) and MX FP4 values are bf16 numbers, and every product is exact.
+// bf16, e4m3 (unscaled) and MX FP4 values are bf16 numbers, and every product is exact
+// (an infinite one times a part that is 0 is a NaN).
 // At 128 columns 12 products (16 cycles each) take the place of 32 of 32 cycles.
 template <int PARTS, int P, int N, int ST>
 __device__ __forceinline__ f32x4 dot_parts(const WideRows<P, N, ST> &rows, const uint16_t *x, int part, int stride, int lane,
@@ -456,19 +457,29 @@ __global__ __launch_bounds__((TreeShape<P, N>::NT), DELTA ? (IOB ? 4 : 3) : 1) v
             }
         const float all = __shfl(pre, LP - 1);
         suf = __shfl_down(suf, 1);
-        // up from node `lane`, the nearest first: D[w][j] for the j on the way, and who they are
+        // up from node `lane`, the nearest first, two steps a turn: D[w][j] for the
+        // j on the way, and who they are
         uint64_t anc = 0;
         float path = 1.f;
         int x = lane < n ? lane : -1;
+        const int up = tree.parent < 0 ? 0 : tree.parent;
+        const float na2 = __shfl(na, up);
+        const int up2 = __shfl(tree.parent, up);
         while (__any(x >= 0)) {
-            const int from = x < 0 ? 0 : x;
-            const float f = __shfl(na, from);
-            const int u = __shfl(tree.parent, from);
+            const int at_x = x < 0 ? 0 : x;
+            const float f = __shfl(na, at_x), f2 = __shfl(na2, at_x);
+            const int u = __shfl(tree.parent, at_x), u2 = __shfl(up2, at_x);
             if (x >= 0) {
                 s_D[lane * WP + x] = path;
                 path *= f;
                 anc |= 1ull << x;
-                x = u;
+                x = -1;
+                if (u >= 0) {
+                    s_D[lane * WP + u] = path;
+                    path *= f2;
+                    anc |= 1ull << u;
+                    x = u2;
+                }
             }
         }
         if (lane < kMaxRing) {
