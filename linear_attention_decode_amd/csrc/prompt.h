@@ -64,6 +64,7 @@ struct ScanArgs {
     // the gated delta rule's bf16 kernels: chunks of a sequence in the
     // workspace at a time, and the first of them
     int32_t window, chunk0;
+    int32_t share;                 // log2 of the XCDs that share a group's workgroups
 };
 
 // Sampling (sample.hip).

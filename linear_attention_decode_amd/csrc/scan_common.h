@@ -17,13 +17,17 @@ constexpr int kScanChunk = 64;   // segments are whole chunks of either kernel
 // each, ranked by 64 comparisons): the last workgroups to start are then the
 // shortest.  False for the places that fill up the last round.
 // CB workgroups share a head, each with its columns of v: block cb of them.
+// 2^a.share XCDs share a group's workgroups.
 struct Place {
     int b, seg, h, g, cb;
 };
 __device__ __forceinline__ bool find_place(const ScanArgs &a, int HB, Place *p, int CB = 1) {
-    const int per = a.H / a.G / HB * CB, x = blockIdx.x & 7, j = blockIdx.x >> 3;
-    const int64_t unit = (int64_t)(j / per) * 8 + x;
-    if (unit >= (int64_t)a.B * a.nseg * a.G) return false;
+    const int per = a.H / a.G / HB * CB, others = (1 << a.share) - 1, part = (per + others) >> a.share;
+    const int x = blockIdx.x & 7, j = blockIdx.x >> 3;
+    int64_t unit = (int64_t)(j / part) * 8 + x;
+    const int i = ((int)unit & others) * part + j % part;   // of the group's workgroups
+    unit >>= a.share;
+    if (unit >= (int64_t)a.B * a.nseg * a.G || i >= per) return false;
     p->g = (int)(unit % a.G);
     p->seg = (int)(unit / a.G % a.nseg);
     p->b = (int)(unit / a.G / a.nseg);
@@ -37,13 +41,13 @@ __device__ __forceinline__ bool find_place(const ScanArgs &a, int HB, Place *p, 
         }
         p->b = __builtin_ctzll(__ballot(lane < a.B && rank == p->b));
     }
-    p->h = p->g * (a.H / a.G) + j % per / CB * HB;
-    p->cb = j % per % CB;
+    p->h = p->g * (a.H / a.G) + i / CB * HB;
+    p->cb = i % CB;
     return true;
 }
 inline unsigned scan_blocks(const ScanArgs &a, int HB, int CB = 1) {
-    const int64_t units = (int64_t)a.B * a.nseg * a.G;
-    return (unsigned)((units + 7) / 8 * 8 * (a.H / a.G / HB * CB));
+    const int64_t units = (int64_t)a.B * a.nseg * a.G << a.share;
+    return (unsigned)((units + 7) / 8 * 8 * ((a.H / a.G / HB * CB + (1 << a.share) - 1) >> a.share));
 }
 
 // Where a workgroup's tokens are.

@@ -48,3 +48,15 @@ def test_one_long_prompt_is_its_halves(P, N):
         assert torch.equal(q.y, y[a:b])
         whole = q.s_out
     assert torch.equal(whole, s) and bool(torch.isfinite(s).all()) and p.err.cpu().eq(0).all()
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("lens,H,G,P,N", [([70], 7, 1, 64, 64), ([33, 1, 100], 14, 2, 64, 128), ([64, 65, 3, 0, 130], 26, 2, 64, 64),
+                                          ([40, 90], 69, 3, 64, 128), ([129], 36, 1, 128, 128), ([5, 66, 17], 20, 1, 16, 16)])
+def test_few_groups(io, lens, H, G, P, N):
+    """Groups that several XCDs share, in parts that their heads do not fill."""
+    gu.note(f"delta scan, few groups {io} {lens} {H} {G} {P} {N}")
+    p = Prompts(lens, H, G, P, N, io, first=2, seed=H + P)
+    p.run()
+    torch.cuda.synchronize()
+    p.check()
