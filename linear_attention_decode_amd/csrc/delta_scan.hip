@@ -249,16 +249,16 @@ __global__ __launch_bounds__((Shape<P, N>::NT)) void delta_scan_kernel(ScanArgs 
     int at = 0;
     while (at < sp.n) {
         int n = sp.n - at < kQ ? sp.n - at : kQ;
-        __syncthreads();   // the last chunk is read to its end
+        lds_barrier();   // the last chunk is read to its end
         if (tid == 0) m.cut = kQ;
-        __syncthreads();
+        lds_barrier();
         ahead.store(m, n);
-        __syncthreads();
+        lds_barrier();
         if (m.cut < n) {   // uniform
             n = m.cut;
-            __syncthreads();
+            lds_barrier();
             ahead.store(m, n);
-            __syncthreads();
+            lds_barrier();
         }
         const int next = at + n;
         if (next < sp.n) ahead.load(s, sp.t0 + next, sp.n - next, h, g);
@@ -268,7 +268,7 @@ __global__ __launch_bounds__((Shape<P, N>::NT)) void delta_scan_kernel(ScanArgs 
             const int y = x % 3;
             weigh(m, y == 0 ? 0 : 1, y == 2 ? 1 : 0, x < 3, c, lg);
         }
-        __syncthreads();
+        lds_barrier();
         if (w == NW - 1) invert(m, lane);
         // K S^T and Q S^T, rows i = 16 ti + 4 lg + r, column p = c of the wavefront's 16
         acc4 ks[2], qs[2];
@@ -292,7 +292,7 @@ __global__ __launch_bounds__((Shape<P, N>::NT)) void delta_scan_kernel(ScanArgs 
                 qs[ti][r] *= m.d0[i];
             }
         }
-        __syncthreads();   // the inverse
+        lds_barrier();   // the inverse
         acc4 u[2];
 #pragma unroll
         for (int ti = 0; ti < 2; ++ti) {

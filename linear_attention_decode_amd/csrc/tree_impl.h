@@ -61,13 +61,13 @@ struct TreeShape {
     static constexpr int TILE = WideTile<P, N, ST>::COAL ? NW * 16 * WideTile<P, N, ST>::TROW : 0;
 };
 
-// LDS, in floats: weights C [WP][CS] and decays D [WP][WP]; for the gated delta rule
-// also A^T [ES][CS], the diagonal blocks' inverses [ES][16] (transposed) and the
-// ring's own decays [LP][LP].  The queries (XF a row) lie behind C and D, or for the
-// gated delta rule in place of what is not needed any more when they are formed: all
-// but C, or all (`parts`: C then goes on as [3][WP][CB] bf16, which lie in place of D
-// and the ring's decays).  Then the gated delta rule's keys [ES][KS], whose place
-// the tile of S0 takes on its way into operands (`tile` floats).
+// LDS, in floats.  Mamba-2: weights C [WP][CS], queries (XF a row), decays D
+// [WP][WP], whose place the tile of S0 takes on its way into operands (`tile`
+// floats).  The gated delta rule: C, D and also A^T [ES][CS], the diagonal blocks' inverses [ES][16] (transposed) and the
+// ring's own decays [LP][LP]; the queries lie in place of what is not needed any
+// more when they are formed, all but C, or all (`parts`: C then goes on as
+// [3][WP][CB] bf16, which lie in place of D and the ring's decays); then the keys
+// [ES][KS], whose place the tile takes.
 struct TreeLds {
     int WP, LP, ES, CS, CB, D, x, A, inv, rr, parts, k, total;
     __host__ __device__ TreeLds(int W, int L, bool delta, bool in_parts, int XF, int KS, int tile) {
@@ -77,18 +77,23 @@ struct TreeLds {
         CS = ES + 4;
         CB = (ES + 31) / 32 * 32 + 8;
         A = WP * CS;
-        inv = A + (delta ? ES * CS : 0);
-        parts = inv + (delta ? ES * 16 : 0);
+        inv = A + ES * CS;
+        parts = inv + ES * 16;
         const int queries = WP * XF;
-        x = in_parts ? 0 : delta ? A : A + WP * WP;
+        if (!delta) {
+            x = A;
+            k = D = rr = x + queries;
+            total = k + (WP * WP > tile ? WP * WP : tile);
+            return;
+        }
+        x = in_parts ? 0 : A;
         if (in_parts && queries > parts) parts = queries;
         D = parts;
         rr = D + WP * WP;
-        k = rr + (delta ? LP * LP : 0);
+        k = rr + LP * LP;
         if (in_parts && parts + 3 * WP * CB / 2 > k) k = parts + 3 * WP * CB / 2;
         if (x + queries > k) k = x + queries;
-        const int keys = delta ? ES * KS : 0;
-        total = k + (keys > tile ? keys : tile);
+        total = k + (ES * KS > tile ? ES * KS : tile);
     }
 };
 
