@@ -99,19 +99,7 @@ __device__ __forceinline__ void invert_corner(float (*m)[kQ + 4], int r0, int j,
 // + 4 lg + r): alpha_{j+1} ... alpha_i; nothing above the diagonal.
 __device__ __forceinline__ f32x4 decays_of(const Decays &d, int ti, int tj, int c, int lg) {
     const int i = 16 * ti + c, j0 = 16 * tj + 4 * lg;
-    if (ti == tj) {
-        // blocks of 4: alpha over those between j's and i, times what is behind j in its block
-        const f32x4 aa = *reinterpret_cast<const f32x4 *>(&d.alpha[j0]);
-        const float R = row_upto(c >= 4 * (lg + 1) ? d.alpha[i] : 1.f);
-        f32x4 D = {R, R, R, R};
-        float f = 1.f;
-#pragma unroll
-        for (int r = 2; r >= 0; --r) {
-            f = j0 + r + 1 <= i ? f * aa[r + 1] : 1.f;
-            D[r] *= f;
-        }
-        return D;
-    }
+    if (ti == tj) return diagonal_decays(&d.alpha[16 * ti], c, lg);
     // the nearest first: every product is one of consecutive tokens
     float p = d.pre[i];
     p *= ti - tj > 1 ? d.tot[(ti - 1) & 3] : 1.f;

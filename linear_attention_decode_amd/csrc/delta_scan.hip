@@ -48,7 +48,9 @@ __device__ __forceinline__ acc4 mma(float a, float b, acc4 c) {
 
 template <int P, int N>
 struct Shape {
-    static constexpr int NW = P / 16, NT = NW * 64;
+    // wavefronts with 16 columns of S^T each; where there is room, one more, which
+    // inverts while they multiply
+    static constexpr int NW = P / 16, ALL = NW <= 4 ? NW + 1 : NW, NT = ALL * 64;
     static constexpr int NR = N + kPad, PR = P + kPad, GR = kQ + kPad;   // LDS row strides
 };
 
@@ -149,42 +151,32 @@ struct Ahead {
     }
 };
 
-// G (A: false) or A, tile (ti, tj), transposed: rows j = 4 lg + r, column i = c
+// G and A, tile (ti, tj), transposed: rows j = 4 lg + r, column i = c
 template <int P, int N>
-__device__ __forceinline__ void weigh(Tile<P, N> &m, int ti, int tj, bool A, int c, int lg) {
-    acc4 d = {0.f, 0.f, 0.f, 0.f};
-    const float(*rows)[Shape<P, N>::NR] = A ? m.k : m.q;
+__device__ __forceinline__ void weigh(Tile<P, N> &m, int ti, int tj, int c, int lg) {
+    acc4 dg = {0.f, 0.f, 0.f, 0.f}, da = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int t = 0; t < N / 16; ++t) {
-        const f32x4 kk = *reinterpret_cast<const f32x4 *>(&m.k[16 * tj + c][16 * t + 4 * lg]);
-        const f32x4 qq = *reinterpret_cast<const f32x4 *>(&rows[16 * ti + c][16 * t + 4 * lg]);
+        const f32x4 kj = *reinterpret_cast<const f32x4 *>(&m.k[16 * tj + c][16 * t + 4 * lg]);
+        const f32x4 qi = *reinterpret_cast<const f32x4 *>(&m.q[16 * ti + c][16 * t + 4 * lg]);
+        const f32x4 ki = *reinterpret_cast<const f32x4 *>(&m.k[16 * ti + c][16 * t + 4 * lg]);
 #pragma unroll
-        for (int r = 0; r < 4; ++r) d = mma(kk[r], qq[r], d);
+        for (int r = 0; r < 4; ++r) {
+            da = mma(kj[r], ki[r], da);
+            dg = mma(kj[r], qi[r], dg);
+        }
     }
     const int i = 16 * ti + c, j0 = 16 * tj + 4 * lg;
-    f32x4 o;
-    if (ti != tj) {
-        const float p = m.pre[i];
+    const f32x4 D = ti != tj ? m.pre[i] * *reinterpret_cast<const f32x4 *>(&m.suf[j0]) : diagonal_decays(&m.alpha[16 * tj], c, lg);
+    const float be = m.beta[i];
+    f32x4 o, a;
 #pragma unroll
-        for (int r = 0; r < 4; ++r) o[r] = d[r] * (p * m.suf[j0 + r]);
-    } else {
-        // alpha_{j+1} ... alpha_i for this lane's four j, by one walk down from the tile's end
-        float p = 1.f;
-        f32x4 dec = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int jj = 15; jj >= 0; --jj) {
-            if (jj < 15) p = c > jj ? p * m.alpha[16 * tj + jj + 1] : 1.f;
-            if (lg == jj / 4) dec[jj & 3] = p;
-        }
-#pragma unroll
-        for (int r = 0; r < 4; ++r) o[r] = j0 + r <= i ? d[r] * dec[r] : 0.f;
+    for (int r = 0; r < 4; ++r) {
+        o[r] = j0 + r <= i ? dg[r] * D[r] : 0.f;
+        a[r] = j0 + r < i ? be * (da[r] * D[r]) : 0.f;
     }
-    if (A) {
-        const float b = m.beta[i];
-#pragma unroll
-        for (int r = 0; r < 4; ++r) o[r] = j0 + r < i ? o[r] * b : 0.f;
-    }
-    *reinterpret_cast<f32x4 *>(A ? &m.a[i][j0] : &m.g[i][j0]) = o;
+    *reinterpret_cast<f32x4 *>(&m.g[i][j0]) = o;
+    *reinterpret_cast<f32x4 *>(&m.a[i][j0]) = a;
 }
 
 // (I + A)^-1, by one wavefront: the diagonal blocks, lane (block, column c)
@@ -225,13 +217,13 @@ template <int P, int N, bool IOB>
 __global__ __launch_bounds__((Shape<P, N>::NT)) void delta_scan_kernel(ScanArgs s) {
     using Sh = Shape<P, N>;
     constexpr int NW = Sh::NW, TN = N / 16;
-    __shared__ Tile<P, N> m;
+    __shared__ __align__(16) Tile<P, N> m;
 
     Place place;
     if (!find_place(s, 1, &place)) return;
     const int h = place.h, b = place.b, g = place.g;
     const Span sp = find_span(s, b, 0);
-    const int tid = threadIdx.x, w = tid >> 6, lane = tid & 63, c = lane & 15, lg = lane >> 4;
+    const int tid = threadIdx.x, w = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, c = lane & 15, lg = lane >> 4;
     if (h == 0 && !sp.run && tid == 0) raise_seq_error(s.err, b, REPLAY_SEQERR_BAD_RANGE);
     if (!sp.run) return;
 
@@ -241,17 +233,16 @@ __global__ __launch_bounds__((Shape<P, N>::NT)) void delta_scan_kernel(ScanArgs 
 #pragma unroll
     for (int t = 0; t < TN; ++t) {
         S[t] = acc4{0.f, 0.f, 0.f, 0.f};
-        if (s.s_in) S[t] = *reinterpret_cast<const acc4 *>(s.s_in + bh * tile + row + 16 * t);
+        if (s.s_in && w < NW) S[t] = *reinterpret_cast<const acc4 *>(s.s_in + bh * tile + row + 16 * t);
     }
 
     Ahead<P, N, IOB> ahead;
     ahead.load(s, sp.t0, sp.n, h, g);
+    if (tid == 0) m.cut = kQ;
     int at = 0;
     while (at < sp.n) {
         int n = sp.n - at < kQ ? sp.n - at : kQ;
         lds_barrier();   // the last chunk is read to its end
-        if (tid == 0) m.cut = kQ;
-        lds_barrier();
         ahead.store(m, n);
         lds_barrier();
         if (m.cut < n) {   // uniform
@@ -263,13 +254,15 @@ __global__ __launch_bounds__((Shape<P, N>::NT)) void delta_scan_kernel(ScanArgs 
         const int next = at + n;
         if (next < sp.n) ahead.load(s, sp.t0 + next, sp.n - next, h, g);
 
-        // A's tiles first: the inverse waits for them
-        for (int x = w; x < 6; x += NW) {
-            const int y = x % 3;
-            weigh(m, y == 0 ? 0 : 1, y == 2 ? 1 : 0, x < 3, c, lg);
-        }
+        for (int x = w; x < 3; x += Sh::ALL) weigh(m, x == 0 ? 0 : 1, x == 2 ? 1 : 0, c, lg);
         lds_barrier();
-        if (w == NW - 1) invert(m, lane);
+        if (tid == 0) m.cut = kQ;   // (all have read it)
+        if (w == Sh::ALL - 1) invert(m, lane);
+        if (w >= NW) {
+            lds_barrier();   // the inverse
+            at = next;
+            continue;
+        }
         // K S^T and Q S^T, rows i = 16 ti + 4 lg + r, column p = c of the wavefront's 16
         acc4 ks[2], qs[2];
 #pragma unroll
@@ -340,6 +333,7 @@ __global__ __launch_bounds__((Shape<P, N>::NT)) void delta_scan_kernel(ScanArgs 
             }
         at = next;
     }
+    if (w >= NW) return;
 #pragma unroll
     for (int t = 0; t < TN; ++t) *reinterpret_cast<acc4 *>(s.s_out + bh * tile + row + 16 * t) = S[t];
 }

@@ -87,6 +87,21 @@ __device__ __forceinline__ float row_from(float x) {
     return x;
 }
 
+// alpha_{j+1} ... alpha_i of a tile of 16, lane (i = c, j = 4 lg + r), for j <= i:
+// alpha over the blocks of 4 between j's and i, times what is behind j in its own
+__device__ __forceinline__ f32x4 diagonal_decays(const float *alpha, int c, int lg) {
+    const f32x4 aa = *reinterpret_cast<const f32x4 *>(alpha + 4 * lg);
+    const float R = row_upto(c >= 4 * (lg + 1) ? alpha[c] : 1.f);
+    f32x4 D = {R, R, R, R};
+    float f = 1.f;
+#pragma unroll
+    for (int r = 2; r >= 0; --r) {
+        f = 4 * lg + r + 1 <= c ? f * aa[r + 1] : 1.f;
+        D[r] *= f;
+    }
+    return D;
+}
+
 __device__ __forceinline__ float lane_value(float x, int lane) {
     return __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(x), lane));
 }
