@@ -23,9 +23,13 @@
 // product before left in accumulators, (column l % 16, rows 4 (l / 16) + r):
 // neither S nor U passes through LDS.
 //
-// Bound by the chain of a chunk's steps, one workgroup's behind the other: three
-// prompts of 97 tokens in all, 4 heads of 64 x 128, 26 us for 2 chunks.  bf16 io
-// with heads of 64 or 128 columns takes delta_mx.hip.
+// Bound by the chain of a chunk's steps, one workgroup's behind the other, and in
+// it by the float32 matrix instructions: three prompts of 97 tokens in all, 4 heads
+// of 64 x 128, 19 us; one of 1000 tokens, 32 heads, 241 us for 32 chunks of 17000 cycles
+// (staging 3000, A and G 3100, K S^T and Q S^T 4900, the inverse 1000 more, U and y
+// 2000, the state 2900).  With heads of up to 64 columns a wavefront of its own
+// inverts while the others multiply (347 us where one of them does both, and A and
+// G come one by one).  bf16 io with heads of 64 or 128 columns takes delta_mx.hip.
 //
 // A value that is no number: one of v is to reach its column alone, from its
 // token on, and one of k, beta or alpha nothing before its token; but the
@@ -195,7 +199,7 @@ __device__ __forceinline__ void invert(Tile<P, N> &m, int lane) {
                 const f32x4 a = *reinterpret_cast<const f32x4 *>(&m.a[b0 + i][b0 + j4]);
 #pragma unroll
                 for (int r = 0; r < 4; ++r)
-                    if (j4 + r < i && j4 + r >= 0) x[i] = j4 + r >= c ? fmaf(-a[r], x[j4 + r], x[i]) : x[i];
+                    if (j4 + r < i) x[i] = fmaf(-a[r], x[j4 + r], x[i]);
             }
             m.t[b0 + i][b0 + c] = x[i];
             if (b0 == 0) m.t[i][16 + c] = 0.f;
@@ -257,7 +261,11 @@ __global__ __launch_bounds__((Shape<P, N>::NT)) void delta_scan_kernel(ScanArgs 
         for (int x = w; x < 3; x += Sh::ALL) weigh(m, x == 0 ? 0 : 1, x == 2 ? 1 : 0, c, lg);
         lds_barrier();
         if (tid == 0) m.cut = kQ;   // (all have read it)
-        if (w == Sh::ALL - 1) invert(m, lane);
+        if (w == Sh::ALL - 1) {
+            __builtin_amdgcn_s_setprio(3);   // the others wait for it
+            invert(m, lane);
+            __builtin_amdgcn_s_setprio(0);
+        }
         if (w >= NW) {
             lds_barrier();   // the inverse
             at = next;
