@@ -611,8 +611,10 @@ replay_status replay_conv_tree(const replay_config *cfg, const replay_conv_param
    dt, a: [B][W][H] f32 (beta, alpha for Gated DeltaNet layers); y: [B][W][H][P]
    f32, 16-byte aligned.  On a chain of nodes this is replay_append(W),
    replay_verify(W), replay_rollback(W) up to the order of sums.  A node's inputs reach
-   its own and its descendants' outputs alone, whatever they hold.  The ring may be
-   empty.  Sequences with BAD_TREE (or a count outside 0..L: TOO_FEW): y is NaN.  An
+   its own and its descendants' outputs alone, whatever they hold.  Nodes of Gated
+   DeltaNet layers whose weights are not finite in float32 (long keys before them on
+   their path) get what the rule gives in float32, token by token: their outputs
+   take longer.  The ring may be empty.  Sequences with BAD_TREE (or a count outside 0..L: TOO_FEW): y is NaN.  An
    infinity in a checkpoint of fewer bits may arrive as NaN.  More than 2^23
    values in a node's row of q, k or v: UNSUPPORTED. */
 replay_status replay_verify_tree(replay_handle *h, int32_t W, const int32_t *parent, const int32_t *n_nodes,

@@ -16,7 +16,10 @@
 //
 // The system is solved in blocks of 16 entries from the last one back: C_J^T =
 // T_JJ^T (G_J^T - sum_{I > J} A_IJ^T C_I^T), T_JJ the inverse of a diagonal block by
-// substitution, all of them at once.
+// substitution, all of them at once.  A row of A or T that is not finite (a value that
+// is no number, or long keys) leaves the system, and the nodes behind it, like those
+// whose weights are not finite, go through the rule token by token: T is every node's,
+// and 0 times its infinity would be every node's NaN.
 //
 // A workgroup takes one (sequence, head), a wavefront 16 of its rows: their
 // tile of S0, and the columns of v that meet it, are on their way while the
@@ -170,6 +173,12 @@ struct DotRow {
 };
 
 __device__ __forceinline__ bool tree_finite(float x) { return (__float_as_uint(x) & 0x7f800000u) != 0x7f800000u; }
+// 0, or a NaN from the first value on that is no number
+__device__ __forceinline__ float none_of(f32x4 x, float none = 0.f) {
+#pragma unroll
+    for (int u = 0; u < 4; ++u) none = fmaf(x[u], 0.f, none);
+    return none;
+}
 
 // 4 values as PARTS bf16 numbers each: 8 bits, then what is left
 template <int PARTS>
@@ -252,6 +261,79 @@ __device__ __forceinline__ f32x4 dot_parts(const WideRows<P, N, ST> &rows, const
     return out;
 }
 
+// Nodes through the gated delta rule token by token, a wavefront the 16 rows that are
+// its own, lane (row lr, columns 16 i + 4 lg + u).  Rare: it takes its arguments from
+// the kernel's again and works out its place again, so that nothing stays in registers
+// for it while the weights are made.
+template <int P, int N, int ST, bool IOB>
+__device__ __forceinline__ void run_rule(uint64_t nodes, const uint64_t *s_anc) {
+    typedef const uint64_t __attribute__((address_space(4))) word;
+    static_assert(sizeof(TreeArgs) % 8 == 0, "whole words");
+    word *from = (word *)__builtin_amdgcn_kernarg_segment_ptr();
+    asm volatile("" : "+s"(from) : : "memory");
+    uint64_t words[sizeof(TreeArgs) / 8];
+#pragma unroll
+    for (size_t i = 0; i < sizeof(TreeArgs) / 8; ++i) words[i] = from[i];
+    TreeArgs t;
+    __builtin_memcpy(&t, words, sizeof t);
+    const RingView &r = t.r;
+    const int lid = xcd_remap(blockIdx.x, gridDim.x), H = r.H, G = r.G, L = r.L, W = t.W;
+    const int b = lid / H, h = lid % H, g = h / (H / G), base = r.base[b], count = r.pos[b] - base;
+    const size_t bh = (size_t)b * H + h, bg = (size_t)b * G + g;
+    const int lane = __builtin_amdgcn_mbcnt_hi(~0u, __builtin_amdgcn_mbcnt_lo(~0u, 0)), lr = lane & 15, lg = lane >> 4;
+    const int row = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) * 16 + lr;
+    const float sc = ST == ST_FP8 ? static_cast<const float *>(t.scale)[bh] : 1.f;
+    f32x4 S[N / 16];
+    auto piece = [&](const void *rows, size_t at, int i) {   // of the row that begins at element `at`
+        IoVec<IOB, 4> x;
+        x.load(rows, at + 16 * i + 4 * lg);
+        float f[4];
+        x.widen(f);
+        return f32x4{f[0], f[1], f[2], f[3]};
+    };
+    auto over = [&](const void *rows, size_t at) {   // S x
+        f32x4 d = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < N / 16; ++i) d += S[i] * piece(rows, at, i);
+        float x = d[0] + d[1] + d[2] + d[3];
+        x += __shfl_xor(x, 16);
+        return x + __shfl_xor(x, 32);
+    };
+    auto token = [&](const void *k, size_t k_at, const void *v, size_t v_at, float beta, float alpha) {
+        const float add = beta * fmaf(-alpha, over(k, k_at), load_io1<IOB>(v, v_at + row));
+#pragma unroll
+        for (int i = 0; i < N / 16; ++i) S[i] = alpha * S[i] + add * piece(k, k_at, i);
+    };
+#pragma unroll 1
+    for (; nodes; nodes &= nodes - 1) {
+        asm volatile("" ::: "memory");
+        const int w = __builtin_ctzll(nodes);
+#pragma unroll
+        for (int i = 0; i < N / 16; ++i) {
+            const size_t e = (bh * P + row) * N + 16 * i + 4 * lg;
+            WideA<ST, false> a;
+            if constexpr (ST == ST_FP4) a.load_mx(t.S, t.scale, e);
+            else a.load(t.S, e);
+            S[i] = sc * a.f32();
+            __builtin_amdgcn_sched_barrier(0);
+        }
+#pragma unroll 1
+        for (int e = 0; e < count; ++e) {
+            const int slot = ring_slot(base % L, e, L);
+            const size_t at = dta_index(b, bh, H, L, slot);
+            token(r.k, (bg * L + slot) * N, r.v, (bh * L + slot) * P, r.dt[at], r.a[at]);
+        }
+#pragma unroll 1
+        for (uint64_t on = s_anc[w]; on; on &= on - 1) {   // a node's ancestors come before it
+            const size_t j = (size_t)b * W + __builtin_ctzll(on);
+            token(t.k, (j * G + g) * N, t.v, (j * H + h) * P, t.dt[j * H + h], t.a[j * H + h]);
+        }
+        const size_t at = (size_t)b * W + w;
+        const float y = over(t.q, (at * G + g) * N);
+        if (lg == 0) t.y[(at * H + h) * P + row] = y;
+    }
+}
+
 template <int P, int N, int ST, bool IOB, bool DELTA>
 __global__ __launch_bounds__((TreeShape<P, N>::NT), DELTA ? (IOB ? 4 : 3) : 1) void verify_tree_kernel(TreeArgs t) {
     using Sh = TreeShape<P, N>;
@@ -266,6 +348,8 @@ __global__ __launch_bounds__((TreeShape<P, N>::NT), DELTA ? (IOB ? 4 : 3) : 1) v
     __shared__ __align__(16) float s_gam[kMaxRing + kMaxTree], s_dt[kMaxRing + kMaxTree];
     __shared__ __align__(16) float s_path[kMaxTree], s_R[kMaxRing];
     __shared__ uint32_t s_odd[NW];   // a wavefront's keys hold a value that is no number
+    // the gated delta rule: ring entries and nodes whose row of A or T is not finite; nodes whose weights are not
+    __shared__ uint32_t s_lost[3], s_redo[2];
 
     const RingView &r = t.r;
     const int lid = xcd_remap(blockIdx.x, gridDim.x);
@@ -392,6 +476,9 @@ __global__ __launch_bounds__((TreeShape<P, N>::NT), DELTA ? (IOB ? 4 : 3) : 1) v
         fail();
         return;
     }
+    if (DELTA && tid < 5) (tid < 3 ? s_lost[tid] : s_redo[tid - 3]) = 0;
+    auto lose = [&](int e) { atomicOr(&s_lost[e < LP ? 0 : 1 + (e - LP) / 32], 1u << (e < LP ? e : (e - LP) % 32)); };
+    auto redo = [&](int w) { atomicOr(&s_redo[w / 32], 1u << w % 32); };
 
     // raw dots: C[w][e] = k_e . q_w, and A^T[j][i] = k_j . k_i of tiles i >= j
     if constexpr (DELTA) {
@@ -558,8 +645,7 @@ __global__ __launch_bounds__((TreeShape<P, N>::NT), DELTA ? (IOB ? 4 : 3) : 1) v
         *reinterpret_cast<f32x4 *>(s_C + w * CS + e) = c;
     }
     if constexpr (DELTA) {
-        // A^T, tiles i >= j; of values that are no numbers nothing: what they have to
-        // reach, G, beta and the decays carry
+        // A^T, tiles i >= j; of values that are no numbers nothing, their entries are lost
         for (int x = NW - 1 - wave; x < et_n * (et_n + 1) / 2; x += NW) {
             int ot = 0, et = x;
             while (et > ot) et -= ++ot;
@@ -582,7 +668,14 @@ __global__ __launch_bounds__((TreeShape<P, N>::NT), DELTA ? (IOB ? 4 : 3) : 1) v
             f32x4 c = d * vec(s_A + j * CS + i) * vec(s_dt + i);
 #pragma unroll
             for (int u = 0; u < 4; ++u)
-                if (!(on >> u & 1) || i + u <= j || i + u >= e_end || !tree_finite(c[u])) c[u] = 0.f;
+                if (!(on >> u & 1) || i + u <= j || i + u >= e_end) c[u] = 0.f;
+            if (none_of(c) != 0.f)
+#pragma unroll
+                for (int u = 0; u < 4; ++u)
+                    if (!tree_finite(c[u])) {
+                        lose(i + u);
+                        c[u] = 0.f;
+                    }
             *reinterpret_cast<f32x4 *>(s_A + j * CS + i) = c;
         }
         if constexpr (CP) {
@@ -612,6 +705,13 @@ __global__ __launch_bounds__((TreeShape<P, N>::NT), DELTA ? (IOB ? 4 : 3) : 1) v
                 }
                 s_inv[(b0 + j) * 16 + row] = y[j];   // T^T
                 __builtin_amdgcn_sched_barrier(0);
+            }
+            float none = 0.f;
+#pragma unroll
+            for (int j = 0; j < 16; j += 4) none = none_of(f32x4{y[j], y[j + 1], y[j + 2], y[j + 3]}, none);
+            if (none != 0.f) {   // its zeros off the path would be NaN, and reach every node: the entry is lost
+                lose(x);
+                for (int j = 0; j < 16; ++j) s_inv[(b0 + j) * 16 + row] = 0.f;
             }
         }
         lds_barrier();
@@ -643,6 +743,7 @@ __global__ __launch_bounds__((TreeShape<P, N>::NT), DELTA ? (IOB ? 4 : 3) : 1) v
                         for (int u = 0; u < 4; ++u) c[I] = __builtin_amdgcn_mfma_f32_16x16x4f32(-m[u], c[J][u], c[I], 0, 0, 0);
                     }
                 }
+            float none = 0.f;
 #pragma unroll
             for (int J = 0; J < Sh::MT; ++J)
                 if (J < et_n) {
@@ -651,9 +752,11 @@ __global__ __launch_bounds__((TreeShape<P, N>::NT), DELTA ? (IOB ? 4 : 3) : 1) v
                     const uint32_t on = 16 * J < LP ? in_ring >> 16 * J : (uint32_t)(nodes >> (16 * J - LP));
 #pragma unroll
                     for (int u = 0; u < 4; ++u) o[u] = on >> u & 1 ? c[J][u] * beta[u] : 0.f;
+                    none = none_of(o, none);
                     if constexpr (CP) put_parts<3>(s_P + w * at.CB + 16 * J + 4 * lg, cpart, o);
                     else *reinterpret_cast<f32x4 *>(row + 16 * J) = o;
                 }
+            if (none != 0.f) redo(w);
             if constexpr (CP)
                 if (et_n & 1)   // the other half of the last 32
 #pragma unroll
@@ -700,6 +803,7 @@ __global__ __launch_bounds__((TreeShape<P, N>::NT), DELTA ? (IOB ? 4 : 3) : 1) v
                     return __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(qs, nt < N / 16 ? (uint32_t)w * ks.stride + (16 * nt + 4 * lg) * ESZ : 0x80000000u, 0, 0));
                 };
                 u32x2 q = query(first);
+                float none = 0.f;
                 for (int nt = first; nt < N / 16; nt += turns) {
                     const u32x2 next = query(nt + turns);
                     f32x4 x = {0.f, 0.f, 0.f, 0.f};
@@ -714,9 +818,11 @@ __global__ __launch_bounds__((TreeShape<P, N>::NT), DELTA ? (IOB ? 4 : 3) : 1) v
 #pragma unroll
                     for (int rr = 0; rr < 4; ++rr)
                         o[rr] = w < n ? fmaf(gw, bf16_bits_to_f32(rr & 1 ? q[rr >> 1] >> 16 : q[rr >> 1] & 0xffffu), -x[rr]) : 0.f;
+                    none = none_of(o, none);
                     put_query(w, 16 * nt + 4 * lg, o);
                     q = next;
                 }
+                if (none != 0.f) redo(w);
             }
     } else if constexpr (DELTA) {
         for (int nt = wave; nt < N / 16; nt += NW) {
@@ -755,11 +861,20 @@ __global__ __launch_bounds__((TreeShape<P, N>::NT), DELTA ? (IOB ? 4 : 3) : 1) v
                 for (int rr = 0; rr < 4; ++rr) {
                     o[rr] = w < n ? fmaf(gw, __uint_as_float(q[wt][rr]), -x[rr]) : 0.f;
                 }
+                if (none_of(o) != 0.f) redo(w);
                 put_query(w, 16 * nt + 4 * lg, o);
             }
         }
     }
-    if constexpr (DELTA) lds_barrier();
+    uint64_t by_rule = 0;   // nodes with a lost entry on their path, or weights that are not finite
+    if constexpr (DELTA) {
+        lds_barrier();
+        auto word = [](uint32_t x) { return (uint32_t)__builtin_amdgcn_readfirstlane((int)x); };
+        by_rule = word(s_redo[0]) | (uint64_t)word(s_redo[1]) << 32;
+        const uint32_t ring = word(s_lost[0]);
+        const uint64_t lost = word(s_lost[1]) | (uint64_t)word(s_lost[2]) << 32;
+        if (ring | lost) by_rule |= __ballot(lane < n && (ring || (s_anc[lane] & lost)));
+    }
 
     // y^T: rows p0 + 4 lg + rr, nodes 16 wt + lr
     rows.transpose(reinterpret_cast<uint32_t (*)[WT::TROW]>(s_K + (WT::COAL ? wave * 16 * WT::TROW : 0)), lane);
@@ -788,7 +903,7 @@ __global__ __launch_bounds__((TreeShape<P, N>::NT), DELTA ? (IOB ? 4 : 3) : 1) v
 #pragma unroll
                 for (int u = 0; u < 4; ++u) y = __builtin_amdgcn_mfma_f32_16x16x4f32(vf[i][u], c[u], y, 0, 0, 0);
             }
-        if (w >= n) continue;
+        if (w >= n || (DELTA && by_rule >> w & 1)) continue;
         if (odd) {   // a value that is no number, for the nodes behind it alone
             for (int e = 0; e < e_end; ++e) {
                 if (!on_path(w, e)) continue;
@@ -803,6 +918,9 @@ __global__ __launch_bounds__((TreeShape<P, N>::NT), DELTA ? (IOB ? 4 : 3) : 1) v
         }
         *reinterpret_cast<f32x4 *>(&t.y[(((size_t)b * W + w) * H + h) * P + p0 + 4 * lg]) = y;
     }
+
+    if constexpr (DELTA)
+        if (by_rule) run_rule<P, N, ST, IOB>(by_rule, s_anc);
 }
 
 template <int P, int N, int ST, bool IOB, bool DELTA>
