@@ -139,7 +139,11 @@ __global__ __launch_bounds__(kNT) void logprobs_part_kernel(LogprobArgs a) {
     double sum = 0., spread = 0.;
     uint32_t ones = 0;
     uint64_t lead = ~0ull;
-    const float c = scales(T) && m > -__builtin_inff() ? 1.44269504088896340736f / T : 0.f;
+    // (m - x) log2(e) / T as (m p - x p) log2(e) / (T p), p a power of two: the distance of two
+    // logits may be past float32's range, and so may 1 / T.  With p = 2^64 m p may be infinite:
+    // logits that differ are 2^100 T apart then, and but the largest weigh nothing.
+    const float p = T > 1.f ? 0.5f : T < 0x1p-60f ? 0x1p64f : 1.f, mp = m * p;
+    const float c = scales(T) && m > -__builtin_inff() ? 1.44269504088896340736f / (T * p) : 0.f;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
         float x[E], w[E], d[E];
@@ -147,7 +151,7 @@ __global__ __launch_bounds__(kNT) void logprobs_part_kernel(LogprobArgs a) {
         if (c != 0.f) {
 #pragma unroll
             for (int e = 0; e < E; ++e) {
-                d[e] = fminf((m - x[e]) * c, 200.f);   // 2^-200 is no float32: -infinity and the far ones weigh nothing
+                d[e] = fminf(fmaf(-x[e], p, mp) * c, 200.f);   // 2^-200 is no float32: -infinity and the far ones weigh nothing
                 w[e] = __builtin_amdgcn_exp2f(-d[e]);
                 d[e] *= w[e];
             }
