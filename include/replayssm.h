@@ -555,8 +555,8 @@ replay_status replay_logprobs(int32_t B, int32_t W, int32_t V, const void *logit
    q_in, k_in, q, k: [T][G][N] (io dtype; q may be q_in and k k_in).  b_raw,
    a_raw: H values a row in the io dtype, rows b_stride and a_stride apart.
    dt_bias (or NULL) and a_log: [H] f32.  beta, alpha: [T][H] f32, which take
-   the places of dt and a.  Sums are float32, and the squares' sum has to be
-   finite there; every row is written.  Gated DeltaNet layers only. */
+   the places of dt and a.  Sums are float32, of rows scaled where their
+   squares are no float32; every row is written.  Gated DeltaNet layers only. */
 replay_status replay_delta_inputs(const replay_config *cfg, int32_t T, const void *q_in, const void *k_in,
                                   const void *b_raw, int64_t b_stride, const void *a_raw, int64_t a_stride,
                                   const float *dt_bias, const float *a_log, float q_scale, float eps, void *q, void *k,

@@ -36,9 +36,19 @@ __global__ __launch_bounds__(kNT) void delta_inputs_kernel(DeltaInputsArgs a, un
         float ss = 0.f;
 #pragma unroll
         for (int e = 0; e < E; ++e) ss = fmaf(x[e], x[e], ss);
-        ss = group_sum<LPV>(ss);
+        ss = group_sum<LPV>(ss) + a.eps;
+        if (!(ss >= 0x1p-80f && ss < 0x1p126f)) {   // squares that float32 may not hold: of the vector times a power of two
+            const float by = ss < 0x1p-80f ? 0x1p100f : 0x1p-70f;
+            ss = 0.f;
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                x[e] *= by;
+                ss = fmaf(x[e], x[e], ss);
+            }
+            ss = group_sum<LPV>(ss) + a.eps * by * by;   // the lanes of a vector are here together
+        }
         if (!in) return;
-        const float f = (key ? 1.f : a.q_scale) / sqrtf(ss + a.eps);
+        const float f = (key ? 1.f : a.q_scale) / sqrtf(ss);
 #pragma unroll
         for (int e = 0; e < E; ++e) x[e] *= f;
         void *dst = key ? a.k : a.q;
