@@ -569,7 +569,8 @@ replay_status replay_delta_inputs(const replay_config *cfg, int32_t T, const voi
    |alpha| <= 1 keep the rule from growing and are always right; beyond them the
    corrections of 64 consecutive tokens and the products of their alphas have
    to be finite in float32.  Sums, corrections and states are float32 (with bf16 io
-   products take parts that hold 24 bits of them), y is rounded once to the io dtype.
+   products take parts that hold 24 bits of them, and lack 2^-20 of a term at most), y is
+   rounded once to the io dtype.
    What is not finite in an input reaches the outputs and states that the rule lets
    it reach, and no others (an infinity may arrive as NaN).
    workspace: as for replay_scan, by replay_delta_scan_workspace.  Gated DeltaNet

@@ -4,15 +4,16 @@
 // TH of them (two or four) have the state, wavefront th the chunk's tokens 64 / TH th
 // .. in R and U and the state's rows N / TH th .. of S^T.  What one of them makes
 // enters the others' products as an operand of 32 steps or as half of one, through
-// LDS.  Two more make y, 32 tokens each, from the operands of S^T and U that lie
-// there anyway.
+// LDS.  Two more make y, tokens 0 .. 15 and 48 .. 63 or those between, from the
+// operands of S^T and U that lie there anyway.
 //
 // Bound by the chain of a chunk's steps: K S^T, R = V - diag(g) K S^T, U = T R, the
 // state, each with its cutting into parts of 8 bits, four barriers apart.  One
-// sequence of 8192 tokens (32 heads of 128 x 128), 128 chunks: 255 us with TH = 4, 293
-// with TH = 2, 343 without wavefronts for y.  Of a chunk's 4500 cycles K S^T takes 750,
-// R 400, U 1100 with its parts, the state 500, handing it on 400, what comes from
-// and goes to memory 500, the barriers 850.
+// sequence of 8192 tokens (32 heads of 128 x 128), 128 chunks: 275 us with TH = 4, some
+// 5000 cycles a chunk, of which K S^T takes 750, R 400, U with its parts more than 1100, the
+// state 500, handing it on 400, what comes from and goes to memory 500, the barriers
+// 850.  With tokens 0 .. 31 and 32 .. 63 on the wavefronts that make y, two products of G
+// and U on one and four on the other, 289.
 #include "delta_mx.h"
 
 namespace replay {
@@ -27,7 +28,7 @@ struct Few {
     static constexpr int QB = 2 * N, KN = N / 32;                      // bytes of a row; steps over it
     static constexpr int X = 4 / TH, KT = N / 16 / TH;                 // a wavefront's tiles of tokens, and of S^T
     __align__(16) uint8_t k[kQ * QB], q[kQ * QB];
-    __align__(16) uint8_t s[KN][3][kFrag], r[2][3][kFrag], e[2][3][kFrag], u[2][2][kFrag];   // operands
+    __align__(16) uint8_t s[KN][3][kFrag], r[2][3][kFrag], e[2][3][kFrag], u[2][3][kFrag];   // operands
     uint32_t odd;
 };
 
@@ -104,26 +105,26 @@ __global__ __launch_bounds__((Few<N, TH>::NT)) void delta_few_kernel(ScanArgs s)
 
     if (w >= TH) {   // y; the same barriers as below
         if (upto == from) return;
-        const int th = w - TH;   // tokens 32 th ..
+        const int tile[2] = {w - TH, 3 - (w - TH)};   // of 16 tokens: three products of G and U in all for either wavefront
         const char *qp = static_cast<const char *>(s.q) + t0 * rqk + (size_t)g * QB;
         char *yp = static_cast<char *>(s.y) + t0 * rv + ((size_t)h * P + p0) * 2;
-        const uint32_t yo = (32 * th + c) * rv + 8 * lg;
+        const uint32_t yo = c * rv + 8 * lg;
         int at[4];
-        pieces(at, 32 * th);
+        pieces(at, 0);
         Rows<N, Sh::NT - Sh::NS> rows;
-        bf8 G[2][2], G0[2][2];   // at its own step; (th = 1) at step 0
-        float gt[2];             // g of tokens 32 th + 16 x + c
+        bf8 G[3][3];   // tile[0] at step 0, tile[1] at step 1, and at step 0
+        float gt[2];   // g of tokens 16 tile[x] + c
         auto load_slot = [&](const uint8_t *from_) {   // (null: nothing is read)
-            const auto ws = make_rsrc(from_, from_ ? kSlot : 0), wx = make_rsrc(from_, from_ && th ? kSlot : 0);
+            const auto ws = make_rsrc(from_, from_ ? kSlot : 0);
+            const int at_[3] = {frag(tile[0], 0), frag(tile[1], 1), frag(tile[1], 0)};
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                gt[x] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(ws, (32 * th + 16 * x + c) * 4, kTBytes + kGBytes, 0));
+            for (int x = 0; x < 2; ++x)
+                gt[x] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(ws, (16 * tile[x] + c) * 4, kTBytes + kGBytes, 0));
 #pragma unroll
-                for (int z = 0; z < 2; ++z) {
-                    G[x][z] = __builtin_bit_cast(bf8, __builtin_amdgcn_raw_buffer_load_b128(ws, 16 * lane, kTBytes + (4 * th + 2 * x + z) * kFrag, 0));
-                    G0[x][z] = __builtin_bit_cast(bf8, __builtin_amdgcn_raw_buffer_load_b128(wx, 16 * lane, kTBytes + (8 + 2 * x + z) * kFrag, 0));
-                }
-            }
+            for (int i = 0; i < 3; ++i)
+#pragma unroll
+                for (int z = 0; z < 3; ++z)
+                    G[i][z] = __builtin_bit_cast(bf8, __builtin_amdgcn_raw_buffer_load_b128(ws, 16 * lane, kTBytes + (3 * at_[i] + z) * kFrag, 0));
         };
         rows.load(qp, rqk, upto - from, tid - Sh::NS);
         load_slot(slot);
@@ -134,13 +135,13 @@ __global__ __launch_bounds__((Few<N, TH>::NT)) void delta_few_kernel(ScanArgs s)
             qp += (size_t)kQ * rqk;
             slot += next_slot;
             rows.load(qp, rqk, left, tid - Sh::NS);
-            // S Q^T, rows p = 4 lg + r, column token 32 th + 16 x + c
+            // S Q^T, rows p = 4 lg + r, column token 16 tile[x] + c
             acc4 y[2] = {acc4{0.f, 0.f, 0.f, 0.f}, acc4{0.f, 0.f, 0.f, 0.f}};
 #pragma unroll
             for (int st = 0; st < KN; ++st) {
-                const bf8 q[2] = {operand(m.q, at, st), operand(m.q + 16 * QB, at, st)};
+                const bf8 q[2] = {operand(m.q + 16 * tile[0] * QB, at, st), operand(m.q + 16 * tile[1] * QB, at, st)};
 #pragma unroll
-                for (int z = 1; z >= 0; --z) {
+                for (int z = 2; z >= 0; --z) {
                     const bf8 p = frag16(m.s[st][z] + 16 * lane);
 #pragma unroll
                     for (int x = 0; x < 2; ++x) y[x] = mma16(p, q[x], y[x]);
@@ -152,27 +153,24 @@ __global__ __launch_bounds__((Few<N, TH>::NT)) void delta_few_kernel(ScanArgs s)
             const bool odd = m.odd != 0;
             lds_barrier();   // U
             if (!odd) {   // + U^T G^T
-                if (th) {
-                    bf8 u0[2];
+                bf8 u[2][3];
 #pragma unroll
-                    for (int z = 0; z < 2; ++z) u0[z] = frag16(m.u[0][z] + 16 * lane);
+                for (int st = 0; st < 2; ++st)
 #pragma unroll
-                    for (int z = 2; z >= 0; --z)
+                    for (int z = 0; z < 3; ++z) u[st][z] = frag16(m.u[st][z] + 16 * lane);
+                acc4 more = {0.f, 0.f, 0.f, 0.f};   // three accumulators, so that few products wait for each other
 #pragma unroll
-                        for (int x = 0; x < 2; ++x) y[x] = mma16(u0[z == 2], G0[x][z == 1], y[x]);
+                for (int z = kProducts - 1; z >= 0; --z) {
+                    y[0] = mma16(u[0][kA[z]], G[0][kB[z]], y[0]);
+                    y[1] = mma16(u[1][kA[z]], G[1][kB[z]], y[1]);
+                    more = mma16(u[0][kA[z]], G[2][kB[z]], more);
                 }
-                bf8 u[2];
-#pragma unroll
-                for (int z = 0; z < 2; ++z) u[z] = frag16(m.u[th][z] + 16 * lane);
-#pragma unroll
-                for (int z = 2; z >= 0; --z)
-#pragma unroll
-                    for (int x = 0; x < 2; ++x) y[x] = mma16(u[z == 2], G[x][z == 1], y[x]);
+                y[1] += more;
                 const auto ys = make_rsrc(yp, (uint32_t)(n - 1) * rv + 32);
 #pragma unroll
                 for (int x = 0; x < 2; ++x)
                     __builtin_amdgcn_raw_buffer_store_b64(
-                        u32x2{f32x2_to_bf16_pair(y[x][0], y[x][1]), f32x2_to_bf16_pair(y[x][2], y[x][3])}, ys, yo, 16 * x * rv, 0);
+                        u32x2{f32x2_to_bf16_pair(y[x][0], y[x][1]), f32x2_to_bf16_pair(y[x][2], y[x][3])}, ys, yo, 16 * tile[x] * rv, 0);
             }
             yp += (size_t)kQ * rv;
             load_slot(left > 0 ? slot : nullptr);
@@ -293,7 +291,6 @@ __global__ __launch_bounds__((Few<N, TH>::NT)) void delta_few_kernel(ScanArgs s)
         load_values(left < kQ ? left : kQ);
         if (!odd) {
             // U = T R
-            constexpr int a[6] = {0, 0, 1, 1, 0, 2}, o[6] = {0, 1, 0, 1, 2, 0};   // parts of T and R, the largest first
             acc4 u[X];
 #pragma unroll
             for (int x = 0; x < X; ++x) u[x] = acc4{0.f, 0.f, 0.f, 0.f};
@@ -308,21 +305,21 @@ __global__ __launch_bounds__((Few<N, TH>::NT)) void delta_few_kernel(ScanArgs s)
 #pragma unroll
                 for (int z = 0; z < 3; ++z) R0[z] = frag16(m.r[0][z] + 16 * lane);
 #pragma unroll
-                for (int z = 5; z >= 0; --z)
+                for (int z = kProducts - 1; z >= 0; --z)
 #pragma unroll
                     for (int x = 0; x < X; ++x) {
-                        u0[x] = mma16(T0[x][a[z]], R0[o[z]], u0[x]);
-                        u[x] = mma16(T[x][a[z]], Ro[o[z]], u[x]);
+                        u0[x] = mma16(T0[x][kA[z]], R0[kB[z]], u0[x]);
+                        u[x] = mma16(T[x][kA[z]], Ro[kB[z]], u[x]);
                     }
 #pragma unroll
                 for (int x = 0; x < X; ++x) u[x] += u0[x];
             } else {
 #pragma unroll
-                for (int z = 5; z >= 0; --z)
+                for (int z = kProducts - 1; z >= 0; --z)
 #pragma unroll
-                    for (int x = 0; x < X; ++x) u[x] = mma16(T[x][a[z]], Ro[o[z]], u[x]);
+                    for (int x = 0; x < X; ++x) u[x] = mma16(T[x][kA[z]], Ro[kB[z]], u[x]);
             }
-            put_tiles<2, X>(m.u[0][0], X * th, u, lane);
+            put_tiles<3, X>(m.u[0][0], X * th, u, lane);
 #pragma unroll
             for (int x = 0; x < X; ++x) u[x] *= e[x];
             put_tiles<3, X>(m.e[0][0], X * th, u, lane);
@@ -379,9 +376,9 @@ hipError_t launch_one(const ScanArgs &a, hipStream_t s) {
 
 // Whether every workgroup has a CU of its own.  Two of TH = 4 and 128 columns of
 // state on one are slower than two of TH = 2: 2048 tokens of 32 heads of 128 x 128 take
-// 87 us with TH = 4 and 96 with TH = 2, of 64 heads 156 and 131.  With 64 columns of
-// state, half the LDS traffic, TH = 4 is ahead in both: 64 heads of 64 x 64 77 and
-// 93 us, 128 heads 109 and 120.
+// 79 us with TH = 4 and 92 with TH = 2, of 64 heads 143 and 123.  With 64 columns of
+// state, half the LDS traffic, TH = 4 is ahead in both: 64 heads of 64 x 64 73 and
+// 81 us, 128 heads 110 and 115.
 bool alone(int P, const ScanArgs &a) { return (int64_t)a.B * a.H * P / 16 <= kFewCUs; }
 
 }  // namespace

@@ -15,15 +15,18 @@ typedef float acc4 __attribute__((ext_vector_type(4)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 
 // A head's chunk in the workspace: T's operands (tiles of 16 tokens by steps of
-// 32, three parts each), G's (two parts), g and e, and whether the chunk holds a value
+// 32, three parts each), G's, g and e, and whether the chunk holds a value
 // that is no number.  Operand x < 4 is tile x at the step its tokens are in,
 // the two behind them are tiles 2 and 3 at step 0.
 constexpr int kFrag = 1024, kFrags = 6;
-constexpr int kTBytes = kFrags * 3 * kFrag, kGBytes = kFrags * 2 * kFrag;
+constexpr int kTBytes = kFrags * 3 * kFrag, kGBytes = kTBytes;
 constexpr int kImage = kTBytes + kGBytes + 2 * kQ * 4;
 constexpr int kSlot = (kImage + 16 + 255) / 256 * 256;
 static_assert(kImage % 16 == 0, "whole pieces");
 __host__ __device__ constexpr int frag(int tile, int step) { return step == tile >> 1 ? tile : tile + 2; }
+// A product of two operands in three parts: parts kA[z] and kB[z], the largest first.
+// What is left out is 2^-20 of a term at most.
+constexpr int kProducts = 6, kA[kProducts] = {0, 0, 1, 1, 0, 2}, kB[kProducts] = {0, 1, 0, 1, 2, 0};
 
 __device__ __forceinline__ acc4 mma16(bf8 a, bf8 b, acc4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);

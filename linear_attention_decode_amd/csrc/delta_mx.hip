@@ -11,16 +11,16 @@
 // columns: each has half of a chunk's tokens, and half of S^T's rows, which stay in
 // its accumulators; where heads are fewer still, delta_few.hip has more of them.
 // What bounds it: the chain of a chunk's steps, four barriers apart.  Sixteen
-// ragged sequences of 15013 tokens (32 heads of 128 x 128): 88 us for T and G, 329 for
+// ragged sequences of 15013 tokens (32 heads of 128 x 128): 89 us for T and G, 366 for
 // the chunks, eight wavefronts a CU that wait for LDS, for the matrix instructions
-// and for each other in turn; one of 8192 tokens 44, and 255 in delta_few.hip.  The
-// float32 kernel takes 889 and 3410 us.
+// and for each other in turn; one of 8192 tokens 47, and 275 in delta_few.hip.
 //
-// What bf16 operands leave out: k and q are bf16 as they are; S, R, T and e U
-// go into the products that make the state as three parts of 8 bits, which
-// hold their 24 (of T R the six products that weigh 2^-16 or more), so U and
-// the state are what float32 products give; S, U and G enter y's products as two
-// parts, so that a term lacks 2^-15 of itself at most, and y is rounded once.
+// What bf16 operands leave out: k and q are bf16 as they are; S, R, T, U, e U and G
+// go into the products as three parts of 8 bits, which hold their 24 (of T R and G U
+// the six products that weigh 2^-16 or more: what is left out is 2^-20 of a term at
+// most), so U, the state and y are what float32 products give, and y is rounded once.
+// With two parts in y's products one value in 160 rounds otherwise, and one long prompt
+// takes 291 us instead of 302, the ragged batch below 382 instead of 427.
 //
 // Layouts (16 x 16 x 32 products).  An accumulator tile holds in lane (column
 // c, group lg) rows 4 lg .. 4 lg + 3; an operand of 32 steps in lane (row or
@@ -109,7 +109,7 @@ __device__ __forceinline__ f32x4 decays_of(const Decays &d, int ti, int tj, int 
 
 // A workgroup makes a chunk of HP heads of a group, which share k . k and k . q.  Bound
 // by its own chain (products, decays, the inverse by blocks of 16, their products)
-// and by what it writes: 8192 tokens of 32 heads 44 us, 2.9 TB/s of the 129 MB.
+// and by what it writes: 8192 tokens of 32 heads 47 us, 3.3 TB/s of the 154 MB.
 template <int N, int HP>
 __global__ __launch_bounds__(kPrepNT) void delta_prep_kernel(ScanArgs s) {
     __shared__ __align__(16) PrepTile m[HP];
@@ -125,7 +125,7 @@ __global__ __launch_bounds__(kPrepNT) void delta_prep_kernel(ScanArgs s) {
 
     // tiles (ti, tj) of K K^T and K Q^T, lane (column i = c, rows j = 4 lg + r): a
     // wavefront has one ti and the pairs of tj that make G's operands of it, so that
-    // it writes them whole (written half by half all takes 55 us for 44).  Two of the tiles lie above the
+    // it writes them whole (written half by half they take a fourth longer).  Two of the tiles lie above the
     // diagonal, zeros of T and G.  Rows past the chunk's tokens read zero.
     const int ti = w < 2 ? w + 2 : w - 2, pairs = w < 2 ? 2 : 1;
     acc4 kk[4], qk[4];
@@ -198,27 +198,25 @@ __global__ __launch_bounds__(kPrepNT) void delta_prep_kernel(ScanArgs s) {
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
             if (x == pairs) break;
-            u32x4 hi, lo;   // G's operand, upper and lower parts
+            acc4 o[2];   // G's operand
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
                 const int z = 2 * x + half, j0 = 16 * z + 4 * lg;
                 f32x4 D = {0.f, 0.f, 0.f, 0.f};
                 if (z <= ti) D = decays_of(m[y].d, ti, z, c, lg);
-                f32x4 a, o;
+                f32x4 a;
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
                     a[r] = j0 + r < i ? be * (kk[z][r] * D[r]) : 0.f;
-                    o[r] = j0 + r <= i ? qk[z][r] * D[r] : 0.f;
+                    o[half][r] = j0 + r <= i ? qk[z][r] * D[r] : 0.f;
                 }
                 *reinterpret_cast<f32x4 *>(&m[y].a[i][j0]) = a;   // (zeros above the diagonal are T's too)
-                hi[2 * half] = upper_pair(o[0], o[1]);
-                hi[2 * half + 1] = upper_pair(o[2], o[3]);
-                lo[2 * half] = lower_pair(o[0], o[1]);
-                lo[2 * half + 1] = lower_pair(o[2], o[3]);
             }
-            uint8_t *to = to_head + frag(ti, x) * 2 * kFrag + lane * 16;
-            *reinterpret_cast<u32x4 *>(to) = hi;
-            *reinterpret_cast<u32x4 *>(to + kFrag) = lo;
+            bf8 parts[3];
+            split<3>(o[0], o[1], parts);
+            uint8_t *to = to_head + frag(ti, x) * 3 * kFrag + lane * 16;
+#pragma unroll
+            for (int z = 0; z < 3; ++z) put_frag(to + z * kFrag, parts[z]);
         }
     }
     lds_barrier();
@@ -280,10 +278,11 @@ struct Shape {
     static_assert(P % PC == 0 && kQ * QB / 16 % NT == 0, "whole pieces");
 };
 
-// What the two wavefronts of 16 columns hand each other, as operands.
+// What the two wavefronts of 16 columns hand each other, as operands.  Once K S^T is made
+// U lies in place of s: of either's tokens where the other, which reads it, has its part.
 template <int KN>
 struct Exchange {
-    uint8_t s[KN][3][kFrag], e[2][3][kFrag], r[3][kFrag], u[2][kFrag];
+    uint8_t s[KN][3][kFrag], e[2][3][kFrag], r[3][kFrag];
 };
 template <int P, int N>
 struct Tile {
@@ -343,8 +342,9 @@ struct Values {
     }
 };
 
-// What a wavefront takes of a chunk's slot, from the copy in LDS: T and G at its own
-// step and (th = 1) at step 0, g and e of the tokens of v, g of tokens 32 th + 16 x + c and of the last.
+// What a wavefront takes of a chunk's slot, from the copy in LDS: T at its own step and
+// (th = 1) at step 0, g and e of the tokens of v, g of the last; for its two tiles of y,
+// th and 3 - th, G of the first at step 0, of the other at step 1 and at step 0, and g.
 struct Slot {
     const uint8_t *frags, *decay, *natural, *base;
     int step;
@@ -352,23 +352,25 @@ struct Slot {
         base = m;
         frags = m + 16 * lane;
         decay = m + kTBytes + kGBytes + (32 * th + 4 * (lane >> 4)) * 4;
-        natural = m + kTBytes + kGBytes + (32 * th + (lane & 15)) * 4;
+        natural = m + kTBytes + kGBytes + (lane & 15) * 4;
         step = th;
     }
     __device__ __forceinline__ bf8 t(int x, int z) const { return frag16(frags + (6 * step + 3 * x + z) * kFrag); }
     __device__ __forceinline__ bf8 tx(int x, int z) const { return frag16(frags + (12 + 3 * x + z) * kFrag); }
-    __device__ __forceinline__ bf8 g(int x, int z) const { return frag16(frags + kTBytes + (4 * step + 2 * x + z) * kFrag); }
-    __device__ __forceinline__ bf8 gx(int x, int z) const { return frag16(frags + kTBytes + (8 + 2 * x + z) * kFrag); }
+    __device__ __forceinline__ bf8 g(int i, int z) const {
+        return frag16(frags + kTBytes + (3 * (i == 0 ? frag(step, 0) : frag(3 - step, i == 1)) + z) * kFrag);
+    }
     __device__ __forceinline__ f32x4 d(int x) const { return *reinterpret_cast<const f32x4 *>(decay + 64 * x); }
     __device__ __forceinline__ f32x4 e(int x) const { return *reinterpret_cast<const f32x4 *>(decay + 4 * kQ + 64 * x); }
-    __device__ __forceinline__ float dn(int x) const { return *reinterpret_cast<const float *>(natural + 64 * x); }
+    __device__ __forceinline__ float dn(int x) const { return *reinterpret_cast<const float *>(natural + 64 * (x ? 3 - step : step)); }
     __device__ __forceinline__ float all() const { return *reinterpret_cast<const float *>(base + kTBytes + kGBytes + 4 * (kQ - 1)); }
     __device__ __forceinline__ uint32_t odd() const { return *reinterpret_cast<const uint32_t *>(base + kImage); }
 };
 
 // Two wavefronts take 16 columns: th = 0, 1 have the chunk's tokens 32 th ..
-// in R, U and y, and the state's rows N / 2 th .. in S^T.  The system is lower
-// triangular, so that th = 0 needs nothing of th = 1 for R, U and y.
+// in R and U, the state's rows N / 2 th .. in S^T, and of y's four tiles of 16 tokens
+// th and 3 - th, three products of G and U either (with 32 tokens each th = 1 has four and
+// th = 0 two).  The system is lower triangular, so that th = 0 needs nothing of th = 1 for R and U.
 template <int P, int N>
 __global__ __launch_bounds__((Shape<P, N>::NT), 2) void delta_mx_kernel(ScanArgs s) {
     using Sh = Shape<P, N>;
@@ -427,7 +429,7 @@ __global__ __launch_bounds__((Shape<P, N>::NT), 2) void delta_mx_kernel(ScanArgs
     char *yp = static_cast<char *>(s.y) + t0 * rv + ((size_t)h * P + p0) * 2;
     const uint8_t *slot = reinterpret_cast<const uint8_t *>(s.ws) + ((size_t)b * s.window * s.H + h) * kSlot;
     const size_t next_slot = (size_t)s.H * kSlot;
-    const uint32_t vo = (32 * th + 4 * lg) * rv + 2 * c, yo = (32 * th + c) * rv + 8 * lg;
+    const uint32_t vo = (32 * th + 4 * lg) * rv + 2 * c, yo = c * rv + 8 * lg;
     // places in a row's 128 bytes of the four pieces 4 i + lg, and of k^T's 4 i + c % 4
     int piece[4], col[4];
 #pragma unroll
@@ -439,8 +441,9 @@ __global__ __launch_bounds__((Shape<P, N>::NT), 2) void delta_mx_kernel(ScanArgs
         const int o = 16 * QB * x + 128 * (st >> 1), i = 2 * (st & 1);
         return row8(rows + piece[i] + o, rows + piece[i + 1] + o);
     };
+    const int tile[2] = {th, 3 - th};   // of y
     const uint8_t *const xl = reinterpret_cast<const uint8_t *>(&ex) + 16 * lane;
-    constexpr int kE = KN * 3 * kFrag, kR = kE + 6 * kFrag, kU = kR + 3 * kFrag;       // places in Exchange
+    constexpr int kE = KN * 3 * kFrag, kR = kE + 6 * kFrag, kU = KH * 3 * kFrag;       // places in Exchange (kU: of th = 1)
     Ahead<P, N> ahead;
     Values val;
     Slot my;
@@ -459,10 +462,10 @@ __global__ __launch_bounds__((Shape<P, N>::NT), 2) void delta_mx_kernel(ScanArgs
         slot += next_slot;
         ahead.load(kp, qp, rqk, left, slot);
         // K S^T, rows token 32 th + 16 x + 4 lg + r, column c.  S Q^T, rows p = 4
-        // lg + r, column token 32 th + 16 x + c, comes behind U: here all wavefronts would
+        // lg + r, column token 16 tile[x] + c, comes behind U: here all wavefronts would
         // read k, q and S at once.
         acc4 ks[2], y[2];
-        bf8 part[KN][2];   // S's first two parts, kept for S Q^T
+        bf8 part[KN][3];   // S, kept for S Q^T
 #pragma unroll
         for (int st = 0; st < KN; ++st) {
             bf8 k[2];
@@ -470,8 +473,7 @@ __global__ __launch_bounds__((Shape<P, N>::NT), 2) void delta_mx_kernel(ScanArgs
             for (int x = 0; x < 2; ++x) k[x] = operand(m.k, x, st);
 #pragma unroll
             for (int z = 2; z >= 0; --z) {
-                const bf8 p = frag16(xl + (3 * st + z) * kFrag);
-                if (z < 2) part[st][z] = p;
+                const bf8 p = part[st][z] = frag16(xl + (3 * st + z) * kFrag);
 #pragma unroll
                 for (int x = 0; x < 2; ++x) ks[x] = mma16(k[x], p, st == 0 && z == 2 ? acc4{0.f, 0.f, 0.f, 0.f} : ks[x]);
             }
@@ -497,29 +499,27 @@ __global__ __launch_bounds__((Shape<P, N>::NT), 2) void delta_mx_kernel(ScanArgs
         lds_barrier();   // R of the first tokens
         const bool odd = odd_chunk != 0;
         val.load(vp, rv, left < kQ ? left : kQ, vo);
-        bf8 up[2], ep[3];
+        bf8 up[3], ep[3];
         if (!odd) {
             acc4 u[2];
 #pragma unroll
             for (int x = 0; x < 2; ++x) u[x] = acc4{0.f, 0.f, 0.f, 0.f};
-            constexpr int a[6] = {0, 0, 1, 1, 0, 2}, o[6] = {0, 1, 0, 1, 2, 0};   // parts of T and R, the largest first
             if (th) {
                 bf8 rx[3];
 #pragma unroll
                 for (int z = 0; z < 3; ++z) rx[z] = frag16(xl + kR + z * kFrag);
 #pragma unroll
-                for (int z = 5; z >= 0; --z)
+                for (int z = kProducts - 1; z >= 0; --z)
 #pragma unroll
-                    for (int x = 0; x < 2; ++x) u[x] = mma16(my.tx(x, a[z]), rx[o[z]], u[x]);
+                    for (int x = 0; x < 2; ++x) u[x] = mma16(my.tx(x, kA[z]), rx[kB[z]], u[x]);
             }
 #pragma unroll
-            for (int z = 5; z >= 0; --z)
+            for (int z = kProducts - 1; z >= 0; --z)
 #pragma unroll
-                for (int x = 0; x < 2; ++x) u[x] = mma16(my.t(x, a[z]), rp[o[z]], u[x]);
-            split<2>(u[0], u[1], up);
-            if (th == 0)
+                for (int x = 0; x < 2; ++x) u[x] = mma16(my.t(x, kA[z]), rp[kB[z]], u[x]);
+            split<3>(u[0], u[1], up);
 #pragma unroll
-                for (int z = 0; z < 2; ++z) put_frag(ex.u[z] + 16 * lane, up[z]);
+            for (int z = 0; z < 3; ++z) put_frag(ex.s[th ? 0 : KH][z] + 16 * lane, up[z]);
 #pragma unroll
             for (int x = 0; x < 2; ++x) u[x] *= my.e(x);
             split<3>(u[0], u[1], ep);
@@ -529,11 +529,11 @@ __global__ __launch_bounds__((Shape<P, N>::NT), 2) void delta_mx_kernel(ScanArgs
             for (int st = 0; st < KN; ++st) {
                 bf8 q[2];
 #pragma unroll
-                for (int x = 0; x < 2; ++x) q[x] = operand(m.q, x, st);
+                for (int x = 0; x < 2; ++x) q[x] = operand(m.q + (16 * tile[x] - 32 * th) * QB, 0, st);
 #pragma unroll
-                for (int z = 1; z >= 0; --z)
+                for (int z = 2; z >= 0; --z)
 #pragma unroll
-                    for (int x = 0; x < 2; ++x) y[x] = mma16(part[st][z], q[x], st == 0 && z == 1 ? acc4{0.f, 0.f, 0.f, 0.f} : y[x]);
+                    for (int x = 0; x < 2; ++x) y[x] = mma16(part[st][z], q[x], st == 0 && z == 2 ? acc4{0.f, 0.f, 0.f, 0.f} : y[x]);
             }
 #pragma unroll
             for (int x = 0; x < 2; ++x) y[x] *= my.dn(x);
@@ -542,27 +542,29 @@ __global__ __launch_bounds__((Shape<P, N>::NT), 2) void delta_mx_kernel(ScanArgs
             __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup");
         }
         const float all = my.all();   // (before the slot's next chunk is loaded)
-        lds_barrier();   // U of the first tokens, e U of all
+        lds_barrier();   // U and e U
         if (!odd) {
-            // y^T: + U^T G^T
-            if (th) {
-                bf8 ux[2];
+            // y^T: + U^T G^T, in three accumulators, so that few products wait for each other
+            bf8 ux[3];
 #pragma unroll
-                for (int z = 0; z < 2; ++z) ux[z] = frag16(xl + kU + z * kFrag);
+            for (int z = 0; z < 3; ++z) ux[z] = frag16(xl + (th ? kU : 0) + z * kFrag);
+            acc4 more = {0.f, 0.f, 0.f, 0.f};
+            auto add = [&](const bf8 *u0, const bf8 *u1) {
 #pragma unroll
-                for (int z = 2; z >= 0; --z)
-#pragma unroll
-                    for (int x = 0; x < 2; ++x) y[x] = mma16(ux[z == 2], my.gx(x, z == 1), y[x]);
-            }
-#pragma unroll
-            for (int z = 2; z >= 0; --z)
-#pragma unroll
-                for (int x = 0; x < 2; ++x) y[x] = mma16(up[z == 2], my.g(x, z == 1), y[x]);
+                for (int z = kProducts - 1; z >= 0; --z) {
+                    y[0] = mma16(u0[kA[z]], my.g(0, kB[z]), y[0]);
+                    y[1] = mma16(u1[kA[z]], my.g(1, kB[z]), y[1]);
+                    more = mma16(u0[kA[z]], my.g(2, kB[z]), more);
+                }
+            };
+            if (th) add(ux, up);
+            else add(up, ux);
+            y[1] += more;
             const auto ys = make_rsrc(yp, (uint32_t)(n - 1) * rv + 32);
 #pragma unroll
             for (int x = 0; x < 2; ++x)
                 __builtin_amdgcn_raw_buffer_store_b64(
-                    u32x2{f32x2_to_bf16_pair(y[x][0], y[x][1]), f32x2_to_bf16_pair(y[x][2], y[x][3])}, ys, yo, 16 * x * rv, 0);
+                    u32x2{f32x2_to_bf16_pair(y[x][0], y[x][1]), f32x2_to_bf16_pair(y[x][2], y[x][3])}, ys, yo, 16 * tile[x] * rv, 0);
             // S^T <- (whole decay) S^T + K^T (e U), the wavefront's own tokens first
             bf8 ox[3];
 #pragma unroll
@@ -623,8 +625,8 @@ hipError_t launch_pn(ScanArgs a, hipStream_t s) {
         if (e != hipSuccess) return e;
         // delta_few.hip's workgroups of 16 columns read k, q and T four times as often,
         // but there are four times as many to keep the card busy.  2048 tokens, 64
-        // columns of a head counted as one, state of 128 columns: 128 of them 131 us there,
-        // 160 here; 192: 207 and 200; state of 64: 128 of them 109 and 143, 192: 193 and 171.
+        // columns of a head counted as one, state of 128 columns: 128 of them 123 us there,
+        // 168 here; 192: 194 and 183; state of 64: 128 of them 110 and 157, 192: 218 and 210.
         e = (int64_t)a.B * a.H * P / 64 > 128 ? launch_chain<P, N>(a, s) : launch_delta_few(P, N, a, s);
         if (e != hipSuccess) return e;
     }
