@@ -573,7 +573,9 @@ replay_status replay_delta_inputs(const replay_config *cfg, int32_t T, const voi
    rounded once to the io dtype.
    What is not finite in an input reaches the outputs and states that the rule lets
    it reach, and no others (an infinity may arrive as NaN).
-   workspace: as for replay_scan, by replay_delta_scan_workspace.  Gated DeltaNet
+   workspace: as for replay_scan, by replay_delta_scan_workspace.  With bf16 io and heads
+   of 64 or more it holds 64 tokens of every sequence and head in 37632 bytes, as many
+   times as there are such chunks and 512 MiB hold, but once at least.  Gated DeltaNet
    layers only (Mamba-2: UNSUPPORTED). */
 replay_status replay_delta_scan_workspace(const replay_config *cfg, int32_t T, int32_t max_len, size_t *bytes);
 replay_status replay_delta_scan(const replay_config *cfg, int32_t T, int32_t max_len, const int32_t *cu_seqlens,
