@@ -38,7 +38,7 @@ __device__ __forceinline__ bool odd_pair(uint32_t w) {   // a bf16 pair with a v
     return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
 }
 
-// Eight (four) floats as one, two or three operands that hold 8 bits each, the last one rounded.
+// Eight (four) floats as PARTS operands that hold 8 bits each, the last one rounded.
 template <int PARTS>
 __device__ __forceinline__ void split(const acc4 &lo, const acc4 &hi, bf8 *out) {
     float x[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};

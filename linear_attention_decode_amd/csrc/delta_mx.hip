@@ -638,10 +638,6 @@ constexpr size_t kMostWorkspace = (size_t)512 << 20;
 
 }  // namespace
 
-bool delta_mx_supported(int P, int N, const ScanArgs &a) {
-    return a.io_bf16 && a.window > 0;
-}
-
 int delta_window(int P, int N, int B, int H, bool bf16, int longest, size_t *bytes) {
     *bytes = 0;
     if (!bf16 || P < 64) return 0;

@@ -352,20 +352,16 @@ hipError_t launch_one(const ScanArgs &a, hipStream_t s) {
     return hipGetLastError();
 }
 
-template <bool IOB>
-hipError_t launch_io(int P, int N, const ScanArgs &a, hipStream_t s) {
-    if (P == 16 && N == 16) return launch_one<16, 16, IOB>(a, s);
-    if (P == 64 && N == 64) return launch_one<64, 64, IOB>(a, s);
-    if (P == 64 && N == 128) return launch_one<64, 128, IOB>(a, s);
-    if (P == 128 && N == 128) return launch_one<128, 128, IOB>(a, s);
-    return hipErrorInvalidValue;
-}
-
 }  // namespace
 
 hipError_t launch_delta_scan(int P, int N, const ScanArgs &a, hipStream_t s) {
-    if (delta_mx_supported(P, N, a)) return launch_delta_mx(P, N, a, s);
-    return a.io_bf16 ? launch_io<true>(P, N, a, s) : launch_io<false>(P, N, a, s);
+    if (a.window > 0) return launch_delta_mx(P, N, a, s);   // bf16, but for heads of 16 columns (delta_window)
+    if (P == 16 && N == 16) return a.io_bf16 ? launch_one<16, 16, true>(a, s) : launch_one<16, 16, false>(a, s);
+    if (a.io_bf16) return hipErrorInvalidValue;
+    if (P == 64 && N == 64) return launch_one<64, 64, false>(a, s);
+    if (P == 64 && N == 128) return launch_one<64, 128, false>(a, s);
+    if (P == 128 && N == 128) return launch_one<128, 128, false>(a, s);
+    return hipErrorInvalidValue;
 }
 
 }  // namespace replay

@@ -488,6 +488,8 @@ __device__ __forceinline__ float bcast(float x, int lane) {
     return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(x), lane));
 }
 
+__device__ __forceinline__ bool finite(float x) { return (__float_as_uint(x) & 0x7f800000u) != 0x7f800000u; }
+
 // Sum over aligned groups of TS lanes (TS a power of two, <= 64); every lane
 // of the group gets the sum.
 template <int TS>

@@ -65,8 +65,6 @@ __device__ __forceinline__ Span find_span(const ScanArgs &a, int b, int seg) {
     return {s0 + at, left < a.seg_len ? left : a.seg_len, true, left <= a.seg_len};
 }
 
-__device__ __forceinline__ bool finite(float x) { return (__float_as_uint(x) & 0x7f800000u) != 0x7f800000u; }
-
 // The value of the lane d before (behind) this one in its row of 16, 1 past the row's end.
 template <int CTRL>
 __device__ __forceinline__ float row_move(float x) {
@@ -120,10 +118,9 @@ __device__ __forceinline__ uint32_t lower_pair(float x, float y) { return f32x2_
 // states into the workspace).
 bool scan_mx_supported(int P, int N, const ScanArgs &a);
 int scan_mx_heads(int P, int H, int G);
-// The same of launch_delta_scan (delta_mx.hip), with the bytes of workspace it
-// needs and the chunks of a sequence that it covers at a time.
-bool delta_mx_supported(int P, int N, const ScanArgs &a);
-hipError_t launch_delta_mx(int P, int N, const ScanArgs &a, hipStream_t s);
 hipError_t launch_scan_mx(int P, int N, const ScanArgs &a, bool state_only, hipStream_t s);
+// The bf16 kernels' part of launch_delta_scan (delta_mx.hip): where the workspace
+// holds chunks (a.window > 0).
+hipError_t launch_delta_mx(int P, int N, const ScanArgs &a, hipStream_t s);
 
 }  // namespace replay

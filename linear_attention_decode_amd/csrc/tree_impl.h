@@ -172,7 +172,6 @@ struct DotRow {
     }
 };
 
-__device__ __forceinline__ bool tree_finite(float x) { return (__float_as_uint(x) & 0x7f800000u) != 0x7f800000u; }
 // 0, or a NaN from the first value on that is no number
 __device__ __forceinline__ float none_of(f32x4 x, float none = 0.f) {
 #pragma unroll
@@ -191,7 +190,7 @@ __device__ __forceinline__ void split_parts(f32x4 x, u32x2 *out) {
             u[i] = __float_as_uint(z == 0 ? __builtin_canonicalizef(x[i]) : x[i]);   // a NaN stays one
             if (z + 1 < PARTS) {
                 const float left = x[i] - __uint_as_float(u[i] & 0xffff0000u);
-                x[i] = z > 0 || tree_finite(x[i]) ? left : 0.f;
+                x[i] = z > 0 || finite(x[i]) ? left : 0.f;
             }
         }
         out[z] = u32x2{u[0] >> 16 | (u[1] & 0xffff0000u), u[2] >> 16 | (u[3] & 0xffff0000u)};
@@ -608,7 +607,7 @@ __global__ __launch_bounds__((TreeShape<P, N>::NT), DELTA ? (IOB ? 4 : 3) : 1) v
         for (int u = 0; u < 4; ++u) {
             asm volatile("" : "+v"(vc[i][u]));   // its load ends here, not where it was sent
             vf[i][u] = entry_value<IOB>(vc[i][u]);
-            if (!tree_finite(vf[i][u])) {
+            if (!finite(vf[i][u])) {
                 vf[i][u] = 0.f;
                 vc[i][u] = 0;
                 odd = true;
@@ -672,7 +671,7 @@ __global__ __launch_bounds__((TreeShape<P, N>::NT), DELTA ? (IOB ? 4 : 3) : 1) v
             if (none_of(c) != 0.f)
 #pragma unroll
                 for (int u = 0; u < 4; ++u)
-                    if (!tree_finite(c[u])) {
+                    if (!finite(c[u])) {
                         lose(i + u);
                         c[u] = 0.f;
                     }
@@ -839,7 +838,7 @@ __global__ __launch_bounds__((TreeShape<P, N>::NT), DELTA ? (IOB ? 4 : 3) : 1) v
 #pragma unroll
                     for (int u = 0; u < 4; ++u) {
                         const float k = s_K[(16 * i + 4 * lg + u) * KS + 16 * nt + lr];
-                        kc[i][u] = tree_finite(k) ? k : 0.f;   // another's weight makes its nodes NaN as it is
+                        kc[i][u] = finite(k) ? k : 0.f;   // another's weight makes its nodes NaN as it is
                     }
 #pragma unroll
             for (int wt = 0; wt < kMaxTree / 16; ++wt) {
@@ -910,7 +909,7 @@ __global__ __launch_bounds__((TreeShape<P, N>::NT), DELTA ? (IOB ? 4 : 3) : 1) v
 #pragma unroll
                 for (int rr = 0; rr < 4; ++rr) {
                     const float v = entry_value<IOB>(load_raw<IOB>(vs.rows_of(e & ~15), vs.at(e & ~15, e & 15), p0 + 4 * lg + rr));
-                    if (tree_finite(v)) continue;
+                    if (finite(v)) continue;
                     if constexpr (CP) y[rr] = fmaf(bf16_bits_to_f32(s_P[w * at.CB + e]), v, y[rr]);   // its sign and whether it is 0
                     else y[rr] = fmaf(s_C[w * CS + e], v, y[rr]);
                 }
