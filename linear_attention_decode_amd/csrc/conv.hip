@@ -383,9 +383,10 @@ __global__ __launch_bounds__(kStepNT) void conv_step_kernel(ConvArgs a, int CB) 
 // those before the tree in the state: neighbours in a tree find them in the
 // caches, and no load waits for another.
 //
-// 256 sequences of 16 nodes, 6144 channels in bf16: 33 us, 3.4 TB/s of 111 MB, three
-// wavefronts a SIMD and their vector instructions; with 8 and 4 nodes a workgroup,
-// which read more of their ancestors again, 8 and 22 us more.  One sequence of 10240
+// 256 sequences of 16 nodes, 6144 channels in bf16: 33 us, 3.4 TB/s of 111 MB, 77 of them
+// at HBM: three wavefronts a SIMD, each of which four times over sends 16 loads and
+// waits for them (its 1560 vector instructions are a ninth of its cycles); with 8 and 4
+// nodes a workgroup, which read more of their ancestors again, 8 and 22 us more.  One sequence of 10240
 // channels has too few workgroups of 16: 5.6 us, a launch and one chain of loads.
 template <bool BF16, bool AL, int K>
 __global__ __launch_bounds__(kStepNT) void conv_tree_kernel(ConvArgs a, int CB, int NB, int per, int gates) {

@@ -28,14 +28,15 @@
 // k of the gated delta rule) holds bf16 numbers or fewer bits, on v_mfma_f32_16x16x32_bf16
 // with x and C as three numbers of 8 bits each, which is exact.
 //
-// Mamba-2 is bound by HBM: 256 sequences of 64 heads of 64 x 128, rings of up to 16
-// and trees of up to 16 nodes, 158 us, 4.1 TB/s of 648 MB.  The gated delta rule by
-// the chain of a workgroup's steps, two workgroups a CU (LDS): 96 sequences of 32
-// heads of 128 x 128, trees of up to 41 nodes against an e4m3 copy, 126 us for 169 MB;
-// of a workgroup's 42000 cycles 8500 wait for its loads, the dots take 8000, the
-// inverses 4000, the solve 4700, the queries 6800, the outputs 5400.  The order of the
-// loads is worth 41 and 86 us (S0 first kept all others waiting), the bf16
-// instructions 30.
+// Bound by workgroups that load, wait and compute in turn.  Mamba-2, four of them a CU: 256
+// sequences of 64 heads of 64 x 128, rings of up to 16 and trees of up to 16 nodes, 155 us
+// for 678 MB, of which 286 come from HBM and the rest from the last-level cache (a copy
+// in bf16 116 us for 410 MB, e4m3 102 for 276, FP4, whose blocks have a product each,
+// 129 for 213).  The gated delta rule, two a CU (LDS): 96 sequences of 32 heads of 128 x 128,
+// trees of up to 41 nodes against an e4m3 copy, 126 us for 190 MB; of a workgroup's 43000
+// cycles 8500 wait for its loads, the dots take 8000, the inverses 4000, the solve
+// 4700, the queries 6800, the outputs 5400.  The order of the loads is worth 41 and 86 us
+// (S0 first kept all others waiting), the bf16 instructions 30.
 #pragma once
 
 #include "tree.h"
